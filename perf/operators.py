@@ -12,7 +12,7 @@ import torch
 own = False
 
 ATTENTION, APPEND, GATHER, ACCEPT = "attention", "append", "gather", "accept"
-E_MIN, E_MAX = -100, 120      # exponents of the cache's power-of-two scales
+E_MIN, E_MAX = -100, 119      # exponents of the cache's power-of-two scales
 WEIGHT = 2.0 ** 40            # probabilities become whole numbers of this size
 
 
