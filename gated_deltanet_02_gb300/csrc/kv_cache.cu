@@ -1,0 +1,198 @@
+// kv_cache.cu -- writing new tokens' keys and values to the paged cache and
+// reading cached rows back (glinattn_kv_append, glinattn_kv_gather).
+//
+// Mathematics: a row x of d elements becomes e4m3 values times a power of two
+// 2^e, e the smallest exponent for which max |x| <= 448 * 2^e.  A power of two
+// makes x * 2^-e exact, so the one rounding is that to e4m3 (half a step,
+// 2^-4 relative), and the way back is exact in bf16.
+//
+// Bound: HBM bytes, 2 d bytes of bf16 and d (+ 1) of e4m3 per row and head.
+// One warp owns one packed row: it finds the row's request (32-way search, all
+// lanes), then moves every (head, k / v) row of it, 8 elements a lane, with
+// all loads of a round in flight before the first store.
+#include "paged.cuh"
+
+namespace glinattn {
+namespace paged {
+
+glinattn_status check_cache(int cache_dtype, int num_req, int num_tok, int kv_heads, int head_dim, int page_size,
+                            int num_pages, int max_pages, const void *k_cache, const void *v_cache, const void *k_scale,
+                            const void *v_scale, const void *page_table, const void *kv_len, const void *q_start) {
+  if (cache_dtype != GLINATTN_BF16 && cache_dtype != GLINATTN_E4M3) return GLINATTN_ERR_INVALID_ARG;
+  if (num_req < 0 || num_req > 65536 || num_tok < 0 || kv_heads <= 0 || head_dim <= 0 || page_size <= 0 ||
+      num_pages < 0 || max_pages < 0)
+    return GLINATTN_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return GLINATTN_ERR_UNSUPPORTED;
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return GLINATTN_ERR_UNSUPPORTED;
+  // the (page, head) planes of the cache and the positions of a request are 32-bit numbers
+  if ((long long)num_pages * kv_heads > (1ll << 30) || (long long)max_pages * page_size > (1ll << 30))
+    return GLINATTN_ERR_INVALID_ARG;
+  if (num_req == 0 || num_tok == 0) return GLINATTN_OK;
+  if (!kv_len || !q_start || (max_pages > 0 && !page_table) || (num_pages > 0 && (!k_cache || !v_cache)))
+    return GLINATTN_ERR_INVALID_ARG;
+  if (cache_dtype == GLINATTN_E4M3 && num_pages > 0 && (!k_scale || !v_scale)) return GLINATTN_ERR_INVALID_ARG;
+  const void *list[] = {k_cache, v_cache, k_scale, v_scale};
+  for (const void *p : list)
+    if ((uintptr_t)p & 15u) return GLINATTN_ERR_INVALID_ARG;
+  const void *ints[] = {page_table, kv_len, q_start};
+  for (const void *p : ints)
+    if ((uintptr_t)p & 3u) return GLINATTN_ERR_INVALID_ARG;
+  return GLINATTN_OK;
+}
+
+namespace {
+
+constexpr int kWarps = 4;   // rows per CTA
+constexpr int kRound = 4;   // (head, k / v) rows a lane has in flight
+
+// Exponent of a row's scale, plus 127, from the largest finite |x| as bf16
+// bits: x = 1.m * 2^(E - 127) <= 1.75 * 2^8 * 2^e.
+__device__ __forceinline__ uint32_t scale_code(uint32_t amax) {
+  const int E = (int)(amax >> 7), m = (int)(amax & 0x7f);
+  const int e = E == 0 ? -100 : E - 127 - 8 + (m > 0x60);
+  return (uint32_t)(min(max(e, -100), 119) + 127);
+}
+
+__device__ __forceinline__ uint32_t finite_mag(uint32_t bits16) {
+  const uint32_t a = bits16 & 0x7fffu;
+  return a < 0x7f80u ? a : 0u;
+}
+
+// A warp's row: its page and row in the page, or false when nothing is to be moved.
+__device__ __forceinline__ bool locate(const glinattn_kv_args &a, int i, int lane, int &page, int &row) {
+  const int r = find_request(a.q_start, a.num_req, i, lane);
+  const int s0 = a.q_start[r], s1 = a.q_start[r + 1], len = a.kv_len[r];
+  if (i < s0 || i >= s1) {
+    // in no request's range; a range that the search cannot land in is the first one's or a decreasing one
+    return false;
+  }
+  if (!request_ok(s0, s1, len, a.num_tok, (long long)a.max_pages * a.page_size)) return false;
+  const int pos = len - (s1 - i);
+  if (pos < 0) return false;
+  page = a.page_table[(size_t)r * a.max_pages + pos / a.page_size];
+  row = pos % a.page_size;
+  if (page < 0 || page >= a.num_pages) {
+    if (lane == 0 && a.dev_status) atomicOr(a.dev_status, GLINATTN_DEV_BAD_SLOT);
+    return false;
+  }
+  return true;
+}
+
+// The ranges themselves are checked once, request by request, by the first CTAs.
+__device__ __forceinline__ void check_requests(const glinattn_kv_args &a) {
+  if (!a.dev_status) return;
+  const long long max_len = (long long)a.max_pages * a.page_size;
+  for (int r = blockIdx.x * blockDim.x + threadIdx.x; r < a.num_req; r += gridDim.x * blockDim.x)
+    if (!request_ok(a.q_start[r], a.q_start[r + 1], a.kv_len[r], a.num_tok, max_len))
+      atomicOr(a.dev_status, GLINATTN_DEV_BAD_COUNT);
+}
+
+template <int D, bool kE4m3, bool kAppend>
+__global__ void __launch_bounds__(32 * kWarps) kv_move_kernel(const glinattn_kv_args a) {
+  constexpr int kLanes = D / 8;             // lanes of one (head, k / v) row
+  constexpr int kPer = 32 / kLanes;         // such rows a warp moves at a time
+  check_requests(a);
+  const int lane = threadIdx.x & 31;
+  const int i = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (i >= a.num_tok) return;               // whole warps
+  int page = 0, row = 0;
+  if (!locate(a, i, lane, page, row)) return;
+  const int H = a.kv_heads, n = 2 * H;      // k rows of every head, then v rows
+  const int sub = lane / kLanes, c = lane % kLanes;
+  for (int j0 = 0; j0 < n; j0 += kPer * kRound) {
+    uint4 x[kRound];
+    uint32_t code[kRound];
+#pragma unroll
+    for (int u = 0; u < kRound; ++u) {
+      const int j = j0 + u * kPer + sub;
+      x[u] = make_uint4(0, 0, 0, 0);
+      code[u] = 0;
+      if (j >= n) continue;
+      const int h = j < H ? j : j - H;
+      const size_t tok = ((size_t)i * H + h) * D + c * 8;
+      const size_t cr = ((size_t)page * H + h) * a.page_size + row;
+      if (kAppend) {
+        x[u] = __ldcs(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(j < H ? a.k : a.v) + tok));
+      } else if (kE4m3) {
+        const uint2 y = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint8_t *>(j < H ? a.k_cache : a.v_cache) + cr * D + c * 8);
+        x[u].x = y.x;
+        x[u].y = y.y;
+        code[u] = (j < H ? a.k_scale : a.v_scale)[cr];
+      } else {
+        x[u] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(j < H ? a.k_cache : a.v_cache) + cr * D + c * 8);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRound; ++u) {
+      const int j = j0 + u * kPer + sub;
+      const int h = j < H ? j : j - H;
+      const size_t tok = ((size_t)i * H + h) * D + c * 8;
+      const size_t cr = ((size_t)page * H + h) * a.page_size + row;
+      if (kAppend && kE4m3) {
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m = max(m, max(finite_mag(w[k]), finite_mag(w[k] >> 16)));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const uint32_t sc = scale_code(m);
+        const float f = __uint_as_float((254u - sc) << 23);  // 2^-e
+        uint32_t q[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          q[k] = to_e4m3x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
+        if (j < n) {
+          *reinterpret_cast<uint2 *>(reinterpret_cast<uint8_t *>(j < H ? a.k_cache : a.v_cache) + cr * D + c * 8) =
+              make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+          if (c == 0) (j < H ? a.k_scale : a.v_scale)[cr] = (uint8_t)sc;
+        }
+      } else if (j < n) {
+        if (kAppend) {
+          *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(j < H ? a.k_cache : a.v_cache) + cr * D + c * 8) = x[u];
+        } else {
+          uint4 y = x[u];
+          if (kE4m3) {
+            const float s = scale_value(code[u]);
+            const float2 f0 = e4m3x2(x[u].x & 0xffffu), f1 = e4m3x2(x[u].x >> 16);
+            const float2 f2 = e4m3x2(x[u].y & 0xffffu), f3 = e4m3x2(x[u].y >> 16);
+            y = make_uint4(pack_bf16(f0.x * s, f0.y * s), pack_bf16(f1.x * s, f1.y * s), pack_bf16(f2.x * s, f2.y * s),
+                           pack_bf16(f3.x * s, f3.y * s));
+          }
+          __stcs(reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(j < H ? a.k : a.v) + tok), y);
+        }
+      }
+    }
+  }
+}
+
+template <bool kAppend>
+glinattn_status move(const glinattn_kv_args *a, cudaStream_t stream) {
+  if (!a) return GLINATTN_ERR_INVALID_ARG;
+  const glinattn_status st =
+      check_cache(a->cache_dtype, a->num_req, a->num_tok, a->kv_heads, a->head_dim, a->page_size, a->num_pages,
+                  a->max_pages, a->k_cache, a->v_cache, a->k_scale, a->v_scale, a->page_table, a->kv_len, a->q_start);
+  if (st != GLINATTN_OK) return st;
+  if (a->num_req == 0 || a->num_tok == 0) return GLINATTN_OK;
+  if (!a->k || !a->v || (((uintptr_t)a->k | (uintptr_t)a->v) & 15u)) return GLINATTN_ERR_INVALID_ARG;
+  const bool f8 = a->cache_dtype == GLINATTN_E4M3;
+  auto kernel = a->head_dim == 128 ? (f8 ? kv_move_kernel<128, true, kAppend> : kv_move_kernel<128, false, kAppend>)
+                                   : (f8 ? kv_move_kernel<64, true, kAppend> : kv_move_kernel<64, false, kAppend>);
+  kernel<<<(unsigned)((a->num_tok - 1) / kWarps + 1), 32 * kWarps, 0, stream>>>(*a);
+  return cudaGetLastError() == cudaSuccess ? GLINATTN_OK : GLINATTN_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace paged
+}  // namespace glinattn
+
+extern "C" {
+
+glinattn_status glinattn_kv_append(const glinattn_kv_args *args, glinattn_stream_t stream) {
+  return glinattn::paged::move<true>(args, (cudaStream_t)stream);
+}
+
+glinattn_status glinattn_kv_gather(const glinattn_kv_args *args, glinattn_stream_t stream) {
+  return glinattn::paged::move<false>(args, (cudaStream_t)stream);
+}
+
+}  // extern "C"

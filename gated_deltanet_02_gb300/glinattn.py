@@ -13,10 +13,17 @@ The entry points keep the C names:
 * ``glinattn_state_copy``  -- whole-slot copies inside a state pool (copy on write)
 * ``glinattn_selective_scan`` / ``glinattn_selective_scan_decode`` -- Mamba's
   selective scan (chunked prefill; one step from a slot-indexed pool)
+* ``glinattn_kv_append`` / ``glinattn_kv_gather`` -- write new tokens' keys and
+  values to a paged cache (bf16, or e4m3 with a scale per row), read them back
+* ``glinattn_paged_attention`` -- causal softmax attention of new tokens (one,
+  drafts, a piece of a prompt, packed prompts) over the paged cache
+* ``glinattn_accept_drafts`` -- accepted drafts and the next token from the
+  target's probabilities and given random numbers
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import threading
 
 import torch
@@ -24,12 +31,14 @@ import torch
 from . import build as _build
 
 GLA, GDN, NLA = 0, 1, 2
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
 
 DEV_BAD_SLOT = 0x1
 DEV_BAD_GATE = 0x2
 DEV_WAIT_TIMEOUT = 0x4
 DEV_BAD_COUNT = 0x8
+DEV_BAD_TOKEN = 0x10
+DEV_BAD_PROB = 0x20
 
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration", 3: "CUDA error",
            4: "device reported an error status", 5: "device wait timed out"}
@@ -102,6 +111,27 @@ class CopyArgs(ctypes.Structure):
                 ("dst_slots", _vp), ("dev_status", _vp)]
 
 
+class KvArgs(ctypes.Structure):
+    _fields_ = [("cache_dtype", _i32), ("num_req", _i32), ("num_tok", _i32), ("kv_heads", _i32), ("head_dim", _i32),
+                ("page_size", _i32), ("num_pages", _i32), ("max_pages", _i32), ("k", _vp), ("v", _vp),
+                ("k_cache", _vp), ("v_cache", _vp), ("k_scale", _vp), ("v_scale", _vp), ("page_table", _vp),
+                ("kv_len", _vp), ("q_start", _vp), ("dev_status", _vp)]
+
+
+class PagedAttnArgs(ctypes.Structure):
+    _fields_ = [("cache_dtype", _i32), ("num_req", _i32), ("num_tok", _i32), ("heads", _i32), ("kv_heads", _i32),
+                ("head_dim", _i32), ("page_size", _i32), ("num_pages", _i32), ("max_pages", _i32), ("max_q_len", _i32),
+                ("scale", ctypes.c_float), ("q", _vp), ("k_cache", _vp), ("v_cache", _vp), ("k_scale", _vp),
+                ("v_scale", _vp), ("page_table", _vp), ("kv_len", _vp), ("q_start", _vp), ("o", _vp),
+                ("dev_status", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class AcceptArgs(ctypes.Structure):
+    _fields_ = [("num_req", _i32), ("draft_len", _i32), ("vocab", _i32), ("target_probs", _vp), ("draft_probs", _vp),
+                ("draft_tokens", _vp), ("num_drafts", _vp), ("uniforms", _vp), ("accept", _vp), ("tokens", _vp),
+                ("dev_status", _vp)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -116,7 +146,10 @@ def library() -> ctypes.CDLL:
             for name, argt in (("glinattn_prefill", PrefillArgs), ("glinattn_decode", DecodeArgs),
                                ("glinattn_spec_decode", SpecArgs), ("glinattn_replay", ReplayArgs),
                                ("glinattn_state_copy", CopyArgs), ("glinattn_selective_scan", ScanArgs),
-                               ("glinattn_selective_scan_decode", ScanDecodeArgs)):
+                               ("glinattn_selective_scan_decode", ScanDecodeArgs),
+                               ("glinattn_kv_append", KvArgs), ("glinattn_kv_gather", KvArgs),
+                               ("glinattn_paged_attention", PagedAttnArgs),
+                               ("glinattn_accept_drafts", AcceptArgs)):
                 f = getattr(lib, name)
                 f.argtypes = [ctypes.POINTER(argt), _vp]
                 f.restype = ctypes.c_int
@@ -129,6 +162,8 @@ def library() -> ctypes.CDLL:
             lib.glinattn_prefill_workspace_size.restype = ctypes.c_size_t
             lib.glinattn_selective_scan_workspace_size.argtypes = [ctypes.POINTER(ScanArgs)]
             lib.glinattn_selective_scan_workspace_size.restype = ctypes.c_size_t
+            lib.glinattn_paged_attention_workspace_size.argtypes = [ctypes.POINTER(PagedAttnArgs)]
+            lib.glinattn_paged_attention_workspace_size.restype = ctypes.c_size_t
             _lib = lib
     return _lib
 
@@ -456,6 +491,156 @@ def glinattn_selective_scan_decode(x, delta, Bm, Cm, A, state_pool, slot_ids, *,
                        dev_status=_ptr(dev_status))
     _call("glinattn_selective_scan_decode", a, _stream_handle(stream, dev))
     return y
+
+
+def _cache_dims(k_cache, v_cache, page_table, kv_len, q_start, k_scale, v_scale, dev):
+    """The checks that the calls on a paged cache share; (cache dtype, P, Hkv, page, d, R, max_pages)."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [P, Hkv, page, d]")
+    P, Hkv, page, d = k_cache.shape
+    if k_cache.dtype == torch.bfloat16:
+        code = BF16
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale and v_scale belong to an e4m3 cache")
+    elif k_cache.dtype == torch.float8_e4m3fn:
+        code = E4M3
+        if k_scale is None or v_scale is None:
+            raise ValueError("an e4m3 cache needs k_scale and v_scale")
+        _need(k_scale, "k_scale", torch.uint8, (P, Hkv, page), dev)
+        _need(v_scale, "v_scale", torch.uint8, (P, Hkv, page), dev)
+    else:
+        raise TypeError(f"the cache must be bf16 or float8_e4m3fn, got {k_cache.dtype}")
+    _need(k_cache, "k_cache", None, None, dev)
+    _need(v_cache, "v_cache", k_cache.dtype, (P, Hkv, page, d), dev)
+    if kv_len.dim() != 1 or page_table.dim() != 2:
+        raise ValueError("kv_len must be [R] and page_table [R, max_pages]")
+    R = kv_len.shape[0]
+    _need(kv_len, "kv_len", torch.int32, None, dev)
+    _need(q_start, "q_start", torch.int32, (R + 1,), dev)
+    _need(page_table, "page_table", torch.int32, (R, page_table.shape[1]), dev)
+    return code, P, Hkv, page, d, R, page_table.shape[1]
+
+
+def _status_word(dev_status, dev):
+    if dev_status is not None and (dev_status.dtype not in (torch.int32, torch.uint32) or dev_status.device != dev):
+        raise ValueError(f"dev_status must be a 32-bit word on {dev}")
+
+
+def _launch(name, args, stream, dev):
+    """One call on the tensors' own device, whichever is current."""
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors must be on a CUDA device, got {dev}")
+    with torch.cuda.device(dev):
+        _call(name, args, _stream_handle(stream, dev))
+
+
+def glinattn_kv_append(k, v, k_cache, v_cache, page_table, kv_len, q_start, *, k_scale=None, v_scale=None,
+                       dev_status=None, stream=None):
+    """Write new tokens' keys and values to a paged cache, in place.  k, v
+    [num_tok,Hkv,d] bf16; k_cache, v_cache [P,Hkv,page,d] bf16, or
+    float8_e4m3fn with k_scale, v_scale [P,Hkv,page] uint8 (a power-of-two
+    exponent plus 127 per row); page_table [R,max_pages], kv_len [R], q_start
+    [R+1] int32: rows q_start[r]..q_start[r+1]-1 are request r's last positions
+    below kv_len[r].  Returns (k_cache, v_cache)."""
+    dev = k.device
+    code, P, Hkv, page, d, R, max_pages = _cache_dims(k_cache, v_cache, page_table, kv_len, q_start, k_scale, v_scale, dev)
+    n = k.shape[0]
+    _need(k, "k", torch.bfloat16, (n, Hkv, d), dev)
+    _need(v, "v", torch.bfloat16, (n, Hkv, d), dev)
+    _status_word(dev_status, dev)
+    a = KvArgs(code, R, n, Hkv, d, page, P, max_pages, _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+               _ptr(v_scale), _ptr(page_table), _ptr(kv_len), _ptr(q_start), _ptr(dev_status))
+    _launch("glinattn_kv_append", a, stream, dev)
+    return k_cache, v_cache
+
+
+def glinattn_kv_gather(k_cache, v_cache, page_table, kv_len, q_start, *, num_tok=None, k=None, v=None, k_scale=None,
+                       v_scale=None, dev_status=None, stream=None):
+    """Read cached rows back as packed bf16 rows: k, v [num_tok,Hkv,d], row
+    q_start[r] + i holding request r's position kv_len[r] - (its number of rows)
+    + i.  The cache's arguments are glinattn_kv_append's.  k and v are allocated
+    when not given (num_tok rows; rows of no request, or at negative positions,
+    are not written).  Returns (k, v)."""
+    dev = k_cache.device
+    code, P, Hkv, page, d, R, max_pages = _cache_dims(k_cache, v_cache, page_table, kv_len, q_start, k_scale, v_scale, dev)
+    if num_tok is None:
+        if k is None and v is None:
+            raise ValueError("num_tok is needed when k and v are not given")
+        num_tok = (v if k is None else k).shape[0]
+    if k is None:
+        k = torch.empty((num_tok, Hkv, d), dtype=torch.bfloat16, device=dev)
+    if v is None:
+        v = torch.empty((num_tok, Hkv, d), dtype=torch.bfloat16, device=dev)
+    _need(k, "k", torch.bfloat16, (num_tok, Hkv, d), dev)
+    _need(v, "v", torch.bfloat16, (num_tok, Hkv, d), dev)
+    _status_word(dev_status, dev)
+    a = KvArgs(code, R, num_tok, Hkv, d, page, P, max_pages, _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache),
+               _ptr(k_scale), _ptr(v_scale), _ptr(page_table), _ptr(kv_len), _ptr(q_start), _ptr(dev_status))
+    _launch("glinattn_kv_gather", a, stream, dev)
+    return k, v
+
+
+def glinattn_paged_attention(q, k_cache, v_cache, page_table, kv_len, q_start, *, max_q_len=None, scale=None,
+                             k_scale=None, v_scale=None, o=None, workspace=None, dev_status=None, stream=None):
+    """Causal softmax attention of new tokens over a paged cache that already
+    holds their own keys and values.  q [num_tok,H,d] bf16, H a multiple of the
+    cache's Hkv (head h reads key / value head h // (H // Hkv)); the cache's
+    arguments are glinattn_kv_append's.  max_q_len: an upper bound of the
+    requests' numbers of new tokens (num_tok when not given; a tight one selects
+    the faster kernel for few tokens per request).  scale defaults to
+    1 / sqrt(d).  Returns o [num_tok,H,d] bf16 (rows of no request are not
+    written)."""
+    dev = q.device
+    code, P, Hkv, page, d, R, max_pages = _cache_dims(k_cache, v_cache, page_table, kv_len, q_start, k_scale, v_scale, dev)
+    n, H = q.shape[0], q.shape[1]
+    _need(q, "q", torch.bfloat16, (n, H, d), dev)
+    if o is None:
+        o = torch.empty_like(q)
+    _need(o, "o", torch.bfloat16, (n, H, d), dev)
+    _status_word(dev_status, dev)
+    a = PagedAttnArgs(code, R, n, H, Hkv, d, page, P, max_pages, n if max_q_len is None else max_q_len,
+                      1.0 / math.sqrt(d) if scale is None else scale, _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                      _ptr(k_scale), _ptr(v_scale), _ptr(page_table), _ptr(kv_len), _ptr(q_start), _ptr(o),
+                      _ptr(dev_status))
+    need = library().glinattn_paged_attention_workspace_size(ctypes.byref(a))
+    if need:
+        if workspace is None or workspace.numel() * workspace.element_size() < need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        a.workspace = _ptr(workspace)
+        a.workspace_bytes = need
+    _launch("glinattn_paged_attention", a, stream, dev)
+    return o
+
+
+def glinattn_accept_drafts(target_probs, draft_probs, draft_tokens, uniforms, *, num_drafts=None, accept=None,
+                           tokens=None, dev_status=None, stream=None):
+    """Accepted drafts of a speculative round and the token that follows them.
+    target_probs [R,D+1,V] fp32; draft_probs [R,D,V] fp32, or None for drafts
+    that were picked deterministically; draft_tokens [R,D] int32; uniforms
+    [R,D+1] fp32 in [0, 1); num_drafts [R] int32 or None (all D).  Returns
+    (accept [R] int32, which glinattn_replay takes, and tokens [R,D+1] int32:
+    the accepted drafts, the drawn token, then -1)."""
+    R, D1, V = target_probs.shape
+    D = D1 - 1
+    dev = target_probs.device
+    if D < 0:
+        raise ValueError("target_probs must be [R, D + 1, V]")
+    _need(target_probs, "target_probs", torch.float32, (R, D + 1, V), dev)
+    _need(draft_probs, "draft_probs", torch.float32, (R, D, V), dev)
+    _need(draft_tokens, "draft_tokens", torch.int32, (R, D), dev)
+    _need(uniforms, "uniforms", torch.float32, (R, D + 1), dev)
+    _need(num_drafts, "num_drafts", torch.int32, (R,), dev)
+    if accept is None:
+        accept = torch.empty((R,), dtype=torch.int32, device=dev)
+    if tokens is None:
+        tokens = torch.empty((R, D + 1), dtype=torch.int32, device=dev)
+    _need(accept, "accept", torch.int32, (R,), dev)
+    _need(tokens, "tokens", torch.int32, (R, D + 1), dev)
+    _status_word(dev_status, dev)
+    a = AcceptArgs(R, D, V, _ptr(target_probs), _ptr(draft_probs), _ptr(draft_tokens), _ptr(num_drafts),
+                   _ptr(uniforms), _ptr(accept), _ptr(tokens), _ptr(dev_status))
+    _launch("glinattn_accept_drafts", a, stream, dev)
+    return accept, tokens
 
 
 def version() -> int:

@@ -82,13 +82,16 @@ typedef enum {
  * L2 norm; the normaliser z [.., H, dk] fp32 travels beside the state.
  */
 typedef enum { GLINATTN_GLA = 0, GLINATTN_GDN = 1, GLINATTN_NLA = 2 } glinattn_variant;
-typedef enum { GLINATTN_F32 = 0, GLINATTN_BF16 = 1 } glinattn_dtype;
+/* GLINATTN_E4M3 is a dtype of the paged key / value cache only. */
+typedef enum { GLINATTN_F32 = 0, GLINATTN_BF16 = 1, GLINATTN_E4M3 = 2 } glinattn_dtype;
 
 /* Bits OR-ed into *dev_status by the kernels. */
-#define GLINATTN_DEV_BAD_SLOT 0x1u    /* slot id outside [0, pool_slots): unit skipped */
+#define GLINATTN_DEV_BAD_SLOT 0x1u    /* slot (or page) id outside its pool: unit skipped */
 #define GLINATTN_DEV_BAD_GATE 0x2u    /* alpha outside (0, 1] or not finite: unit skipped */
 #define GLINATTN_DEV_WAIT_TIMEOUT 0x4u /* an on-chip barrier wait exceeded its bound */
-#define GLINATTN_DEV_BAD_COUNT 0x8u   /* accepted length outside [0, draft_len]: request skipped */
+#define GLINATTN_DEV_BAD_COUNT 0x8u   /* a length outside its range (accepted drafts, tokens, cache): request skipped */
+#define GLINATTN_DEV_BAD_TOKEN 0x10u  /* draft token outside [0, vocab): request skipped */
+#define GLINATTN_DEV_BAD_PROB 0x20u   /* a probability row without any mass: request skipped */
 
 /*
  * glinattn_prefill -- chunked prefill of one segment for B sequences.
@@ -398,6 +401,147 @@ typedef struct {
 } glinattn_scan_decode_args;
 
 glinattn_status glinattn_selective_scan_decode(const glinattn_scan_decode_args *args, glinattn_stream_t stream);
+
+/*
+ * The paged key / value cache of the softmax-attention layers ("Inference for
+ * linear attention and hybrid architectures": a hybrid stack keeps a paged KV
+ * pool for its full-attention layers beside the per-request state pool).  The
+ * three calls below share its conventions.
+ *
+ *   k_cache, v_cache [P, Hkv, page, d]   (cache_dtype: GLINATTN_BF16 or GLINATTN_E4M3)
+ *   k_scale, v_scale [P, Hkv, page] uint8, with GLINATTN_E4M3 only: one
+ *     power-of-two scale per cached row, stored as its exponent plus 127, so a
+ *     row's elements stand for e4m3 * 2^(code - 127)
+ *   page_table [R, max_pages] int32: position t of request r is row t % page
+ *     of page page_table[r, t / page]; entries past a request's last position
+ *     are not read
+ *   kv_len [R] int32: positions of request r in the cache, the new tokens of
+ *     this call among them
+ *   q_start [R + 1] int32, not decreasing: rows q_start[r] .. q_start[r + 1] - 1
+ *     of the packed token arrays (num_tok rows) are the new tokens of request
+ *     r, the LAST positions below kv_len[r]: row q_start[r] + i is at position
+ *     kv_len[r] - (q_start[r + 1] - q_start[r]) + i.  Rows outside every
+ *     request's range (a padded batch) are neither read nor written.
+ *   head_dim d is 64 or 128; page is 16, 32, 64 or 128.
+ *
+ *   A request whose range or kv_len is out of bounds (a range outside
+ *   [0, num_tok] or decreasing, kv_len outside [0, max_pages * page]) sets
+ *   GLINATTN_DEV_BAD_COUNT and is skipped; a page id outside [0, P) sets
+ *   GLINATTN_DEV_BAD_SLOT and skips what needed that page.  num_req <= 65536.
+ *
+ * glinattn_kv_append -- write the new tokens' keys and values to the cache.
+ *   k, v [num_tok, Hkv, d] bf16 are read.  GLINATTN_BF16 copies them.
+ *   GLINATTN_E4M3 quantises each row of d elements on its own: with e the
+ *   smallest integer in [-100, 119] for which every finite |x| <= 448 * 2^e (119
+ *   when there is none), the row stores x * 2^-e rounded to the nearest e4m3
+ *   (ties to even), and e as its scale.  Infinities, and what lies beyond, become
+ *   +-448 * 2^e (at e = 119 the largest that bf16 still holds), NaN stays NaN.  Tokens at
+ *   negative positions (more new tokens than kv_len) are not stored.  Two rows
+ *   of one call must not be the same cache position (not checked: they race).
+ *
+ * glinattn_kv_gather -- the way back: k, v [num_tok, Hkv, d] bf16 are written
+ *   with the cached rows at the same positions (q_start / kv_len as above; a
+ *   whole prefix is read with a range of kv_len rows).  An e4m3 row times its
+ *   scale is exact in bf16 for every row that glinattn_kv_append wrote.  Rows at negative
+ *   positions are left as they were.
+ */
+typedef struct {
+  int32_t cache_dtype;
+  int32_t num_req, num_tok, kv_heads, head_dim, page_size, num_pages, max_pages;
+  void *k, *v;             /* append: read; gather: written */
+  void *k_cache, *v_cache; /* append: written; gather: read */
+  uint8_t *k_scale, *v_scale;
+  const int32_t *page_table, *kv_len, *q_start;
+  uint32_t *dev_status;
+} glinattn_kv_args;
+
+glinattn_status glinattn_kv_append(const glinattn_kv_args *args, glinattn_stream_t stream);
+glinattn_status glinattn_kv_gather(const glinattn_kv_args *args, glinattn_stream_t stream);
+
+/*
+ * glinattn_paged_attention -- causal softmax attention of the new tokens over
+ *   the paged cache (which already holds their own keys and values: call
+ *   glinattn_kv_append first).  One call serves single-token decode, the
+ *   drafts of a speculative round, a piece of a long prompt and whole packed
+ *   prompts, in any mixture of lengths.  For a token at position p and head h,
+ *   with key / value head h / (H / Hkv):
+ *     o = sum_{j <= p} softmax_j(scale * q . k_j) v_j
+ *   A row that sees no key (a negative position) or whose every score is
+ *   -infinity gives zeros.  Scores, softmax statistics and sums are fp32.
+ *
+ *   q, o [num_tok, H, d] bf16; Hkv divides H.
+ *   scale: finite and > 0.  max_q_len: an upper bound of the ranges' lengths
+ *     (it selects the kernel); a longer range sets GLINATTN_DEV_BAD_COUNT and
+ *     its request is skipped.
+ *   A request with a bad page among the pages that a group of its query rows
+ *   reads leaves those output rows as they were.
+ *   Cache rows at and behind kv_len may hold anything, NaN included.  A
+ *   non-finite value in a row below kv_len can reach any output row of its own
+ *   request, that of an earlier token too; other requests are not affected.
+ *   workspace: at least glinattn_paged_attention_workspace_size() bytes,
+ *   16-byte aligned: partial results where the cache of one request is shared
+ *   out over several SMs.  The size depends on the sizes of the struct only,
+ *   not on the lengths in device memory.  Calls that may overlap on the GPU
+ *   need a workspace each.
+ */
+typedef struct {
+  int32_t cache_dtype;
+  int32_t num_req, num_tok, heads, kv_heads, head_dim, page_size, num_pages, max_pages;
+  int32_t max_q_len;
+  float scale;
+  const void *q;
+  const void *k_cache, *v_cache;
+  const uint8_t *k_scale, *v_scale;
+  const int32_t *page_table, *kv_len, *q_start;
+  void *o;
+  uint32_t *dev_status;
+  void *workspace;
+  size_t workspace_bytes;
+} glinattn_paged_attn_args;
+
+size_t glinattn_paged_attention_workspace_size(const glinattn_paged_attn_args *args);
+glinattn_status glinattn_paged_attention(const glinattn_paged_attn_args *args, glinattn_stream_t stream);
+
+/*
+ * glinattn_accept_drafts -- the verification step of a speculative round: how
+ *   many of a request's drafts the target accepts, and the token that follows
+ *   them, from given random numbers.  `accept` is what glinattn_replay takes.
+ *
+ *   target_probs [R, D + 1, V] fp32: the target's distribution before each
+ *     draft and after the last one
+ *   draft_probs [R, D, V] fp32: the distributions that the drafts were drawn
+ *     from, or NULL when each draft was picked deterministically (a point mass)
+ *   draft_tokens [R, D] int32    num_drafts [R] int32 or NULL (all D)
+ *   uniforms [R, D + 1] fp32 in [0, 1)
+ *   accept [R] int32    tokens [R, D + 1] int32 (outputs)
+ *
+ *   Draft i < n = num_drafts[r] with token x is accepted iff
+ *   uniforms[r, i] * q_i(x) < p_i(x) (the fp32 product; q_i(x) = 1 for a point
+ *   mass), and accept[r] = a is the number of drafts before the first rejected
+ *   one.  The next token is drawn from w(v) = max(p_a(v) - q_a(v), 0) after a
+ *   rejection (q_a the point mass at the draft when draft_probs is NULL), from
+ *   w = p_n otherwise.  The draw is a cumulative one over whole numbers, so
+ *   that it does not depend on the order of the sums:
+ *     W(v) = trunc(min(max(w(v), 0), 1) * 2^40), the difference in fp32, NaN
+ *     counting as 0; the token is the lowest v with W(0) + .. + W(v) > t,
+ *     t = min(trunc(uniforms[r, D] * sum W), sum W - 1), the product in fp64.
+ *   When a residual has no mass left, w = p_a takes its place.
+ *   tokens[r] is the a accepted drafts, the drawn token, then -1.
+ *   A count outside [0, D] sets GLINATTN_DEV_BAD_COUNT, a draft among the
+ *   first n outside [0, V) GLINATTN_DEV_BAD_TOKEN, a target row without mass
+ *   GLINATTN_DEV_BAD_PROB; each skips the request.  D may be 0 (plain sampling of one token).
+ *   D <= 1024, 1 <= V <= 2^22.
+ */
+typedef struct {
+  int32_t num_req, draft_len, vocab;
+  const float *target_probs, *draft_probs;
+  const int32_t *draft_tokens, *num_drafts;
+  const float *uniforms;
+  int32_t *accept, *tokens;
+  uint32_t *dev_status;
+} glinattn_accept_args;
+
+glinattn_status glinattn_accept_drafts(const glinattn_accept_args *args, glinattn_stream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *glinattn_status_string(glinattn_status status);
