@@ -6,7 +6,7 @@
 // is rescaled by 2^(m_old - m_new) whenever m grows; scores in log2 units.
 #include <math.h>
 
-#include "paged.cuh"
+#include "paged_sched.cuh"
 
 namespace glinattn {
 namespace paged {
@@ -99,13 +99,53 @@ glinattn_status check(const glinattn_paged_attn_args *a) {
   return GLINATTN_OK;
 }
 
+// Rows of an item that the decode kernel's accumulators are built for.
+int item_rows(const glinattn_paged_attn_args *a) {
+  const long long rows = (long long)a->max_q_len * (a->heads / a->kv_heads);
+  return rows <= 16 ? 16 : rows <= kDecodeRows ? 32 : 0;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 152;
+  return n;
+}
+
+// The workspace's parts, each 16-byte aligned: desc, skip, ml, part.
+size_t carve(int ctas, int rows, int d, AttnParams *p, uint8_t *base) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t *x = base + at;
+    at += (bytes + 15) & ~(size_t)15;
+    return x;
+  };
+  uint8_t *desc = take((size_t)ctas * sizeof(int4));
+  uint8_t *skip = take((size_t)ctas * 2 * sizeof(int));
+  uint8_t *ml = take((size_t)ctas * 2 * rows * sizeof(float2));
+  uint8_t *part = take((size_t)ctas * 2 * rows * d * sizeof(float));
+  if (p) {
+    p->desc = reinterpret_cast<int4 *>(desc);
+    p->skip = reinterpret_cast<int *>(skip);
+    p->ml = reinterpret_cast<float2 *>(ml);
+    p->part = reinterpret_cast<float *>(part);
+  }
+  return at;
+}
+
 }  // namespace
 }  // namespace paged
 }  // namespace glinattn
 
 extern "C" {
 
-size_t glinattn_paged_attention_workspace_size(const glinattn_paged_attn_args *) { return 0; }
+size_t glinattn_paged_attention_workspace_size(const glinattn_paged_attn_args *a) {
+  using namespace glinattn::paged;
+  if (check(a) != GLINATTN_OK || a->num_req == 0 || a->num_tok == 0) return 0;
+  const int rows = item_rows(a);
+  return rows ? carve(2 * sm_count(), rows, a->head_dim, nullptr, nullptr) : 0;
+}
 
 glinattn_status glinattn_paged_attention(const glinattn_paged_attn_args *a, glinattn_stream_t stream) {
   using namespace glinattn::paged;
@@ -113,6 +153,37 @@ glinattn_status glinattn_paged_attention(const glinattn_paged_attn_args *a, glin
   if (st != GLINATTN_OK) return st;
   if (a->num_req == 0 || a->num_tok == 0) return GLINATTN_OK;
   const bool f8 = a->cache_dtype == GLINATTN_E4M3;
+  if (const int rows = item_rows(a)) {
+    const int ctas = 2 * sm_count();
+    if (!a->workspace || ((uintptr_t)a->workspace & 15u) ||
+        a->workspace_bytes < carve(ctas, rows, a->head_dim, nullptr, nullptr))
+      return GLINATTN_ERR_INVALID_ARG;
+    AttnParams p = {};
+    p.R = a->num_req;
+    p.N = a->num_tok;
+    p.H = a->heads;
+    p.Hkv = a->kv_heads;
+    p.G = a->heads / a->kv_heads;
+    p.page = a->page_size;
+    p.page_shift = a->page_size == 16 ? 4 : a->page_size == 32 ? 5 : a->page_size == 64 ? 6 : 7;
+    p.P = a->num_pages;
+    p.max_pages = a->max_pages;
+    p.max_q = a->max_q_len;
+    p.tp = 1 << 30;
+    p.c = a->scale * 1.44269504088896341f;
+    p.q = reinterpret_cast<const __nv_bfloat16 *>(a->q);
+    p.k_scale = a->k_scale;
+    p.v_scale = a->v_scale;
+    p.table = a->page_table;
+    p.kv_len = a->kv_len;
+    p.q_start = a->q_start;
+    p.o = reinterpret_cast<__nv_bfloat16 *>(a->o);
+    p.dev_status = a->dev_status;
+    carve(ctas, rows, a->head_dim, &p, reinterpret_cast<uint8_t *>(a->workspace));
+    return launch_decode(p, f8, a->head_dim, rows, a->k_cache, a->v_cache, ctas, (cudaStream_t)stream) == cudaSuccess
+               ? GLINATTN_OK
+               : GLINATTN_ERR_CUDA;
+  }
   auto kernel = a->head_dim == 128 ? (f8 ? attn_row_kernel<128, true> : attn_row_kernel<128, false>)
                                    : (f8 ? attn_row_kernel<64, true> : attn_row_kernel<64, false>);
   const long long units = (long long)a->num_tok * a->heads;

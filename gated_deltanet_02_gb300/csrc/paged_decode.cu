@@ -1,0 +1,678 @@
+// paged_decode.cu -- attention over the paged cache for few query rows per
+// (request, key / value head): single tokens and drafts (glinattn_paged_attention).
+//
+// Mathematics: one pass over the keys with the running maximum m of the
+// softmax (log2 units), in the transposed form
+//   S^T = K Q^T   [128 keys x rows],   W = 2^(S^T - m),   O^T += V^T W   [d x rows]
+// so that the 128-wide side of the tensor-core tile is filled by keys and
+// channels and the few query rows (tokens x heads of the group) are the N side.  m only
+// moves when a tile exceeds it by 2^kSlack (then O^T and the sums are
+// rescaled), which leaves the result unchanged: m is a common factor.
+//
+// Precision: scores, m, sums and O^T are fp32.  The weights enter the second
+// product as two bf16 parts (bf16 cache; 2^-16 relative) or three e4m3 parts
+// (e4m3 cache; 2^-12), so the output's rounding to bf16 is the only one that
+// counts.  With an e4m3 cache both products run on the stored values
+// (kind::f8f6f4): q is split into two e4m3 parts of 4 bits (bf16 has 8) with a
+// power-of-two scale per row, the key's scale multiplies its score, and the
+// value's scale 2^e is folded into the weight's exponent: W = 2^(S + e - m)
+// with m the maximum of S + e, while the sums use 2^(S - m).
+//
+// Bound: HBM, one read of the cache; 2 CTAs per SM, each with a ring of 16 KiB
+// stages (TMA, one box per page), so that about 190 KiB per SM are in flight.  Warps:
+// 0 TMA and the walk over the items, 1 MMA issue, 2-5 softmax, a key per thread.
+#include "paged_sched.cuh"
+#include "prefill_tc.cuh"
+#include "tc_common.cuh"
+
+namespace glinattn {
+namespace paged {
+namespace {
+
+using namespace sm100;
+using tc::wait_bar;
+using tc::wait_bar_warp;
+using tc::warp_arrive;
+
+constexpr int kThreads = 192;
+constexpr int kItems = 4;              // depth of the item queue
+constexpr int kScaleSlots = 12;        // tiles of scales in flight, see ScaleRing below
+constexpr uint32_t kStageBytes = 16384;
+
+template <int D, bool kF8, int N>
+struct Cfg {
+  static constexpr int kTQ = kF8 ? 2 : 1;            // parts of q
+  static constexpr int kTP = kF8 ? 3 : 2;            // parts of a weight
+  static constexpr int kNS = N * kTQ, kNO = N * kTP;  // columns of S^T and O^T
+  static constexpr int kEsz = kF8 ? 1 : 2;
+  static constexpr int kTileStages = D * kEsz * kTileKeys > (int)kStageBytes ? 2 : 1;
+  static constexpr uint32_t kBytesQ = N * kTQ * D * kEsz;
+  static constexpr uint32_t kBytesP = N * kTP * kTileKeys * kEsz;
+  static constexpr uint32_t kBytesScale = kF8 ? kScaleSlots * 2 * kTileKeys : 0;
+  static constexpr uint32_t kBytesMax = 2 * 4 * N * 4;  // [2][row][warp]
+  static constexpr uint32_t kBytesBars = 640;
+  static constexpr uint32_t kFixed = kBytesQ + kBytesP + kBytesScale + kBytesMax + kBytesBars + 1024;
+  // two CTAs of an SM share 228 KiB, 1 KiB of each reserved
+  static constexpr int kStages = (int)((112 * 1024 - kFixed) / kStageBytes) < 6 ? (int)((112 * 1024 - kFixed) / kStageBytes) : 6;
+  static constexpr uint32_t kSmem = kFixed + kStages * kStageBytes;
+  static constexpr uint32_t kOffQ = kStages * kStageBytes, kOffP = kOffQ + kBytesQ, kOffScale = kOffP + kBytesP,
+                            kOffMax = kOffScale + kBytesScale, kOffBars = kOffMax + kBytesMax;
+  static constexpr uint32_t kColO = 2 * kNS;
+  static constexpr uint32_t kCols = kColO + kNO <= 64 ? 64 : kColO + kNO <= 128 ? 128 : 256;
+  static_assert(kColO + kNO <= 256, "two CTAs share the SM's 512 columns");
+  static_assert(kStages >= 2 * kTileStages + (kF8 ? 1 : 0), "K and V tiles of one step");
+  // the first tile index whose scales the producer may be loading is that of
+  // the oldest unread tile + 1 (its S issued early) + the ring's K tiles
+  static_assert(!kF8 || kScaleSlots >= kStages + 3, "scale slots");
+};
+
+struct Bars {
+  uint64_t full[6], empty[6];
+  uint64_t s_ready[2], s_free[2], q_ready, p_ready, o_done;
+  uint64_t item_full[kItems], item_empty[kItems];
+  Item item[kItems];
+  PlanShared plan;
+  uint64_t sync;  // the four softmax warps among themselves
+  uint32_t tmem;
+  int abort;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// D[tmem] (+)= A[smem] B[smem], e4m3 x e4m3 -> fp32.
+__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+// 64-byte swizzle: rows of 64 bytes, 8-row groups 512 bytes apart (layout type 4).
+__device__ __forceinline__ uint64_t desc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)4 << 61;
+  return d;
+}
+
+template <int kCnt>
+__device__ __forceinline__ void tmem_ld(uint32_t a, float *v) {
+  static_assert(kCnt % 16 == 0, "columns");
+#pragma unroll
+  for (int k = 0; k < kCnt; k += 16) {
+    float t[16];
+    tmem_ld16(a + k, t);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[k + j] = t[j];
+  }
+}
+template <int kCnt>
+__device__ __forceinline__ void tmem_scale(uint32_t a, const float *f, int n) {
+  // columns a .. a + kCnt of this thread's lane, times f[column % n]
+#pragma unroll
+  for (int k = 0; k < kCnt; k += 16) {
+    float t[16];
+    tmem_ld16(a + k, t);
+    uint32_t u[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(t[j] * f[(k + j) % n]);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(a + k),
+        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+        "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+        : "memory");
+  }
+  tmem_wait_st();
+}
+
+template <int D, bool kF8, int N>
+__global__ void __launch_bounds__(kThreads, 2)
+    decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnParams p) {
+  using C = Cfg<D, kF8, N>;
+  constexpr int ST = C::kStages, NS = C::kTileStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Bars *bars = reinterpret_cast<Bars *>(smem + C::kOffBars);
+  static_assert(sizeof(Bars) <= C::kBytesBars, "barrier block");
+  __shared__ float s_qs[N];   // e4m3: the scale of a row's q
+  __shared__ int s_bad[kItems];
+  volatile int *abort = &bars->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->s_ready[i], 1);
+      mbar_init(&bars->s_free[i], 4);
+    }
+    mbar_init(&bars->q_ready, 4);
+    mbar_init(&bars->p_ready, 4);
+    mbar_init(&bars->o_done, 1);
+    mbar_init(&bars->sync, 4);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&bars->item_full[i], 1);
+      mbar_init(&bars->item_empty[i], 5);
+      s_bad[i] = 0;
+    }
+    bars->abort = 0;
+    p.desc[blockIdx.x].w = -1;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem, C::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  const Plan plan = make_plan<true>(p, &bars->plan);  // has CTA barriers
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (warp == 0) {
+    // ============ the walk over the items, and TMA (a page per lane) ============
+    Walk<true> walk(p, plan, lane);
+    Item it;
+    uint32_t sc = 0;                 // stages used so far
+    uint32_t g = 0;                  // tiles so far
+    const int pages = kTileKeys >> p.page_shift;  // pages of a tile
+    bool ok = true;
+    uint32_t slot = 0;
+    if (lane == 0) {
+      prefetch_tensormap(&tk);
+      prefetch_tensormap(&tv);
+    }
+    while (ok) {
+      const bool more = walk.next(it, lane);
+      const int si = slot % kItems;
+      if (!(ok = wait_bar_warp(&bars->item_empty[si], ((slot / kItems) & 1u) ^ 1u, abort))) break;
+      if (!more) it.kind = -1;
+      if (lane == 0) {
+        bars->item[si] = it;
+        s_bad[si] = 0;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->item_full[si]);
+      ++slot;
+      if (!more) break;
+      const int npage = (int)(((long long)it.pos0 + it.ntok + p.page - 1) >> p.page_shift);  // pages of the request
+      const int32_t *table = p.table + (size_t)it.r * p.max_pages;
+      // ids of pages base + lane, and of the 32 behind them
+      int base = it.j0 * pages;
+      int ids = base + lane < npage ? table[base + lane] : 0;
+      int ids_next = base + 32 + lane < npage ? table[base + 32 + lane] : 0;
+      int vbase = base, vids = ids;  // the value tiles come one tile behind
+      // One tile's loads.  K: [16-byte swizzled columns of 64][128 keys], a stage per
+      // 64 bf16 columns; V: a stage per 64 keys when the tile has two stages.
+      auto load = [&](int j, bool isv, int b0, int id_reg) -> bool {
+        const int pg0 = j * pages, np = min(pages, npage - pg0);
+        const int id = __shfl_sync(0xffffffffu, id_reg, (pg0 - b0) + (lane & (pages - 1)));
+        const bool mine = (lane & (pages - 1)) < np;
+        const bool good = id >= 0 && id < p.P;
+        const unsigned bad = __ballot_sync(0xffffffffu, mine && !good);
+        if (bad && lane == 0) s_bad[si] = 1;
+        const int ngood = __popc(__ballot_sync(0xffffffffu, lane < np && good));
+        const int pl = lane & (pages - 1);
+        const int plane = id * p.Hkv + it.hk;
+        const CUtensorMap *map = isv ? &tv : &tk;
+        if constexpr (NS == 2) {
+          // ops per page: 2 column blocks (x 2 key halves of a 128-key page for V)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t s = (sc + h) % ST;
+            if (!wait_bar_warp(&bars->empty[s], (((sc + h) / ST) & 1u) ^ 1u, abort)) return false;
+            uint8_t *dst = smem + s * kStageBytes;
+            if (!isv) {
+              if (lane == 0) mbar_arrive_expect_tx(&bars->full[s], (uint32_t)ngood << (p.page_shift + 7));
+              __syncwarp();
+              if (lane < np && good) tma_load_3d(dst + (pl << (p.page_shift + 7)), map, &bars->full[s], 64 * h, 0, plane);
+            } else {
+              // keys 64 h .. 64 h + 63: pages of this half (a page of 128 keys: its half)
+              const int per = pages > 1 ? pages / 2 : 1;
+              const bool in = pages > 1 ? (pl / per == h) : true;
+              const int rows = min(p.page, 64);
+              const int n = __popc(__ballot_sync(0xffffffffu, lane < np && good && in));
+              // of a 128-key page the second half is loaded only when it has keys
+              if (lane == 0) mbar_arrive_expect_tx(&bars->full[s], (uint32_t)(n * rows) * 256u);
+              __syncwarp();
+              const int l2 = lane & 15, col = lane >> 4;  // lanes 16 .. 31: the second column block
+              const int idv = __shfl_sync(0xffffffffu, id, l2 & (pages - 1));
+              const bool goodv = idv >= 0 && idv < p.P;
+              const int plv = l2 & (pages - 1);
+              if (l2 < np && goodv && (pages > 1 ? plv / per == h : true))
+                tma_load_3d(dst + col * 8192 + (pages > 1 ? (plv % per) << (p.page_shift + 7) : 0), map, &bars->full[s], 64 * col,
+                            pages > 1 ? 0 : 64 * h, idv * p.Hkv + it.hk);
+            }
+          }
+        } else {
+          const uint32_t s = sc % ST;
+          if (!wait_bar_warp(&bars->empty[s], ((sc / ST) & 1u) ^ 1u, abort)) return false;
+          uint8_t *dst = smem + s * kStageBytes;
+          constexpr int kRow = D * C::kEsz;  // bytes of a cached row
+          const uint32_t bytes = (uint32_t)ngood * (uint32_t)p.page * (kRow + (kF8 && !isv ? 2 : 0));
+          if (lane == 0) mbar_arrive_expect_tx(&bars->full[s], bytes);
+          __syncwarp();
+          if (lane < np && good) {
+            tma_load_3d(dst + pl * p.page * kRow, map, &bars->full[s], 0, 0, plane);
+            if (kF8 && !isv) {  // both scales travel with the keys
+              uint8_t *ss = smem + C::kOffScale + (g % kScaleSlots) * 2 * kTileKeys + pl * p.page;
+              bulk_load(ss, p.k_scale + (size_t)plane * p.page, (uint32_t)p.page, &bars->full[s]);
+              bulk_load(ss + kTileKeys, p.v_scale + (size_t)plane * p.page, (uint32_t)p.page, &bars->full[s]);
+            }
+          }
+        }
+        sc += NS;
+        return true;
+      };
+      for (int j = it.j0; j < it.j1 && ok; ++j) {
+        if (j * pages >= base + 32) {
+          base += 32;
+          ids = ids_next;
+          ids_next = base + 32 + lane < npage ? table[base + 32 + lane] : 0;
+        }
+        ok = load(j, false, base, ids);
+        ++g;
+        if (ok && j > it.j0) {
+          ok = load(j - 1, true, vbase, vids);
+        }
+        vbase = base;
+        vids = ids;
+      }
+      if (ok) ok = load(it.j1 - 1, true, vbase, vids);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ============ MMA issue ============
+      constexpr uint32_t id_s = kF8 ? idesc_f8(128, C::kNS, false, false) : idesc_bf16(128, C::kNS, false, false);
+      constexpr uint32_t id_o = kF8 ? idesc_f8(D, C::kNO, true, false) : idesc_bf16(D, C::kNO, true, false);
+      const uint32_t sb = smem_u32(smem), sQ = sb + C::kOffQ, sP = sb + C::kOffP;
+      uint32_t sc = 0, g = 0, slot = 0;
+      auto issue_s = [&](uint32_t gi) -> bool {
+        for (int h = 0; h < NS; ++h)
+          if (!wait_bar(&bars->full[(sc + h) % ST], ((sc + h) / ST) & 1u, abort)) return false;
+        if (!wait_bar(&bars->s_free[gi & 1], ((gi >> 1) & 1u) ^ 1u, abort)) return false;
+        tc_fence_after();
+        const uint32_t d = tmem + (gi & 1) * C::kNS;
+        if constexpr (!kF8) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t a = sb + ((sc + (ks >> 2)) % ST) * kStageBytes + (ks & 3) * 32;
+            umma_bf16(d, desc_sw128(a, 16, 1024), desc_sw128(sQ + (ks >> 2) * (N * 128) + (ks & 3) * 32, 16, 1024), id_s, ks > 0);
+          }
+        } else {
+          const uint32_t a = sb + (sc % ST) * kStageBytes;
+#pragma unroll
+          for (int ks = 0; ks < D / 32; ++ks) {
+            if (D == 128)
+              umma_f8(d, desc_sw128(a + ks * 32, 16, 1024), desc_sw128(sQ + ks * 32, 16, 1024), id_s, ks > 0);
+            else
+              umma_f8(d, desc_sw64(a + ks * 32, 16, 512), desc_sw64(sQ + ks * 32, 16, 512), id_s, ks > 0);
+          }
+        }
+        umma_commit(&bars->s_ready[gi & 1]);
+        for (int h = 0; h < NS; ++h) umma_commit(&bars->empty[(sc + h) % ST]);
+        sc += NS;
+        return true;
+      };
+      auto issue_o = [&](uint32_t gi, bool first) -> bool {
+        if (!wait_bar(&bars->p_ready, gi & 1u, abort)) return false;
+        for (int h = 0; h < NS; ++h)
+          if (!wait_bar(&bars->full[(sc + h) % ST], ((sc + h) / ST) & 1u, abort)) return false;
+        tc_fence_after();
+        const uint32_t d = tmem + C::kColO;
+        if constexpr (!kF8) {
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            const uint32_t a = NS == 2 ? sb + ((sc + (ks >> 2)) % ST) * kStageBytes + (ks & 3) * 2048
+                                       : sb + (sc % ST) * kStageBytes + ks * 2048;
+            umma_bf16(d, desc_sw128(a, 8192, 1024), desc_sw128(sP + (ks >> 2) * (C::kNO * 128) + (ks & 3) * 32, 16, 1024), id_o,
+                      ks > 0 || !first);
+          }
+        } else {
+          const uint32_t a = sb + (sc % ST) * kStageBytes;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint64_t b = desc_sw128(sP + ks * 32, 16, 1024);
+            if (D == 128)
+              umma_f8(d, desc_sw128(a + ks * 4096, 16, 1024), b, id_o, ks > 0 || !first);
+            else
+              umma_f8(d, desc_sw64(a + ks * 2048, 16, 512), b, id_o, ks > 0 || !first);
+          }
+        }
+        umma_commit(&bars->o_done);
+        for (int h = 0; h < NS; ++h) umma_commit(&bars->empty[(sc + h) % ST]);
+        sc += NS;
+        return true;
+      };
+      for (bool ok = true; ok;) {
+        const int si = slot % kItems;
+        if (!wait_bar(&bars->item_full[si], (slot / kItems) & 1u, abort)) break;
+        const int kind = bars->item[si].kind, n = bars->item[si].j1 - bars->item[si].j0;
+        mbar_arrive(&bars->item_empty[si]);
+        if (kind < 0) break;
+        if (!wait_bar(&bars->q_ready, slot & 1u, abort)) break;
+        ++slot;
+        for (int j = 0; j < n && ok; ++j) {
+          ok = issue_s(g + j);
+          if (ok && j > 0) ok = issue_o(g + j - 1, j == 1);
+        }
+        if (ok) ok = issue_o(g + n - 1, n == 1);
+        g += n;
+      }
+    }
+  } else {
+    // ============ softmax: thread = key ============
+    const int q4 = warp & 3, kk = 32 * q4 + lane;
+    const int st = tid - 64;                         // 0 .. 127
+    const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
+    const uint32_t sb = smem_u32(smem);
+    float *s_max = reinterpret_cast<float *>(smem + C::kOffMax);
+    constexpr float kSlack = kF8 ? 4.f : 8.f;        // log2 of the largest weight
+    uint32_t sc = 0, g = 0, slot = 0, syncs = 0;
+    // the softmax warps' barrier; like every wait here it gives up after a limit
+    auto softmax_sync = [&]() -> bool {
+      warp_arrive(&bars->sync);
+      return wait_bar_warp(&bars->sync, syncs++ & 1u, abort);
+    };
+    for (bool ok = true; ok;) {
+      const int si = slot % kItems;
+      if (!(ok = wait_bar_warp(&bars->item_full[si], (slot / kItems) & 1u, abort))) break;
+      const Item it = bars->item[si];
+      if (it.kind < 0) break;
+      ++slot;
+      const int nrow = it.ntok * p.G, n = it.j1 - it.j0;
+      // ---- q: rows of tokens x heads, 8 channels a lane, swizzled; rows past nrow are zero
+      {
+        constexpr int kLanes = D / 8, kPer = 128 / kLanes;
+        const int c = st % kLanes;
+#pragma unroll
+        for (int r0 = 0; r0 < N; r0 += kPer) {
+          const int row = r0 + st / kLanes;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (row < nrow) {
+            const int tok = row / p.G, gh = row - tok * p.G;
+            x = *reinterpret_cast<const uint4 *>(p.q + ((size_t)(it.row0 + tok) * p.H + it.hk * p.G + gh) * D + c * 8);
+          }
+          if constexpr (!kF8) {
+            sts128(sb + C::kOffQ + sw128_offset(row, c * 8, N), x);
+          } else {
+            // 2^-e q in two e4m3 parts; an infinite or NaN element makes the row's scores NaN
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            float f[8];
+            float am = 0.f;
+            bool odd = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              f[2 * k] = __uint_as_float(w[k] << 16);
+              f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              odd |= !(fabsf(f[k]) <= 3.4e38f);
+              am = fmaxf(am, fabsf(f[k]));
+            }
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+            // the power of two that brings the largest element into [128, 256)
+            int e = (int)(__float_as_uint(am) >> 23) - 127 - 7;
+            e = min(max(e, -100), 120);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float a = odd ? __int_as_float(0x7fffffff) : f[2 * k] * down, b = odd ? a : f[2 * k + 1] * down;
+              hi[k] = to_e4m3x2(a, b);
+              const float2 h = e4m3x2(hi[k]);
+              lo[k] = to_e4m3x2((a - h.x) * 16.f, (b - h.y) * 16.f);
+            }
+            if (c == 0) s_qs[row] = __uint_as_float((uint32_t)(127 + e) << 23) * p.c;
+            const uint2 vh = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            const uint2 vl = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            const uint32_t ch = c >> 1, in = (c & 1) * 8;
+            auto at = [&](int rr) {
+              return D == 128 ? rr * 128u + ((ch ^ (rr & 7u)) << 4) + in : rr * 64u + ((ch ^ ((rr >> 1) & 3u)) << 4) + in;
+            };
+            *reinterpret_cast<uint2 *>(smem + C::kOffQ + at(row)) = vh;
+            *reinterpret_cast<uint2 *>(smem + C::kOffQ + at(N + row)) = vl;
+          }
+        }
+        fence_proxy_async_smem();
+        warp_arrive(&bars->q_ready);
+        if (kF8 && !(ok = softmax_sync())) break;  // s_qs
+      }
+      float m[N], l[N];
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+      }
+      for (int j = it.j0; j < it.j1; ++j, ++g) {
+        if (!(ok = wait_bar_warp(&bars->s_ready[g & 1], (g >> 1) & 1u, abort))) break;
+        tc_fence_after();
+        float s[C::kNS];
+        tmem_ld<C::kNS>(tmem + (g & 1) * C::kNS + lane_base, s);
+        float ev = 0.f;
+        if constexpr (kF8) {
+          const uint8_t *ss = smem + C::kOffScale + (g % kScaleSlots) * 2 * kTileKeys;
+          const float ks = scale_value(ss[kk]);
+          const uint32_t vc = ss[kTileKeys + kk];
+          ev = vc == 255 ? __int_as_float(0x7fffffff) : (float)((int)vc - 127);
+#pragma unroll
+          for (int r = 0; r < N; ++r) s[r] = fmaf(s[N + r], 0.0625f, s[r]) * (ks * s_qs[r]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < N; ++r) s[r] *= p.c;
+        }
+        tc_fence_before();
+        warp_arrive(&bars->s_free[g & 1]);
+        const int key = j * kTileKeys + kk;
+        if (j * kTileKeys + kTileKeys - 1 > it.pos0) {  // some row does not see the whole tile
+          int lim = it.pos0, gh = 0;
+#pragma unroll
+          for (int r = 0; r < N; ++r) {
+            if (r < nrow && key > lim) s[r] = -INFINITY;
+            if (++gh == p.G) {
+              gh = 0;
+              ++lim;
+            }
+          }
+          if (kF8 && key >= it.pos0 + it.ntok) ev = 0.f;  // a stale scale may be anything
+        }
+        // ---- the tile's maxima
+        float *mx = s_max + (g & 1) * 4 * N;
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+          const float v = warp_max(s[r] + ev);
+          if (lane == (r & 31)) mx[r * 4 + q4] = v;
+        }
+        if (!(ok = softmax_sync())) break;
+        bool need = false;
+        float mt[N];
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+          const float4 v = *reinterpret_cast<const float4 *>(mx + r * 4);
+          mt[r] = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+          need |= mt[r] > m[r] + kSlack;
+        }
+        if (g > 0 && !(ok = wait_bar_warp(&bars->o_done, (g - 1) & 1u, abort))) break;  // W is read, O^T complete
+        if (need) {  // the same in every thread
+          tc_fence_after();
+          float f[N];
+#pragma unroll
+          for (int r = 0; r < N; ++r) {
+            const float mn = fmaxf(m[r], mt[r]);
+            f[r] = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
+            m[r] = mn;
+            l[r] *= f[r];
+          }
+          if (j > it.j0) tmem_scale<C::kNO>(tmem + C::kColO + lane_base, f, N);
+        }
+        // ---- weights, rounded into their parts, as the second product's B operand [row][key]
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+          const float ms = m[r] == -INFINITY ? 0.f : m[r];
+          if constexpr (!kF8) {
+            const float w = ex2(s[r] - ms);
+            l[r] += w;
+            const uint32_t off = (kk >> 6) * (C::kNO * 128) + r * 128 + ((((kk & 63) >> 3) ^ (r & 7)) << 4) + (kk & 7) * 2;
+            const __nv_bfloat16 h = __float2bfloat16_rn(w);
+            const __nv_bfloat16 lo = __float2bfloat16_rn(w - __bfloat162float(h));
+            *reinterpret_cast<__nv_bfloat16 *>(smem + C::kOffP + off) = h;
+            *reinterpret_cast<__nv_bfloat16 *>(smem + C::kOffP + off + N * 128) = lo;
+          } else {
+            l[r] += ex2(s[r] - ms);
+            const float w = ex2(s[r] + ev - ms) * 16.f;
+            const uint32_t off = r * 128 + (((kk >> 4) ^ (r & 7)) << 4) + (kk & 15);
+            const uint32_t h = to_e4m3x2(w, 0.f);
+            const float r1 = (w - e4m3x2(h).x) * 16.f;
+            const uint32_t h1 = to_e4m3x2(r1, 0.f);
+            const float r2 = (r1 - e4m3x2(h1).x) * 16.f;
+            const uint32_t h2 = to_e4m3x2(r2, 0.f);
+            smem[C::kOffP + off] = (uint8_t)h;
+            smem[C::kOffP + off + N * 128] = (uint8_t)h1;
+            smem[C::kOffP + off + 2 * N * 128] = (uint8_t)h2;
+          }
+        }
+        if (j == it.j1 - 1) {
+          // the last tile: its values have landed, and rows behind the cache's end become zeros
+          const int jj = n - 1;
+          const uint32_t vs = sc + NS * (2 * jj + 1);  // K of every tile and V of the earlier ones come first
+          for (int h = 0; h < NS && ok; ++h) ok = wait_bar_warp(&bars->full[(vs + h) % ST], ((vs + h) / ST) & 1u, abort);
+          if (!ok) break;
+          if (key >= it.pos0 + it.ntok) {
+            if constexpr (NS == 2) {
+              const uint32_t a = sb + ((vs + (kk >> 6)) % ST) * kStageBytes + (kk & 63) * 128;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                sts128(a + 16 * k, make_uint4(0, 0, 0, 0));
+                sts128(a + 8192 + 16 * k, make_uint4(0, 0, 0, 0));
+              }
+            } else {
+              constexpr int kRow = D * C::kEsz;
+              const uint32_t a = sb + (vs % ST) * kStageBytes + kk * kRow;
+#pragma unroll
+              for (int k = 0; k < kRow / 16; ++k) sts128(a + 16 * k, make_uint4(0, 0, 0, 0));
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        warp_arrive(&bars->p_ready);
+      }
+      if (!ok) break;
+      sc += NS * 2 * n;
+      // ---- sums over the keys; the item's outputs or its partial result
+      const int bad = s_bad[si];
+      float *red = s_max;  // [4 warps][N]; the maxima of the last tile have been read
+      if (!(ok = softmax_sync())) break;
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        float v = l[r];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == (r & 31)) red[r * 4 + q4] = v;
+      }
+      if (!(ok = softmax_sync())) break;
+      if (!(ok = wait_bar_warp(&bars->o_done, (g - 1) & 1u, abort))) break;
+      tc_fence_after();
+      float o[C::kNO];
+      tmem_ld<C::kNO>(tmem + C::kColO + lane_base, o);
+      tc_fence_before();
+      const int ch = D == 128 ? kk : 16 * q4 + lane;   // channel of this TMEM lane
+      const bool has = D == 128 || lane < 16;
+      const int pslot = 2 * blockIdx.x + (it.kind == 1 ? 1 : 0);
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        const float4 v = *reinterpret_cast<const float4 *>(red + r * 4);
+        const float lt = (v.x + v.y) + (v.z + v.w);
+        float x;
+        if constexpr (!kF8) x = o[r] + o[N + r];
+        else x = (o[r] + 0.0625f * (o[N + r] + 0.0625f * o[2 * N + r])) * 0.0625f;
+        if (r < nrow && has) {
+          if (it.kind == 0) {
+            if (!bad) {
+              const int tok = r / p.G, gh = r - tok * p.G;
+              p.o[((size_t)(it.row0 + tok) * p.H + it.hk * p.G + gh) * D + ch] = __float2bfloat16_rn(lt == 0.f ? 0.f : x / lt);
+            }
+          } else {
+            p.part[((size_t)pslot * N + r) * D + ch] = x;
+            if (ch == 0) p.ml[(size_t)pslot * N + r] = make_float2(m[r], lt);
+          }
+        }
+      }
+      if (st == 0) {
+        if (it.kind != 0) p.skip[pslot] = bad;
+        if (bad && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_BAD_SLOT);
+      }
+      if (!(ok = softmax_sync())) break;  // red is rewritten by the next item
+      warp_arrive(&bars->item_empty[si]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (*abort && tid == 0 && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_WAIT_TIMEOUT);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+template <int D, bool kF8, int N>
+cudaError_t launch(const AttnParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t stream) {
+  auto kernel = decode_kernel<D, kF8, N>;
+  const int bytes = (int)Cfg<D, kF8, N>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  kernel<<<ctas, kThreads, bytes, stream>>>(tk, tv, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_merge<D, N>(p, ctas, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_decode(const AttnParams &p, bool f8, int d, int rows, const void *k_cache, const void *v_cache,
+                          int ctas, cudaStream_t stream) {
+  const int esz = f8 ? 1 : 2;
+  const CUtensorMapDataType type = f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle sw = f8 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  const long long dims[3] = {d, p.page, p.P > 0 ? (long long)p.P * p.Hkv : 1};
+  if (p.P == 0) k_cache = v_cache = p.q;  // an empty pool: nothing is ever loaded
+  const int inner = f8 ? d : 64;
+  const int kbox[3] = {inner, p.page, 1};
+  const int vbox[3] = {inner, !f8 && d == 128 ? min(p.page, 64) : p.page, 1};
+  CUtensorMap tk, tv;
+  if (!encode_3d_map_swizzled(&tk, k_cache, type, esz, dims, kbox, sw) ||
+      !encode_3d_map_swizzled(&tv, v_cache, type, esz, dims, vbox, sw))
+    return cudaErrorInvalidValue;
+  const bool small = rows <= 16;
+  if (d == 128) {
+    if (f8) return small ? launch<128, true, 16>(p, tk, tv, ctas, stream) : launch<128, true, 32>(p, tk, tv, ctas, stream);
+    return small ? launch<128, false, 16>(p, tk, tv, ctas, stream) : launch<128, false, 32>(p, tk, tv, ctas, stream);
+  }
+  if (f8) return small ? launch<64, true, 16>(p, tk, tv, ctas, stream) : launch<64, true, 32>(p, tk, tv, ctas, stream);
+  return small ? launch<64, false, 16>(p, tk, tv, ctas, stream) : launch<64, false, 32>(p, tk, tv, ctas, stream);
+}
+
+}  // namespace paged
+}  // namespace glinattn
