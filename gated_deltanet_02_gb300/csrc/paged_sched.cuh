@@ -264,81 +264,116 @@ struct Walk {
   }
 };
 
+// A running (maximum, sum, outputs) triple of one row, kE channels a lane.
+template <int kE>
+struct Partial {
+  float m = -INFINITY, l = 0.f, o[kE] = {};
+  // Adds a piece; one without weight adds nothing, whatever its outputs hold.
+  __device__ __forceinline__ void add(float pm, float pl, const float (&x)[kE]) {
+    const float mn = fmaxf(m, pm), ms = mn == -INFINITY ? 0.f : mn;
+    const float f = exp2f(m - ms), g = exp2f(pm - ms);
+    l = l * f + (pm == -INFINITY ? 0.f : pl * g);
+#pragma unroll
+    for (int e = 0; e < kE; ++e) o[e] = o[e] * f + (pm == -INFINITY ? 0.f : x[e] * g);
+    m = mn;
+  }
+};
+
 // Joins the pieces of the item that begins in CTA blockIdx.x and goes on
-// behind it: blockIdx.y = its row; 8 warps share the pieces, a lane holds D / 32
-// channels.  Bound by latency: a few L2 reads per piece.
-template <int D, int kRows>
+// behind it, kRowsPerCta rows per CTA (blockIdx.y); a lane holds D / 32
+// channels.  Bound by latency, a few L2 reads per piece: with few pieces a
+// warp takes a row, with many the 8 warps share the pieces of one row at a time.
+template <int D, int kRows, int kRowsPerCta>
 __global__ void __launch_bounds__(256) merge_kernel(const AttnParams p) {
   constexpr int kE = D / 32;
   __shared__ float s_m[8], s_l[8], s_o[8][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c0 = blockIdx.x, row = blockIdx.y;
+  const int c0 = blockIdx.x;
   const int4 d = p.desc[c0];
-  if (d.w < 0 || row >= d.z * p.G) return;
+  const int nrow = d.z * p.G, row0 = blockIdx.y * kRowsPerCta;
+  if (d.w < 0 || row0 >= nrow) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float m = -INFINITY, l = 0.f, o[kE];
   int bad = 0;
-#pragma unroll
-  for (int e = 0; e < kE; ++e) o[e] = 0.f;
-#pragma unroll 4
-  for (int c = c0 + warp; c <= d.w; c += 8) {
-    const int slot = 2 * c + (c == c0 ? 1 : 0);
-    bad |= p.skip[slot];
-    const float2 ml = p.ml[(size_t)slot * kRows + row];
-    float x[kE];
-#pragma unroll
-    for (int e = 0; e < kE; ++e) x[e] = p.part[((size_t)slot * kRows + row) * D + lane * kE + e];
-    const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
-    const float f = exp2f(m - ms), g = exp2f(ml.x - ms);
-    // a piece without weight adds nothing, whatever its outputs hold
-    l = l * f + (ml.x == -INFINITY ? 0.f : ml.y * g);
-#pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] = o[e] * f + (ml.x == -INFINITY ? 0.f : x[e] * g);
-    m = mn;
-  }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-#pragma unroll
-  for (int e = 0; e < kE; ++e) s_o[warp][lane * kE + e] = o[e];
+  for (int c = c0 + (int)threadIdx.x; c <= d.w; c += 256) bad |= p.skip[2 * c + (c == c0 ? 1 : 0)];
   if (__syncthreads_or(bad)) return;
-  if (threadIdx.x < D) {
-    float mt = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) mt = fmaxf(mt, s_m[w]);
-    const float ms = mt == -INFINITY ? 0.f : mt;
-    float lt = 0.f, ot = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      const float f = exp2f(s_m[w] - ms);
-      lt += s_l[w] * f;
-      ot += s_o[w][threadIdx.x] * f;
+  auto pieces = [&](int row, int first, int step, Partial<kE> &a) {
+#pragma unroll 4
+    for (int c = c0 + first; c <= d.w; c += step) {
+      const size_t at = (size_t)(2 * c + (c == c0 ? 1 : 0)) * kRows + row;
+      const float2 ml = p.ml[at];
+      float x[kE];
+      if constexpr (kE == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(p.part + at * D + lane * 4);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2 *>(p.part + at * D + lane * 2);
+        x[0] = v.x, x[1] = v.y;
+      }
+      a.add(ml.x, ml.y, x);
     }
-    const int tok = row / p.G, g = row % p.G;
-    p.o[((size_t)(d.x + tok) * p.H + d.y * p.G + g) * D + threadIdx.x] = __float2bfloat16_rn(lt == 0.f ? 0.f : ot / lt);
+  };
+  auto out = [&](int row) {
+    const int tok = row / p.G, g = row - tok * p.G;
+    return p.o + ((size_t)(d.x + tok) * p.H + d.y * p.G + g) * D;
+  };
+  if (kRowsPerCta == 8 && d.w - c0 < 8) {
+    const int row = row0 + warp;
+    if (row >= nrow) return;
+    Partial<kE> a;
+    pieces(row, 0, 1, a);
+    __nv_bfloat16 *o = out(row) + lane * kE;
+#pragma unroll
+    for (int e = 0; e < kE; e += 2)
+      *reinterpret_cast<uint32_t *>(o + e) = a.l == 0.f ? 0u : pack_bf16(a.o[e] / a.l, a.o[e + 1] / a.l);
+    return;
+  }
+  for (int row = row0; row < min(row0 + kRowsPerCta, nrow); ++row) {
+    Partial<kE> a;
+    pieces(row, warp, 8, a);
+    if (lane == 0) {
+      s_m[warp] = a.m;
+      s_l[warp] = a.l;
+    }
+#pragma unroll
+    for (int e = 0; e < kE; ++e) s_o[warp][lane * kE + e] = a.o[e];
+    __syncthreads();
+    if (threadIdx.x < D) {
+      Partial<1> b;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float x[1] = {s_o[w][threadIdx.x]};
+        b.add(s_m[w], s_l[w], x);
+      }
+      out(row)[threadIdx.x] = __float2bfloat16_rn(b.l == 0.f ? 0.f : b.o[0] / b.l);
+    }
+    __syncthreads();
   }
 }
 
 // The merge, launched so that it is in place when the attention kernel ends.
-template <int D, int kRows>
+template <int D, int kRows, int kRowsPerCta>
 cudaError_t launch_merge(const AttnParams &p, int ctas, cudaStream_t stream) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas, kRows, 1);
+  cfg.gridDim = dim3((unsigned)ctas, kRows / kRowsPerCta, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<D, kRows>, p);
+  return cudaLaunchKernelEx(&cfg, merge_kernel<D, kRows, kRowsPerCta>, p);
 }
 
 // rows <= kDecodeRows query rows (tokens x heads of a group) per item
 constexpr int kDecodeRows = 32;
 cudaError_t launch_decode(const AttnParams &p, bool f8, int d, int rows, const void *k_cache, const void *v_cache,
                           int ctas, cudaStream_t stream);
+
+// more of them: items of kPrefillRows / G tokens
+constexpr int kPrefillRows = 256;
+cudaError_t launch_prefill(const AttnParams &p, bool f8, int d, const void *k_cache, const void *v_cache, int ctas,
+                           cudaStream_t stream);
 
 }  // namespace paged
 }  // namespace glinattn

@@ -469,7 +469,7 @@ glinattn_status glinattn_kv_gather(const glinattn_kv_args *args, glinattn_stream
  *   A row that sees no key (a negative position) or whose every score is
  *   -infinity gives zeros.  Scores, softmax statistics and sums are fp32.
  *
- *   q, o [num_tok, H, d] bf16; Hkv divides H.
+ *   q, o [num_tok, H, d] bf16; Hkv divides H, H / Hkv <= 256.
  *   scale: finite and > 0.  max_q_len: an upper bound of the ranges' lengths
  *     (it selects the kernel); a longer range sets GLINATTN_DEV_BAD_COUNT and
  *     its request is skipped.

@@ -80,7 +80,7 @@ def test_cache_call_refusals(name, kw, code):
 
 
 @pytest.mark.parametrize("kw,code", CACHE + [
-    (dict(heads=3), INVALID), (dict(heads=0), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(heads=514), UNSUPPORTED), (dict(heads=3), INVALID), (dict(heads=0), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
     (dict(scale=math.inf), INVALID), (dict(scale=math.nan), INVALID), (dict(max_q_len=-1), INVALID),
     (dict(q=None), INVALID), (dict(o=None), INVALID), (dict(q=A + 2), INVALID), (dict(o=A + 4), INVALID),
     (dict(num_tok=1 << 30), INVALID)])
