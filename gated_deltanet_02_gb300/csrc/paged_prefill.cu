@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     } else if (warp == 1 && lane == 0) {
       // ============ MMA issue ============
       constexpr uint32_t id_s = idesc_bf16(128, 128, false, false), id_o = idesc_bf16(128, D, false, true);
-      uint32_t sc = 0, slot = 0, np[2] = {0, 0};
+      uint32_t sc = 0, slot = 0, np[2] = {0, 0}, nq[2] = {0, 0};
       // S_w = Q_w K^T from the stage of number k
       auto issue_s = [&](int w, uint32_t k) {
         const uint32_t a = sb + w * C::kQTile, b = sb + C::kOffRing + (k % ST) * C::kStageBytes;
@@ -237,12 +237,15 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         const Item it = bars->item[si];
         mbar_arrive(&bars->item_empty[si]);
         if (it.kind < 0) break;
-        const uint32_t ph = slot++ & 1u;
+        ++slot;
         const int n = it.j1 - it.j0, n0 = last_tile(it, p.G, 0) - it.j0, n1 = last_tile(it, p.G, 1) - it.j0;
         // tile j of the item: K at stage number sc + 2 j, V behind it
         if (!(ok = landed(sc))) break;
-        for (int w = 0; w < 2 && ok; ++w)
-          if (ok = wait_bar(&bars->q_ready[w], ph, abort); ok && (w ? n1 : n0) > 0) issue_s(w, sc);
+        for (int w = 0; w < 2 && ok; ++w) {
+          if ((w ? n1 : n0) <= 0) continue;
+          ok = wait_bar(&bars->q_ready[w], nq[w]++ & 1u, abort);
+          if (ok) issue_s(w, sc);
+        }
         if (!ok) break;
         umma_commit(&bars->empty[sc % ST]);
         for (int j = 0; j < n && ok; ++j) {
@@ -272,8 +275,11 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
     const uint32_t tS = tmem + C::kColS + 128 * w + lane_base, tO = tmem + C::kColO + D * w + lane_base;
     uint32_t sc = 0, slot = 0, ns = 0, nd = 0;
-    // q of an item's row into shared memory; rows past the last are zero
+    // q of an item's row into shared memory; rows past the last are zero.  Only
+    // for a row tile that has work in the item: its softmax warps then wait for
+    // the MMA warp's answer, so that q_ready is never a phase ahead of its reader.
     auto load_q = [&](const Item &it) {
+      if (it.kind < 0 || last_tile(it, p.G, w) <= it.j0) return;
       const int tok = row / p.G, gh = row - tok * p.G;
       const bool has = row < it.ntok * p.G;
       const uint4 *src = reinterpret_cast<const uint4 *>(p.q + ((size_t)(it.row0 + (has ? tok : 0)) * p.H + it.hk * p.G + gh) * D);
@@ -289,7 +295,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     Item it;
     if (ok) {
       it = bars->item[0];
-      if (it.kind >= 0) load_q(it);
+      load_q(it);
     }
     while (ok && it.kind >= 0) {
       const int si = slot % kItems;
@@ -382,7 +388,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       ++slot;
       if (!(ok = wait_bar_warp(&bars->item_full[slot % kItems], (slot / kItems) & 1u, abort))) break;
       const Item nx = bars->item[slot % kItems];
-      if (nx.kind >= 0) load_q(nx);
+      load_q(nx);
       const int bad = bars->bad[si];
       const bool has = row < it.ntok * p.G;
       const size_t prow = (size_t)(2 * blockIdx.x + (it.kind == 1 ? 1 : 0)) * kPrefillRows + row;

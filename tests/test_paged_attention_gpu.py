@@ -177,6 +177,25 @@ def test_work_is_shared_out(R, kv, H, Hkv):
     _check(c, _q(c, H))
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("q_len", [5, 15, 16, 17, 31])
+def test_many_items_that_fill_half_a_row_tile(q_len, cache):
+    """Several items per SM with 40 .. 248 of 256 rows, some with an empty second half."""
+    c = paged_case([(max(1, q_len - 13 * (r % 2)), 60 + 5 * r) for r in range(160)], 2, 64, 16, cache, seed=q_len)
+    q = _q(c, 16)
+    first, status = _run(c, q)
+    assert status == 0
+    for _ in range(20):
+        again, status = _run(c, q)
+        assert status == 0 and torch.equal(again, first)
+    c["lengths"] = c["lengths"][:6]
+    n = int(c["q_start"][6])
+    for k in ("kv_len", "table"):
+        c[k] = c[k][:6].contiguous()
+    c["q_start"], c["num_tok"] = c["q_start"][:7].contiguous(), n
+    _check(c, q[:n].contiguous())
+
+
 @pytest.mark.parametrize("big", [False, True])
 def test_bad_pages_and_lengths_are_flagged_and_skipped(big):
     n = 150 if big else 2
