@@ -646,7 +646,7 @@ cudaError_t launch(const AttnParams &p, const CUtensorMap &tk, const CUtensorMap
   if (e != cudaSuccess) return e;
   kernel<<<ctas, kThreads, bytes, stream>>>(tk, tv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_merge<D, N, 1>(p, ctas, stream);
+  return launch_merge<D, N, true>(p, ctas, stream);
 }
 
 }  // namespace

@@ -42,9 +42,15 @@ struct Cfg {
   static constexpr int kThreads = kF8 ? 512 : 384;
   static constexpr uint32_t kQTile = 128 * D * 2;
   static constexpr uint32_t kStageBytes = kTileKeys * D * 2;
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? (kF8 ? 3 : 4) : 6;
+  // e4m3: tiles as they are in the cache (with their scales), before the conversion
+  static constexpr int kRawStages = kF8 ? (D == 128 ? 3 : 6) : 0;
+  static constexpr uint32_t kRawBytes = kTileKeys * D;
   static constexpr uint32_t kOffRing = 2 * kQTile;
-  static constexpr uint32_t kOffBars = kOffRing + kStages * kStageBytes;
+  static constexpr uint32_t kOffRaw = kOffRing + kStages * kStageBytes;
+  static constexpr uint32_t kOffScale = kOffRaw + kRawStages * kRawBytes;
+  static constexpr uint32_t kOffOut = kOffScale + kRawStages * kTileKeys;  // 2 KiB per softmax warp
+  static constexpr uint32_t kOffBars = kOffOut + 8 * 2048;
   static constexpr uint32_t kBytesBars = 1024;
   static constexpr uint32_t kSmem = kOffBars + kBytesBars + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -52,8 +58,8 @@ struct Cfg {
 };
 
 struct Bars {
-  uint64_t full[8], empty[8];
-  uint64_t s_ready[2], p_ready[2], q_ready[2], o_done[2];
+  uint64_t full[6], empty[6], raw_full[6], raw_empty[6];
+  uint64_t s_ready[2], p_ready[2][2], q_ready[2], o_done[2];
   uint64_t item_full[kItems], item_empty[kItems];
   Item item[kItems];
   PlanShared plan;
@@ -121,9 +127,14 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       mbar_init(&bars->full[s], kF8 ? 4 : 1);
       mbar_init(&bars->empty[s], 1);
     }
+    for (int s = 0; s < C::kRawStages; ++s) {
+      mbar_init(&bars->raw_full[s], 1);
+      mbar_init(&bars->raw_empty[s], 4);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->s_ready[i], 1);
-      mbar_init(&bars->p_ready[i], 4);
+      mbar_init(&bars->p_ready[i][0], 4);
+      mbar_init(&bars->p_ready[i][1], 4);
       mbar_init(&bars->q_ready[i], 4);
       mbar_init(&bars->o_done[i], 1);
     }
@@ -149,10 +160,10 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
   const int pages = kTileKeys >> p.page_shift;  // pages of a tile
 
   if (warp < 4) {
-    // registers a thread: 56 + 2 x 176 + 104 of 4 x 128 (e4m3), 80 + 2 x 208 of 3 x 168
-    regs_dec<kF8 ? 56 : 80>();
+    // registers a thread: 64 + 2 x 184 + 80 of 4 x 128 (e4m3), 80 + 2 x 208 of 3 x 168
+    regs_dec<kF8 ? 64 : 80>();
     if (warp == 0) {
-      // ============ the walk over the items; bf16: TMA, a page and 64 channels per lane ============
+      // ============ the walk over the items, and TMA ============
       Walk<false> walk(p, plan, lane);
       Item it;
       uint32_t sc = 0, slot = 0;
@@ -169,34 +180,47 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         if (lane == 0) mbar_arrive(&bars->item_full[si]);
         ++slot;
         if (!more) break;
-        if constexpr (!kF8) {
-          const int npage = (int)(((long long)it.pos0 + it.ntok + p.page - 1) >> p.page_shift);
-          const int32_t *table = p.table + (size_t)it.r * p.max_pages;
-          int base = it.j0 * pages;
-          int ids = base + lane < npage ? table[base + lane] : 0;
-          int ids_next = base + 32 + lane < npage ? table[base + 32 + lane] : 0;
-          for (int j = it.j0; j < it.j1 && ok; ++j) {
-            if (j * pages >= base + 32) {
-              base += 32;
-              ids = ids_next;
-              ids_next = base + 32 + lane < npage ? table[base + 32 + lane] : 0;
-            }
-            const int pl = lane & (pages - 1), col = lane / pages;
-            const int np = min(pages, npage - j * pages);
-            const int id = __shfl_sync(0xffffffffu, ids, j * pages - base + pl);
-            const bool good = id >= 0 && id < p.P, op = pl < np && col < D / 64;
-            if (__any_sync(0xffffffffu, op && !good) && lane == 0) bars->bad[si] = 1;
-            const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, op && good)) << (p.page_shift + 7);
-            const int plane = id * p.Hkv + it.hk;
+        const int npage = (int)(((long long)it.pos0 + it.ntok + p.page - 1) >> p.page_shift);
+        const int32_t *table = p.table + (size_t)it.r * p.max_pages;
+        int base = it.j0 * pages;
+        int ids = base + lane < npage ? table[base + lane] : 0;
+        int ids_next = base + 32 + lane < npage ? table[base + 32 + lane] : 0;
+        for (int j = it.j0; j < it.j1 && ok; ++j) {
+          if (j * pages >= base + 32) {
+            base += 32;
+            ids = ids_next;
+            ids_next = base + 32 + lane < npage ? table[base + 32 + lane] : 0;
+          }
+          // bf16: a page and 64 channels per lane; e4m3: a page per lane
+          const int pl = lane & (pages - 1), col = lane / pages;
+          const int np = min(pages, npage - j * pages);
+          const int id = __shfl_sync(0xffffffffu, ids, j * pages - base + pl);
+          const bool good = id >= 0 && id < p.P, op = pl < np && col < (kF8 ? 1 : D / 64);
+          if (__any_sync(0xffffffffu, op && !good) && lane == 0) bars->bad[si] = 1;
+          const uint32_t ops = (uint32_t)__popc(__ballot_sync(0xffffffffu, op && good));
+          const uint32_t bytes = kF8 ? ops * (uint32_t)p.page * (D + 1) : ops << (p.page_shift + 7);
+          const size_t plane = (size_t)(good ? id : 0) * p.Hkv + it.hk;
 #pragma unroll
-            for (int v = 0; v < 2; ++v, ++sc) {
+          for (int v = 0; v < 2; ++v, ++sc) {
+            if constexpr (kF8) {
+              const uint32_t s = sc % C::kRawStages;
+              if (!(ok = wait_bar_warp(&bars->raw_empty[s], ((sc / C::kRawStages) & 1u) ^ 1u, abort))) break;
+              if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[s], bytes);
+              __syncwarp();
+              if (op && good) {
+                bulk_load(smem + C::kOffRaw + s * C::kRawBytes + pl * p.page * D, (v ? v_cache : k_cache) + plane * p.page * D,
+                          (uint32_t)p.page * D, &bars->raw_full[s]);
+                bulk_load(smem + C::kOffScale + s * kTileKeys + pl * p.page, (v ? p.v_scale : p.k_scale) + plane * p.page,
+                          (uint32_t)p.page, &bars->raw_full[s]);
+              }
+            } else {
               const uint32_t s = sc % ST;
               if (!(ok = wait_bar_warp(&bars->empty[s], ((sc / ST) & 1u) ^ 1u, abort))) break;
               if (lane == 0) mbar_arrive_expect_tx(&bars->full[s], bytes);
               __syncwarp();
               if (op && good)
                 tma_load_3d(smem + C::kOffRing + s * C::kStageBytes + col * 16384 + (pl << (p.page_shift + 7)), v ? &tv : &tk,
-                            &bars->full[s], 64 * col, 0, plane);
+                            &bars->full[s], 64 * col, 0, (int)plane);
             }
           }
         }
@@ -217,13 +241,16 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       };
       // O_w (+)= P_w V
       auto issue_o = [&](int w, uint32_t k, bool first) -> bool {
-        if (!wait_bar(&bars->p_ready[w], np[w]++ & 1u, abort)) return false;
-        tc_fence_after();
-        const uint32_t b = sb + C::kOffRing + (k % ST) * C::kStageBytes;
+        const uint32_t b = sb + C::kOffRing + (k % ST) * C::kStageBytes, ph = np[w]++ & 1u;
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
+        for (int ks = 0; ks < 8; ++ks) {
+          if (ks % 4 == 0) {  // 64 keys' weights at a time
+            if (!wait_bar(&bars->p_ready[w][ks / 4], ph, abort)) return false;
+            tc_fence_after();
+          }
           umma_bf16_tmem_a(tmem + C::kColO + D * w, tmem + C::kColS + 128 * w + 8 * ks, desc_sw128(b + ks * 2048, 16384, 1024), id_o,
                            ks > 0 || !first);
+        }
         return true;
       };
       auto landed = [&](uint32_t k) -> bool {
@@ -269,25 +296,38 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     }
   } else if (warp < 12) {
     // ============ softmax: row tile w, thread = row ============
-    regs_inc<kF8 ? 176 : 208>();
+    regs_inc<kF8 ? 184 : 208>();
     const int w = warp >= 8 ? 1 : 0, q4 = warp & 3;
     const int lrow = 32 * q4 + lane, row = 128 * w + lrow;
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
     const uint32_t tS = tmem + C::kColS + 128 * w + lane_base, tO = tmem + C::kColO + D * w + lane_base;
     uint32_t sc = 0, slot = 0, ns = 0, nd = 0;
-    // q of an item's row into shared memory; rows past the last are zero.  Only
-    // for a row tile that has work in the item: its softmax warps then wait for
-    // the MMA warp's answer, so that q_ready is never a phase ahead of its reader.
+    const uint32_t inv_g = (65535u + p.G) / p.G;  // row / G is row * inv_g >> 16 for row, G <= 256
+    // a row's place among the item's rows of q and o, in elements
+    auto row_at = [&](const Item &it, int r) -> size_t {
+      const int tok = (int)((uint32_t)r * inv_g >> 16);
+      return ((size_t)(it.row0 + tok) * p.H + it.hk * p.G + (r - tok * p.G)) * D;
+    };
+    // q of the warp's 32 rows into shared memory, D / 8 lanes a row; rows past
+    // the last are zero.  Only for a row tile that has work in the item: its
+    // softmax warps then wait for the MMA warp's answer, so that q_ready is
+    // never a phase ahead of its reader.
     auto load_q = [&](const Item &it) {
       if (it.kind < 0 || last_tile(it, p.G, w) <= it.j0) return;
-      const int tok = row / p.G, gh = row - tok * p.G;
-      const bool has = row < it.ntok * p.G;
-      const uint4 *src = reinterpret_cast<const uint4 *>(p.q + ((size_t)(it.row0 + (has ? tok : 0)) * p.H + it.hk * p.G + gh) * D);
-      uint4 x[D / 8];
+      constexpr int kLanes = D / 8, kPer = 32 / kLanes;
+      const int c = lane % kLanes, nrow = it.ntok * p.G;
 #pragma unroll
-      for (int k = 0; k < D / 8; ++k) x[k] = has ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+      for (int h = 0; h < 2; ++h) {
+        uint4 x[16 / kPer];
 #pragma unroll
-      for (int k = 0; k < D / 8; ++k) sts128(sb + w * C::kQTile + sw128_offset(lrow, k * 8, 128), x[k]);
+        for (int k = 0; k < 16 / kPer; ++k) {
+          const int r = 128 * w + 32 * q4 + 16 * h + k * kPer + lane / kLanes;
+          x[k] = r < nrow ? __ldg(reinterpret_cast<const uint4 *>(p.q + row_at(it, r)) + c) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 16 / kPer; ++k)
+          sts128(sb + w * C::kQTile + sw128_offset(32 * q4 + 16 * h + k * kPer + lane / kLanes, c * 8, 128), x[k]);
+      }
       fence_proxy_async_smem();
       warp_arrive(&bars->q_ready[w]);
     };
@@ -301,7 +341,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       const int si = slot % kItems;
       const int n = it.j1 - it.j0, nw = last_tile(it, p.G, w) - it.j0;
       const int end = it.pos0 + it.ntok;                    // keys behind it are not there
-      const int lim = it.pos0 + row / p.G;                  // the row's last key
+      const int lim = it.pos0 + (int)((uint32_t)row * inv_g >> 16);  // the row's last key
       const int first_lim = it.pos0 + (128 * w) / p.G;      // the first row's
       const bool zero0 = last_tile(it, p.G, 0) == it.j1;    // tile 0 looks at the last cache tile
       float m = -INFINITY, l = 0.f;
@@ -352,35 +392,36 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         const float2 c2 = make_float2(p.c, p.c), m2 = make_float2(-ms, -ms);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int k = 0; k < 128; k += 64) {
+        for (int h = 0; h < 2; ++h) {
           uint32_t u[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            float2 x = __ffma2_rn(make_float2(s[k + 2 * e], s[k + 2 * e + 1]), c2, m2);
+            float2 x = __ffma2_rn(make_float2(s[64 * h + 2 * e], s[64 * h + 2 * e + 1]), c2, m2);
             x.x = ex2(x.x);
             x.y = ex2(x.y);
             sum[e & 1] = __fadd2_rn(sum[e & 1], x);
             u[e] = pack_bf16(x.x, x.y);
           }
-          tmem_st32(tS + k / 2, u);
-        }
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        if (jj == nw - 1) {
-          // the row tile's last cache tile: its values have landed; rows behind the cache's end become zeros
-          const uint32_t vs = sc + 2 * jj + 1;
-          if (!(ok = wait_bar_warp(&bars->full[vs % ST], (vs / ST) & 1u, abort))) break;
-          if (!kF8 && j == it.j1 - 1 && (w == 0 || !zero0) && j * kTileKeys + lrow >= end) {
-            const uint32_t a = sb + C::kOffRing + (vs % ST) * C::kStageBytes + lrow * 128;
+          if (h == 0 && jj == nw - 1) {
+            // the row tile's last cache tile: its values have landed; rows behind the cache's end become zeros
+            const uint32_t vs = sc + 2 * jj + 1;
+            if (!(ok = wait_bar_warp(&bars->full[vs % ST], (vs / ST) & 1u, abort))) break;
+            if (!kF8 && j == it.j1 - 1 && (w == 0 || !zero0) && j * kTileKeys + lrow >= end) {
+              const uint32_t a = sb + C::kOffRing + (vs % ST) * C::kStageBytes + lrow * 128;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              sts128(a + 16 * k, make_uint4(0, 0, 0, 0));
-              if (D == 128) sts128(a + 16384 + 16 * k, make_uint4(0, 0, 0, 0));
+              for (int k = 0; k < 8; ++k) {
+                sts128(a + 16 * k, make_uint4(0, 0, 0, 0));
+                if (D == 128) sts128(a + 16384 + 16 * k, make_uint4(0, 0, 0, 0));
+              }
             }
+            fence_proxy_async_smem();
           }
-          fence_proxy_async_smem();
+          tmem_st32(tS + 32 * h, u);
+          tc_fence_before();
+          warp_arrive(&bars->p_ready[w][h]);
         }
-        tc_fence_before();
-        warp_arrive(&bars->p_ready[w]);
+        if (!ok) break;
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
       if (!ok) break;
       sc += 2 * n;
@@ -391,48 +432,62 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       load_q(nx);
       const int bad = bars->bad[si];
       const bool has = row < it.ntok * p.G;
-      const size_t prow = (size_t)(2 * blockIdx.x + (it.kind == 1 ? 1 : 0)) * kPrefillRows + row;
+      const size_t pslot = (size_t)(2 * blockIdx.x + (it.kind == 1 ? 1 : 0));
       if (nw > 0) {
         if (!(ok = wait_bar_warp(&bars->o_done[w], nd++ & 1u, abort))) break;
         tc_fence_after();
-        const int tok = row / p.G, gh = row - tok * p.G;
         const float inv = l == 0.f ? 0.f : 1.f / l;
+        // outputs through shared memory, 32 channels of the warp's 32 rows at a
+        // time, so that 4 lanes write 64 contiguous bytes of a row
+        const uint32_t stage = sb + C::kOffOut + (warp - 4) * 2048;
+        __nv_bfloat16 *dst[4];
+        bool put[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 128 * w + 32 * q4 + 8 * i + (lane >> 2);
+          put[i] = it.kind == 0 && !bad && r < it.ntok * p.G;
+          dst[i] = p.o + row_at(it, r) + (lane & 3) * 8;
+        }
 #pragma unroll
         for (int k = 0; k < D; k += 32) {
           float o[32];
           tmem_ld32(tO + k, o);
-          if (!has) continue;
           if (it.kind == 0) {
-            if (!bad) {
-              uint4 *dst = reinterpret_cast<uint4 *>(p.o + ((size_t)(it.row0 + tok) * p.H + it.hk * p.G + gh) * D + k);
+            __syncwarp();
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                uint32_t u[4];
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t u[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                  u[x] = l == 0.f ? 0u : pack_bf16(o[e + 2 * x] * inv, o[e + 2 * x + 1] * inv);
-                dst[e / 8] = make_uint4(u[0], u[1], u[2], u[3]);
-              }
+              for (int x = 0; x < 4; ++x)
+                u[x] = l == 0.f ? 0u : pack_bf16(o[e + 2 * x] * inv, o[e + 2 * x + 1] * inv);
+              sts128(stage + lane * 64 + (((e / 8) ^ ((lane >> 1) & 3)) << 4), make_uint4(u[0], u[1], u[2], u[3]));
             }
-          } else {
-            float4 *dst = reinterpret_cast<float4 *>(p.part + prow * D + k);
+            __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) dst[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int i = 0; i < 4; ++i) {
+              const int r = 8 * i + (lane >> 2);
+              const uint4 v = lds128(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+              if (put[i]) *reinterpret_cast<uint4 *>(dst[i] + k) = v;
+            }
+          } else if (has) {
+            float4 *part = reinterpret_cast<float4 *>(p.part) + (pslot * (D / 4) + k / 4) * kPrefillRows + row;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) part[e / 4 * kPrefillRows] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
         }
         tc_fence_before();
       }
-      if (it.kind != 0 && has) p.ml[prow] = make_float2(m, l);
+      if (it.kind != 0 && has) p.ml[pslot * kPrefillRows + row] = make_float2(m, l);
       if (lrow == 0) {
-        if (it.kind != 0 && w == 0) p.skip[2 * blockIdx.x + (it.kind == 1 ? 1 : 0)] = bad;
+        if (it.kind != 0 && w == 0) p.skip[pslot] = bad;
         if (bad && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_BAD_SLOT);
       }
       warp_arrive(&bars->item_empty[si]);
       it = nx;
     }
   } else if constexpr (kF8) {
-    // ============ e4m3 cache: read, scale, write bf16 tiles ============
-    regs_dec<104>();
+    // ============ e4m3 cache: raw tile -> values times their scale, as the bf16 tile ============
+    regs_dec<80>();
     const int ct = tid - 384;
     constexpr int kLanes = D / 16;                   // lanes of a key's row, 16 values each
     constexpr int kKeys = 128 / kLanes;              // keys a pass of the 128 threads takes: 16 or 32
@@ -442,55 +497,32 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     for (bool ok = true; ok;) {
       const int si = slot % kItems;
       if (!(ok = wait_bar_warp(&bars->item_full[si], (slot / kItems) & 1u, abort))) break;
-      const Item it = bars->item[si];
-      if (it.kind < 0) break;
+      const int kind = bars->item[si].kind, j1 = bars->item[si].j1;
+      const int end = bars->item[si].pos0 + bars->item[si].ntok;
+      int j = bars->item[si].j0;
+      warp_arrive(&bars->item_empty[si]);
+      if (kind < 0) break;
       ++slot;
-      const int end = it.pos0 + it.ntok;
-      const int32_t *table = p.table + (size_t)it.r * p.max_pages;
-      // rows in flight: the next tile's, while this one is written
-      uint4 x[kPass];
-      uint32_t code[kPass];
-      int ids[kPass];
-      auto pages_of = [&](int j) {
-#pragma unroll
-        for (int i = 0; i < kPass; ++i) {
-          const int key = j * kTileKeys + i * kKeys + k0;
-          ids[i] = key < end ? table[key >> p.page_shift] : -1;
-          if (key < end && (ids[i] < 0 || ids[i] >= p.P)) {
-            bars->bad[si] = 1;
-            ids[i] = -1;
-          }
-        }
-      };
-      auto fetch = [&](int j, bool isv) {
-        const uint8_t *cache = isv ? v_cache : k_cache, *scale = isv ? p.v_scale : p.k_scale;
-#pragma unroll
-        for (int i = 0; i < kPass; ++i) {
-          const int key = j * kTileKeys + i * kKeys + k0;
-          const size_t at = ((size_t)(ids[i] < 0 ? 0 : ids[i]) * p.Hkv + it.hk) * p.page + (key & (p.page - 1));
-          x[i] = ids[i] < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4 *>(cache + at * D) + c16);
-          code[i] = ids[i] < 0 ? 127u : __ldg(scale + at);
-        }
-      };
-      pages_of(it.j0);
-      fetch(it.j0, false);
-      for (int j = it.j0; j < it.j1 && ok; ++j) {
-#pragma unroll
+      for (; j < j1 && ok; ++j) {
+#pragma unroll 1
         for (int v = 0; v < 2; ++v, ++sc) {
+          const uint32_t rs = sc % C::kRawStages, s = sc % ST;
+          if (!(ok = wait_bar_warp(&bars->raw_full[rs], (sc / C::kRawStages) & 1u, abort))) break;
+          const uint32_t raw = sb + C::kOffRaw + rs * C::kRawBytes;
+          const uint8_t *scale = smem + C::kOffScale + rs * kTileKeys;
           uint4 y[kPass];
           uint32_t cd[kPass];
 #pragma unroll
           for (int i = 0; i < kPass; ++i) {
-            y[i] = x[i];
-            cd[i] = code[i];
+            const int key = i * kKeys + k0;
+            y[i] = lds128(raw + key * D + c16 * 16);
+            cd[i] = scale[key];
+            if (j * kTileKeys + key >= end) {  // not there: whatever was in the stage
+              y[i] = make_uint4(0, 0, 0, 0);
+              cd[i] = 127;
+            }
           }
-          if (v == 0) {
-            fetch(j, true);
-          } else if (j + 1 < it.j1) {
-            pages_of(j + 1);
-            fetch(j + 1, false);
-          }
-          const uint32_t s = sc % ST;
+          warp_arrive(&bars->raw_empty[rs]);
           if (!(ok = wait_bar_warp(&bars->empty[s], ((sc / ST) & 1u) ^ 1u, abort))) break;
           const uint32_t base = sb + C::kOffRing + s * C::kStageBytes;
 #pragma unroll
@@ -520,7 +552,6 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
           warp_arrive(&bars->full[s]);
         }
       }
-      if (ok) warp_arrive(&bars->item_empty[si]);
     }
   }
 
@@ -550,7 +581,7 @@ cudaError_t launch(const AttnParams &p, const void *k_cache, const void *v_cache
   if (e != cudaSuccess) return e;
   kernel<<<ctas, C::kThreads, C::kSmem, stream>>>(tk, tv, p, (const uint8_t *)k_cache, (const uint8_t *)v_cache);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_merge<D, kPrefillRows, 8>(p, ctas, stream);
+  return launch_merge<D, kPrefillRows, false>(p, ctas, stream);
 }
 
 }  // namespace

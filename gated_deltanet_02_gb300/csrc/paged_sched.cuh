@@ -42,7 +42,7 @@ struct AttnParams {
   int4 *desc;              // [CTAs]
   int *skip;               // [CTAs, 2]: the piece met a bad page
   float2 *ml;              // [CTAs, 2, rows]: maximum (log2 units) and sum
-  float *part;             // [CTAs, 2, rows, D]
+  float *part;             // [CTAs, 2, rows x D], in the order that the merge reads
 };
 
 struct Req {
@@ -69,26 +69,34 @@ __device__ __forceinline__ int tile_units(const AttnParams &p, const Req &x, int
   return vis <= kTileKeys ? 1 : (int)((vis + kTileKeys - 1) / kTileKeys);
 }
 
-// sum of floor((a i + b) / m) over i in [0, n), by the Euclidean recursion.
-__device__ inline long long floor_sum(long long n, unsigned m, unsigned a, unsigned b) {
+// sum of floor((a i + b) / m) over i in [0, n), by the Euclidean recursion;
+// T holds a n + b.
+template <typename T>
+__device__ inline long long floor_sum(T n, unsigned m, unsigned a, unsigned b) {
   long long s = 0;
   while (true) {
     if (a >= m) {
-      s += n * (n - 1) / 2 * (a / m);
+      s += (long long)n * ((long long)n - 1) / 2 * (a / m);
       a %= m;
     }
     if (b >= m) {
-      s += n * (b / m);
+      s += (long long)n * (b / m);
       b %= m;
     }
-    const unsigned long long y = (unsigned long long)a * (unsigned long long)n + b;
+    const T y = (T)a * n + b;
     if (y < m) return s;
-    n = (long long)(y / m);
+    n = y / m;
     b = (unsigned)(y % m);
     const unsigned x = m;
     m = a;
     a = x;
   }
+}
+
+// a / b for non-negative numbers, in 32 bits where they fit (a 64-bit division
+// costs a few hundred cycles of the planning step).
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+  return ((unsigned long long)(a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
 // Units of the tiles before tile t (t = ntile: of one kv head of the request).
@@ -101,9 +109,14 @@ __device__ inline long long units_before(const AttnParams &p, const Req &x, int 
   }
   if (n <= 0) return s;
   const long long room = (long long)kTileKeys - x.pos0;  // tiles that end within the first cache tile: one unit
-  const int z = room < p.tp ? 0 : (int)min((long long)n, room / p.tp);
+  const int z = room < p.tp ? 0 : (int)min((long long)n, div_pos(room, p.tp));
   s += z;
-  if (n > z) s += floor_sum(n - z, kTileKeys, (unsigned)p.tp, (unsigned)(x.pos0 + (long long)(z + 1) * p.tp + kTileKeys - 1));
+  if (n > z) {
+    // the first term's tiles end at b - 127; a n + b is below 2^32 for n < 2^22 (a < 128 after the first step)
+    const unsigned b = (unsigned)(x.pos0 + (long long)(z + 1) * p.tp + kTileKeys - 1);
+    s += n < (1 << 22) ? floor_sum<unsigned>(n - z, kTileKeys, (unsigned)p.tp, b)
+                       : floor_sum<unsigned long long>(n - z, kTileKeys, (unsigned)p.tp, b);
+  }
   return s;
 }
 
@@ -111,21 +124,22 @@ struct Plan {
   long long u0, u1, per;  // this CTA's units; units of a CTA
   int r;                  // request of u0
   long long off;          // u0's offset in that request
+  long long per_head;     // units of one kv head of that request
 };
 
 // Shared memory of the planning step.
 struct PlanShared {
-  long long scan[32];
-  long long first_off;
+  long long scan[16];
+  long long first_off, first_per_head;
   int first_r;
 };
 
-// Called by the whole CTA (blockDim a multiple of 32); kOneTile: p.tp covers
-// any range, so that a request has one tile.
+// Called by the whole CTA (blockDim a multiple of 32, at most 512); kOneTile:
+// p.tp covers any range, so that a request has one tile.
 template <bool kOneTile>
 __device__ inline Plan make_plan(const AttnParams &p, PlanShared *sh) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
-  auto units = [&](int r, bool flag) -> long long {
+  auto head_units = [&](int r, bool flag) -> long long {
     if (r >= p.R) return 0;
     const Req x = load_req(p, r);
     if (!x.ok) {
@@ -133,28 +147,11 @@ __device__ inline Plan make_plan(const AttnParams &p, PlanShared *sh) {
       return 0;
     }
     if (x.ntile == 0) return 0;
-    return (long long)p.Hkv * (kOneTile ? (long long)tile_units(p, x, 0) : units_before(p, x, x.ntile));
+    return kOneTile ? (long long)tile_units(p, x, 0) : units_before(p, x, x.ntile);
   };
-  long long mine = 0;
-  for (int r = tid; r < p.R; r += nt) mine += units(r, blockIdx.x == 0);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sh->scan[warp] = mine;
-  __syncthreads();
-  long long total = 0;
-  for (int w = 0; w < nw; ++w) total += sh->scan[w];
-  __syncthreads();
-  Plan pl;
-  pl.per = max(1ll, (total + gridDim.x - 1) / gridDim.x);
-  pl.u0 = min((long long)blockIdx.x * pl.per, total);
-  pl.u1 = min(pl.u0 + pl.per, total);
-  pl.r = 0;
-  pl.off = 0;
-  if (pl.u0 >= pl.u1) return pl;
-  long long before = 0;
-  for (int base = 0; base < p.R; base += nt) {
-    const long long u = units(base + tid, false);
-    long long upto = u;
+  // the CTA's sum (all) and this thread's inclusive prefix (upto)
+  auto scan = [&](long long u, long long &upto, long long &all) {
+    upto = u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, upto, o);
@@ -162,22 +159,49 @@ __device__ inline Plan make_plan(const AttnParams &p, PlanShared *sh) {
     }
     if (lane == 31) sh->scan[warp] = upto;
     __syncthreads();
-    long long all = 0;
+    all = 0;
     for (int w = 0; w < nw; ++w) {
       if (w < warp) upto += sh->scan[w];
       all += sh->scan[w];
     }
-    const long long a = before + upto - u;
+    __syncthreads();
+  };
+  // up to one request a thread: one scan serves for the total and for the search
+  long long mine = head_units(tid, blockIdx.x == 0), upto, total;
+  long long rest = 0;
+  for (int r = tid + nt; r < p.R; r += nt) rest += head_units(r, blockIdx.x == 0);
+  scan(mine * p.Hkv, upto, total);
+  const long long first_chunk = total;
+  if (p.R > nt) {
+    long long a, b;
+    scan(rest * p.Hkv, a, b);
+    total += b;
+  }
+  Plan pl;
+  pl.per = max(1ll, div_pos(total + gridDim.x - 1, gridDim.x));
+  pl.u0 = min((long long)blockIdx.x * pl.per, total);
+  pl.u1 = min(pl.u0 + pl.per, total);
+  pl.r = 0;
+  pl.off = pl.per_head = 0;
+  if (pl.u0 >= pl.u1) return pl;
+  long long before = 0, all = first_chunk;
+  for (int base = 0;;) {
+    const long long u = mine * p.Hkv, a = before + upto - u;
     if (a <= pl.u0 && pl.u0 < a + u) {
       sh->first_r = base + tid;
       sh->first_off = pl.u0 - a;
+      sh->first_per_head = mine;
     }
     before += all;
-    __syncthreads();
     if (before > pl.u0) break;
+    base += nt;
+    mine = head_units(base + tid, false);
+    scan(mine * p.Hkv, upto, all);
   }
+  __syncthreads();
   pl.r = sh->first_r;
   pl.off = sh->first_off;
+  pl.per_head = sh->first_per_head;
   return pl;
 }
 
@@ -207,9 +231,8 @@ struct Walk {
     hk = t = off = 0;
     if (left <= 0) return;
     x = load_req(p, r);
-    const long long per_head = kOneTile ? tile_units(p, x, 0) : units_before(p, x, x.ntile);
-    hk = (int)(pl.off / per_head);
-    const long long y = pl.off - hk * per_head;
+    hk = (int)div_pos(pl.off, pl.per_head);
+    const long long y = pl.off - hk * pl.per_head;
     if (!kOneTile) {  // the last tile with units_before <= y, 32 ways at a time
       int lo = 0, n = x.ntile;
       while (n > 1) {
@@ -241,7 +264,7 @@ struct Walk {
     it.j1 = off + take;
     it.kind = off > 0 ? 2 : take == units ? 0 : 1;
     if (it.kind == 1 && lane == 0)
-      p.desc[blockIdx.x] = make_int4(it.row0, hk, it.ntok, (int)((at + units - 1) / pl.per));
+      p.desc[blockIdx.x] = make_int4(it.row0, hk, it.ntok, (int)div_pos(at + units - 1, pl.per));
     left -= take;
     at += take;
     off = 0;
@@ -279,90 +302,113 @@ struct Partial {
   }
 };
 
+// Whether a piece of the item that begins in CTA c0 met a bad page (whole CTA).
+__device__ __forceinline__ bool any_bad(const AttnParams &p, int c0, int c1) {
+  int bad = 0;
+  for (int c = c0 + (int)threadIdx.x; c <= c1; c += (int)blockDim.x) bad |= p.skip[2 * c + (c == c0 ? 1 : 0)];
+  return __syncthreads_or(bad) != 0;
+}
+
 // Joins the pieces of the item that begins in CTA blockIdx.x and goes on
-// behind it, kRowsPerCta rows per CTA (blockIdx.y); a lane holds D / 32
-// channels.  Bound by latency, a few L2 reads per piece: with few pieces a
-// warp takes a row, with many the 8 warps share the pieces of one row at a time.
-template <int D, int kRows, int kRowsPerCta>
-__global__ void __launch_bounds__(256) merge_kernel(const AttnParams p) {
+// behind it, with few rows and possibly many pieces: blockIdx.y = its row, 8
+// warps share the pieces, a lane holds D / 32 channels.  Bound by latency, a few
+// L2 reads per piece.  Partial outputs are [row][channel].
+template <int D, int kRows>
+__global__ void __launch_bounds__(256) merge_few_rows_kernel(const AttnParams p) {
   constexpr int kE = D / 32;
   __shared__ float s_m[8], s_l[8], s_o[8][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c0 = blockIdx.x, row = blockIdx.y;
+  const int4 d = p.desc[c0];
+  if (d.w < 0 || row >= d.z * p.G) return;
+  if (any_bad(p, c0, d.w)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Partial<kE> a;
+#pragma unroll 4
+  for (int c = c0 + warp; c <= d.w; c += 8) {
+    const size_t at = (size_t)(2 * c + (c == c0 ? 1 : 0)) * kRows + row;
+    const float2 ml = p.ml[at];
+    float x[kE];
+#pragma unroll
+    for (int e = 0; e < kE; ++e) x[e] = p.part[at * D + lane * kE + e];
+    a.add(ml.x, ml.y, x);
+  }
+  if (lane == 0) {
+    s_m[warp] = a.m;
+    s_l[warp] = a.l;
+  }
+#pragma unroll
+  for (int e = 0; e < kE; ++e) s_o[warp][lane * kE + e] = a.o[e];
+  __syncthreads();
+  if (threadIdx.x < D) {
+    Partial<1> b;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const float x[1] = {s_o[w][threadIdx.x]};
+      b.add(s_m[w], s_l[w], x);
+    }
+    const int tok = row / p.G, g = row - tok * p.G;
+    p.o[((size_t)(d.x + tok) * p.H + d.y * p.G + g) * D + threadIdx.x] = __float2bfloat16_rn(b.l == 0.f ? 0.f : b.o[0] / b.l);
+  }
+}
+
+// The same with many rows and mostly two pieces: 32 rows per CTA (blockIdx.y),
+// lane = row, warp w the D / 8 channels from w D / 8.  Partial outputs are
+// [channel / 4][row][4], so that the lanes' reads (and the attention kernel's
+// writes, a row per lane there too) are contiguous.
+template <int D, int kRows>
+__global__ void __launch_bounds__(256) merge_many_rows_kernel(const AttnParams p) {
+  constexpr int kE = D / 8;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c0 = blockIdx.x;
   const int4 d = p.desc[c0];
-  const int nrow = d.z * p.G, row0 = blockIdx.y * kRowsPerCta;
-  if (d.w < 0 || row0 >= nrow) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int bad = 0;
-  for (int c = c0 + (int)threadIdx.x; c <= d.w; c += 256) bad |= p.skip[2 * c + (c == c0 ? 1 : 0)];
-  if (__syncthreads_or(bad)) return;
-  auto pieces = [&](int row, int first, int step, Partial<kE> &a) {
-#pragma unroll 4
-    for (int c = c0 + first; c <= d.w; c += step) {
-      const size_t at = (size_t)(2 * c + (c == c0 ? 1 : 0)) * kRows + row;
-      const float2 ml = p.ml[at];
-      float x[kE];
-      if constexpr (kE == 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(p.part + at * D + lane * 4);
-        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2 *>(p.part + at * D + lane * 2);
-        x[0] = v.x, x[1] = v.y;
-      }
-      a.add(ml.x, ml.y, x);
-    }
-  };
-  auto out = [&](int row) {
-    const int tok = row / p.G, g = row - tok * p.G;
-    return p.o + ((size_t)(d.x + tok) * p.H + d.y * p.G + g) * D;
-  };
-  if (kRowsPerCta == 8 && d.w - c0 < 8) {
-    const int row = row0 + warp;
-    if (row >= nrow) return;
-    Partial<kE> a;
-    pieces(row, 0, 1, a);
-    __nv_bfloat16 *o = out(row) + lane * kE;
+  const int nrow = d.z * p.G;
+  if (d.w < 0 || (int)blockIdx.y * 32 >= nrow) return;
+  if (any_bad(p, c0, d.w)) return;
+  const int row = blockIdx.y * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
+  if (row >= nrow) return;
+  Partial<kE> a;
+#pragma unroll 2
+  for (int c = c0; c <= d.w; ++c) {
+    const size_t slot = (size_t)(2 * c + (c == c0 ? 1 : 0));
+    const float2 ml = p.ml[slot * kRows + row];
+    const float4 *src = reinterpret_cast<const float4 *>(p.part) + (slot * (D / 4) + warp * (kE / 4)) * kRows + row;
+    float x[kE];
 #pragma unroll
-    for (int e = 0; e < kE; e += 2)
-      *reinterpret_cast<uint32_t *>(o + e) = a.l == 0.f ? 0u : pack_bf16(a.o[e] / a.l, a.o[e + 1] / a.l);
-    return;
+    for (int k = 0; k < kE / 4; ++k) {
+      const float4 v = src[k * kRows];
+      x[4 * k] = v.x, x[4 * k + 1] = v.y, x[4 * k + 2] = v.z, x[4 * k + 3] = v.w;
+    }
+    a.add(ml.x, ml.y, x);
   }
-  for (int row = row0; row < min(row0 + kRowsPerCta, nrow); ++row) {
-    Partial<kE> a;
-    pieces(row, warp, 8, a);
-    if (lane == 0) {
-      s_m[warp] = a.m;
-      s_l[warp] = a.l;
-    }
+  const int tok = row / p.G, g = row - tok * p.G;
+  uint4 *o = reinterpret_cast<uint4 *>(p.o + ((size_t)(d.x + tok) * p.H + d.y * p.G + g) * D + warp * kE);
+  const float inv = a.l == 0.f ? 0.f : 1.f / a.l;
 #pragma unroll
-    for (int e = 0; e < kE; ++e) s_o[warp][lane * kE + e] = a.o[e];
-    __syncthreads();
-    if (threadIdx.x < D) {
-      Partial<1> b;
+  for (int e = 0; e < kE; e += 8) {
+    uint32_t u[4];
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        const float x[1] = {s_o[w][threadIdx.x]};
-        b.add(s_m[w], s_l[w], x);
-      }
-      out(row)[threadIdx.x] = __float2bfloat16_rn(b.l == 0.f ? 0.f : b.o[0] / b.l);
-    }
-    __syncthreads();
+    for (int k = 0; k < 4; ++k) u[k] = a.l == 0.f ? 0u : pack_bf16(a.o[e + 2 * k] * inv, a.o[e + 2 * k + 1] * inv);
+    o[e / 8] = make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
 
 // The merge, launched so that it is in place when the attention kernel ends.
-template <int D, int kRows, int kRowsPerCta>
+template <int D, int kRows, bool kFewRows>
 cudaError_t launch_merge(const AttnParams &p, int ctas, cudaStream_t stream) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas, kRows / kRowsPerCta, 1);
+  cfg.gridDim = dim3((unsigned)ctas, kFewRows ? kRows : kRows / 32, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<D, kRows, kRowsPerCta>, p);
+  if constexpr (kFewRows)
+    return cudaLaunchKernelEx(&cfg, merge_few_rows_kernel<D, kRows>, p);
+  else
+    return cudaLaunchKernelEx(&cfg, merge_many_rows_kernel<D, kRows>, p);
 }
 
 // rows <= kDecodeRows query rows (tokens x heads of a group) per item
