@@ -9,24 +9,33 @@
 //
 // Bound: HBM bytes, one pass over one row of p (and one of q after a
 // rejection); a single request is bound by latency.  One cluster of 8 CTAs
-// owns a request: 64 warps sum one contiguous 64th of the row each, every
-// CTA gets all 64 sums through distributed shared memory, and the CTA whose
-// piece holds the threshold reads that piece (V / 64 elements, from L2) again
-// to find the token.
+// owns a request: every warp sums one contiguous piece of the row, all CTAs
+// get all pieces' sums through distributed shared memory, and the CTA whose
+// piece holds the threshold reads that piece again (from L2; its warps sum an
+// eighth each, then one warp walks to the token).  256 threads with 8 elements
+// each in flight and at least 6 CTAs per SM: 256 requests of V = 160,000 take 61 us
+// (70 us with 16 elements and 4 CTAs, 164 us with CTAs of 1024 threads, which
+// pass the cluster's barriers in fewer phases); one request of V = 100,003 takes
+// 9 us in all of these, most of it launch, barriers and the chain of loads.
 #include "common.cuh"
 
 namespace glinattn {
 namespace {
 
-constexpr int kCluster = 8, kThreads = 256, kWarps = kThreads / 32;
-constexpr int kPieces = kCluster * kWarps;
-constexpr int kAhead = 8;  // elements of a row that a lane has in flight
-constexpr float kWeight = 1099511627776.f;  // 2^40
+constexpr int kCluster = 8;
+constexpr int kThreads = 256;
+constexpr int kAhead = 8;   // elements of a row that a lane has in flight
 
 typedef unsigned long long u64;
 
+// trunc(w 2^40) for w clamped to [0, 1] (NaN: 0): the 24-bit significand, its
+// leading bit at bit 40 for w = 1, shifted down by the exponent.  Integer
+// instructions: with the conversion instruction from fp32 to 64 bits 256
+// requests of V = 160,000 took 103 us instead of 70 us.
 __device__ __forceinline__ u64 weight(float w) {
-  return (u64)(fminf(fmaxf(w, 0.f), 1.f) * kWeight);  // fmaxf(NaN, 0) is 0
+  const uint32_t x = __float_as_uint(fminf(fmaxf(w, 0.f), 1.f));
+  const uint32_t e = (x >> 23) & 0xffu;
+  return ((u64)((x & 0x7fffffu) | 0x800000u) << 17) >> min(127u - e, 63u);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -48,13 +57,51 @@ __device__ __forceinline__ void st_remote(u64 *p, uint32_t rank, u64 v) {
 struct Row {
   const float *p, *q;  // q NULL: none is taken off
   int zero;            // the element without weight (the rejected point mass), or -1
-  __device__ __forceinline__ float at(int v) const { return q ? p[v] - q[v] : v == zero ? 0.f : p[v]; }
+  // elements b + 32 k < end, k < kAhead, all loaded before the first is used
+  __device__ __forceinline__ void load(int b, int end, u64 (&w)[kAhead]) const {
+    float x[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) x[k] = b + 32 * k < end ? __ldg(p + b + 32 * k) : 0.f;
+    if (q) {
+      float y[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) y[k] = b + 32 * k < end ? __ldg(q + b + 32 * k) : 0.f;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) x[k] -= y[k];
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) w[k] = b + 32 * k == zero ? 0 : weight(x[k]);
+  }
+  // the warp's sum over [v0, v1), in every lane
+  __device__ __forceinline__ u64 sum(int v0, int v1, int lane) const {
+    u64 s = 0;
+    for (int b = v0 + lane; b < v1; b += 32 * kAhead) {
+      u64 w[kAhead];
+      load(b, v1, w);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) s += w[k];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+  }
 };
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) accept_kernel(const glinattn_accept_args a) {
+__device__ __forceinline__ u64 warp_scan(u64 x, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 6) accept_kernel(const glinattn_accept_args a) {
+  constexpr int kWarps = kThreads / 32, kPieces = kCluster * kWarps, kPer = kPieces / 32;
   __shared__ u64 s_piece[2][kPieces];
-  __shared__ u64 s_warp[kWarps];
-  __shared__ int s_accept;
+  __shared__ u64 s_sub[kWarps];
+  __shared__ u64 s_t, s_before, s_total;
+  __shared__ int s_accept, s_hit;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int r = blockIdx.x / kCluster;
@@ -106,62 +153,78 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) acc
   const int piece = (int)rank * kWarps + warp;
   const int v0 = min(piece * len, V), v1 = min(v0 + len, V);
   cluster_sync();  // every CTA of the cluster runs: its shared memory may be written
-  u64 total = 0;
   for (int pass = 0; pass < 2; ++pass) {
-    u64 sum = 0;
-    for (int b = v0 + lane; b < v1; b += 32 * kAhead) {
-      float x[kAhead];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) x[k] = b + 32 * k < v1 ? w.at(b + 32 * k) : 0.f;
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) sum += weight(x[k]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const u64 sum = w.sum(v0, v1, lane);
     if (lane < kCluster) st_remote(&s_piece[pass][piece], (uint32_t)lane, sum);
     __syncwarp();
     cluster_sync();
-    total = 0;
-    for (int k = 0; k < kPieces; ++k) total += s_piece[pass][k];
-    if (total > 0) {
-      // ---- the piece that holds the threshold, and in it the token -----------------
-      const double prod = (double)u[D] * (double)total;
-      u64 t = prod > 0. ? (u64)prod : 0;
-      if (!(t < total)) t = total - 1;
-      u64 before = 0;
-      int hit = 0;
-      for (; hit < kPieces - 1 && before + s_piece[pass][hit] <= t; ++hit) before += s_piece[pass][hit];
-      if (hit / kWarps != (int)rank) return;
-      const int h0 = hit * len, h1 = min(h0 + len, V);
-      const int per = (len + kThreads - 1) / kThreads;  // contiguous elements of a thread
-      const int e0 = min(h0 + tid * per, h1), e1 = min(e0 + per, h1);
-      u64 mine = 0;
-      for (int v = e0; v < e1; ++v) mine += weight(w.at(v));
-      u64 upto = mine;  // inclusive scan over the CTA
+    if (warp == 0) {  // lane l has pieces kPer l ..; the threshold and its piece
+      u64 mine[kPer], group = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const u64 y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
-      }
-      if (lane == 31) s_warp[warp] = upto;
-      __syncthreads();
-      for (int k = 0; k < warp; ++k) upto += s_warp[k];
-      const u64 start = before + upto - mine;
-      if (start <= t && t < start + mine) {  // exactly one thread
-        u64 run = start;
-        int v = e0;
-        for (; v < e1 - 1; ++v) {
-          run += weight(w.at(v));
-          if (run > t) break;
+      for (int k = 0; k < kPer; ++k) group += mine[k] = s_piece[pass][kPer * lane + k];
+      const u64 upto = warp_scan(group, lane);
+      const u64 all = __shfl_sync(0xffffffffu, upto, 31);
+      if (lane == 0) s_total = all;
+      if (all > 0) {
+        const double prod = (double)u[D] * (double)all;
+        u64 t = prod > 0. ? (u64)prod : 0;
+        if (!(t < all)) t = all - 1;
+        if (upto - group <= t && t < upto) {  // one lane
+          u64 before = upto - group;
+          int hit = kPer * lane;
+#pragma unroll
+          for (int k = 0; k < kPer - 1; ++k)
+            if (hit == kPer * lane + k && before + mine[k] <= t) {
+              before += mine[k];
+              ++hit;
+            }
+          s_hit = hit;
+          s_before = before;
+          s_t = t;
         }
-        a.tokens[(size_t)r * (D + 1) + acc] = v;
-        a.accept[r] = acc;
       }
+    }
+    __syncthreads();
+    const u64 total = s_total;
+    if (total > 0) {
+      const u64 t = s_t, before = s_before;
+      const int hit = s_hit;
+      if (hit / kWarps != (int)rank) return;
       for (int i = tid; i <= D; i += kThreads)
         if (i != acc) a.tokens[(size_t)r * (D + 1) + i] = i < acc ? tokens[i] : -1;
+      const int h0 = min(hit * len, V), h1 = min(h0 + len, V);
+      const int sl = (len + kWarps - 1) / kWarps;
+      const int e0 = min(h0 + warp * sl, h1), e1 = min(e0 + sl, h1);
+      const u64 s = w.sum(e0, e1, lane);
+      if (lane == 0) s_sub[warp] = s;
+      __syncthreads();
+      u64 run = before;
+      for (int k = 0; k < warp; ++k) run += s_sub[k];
+      if (!(run <= t && t < run + s)) return;  // exactly one warp goes on
+      for (int b = e0; b < e1; b += 32 * kAhead) {
+        u64 x[kAhead];
+        w.load(b + lane, e1, x);
+#pragma unroll 1
+        for (int k = 0; k < kAhead; ++k) {
+          u64 y = 0;
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) y = j == k ? x[j] : y;
+          const u64 c = run + warp_scan(y, lane);
+          const unsigned over = __ballot_sync(0xffffffffu, c > t);
+          if (over) {
+            if (lane == 0) {
+              a.tokens[(size_t)r * (D + 1) + acc] = b + 32 * k + __ffs(over) - 1;
+              a.accept[r] = acc;
+            }
+            return;
+          }
+          run = __shfl_sync(0xffffffffu, c, 31);
+        }
+      }
       return;
     }
     if (!rejected) break;
+    __syncthreads();  // s_total is read
     w.q = nullptr;  // the residual has no mass: the target's own row
     w.zero = -1;
   }
