@@ -1,7 +1,7 @@
 // paged_attn.cu -- the host side of glinattn_paged_attention: argument checks,
 // the workspace, and the choice between the kernels.
 //
-// A call whose items (query tokens x heads of a group) have at most 32 rows
+// A call whose items (query tokens x heads of a group) have at most 48 rows
 // runs the transposed kernel of paged_decode.cu, in which query rows are the
 // narrow side of the tensor-core tile; any other call, mixtures of prompts and
 // single tokens among them, the one of paged_prefill.cu with 256 rows an item.
@@ -31,7 +31,7 @@ glinattn_status check(const glinattn_paged_attn_args *a) {
 // Rows of an item: what the kernel's accumulators are built for.
 int item_rows(const glinattn_paged_attn_args *a) {
   const long long rows = (long long)a->max_q_len * (a->heads / a->kv_heads);
-  return rows <= 16 ? 16 : rows <= kDecodeRows ? kDecodeRows : kPrefillRows;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= kDecodeRows ? kDecodeRows : kPrefillRows;
 }
 
 int sm_count() {

@@ -46,21 +46,26 @@ struct Cfg {
   static constexpr int kNS = N * kTQ, kNO = N * kTP;  // columns of S^T and O^T
   static constexpr int kEsz = kF8 ? 1 : 2;
   static constexpr int kTileStages = D * kEsz * kTileKeys > (int)kStageBytes ? 2 : 1;
+  // S^T of two tiles where TMEM holds them (256 columns a CTA)
+  static constexpr int kSBufs = 2 * kNS + kNO <= 256 ? 2 : 1;
+  // few rows: a thread keeps its scores from the maxima to the weights, else it reads S^T twice
+  static constexpr bool kKeep = N == 16;
   static constexpr uint32_t kBytesQ = N * kTQ * D * kEsz;
   static constexpr uint32_t kBytesP = N * kTP * kTileKeys * kEsz;
   static constexpr uint32_t kBytesScale = kF8 ? kScaleSlots * 2 * kTileKeys : 0;
-  static constexpr uint32_t kBytesMax = 2 * 4 * N * 4;  // [2][row][warp]
+  static constexpr uint32_t kBytesRows = 4 * N * 4 + 4 * N * 4;  // [row][warp] maxima or sums; m, f, limit, q scale
   static constexpr uint32_t kBytesBars = 640;
-  static constexpr uint32_t kFixed = kBytesQ + kBytesP + kBytesScale + kBytesMax + kBytesBars + 1024;
+  static constexpr uint32_t kFixed = kBytesQ + kBytesP + kBytesScale + kBytesRows + kBytesBars + 1024;
   // two CTAs of an SM share 228 KiB, 1 KiB of each reserved
-  static constexpr int kStages = (int)((112 * 1024 - kFixed) / kStageBytes) < 6 ? (int)((112 * 1024 - kFixed) / kStageBytes) : 6;
+  static constexpr int kFit = (int)((112 * 1024 - kFixed) / kStageBytes);
+  static constexpr int kStages = kFit < 6 ? kFit : 6;
   static constexpr uint32_t kSmem = kFixed + kStages * kStageBytes;
   static constexpr uint32_t kOffQ = kStages * kStageBytes, kOffP = kOffQ + kBytesQ, kOffScale = kOffP + kBytesP,
-                            kOffMax = kOffScale + kBytesScale, kOffBars = kOffMax + kBytesMax;
-  static constexpr uint32_t kColO = 2 * kNS;
+                            kOffRows = kOffScale + kBytesScale, kOffBars = kOffRows + kBytesRows;
+  static constexpr uint32_t kColO = kSBufs * kNS;
   static constexpr uint32_t kCols = kColO + kNO <= 64 ? 64 : kColO + kNO <= 128 ? 128 : 256;
   static_assert(kColO + kNO <= 256, "two CTAs share the SM's 512 columns");
-  static_assert(kStages >= 2 * kTileStages + (kF8 ? 1 : 0), "K and V tiles of one step");
+  static_assert(kStages >= 2 * kTileStages, "K and V tiles of one step");
   // the first tile index whose scales the producer may be loading is that of
   // the oldest unread tile + 1 (its S issued early) + the ring's K tiles
   static_assert(!kF8 || kScaleSlots >= kStages + 3, "scale slots");
@@ -112,6 +117,23 @@ __device__ __forceinline__ uint64_t desc_sw64(uint32_t saddr, uint32_t lbo, uint
   return d;
 }
 
+// Two weights as three e4m3 parts each (bytes 0 and 1 of part[]): the value
+// rounded, then 16 times and 256 times what is left.
+__device__ __forceinline__ void split_e4m3x2(float w0, float w1, uint32_t (&part)[3]) {
+  uint32_t x, y;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(w1), "f"(w0));
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    unsigned short e;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(e) : "r"(x));
+    part[k] = e;
+    if (k == 2) break;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(e));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(y));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(0x4c004c00u));  // 16
+  }
+}
+
 template <int kCnt>
 __device__ __forceinline__ void tmem_ld(uint32_t a, float *v) {
   static_assert(kCnt % 16 == 0, "columns");
@@ -123,9 +145,20 @@ __device__ __forceinline__ void tmem_ld(uint32_t a, float *v) {
     for (int j = 0; j < 16; ++j) v[k + j] = t[j];
   }
 }
+// Matrix without swizzle, MN-major: 16-byte units of consecutive rows, a unit's
+// 8 K indices 16 bytes apart; LBO between groups of 8 K indices, SBO between units.
+__device__ __forceinline__ uint64_t desc_units(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1 << 46;
+  return d;
+}
+
 template <int kCnt>
 __device__ __forceinline__ void tmem_scale(uint32_t a, const float *f, int n) {
-  // columns a .. a + kCnt of this thread's lane, times f[column % n]
+  // columns a .. a + kCnt of this thread's lane, times f[column % n] (shared memory)
 #pragma unroll
   for (int k = 0; k < kCnt; k += 16) {
     float t[16];
@@ -152,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars *bars = reinterpret_cast<Bars *>(smem + C::kOffBars);
   static_assert(sizeof(Bars) <= C::kBytesBars, "barrier block");
-  __shared__ float s_qs[N];   // e4m3: the scale of a row's q
+  __shared__ int s_need[4];   // [tile parity][warp]: a row's maximum moves
   __shared__ int s_bad[kItems];
   volatile int *abort = &bars->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -305,15 +338,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) {
       // ============ MMA issue ============
       constexpr uint32_t id_s = kF8 ? idesc_f8(128, C::kNS, false, false) : idesc_bf16(128, C::kNS, false, false);
-      constexpr uint32_t id_o = kF8 ? idesc_f8(D, C::kNO, true, false) : idesc_bf16(D, C::kNO, true, false);
+      constexpr uint32_t id_o = kF8 ? idesc_f8(D, C::kNO, true, true) : idesc_bf16(D, C::kNO, true, true);
       const uint32_t sb = smem_u32(smem), sQ = sb + C::kOffQ, sP = sb + C::kOffP;
       uint32_t sc = 0, g = 0, slot = 0;
       auto issue_s = [&](uint32_t gi) -> bool {
         for (int h = 0; h < NS; ++h)
           if (!wait_bar(&bars->full[(sc + h) % ST], ((sc + h) / ST) & 1u, abort)) return false;
-        if (!wait_bar(&bars->s_free[gi & 1], ((gi >> 1) & 1u) ^ 1u, abort)) return false;
+        const uint32_t buf = gi % C::kSBufs;
+        if (!wait_bar(&bars->s_free[buf], ((gi / C::kSBufs) & 1u) ^ 1u, abort)) return false;
         tc_fence_after();
-        const uint32_t d = tmem + (gi & 1) * C::kNS;
+        const uint32_t d = tmem + buf * C::kNS;
         if constexpr (!kF8) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
@@ -330,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               umma_f8(d, desc_sw64(a + ks * 32, 16, 512), desc_sw64(sQ + ks * 32, 16, 512), id_s, ks > 0);
           }
         }
-        umma_commit(&bars->s_ready[gi & 1]);
+        umma_commit(&bars->s_ready[buf]);
         for (int h = 0; h < NS; ++h) umma_commit(&bars->empty[(sc + h) % ST]);
         sc += NS;
         return true;
@@ -346,14 +380,14 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int ks = 0; ks < 8; ++ks) {
             const uint32_t a = NS == 2 ? sb + ((sc + (ks >> 2)) % ST) * kStageBytes + (ks & 3) * 2048
                                        : sb + (sc % ST) * kStageBytes + ks * 2048;
-            umma_bf16(d, desc_sw128(a, 8192, 1024), desc_sw128(sP + (ks >> 2) * (C::kNO * 128) + (ks & 3) * 32, 16, 1024), id_o,
+            umma_bf16(d, desc_sw128(a, 8192, 1024), desc_units(sP + ks * 256, 128, 2048), id_o,
                       ks > 0 || !first);
           }
         } else {
           const uint32_t a = sb + (sc % ST) * kStageBytes;
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
-            const uint64_t b = desc_sw128(sP + ks * 32, 16, 1024);
+            const uint64_t b = desc_units(sP + ks * 512, 128, 2048);
             if (D == 128)
               umma_f8(d, desc_sw128(a + ks * 4096, 16, 1024), b, id_o, ks > 0 || !first);
             else
@@ -373,6 +407,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (kind < 0) break;
         if (!wait_bar(&bars->q_ready, slot & 1u, abort)) break;
         ++slot;
+        // S of a tile goes before O of the one before it; with one S buffer it is
+        // free once that tile's weights are formed, which is when O can go too
         for (int j = 0; j < n && ok; ++j) {
           ok = issue_s(g + j);
           if (ok && j > 0) ok = issue_o(g + j - 1, j == 1);
@@ -387,7 +423,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int st = tid - 64;                         // 0 .. 127
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
     const uint32_t sb = smem_u32(smem);
-    float *s_max = reinterpret_cast<float *>(smem + C::kOffMax);
+    float *s_red = reinterpret_cast<float *>(smem + C::kOffRows);  // [row][warp]
+    float *s_m = s_red + 4 * N, *s_f = s_m + N, *s_qs = s_f + N;   // per row: maximum, rescale factor, scale of q
+    int *s_lim = reinterpret_cast<int *>(s_qs + N);                // per row: the last key it sees
     constexpr float kSlack = kF8 ? 4.f : 8.f;        // log2 of the largest weight
     uint32_t sc = 0, g = 0, slot = 0, syncs = 0;
     // the softmax warps' barrier; like every wait here it gives up after a limit
@@ -459,100 +497,142 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         fence_proxy_async_smem();
         warp_arrive(&bars->q_ready);
-        if (kF8 && !(ok = softmax_sync())) break;  // s_qs
-      }
-      float m[N], l[N];
-#pragma unroll
-      for (int r = 0; r < N; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
-      }
-      for (int j = it.j0; j < it.j1; ++j, ++g) {
-        if (!(ok = wait_bar_warp(&bars->s_ready[g & 1], (g >> 1) & 1u, abort))) break;
-        tc_fence_after();
-        float s[C::kNS];
-        tmem_ld<C::kNS>(tmem + (g & 1) * C::kNS + lane_base, s);
-        float ev = 0.f;
-        if constexpr (kF8) {
-          const uint8_t *ss = smem + C::kOffScale + (g % kScaleSlots) * 2 * kTileKeys;
-          const float ks = scale_value(ss[kk]);
-          const uint32_t vc = ss[kTileKeys + kk];
-          ev = vc == 255 ? __int_as_float(0x7fffffff) : (float)((int)vc - 127);
-#pragma unroll
-          for (int r = 0; r < N; ++r) s[r] = fmaf(s[N + r], 0.0625f, s[r]) * (ks * s_qs[r]);
-        } else {
-#pragma unroll
-          for (int r = 0; r < N; ++r) s[r] *= p.c;
-        }
-        tc_fence_before();
-        warp_arrive(&bars->s_free[g & 1]);
-        const int key = j * kTileKeys + kk;
-        if (j * kTileKeys + kTileKeys - 1 > it.pos0) {  // some row does not see the whole tile
-          int lim = it.pos0, gh = 0;
-#pragma unroll
-          for (int r = 0; r < N; ++r) {
-            if (r < nrow && key > lim) s[r] = -INFINITY;
-            if (++gh == p.G) {
-              gh = 0;
-              ++lim;
-            }
-          }
-          if (kF8 && key >= it.pos0 + it.ntok) ev = 0.f;  // a stale scale may be anything
-        }
-        // ---- the tile's maxima
-        float *mx = s_max + (g & 1) * 4 * N;
-#pragma unroll
-        for (int r = 0; r < N; ++r) {
-          const float v = warp_max(s[r] + ev);
-          if (lane == (r & 31)) mx[r * 4 + q4] = v;
+        if (st < N) {
+          s_m[st] = -INFINITY;
+          s_lim[st] = it.pos0 + min(st, nrow - 1) / p.G;
         }
         if (!(ok = softmax_sync())) break;
-        bool need = false;
-        float mt[N];
+      }
+      float l[N];
 #pragma unroll
-        for (int r = 0; r < N; ++r) {
-          const float4 v = *reinterpret_cast<const float4 *>(mx + r * 4);
-          mt[r] = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-          need |= mt[r] > m[r] + kSlack;
+      for (int r = 0; r < N; ++r) l[r] = 0.f;
+      for (int j = it.j0; j < it.j1; ++j, ++g) {
+        const uint32_t buf = g % C::kSBufs, tS = tmem + buf * C::kNS + lane_base;
+        if (!(ok = wait_bar_warp(&bars->s_ready[buf], (g / C::kSBufs) & 1u, abort))) break;
+        tc_fence_after();
+        const int key = j * kTileKeys + kk;
+        const bool edge = j * kTileKeys + kTileKeys - 1 > it.pos0;  // some row does not see the whole tile
+        float ks = p.c, ev = 0.f;                                   // e4m3: the key's scale, the value's exponent
+        if constexpr (kF8) {
+          const uint8_t *ss = smem + C::kOffScale + (g % kScaleSlots) * 2 * kTileKeys;
+          const uint32_t vc = ss[kTileKeys + kk];
+          const bool there = key < it.pos0 + it.ntok;               // a stale scale may be anything
+          ks = scale_value(ss[kk]);
+          ev = vc == 255 && there ? __int_as_float(0x7fffffff) : there ? (float)((int)vc - 127) : 0.f;
         }
-        if (g > 0 && !(ok = wait_bar_warp(&bars->o_done, (g - 1) & 1u, abort))) break;  // W is read, O^T complete
-        if (need) {  // the same in every thread
-          tc_fence_after();
-          float f[N];
+        const float ev4 = ev + 4.f;
+        // scores of rows 16 c .. 16 c + 15, in log2 units
+        auto scores = [&](int c, float (&x)[16]) {
+          if constexpr (kF8) {
+            float lo[16];
+            tmem_ld16x2(tS + 16 * c, tS + N + 16 * c, x, lo);
 #pragma unroll
-          for (int r = 0; r < N; ++r) {
-            const float mn = fmaxf(m[r], mt[r]);
-            f[r] = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
-            m[r] = mn;
-            l[r] *= f[r];
-          }
-          if (j > it.j0) tmem_scale<C::kNO>(tmem + C::kColO + lane_base, f, N);
-        }
-        // ---- weights, rounded into their parts, as the second product's B operand [row][key]
-#pragma unroll
-        for (int r = 0; r < N; ++r) {
-          const float ms = m[r] == -INFINITY ? 0.f : m[r];
-          if constexpr (!kF8) {
-            const float w = ex2(s[r] - ms);
-            l[r] += w;
-            const uint32_t off = (kk >> 6) * (C::kNO * 128) + r * 128 + ((((kk & 63) >> 3) ^ (r & 7)) << 4) + (kk & 7) * 2;
-            const __nv_bfloat16 h = __float2bfloat16_rn(w);
-            const __nv_bfloat16 lo = __float2bfloat16_rn(w - __bfloat162float(h));
-            *reinterpret_cast<__nv_bfloat16 *>(smem + C::kOffP + off) = h;
-            *reinterpret_cast<__nv_bfloat16 *>(smem + C::kOffP + off + N * 128) = lo;
+            for (int r = 0; r < 16; r += 4) {
+              const float4 qs = *reinterpret_cast<const float4 *>(s_qs + 16 * c + r);
+              x[r] = fmaf(lo[r], 0.0625f, x[r]) * (ks * qs.x);
+              x[r + 1] = fmaf(lo[r + 1], 0.0625f, x[r + 1]) * (ks * qs.y);
+              x[r + 2] = fmaf(lo[r + 2], 0.0625f, x[r + 2]) * (ks * qs.z);
+              x[r + 3] = fmaf(lo[r + 3], 0.0625f, x[r + 3]) * (ks * qs.w);
+            }
           } else {
-            l[r] += ex2(s[r] - ms);
-            const float w = ex2(s[r] + ev - ms) * 16.f;
-            const uint32_t off = r * 128 + (((kk >> 4) ^ (r & 7)) << 4) + (kk & 15);
-            const uint32_t h = to_e4m3x2(w, 0.f);
-            const float r1 = (w - e4m3x2(h).x) * 16.f;
-            const uint32_t h1 = to_e4m3x2(r1, 0.f);
-            const float r2 = (r1 - e4m3x2(h1).x) * 16.f;
-            const uint32_t h2 = to_e4m3x2(r2, 0.f);
-            smem[C::kOffP + off] = (uint8_t)h;
-            smem[C::kOffP + off + N * 128] = (uint8_t)h1;
-            smem[C::kOffP + off + 2 * N * 128] = (uint8_t)h2;
+            tmem_ld16(tS + 16 * c, x);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[r] *= ks;
           }
+          if (edge) {
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+              const int4 lim = *reinterpret_cast<const int4 *>(s_lim + 16 * c + r);
+              x[r] = key > lim.x ? -INFINITY : x[r];
+              x[r + 1] = key > lim.y ? -INFINITY : x[r + 1];
+              x[r + 2] = key > lim.z ? -INFINITY : x[r + 2];
+              x[r + 3] = key > lim.w ? -INFINITY : x[r + 3];
+            }
+          }
+        };
+        float s[16];
+        // ---- the tile's maxima (of the weights' exponents): per warp, then a row a thread
+#pragma unroll
+        for (int c = 0; c < N / 16; ++c) {
+          scores(c, s);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float v = warp_max(s[r] + ev);
+            if (lane == r) s_red[(16 * c + r) * 4 + q4] = v;
+          }
+        }
+        if constexpr (C::kKeep) {
+          tc_fence_before();
+          warp_arrive(&bars->s_free[buf]);
+        }
+        if (!(ok = softmax_sync())) break;
+        if (st < 64) {
+          bool need = false;
+          if (st < N) {
+            const float4 v = *reinterpret_cast<const float4 *>(s_red + st * 4);
+            const float mt = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)), m = s_m[st];
+            need = mt > m + kSlack;
+            s_f[st] = need ? ex2(m - mt) : 1.f;
+            if (need) s_m[st] = mt;
+          }
+          need = __any_sync(0xffffffffu, need);
+          if (lane == 0) s_need[2 * (g & 1) + (st >> 5)] = need;
+        }
+        if (!(ok = softmax_sync())) break;
+        if (g > 0 && !(ok = wait_bar_warp(&bars->o_done, (g - 1) & 1u, abort))) break;  // W is read, O^T complete
+        if (s_need[2 * (g & 1)] | s_need[2 * (g & 1) + 1]) {
+          tc_fence_after();
+#pragma unroll
+          for (int r = 0; r < N; ++r) l[r] *= s_f[r];
+          if (j > it.j0) tmem_scale<C::kNO>(tmem + C::kColO + lane_base, s_f, N);
+        }
+        // ---- weights, rounded into their parts, as the second product's B operand: a key's
+        // rows are contiguous, 16 bytes a unit
+        const uint32_t wp = sb + C::kOffP + kk * 16;
+#pragma unroll
+        for (int c = 0; c < N / 16; ++c) {
+          if constexpr (!C::kKeep) scores(c, s);
+          if constexpr (!kF8) {
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) {
+              const float2 m = *reinterpret_cast<const float2 *>(s_m + 16 * c + r);
+              const float w0 = ex2(s[r] - (m.x == -INFINITY ? 0.f : m.x)), w1 = ex2(s[r + 1] - (m.y == -INFINITY ? 0.f : m.y));
+              l[16 * c + r] += w0;
+              l[16 * c + r + 1] += w1;
+              const uint32_t h = pack_bf16(w0, w1);
+              hi[r / 2] = h;
+              lo[r / 2] = pack_bf16(w0 - __uint_as_float(h << 16), w1 - __uint_as_float(h & 0xffff0000u));
+            }
+            sts128(wp + (2 * c) * 2048, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            sts128(wp + (2 * c + 1) * 2048, make_uint4(hi[4], hi[5], hi[6], hi[7]));
+            sts128(wp + (N / 8 + 2 * c) * 2048, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+            sts128(wp + (N / 8 + 2 * c + 1) * 2048, make_uint4(lo[4], lo[5], lo[6], lo[7]));
+          } else {
+            uint32_t q[3][4];
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) {
+              const float2 m = *reinterpret_cast<const float2 *>(s_m + 16 * c + r);
+              const float x0 = s[r] - (m.x == -INFINITY ? 0.f : m.x), x1 = s[r + 1] - (m.y == -INFINITY ? 0.f : m.y);
+              l[16 * c + r] += ex2(x0);
+              l[16 * c + r + 1] += ex2(x1);
+              // 16 w in f16 (2^-12 relative), then e4m3 parts of it, each 2^-4 of the one before
+              uint32_t part[3];
+              split_e4m3x2(ex2(x0 + ev4), ex2(x1 + ev4), part);
+#pragma unroll
+              for (int k = 0; k < 3; ++k) {
+                if (r % 4 == 0) q[k][r / 4] = part[k];
+                else q[k][r / 4] |= part[k] << 16;
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+              sts128(wp + (k * (N / 16) + c) * 2048, make_uint4(q[k][0], q[k][1], q[k][2], q[k][3]));
+          }
+        }
+        if constexpr (!C::kKeep) {
+          tc_fence_before();
+          warp_arrive(&bars->s_free[buf]);
         }
         if (j == it.j1 - 1) {
           // the last tile: its values have landed, and rows behind the cache's end become zeros
@@ -584,8 +664,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       sc += NS * 2 * n;
       // ---- sums over the keys; the item's outputs or its partial result
       const int bad = s_bad[si];
-      float *red = s_max;  // [4 warps][N]; the maxima of the last tile have been read
-      if (!(ok = softmax_sync())) break;
+      float *red = s_red;  // the maxima of the last tile have been read
 #pragma unroll
       for (int r = 0; r < N; ++r) {
         float v = l[r];
@@ -617,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
           } else {
             p.part[((size_t)pslot * N + r) * D + ch] = x;
-            if (ch == 0) p.ml[(size_t)pslot * N + r] = make_float2(m[r], lt);
+            if (ch == 0) p.ml[(size_t)pslot * N + r] = make_float2(s_m[r], lt);
           }
         }
       }
@@ -665,13 +744,17 @@ cudaError_t launch_decode(const AttnParams &p, bool f8, int d, int rows, const v
   if (!encode_3d_map_swizzled(&tk, k_cache, type, esz, dims, kbox, sw) ||
       !encode_3d_map_swizzled(&tv, v_cache, type, esz, dims, vbox, sw))
     return cudaErrorInvalidValue;
-  const bool small = rows <= 16;
+#define GLINATTN_DECODE(D, F8)                                          \
+  return rows == 16   ? launch<D, F8, 16>(p, tk, tv, ctas, stream)      \
+         : rows == 32 ? launch<D, F8, 32>(p, tk, tv, ctas, stream)      \
+                      : launch<D, F8, kDecodeRows>(p, tk, tv, ctas, stream)
   if (d == 128) {
-    if (f8) return small ? launch<128, true, 16>(p, tk, tv, ctas, stream) : launch<128, true, 32>(p, tk, tv, ctas, stream);
-    return small ? launch<128, false, 16>(p, tk, tv, ctas, stream) : launch<128, false, 32>(p, tk, tv, ctas, stream);
+    if (f8) GLINATTN_DECODE(128, true);
+    GLINATTN_DECODE(128, false);
   }
-  if (f8) return small ? launch<64, true, 16>(p, tk, tv, ctas, stream) : launch<64, true, 32>(p, tk, tv, ctas, stream);
-  return small ? launch<64, false, 16>(p, tk, tv, ctas, stream) : launch<64, false, 32>(p, tk, tv, ctas, stream);
+  if (f8) GLINATTN_DECODE(64, true);
+  GLINATTN_DECODE(64, false);
+#undef GLINATTN_DECODE
 }
 
 }  // namespace paged

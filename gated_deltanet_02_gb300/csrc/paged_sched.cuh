@@ -411,8 +411,8 @@ cudaError_t launch_merge(const AttnParams &p, int ctas, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, merge_many_rows_kernel<D, kRows>, p);
 }
 
-// rows <= kDecodeRows query rows (tokens x heads of a group) per item
-constexpr int kDecodeRows = 32;
+// rows = 16, 32 or kDecodeRows query rows (tokens x heads of a group) per item
+constexpr int kDecodeRows = 48;
 cudaError_t launch_decode(const AttnParams &p, bool f8, int d, int rows, const void *k_cache, const void *v_cache,
                           int ctas, cudaStream_t stream);
 
