@@ -20,7 +20,8 @@
 //
 // Bound: HBM, one read of the cache; 2 CTAs per SM, each with a ring of 16 KiB
 // stages (TMA, one box per page), so that about 190 KiB per SM are in flight.  Warps:
-// 0 TMA and the walk over the items, 1 MMA issue, 2-5 softmax, a key per thread.
+// 0 TMA and the walk over the items, 1 MMA issue, then groups of four softmax
+// warps, a key per thread and 16 rows per group.
 #include "paged_sched.cuh"
 #include "prefill_tc.cuh"
 #include "tc_common.cuh"
@@ -34,7 +35,6 @@ using tc::wait_bar;
 using tc::wait_bar_warp;
 using tc::warp_arrive;
 
-constexpr int kThreads = 192;
 constexpr int kItems = 4;              // depth of the item queue
 constexpr int kScaleSlots = 12;        // tiles of scales in flight, see ScaleRing below
 constexpr uint32_t kStageBytes = 16384;
@@ -48,8 +48,8 @@ struct Cfg {
   static constexpr int kTileStages = D * kEsz * kTileKeys > (int)kStageBytes ? 2 : 1;
   // S^T of two tiles where TMEM holds them (256 columns a CTA)
   static constexpr int kSBufs = 2 * kNS + kNO <= 256 ? 2 : 1;
-  // few rows: a thread keeps its scores from the maxima to the weights, else it reads S^T twice
-  static constexpr bool kKeep = N == 16;
+  static constexpr int kGroups = N / 16;             // softmax warpgroups, 16 rows each
+  static constexpr int kThreads = 64 + 128 * kGroups;
   static constexpr uint32_t kBytesQ = N * kTQ * D * kEsz;
   static constexpr uint32_t kBytesP = N * kTP * kTileKeys * kEsz;
   static constexpr uint32_t kBytesScale = kF8 ? kScaleSlots * 2 * kTileKeys : 0;
@@ -77,7 +77,7 @@ struct Bars {
   uint64_t item_full[kItems], item_empty[kItems];
   Item item[kItems];
   PlanShared plan;
-  uint64_t sync;  // the four softmax warps among themselves
+  uint64_t sync[3];  // the four warps of a softmax group among themselves
   uint32_t tmem;
   int abort;
 };
@@ -134,17 +134,6 @@ __device__ __forceinline__ void split_e4m3x2(float w0, float w1, uint32_t (&part
   }
 }
 
-template <int kCnt>
-__device__ __forceinline__ void tmem_ld(uint32_t a, float *v) {
-  static_assert(kCnt % 16 == 0, "columns");
-#pragma unroll
-  for (int k = 0; k < kCnt; k += 16) {
-    float t[16];
-    tmem_ld16(a + k, t);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[k + j] = t[j];
-  }
-}
 // Matrix without swizzle, MN-major: 16-byte units of consecutive rows, a unit's
 // 8 K indices 16 bytes apart; LBO between groups of 8 K indices, SBO between units.
 __device__ __forceinline__ uint64_t desc_units(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
@@ -156,36 +145,32 @@ __device__ __forceinline__ uint64_t desc_units(uint32_t saddr, uint32_t lbo, uin
   return d;
 }
 
-template <int kCnt>
-__device__ __forceinline__ void tmem_scale(uint32_t a, const float *f, int n) {
-  // columns a .. a + kCnt of this thread's lane, times f[column % n] (shared memory)
+// Columns a .. a + 15 of this thread's lane, times f[0 .. 15] (shared memory).
+__device__ __forceinline__ void tmem_scale16(uint32_t a, const float *f) {
+  float t[16];
+  tmem_ld16(a, t);
+  uint32_t u[16];
 #pragma unroll
-  for (int k = 0; k < kCnt; k += 16) {
-    float t[16];
-    tmem_ld16(a + k, t);
-    uint32_t u[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(t[j] * f[(k + j) % n]);
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16};" ::"r"(a + k),
-        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
-        "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
-        : "memory");
-  }
+  for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(t[j] * f[j]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(a),
+      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+      : "memory");
   tmem_wait_st();
 }
 
 template <int D, bool kF8, int N>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(64 + 8 * N, 2)
     decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnParams p) {
   using C = Cfg<D, kF8, N>;
-  constexpr int ST = C::kStages, NS = C::kTileStages;
+  constexpr int ST = C::kStages, NS = C::kTileStages, W = C::kGroups;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars *bars = reinterpret_cast<Bars *>(smem + C::kOffBars);
   static_assert(sizeof(Bars) <= C::kBytesBars, "barrier block");
-  __shared__ int s_need[4];   // [tile parity][warp]: a row's maximum moves
+  __shared__ int s_need[2][W];  // [tile parity]: a row's maximum moves
   __shared__ int s_bad[kItems];
   volatile int *abort = &bars->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -197,15 +182,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->s_ready[i], 1);
-      mbar_init(&bars->s_free[i], 4);
+      mbar_init(&bars->s_free[i], 4 * W);
     }
-    mbar_init(&bars->q_ready, 4);
-    mbar_init(&bars->p_ready, 4);
+    mbar_init(&bars->q_ready, 4 * W);
+    mbar_init(&bars->p_ready, 4 * W);
     mbar_init(&bars->o_done, 1);
-    mbar_init(&bars->sync, 4);
+    for (int i = 0; i < W; ++i) mbar_init(&bars->sync[i], 4);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bars->item_full[i], 1);
-      mbar_init(&bars->item_empty[i], 5);
+      mbar_init(&bars->item_empty[i], 1 + 4 * W);
       s_bad[i] = 0;
     }
     bars->abort = 0;
@@ -418,20 +403,21 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   } else {
-    // ============ softmax: thread = key ============
-    const int q4 = warp & 3, kk = 32 * q4 + lane;
-    const int st = tid - 64;                         // 0 .. 127
+    // ============ softmax: thread = key, group w = rows 16 w .. 16 w + 15 ============
+    const int w = (warp - 2) >> 2, q4 = warp & 3, kk = 32 * q4 + lane;
+    const int st = tid - 64 - 128 * w;               // 0 .. 127
+    const int rb = 16 * w;                           // the group's first row
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
     const uint32_t sb = smem_u32(smem);
-    float *s_red = reinterpret_cast<float *>(smem + C::kOffRows);  // [row][warp]
-    float *s_m = s_red + 4 * N, *s_f = s_m + N, *s_qs = s_f + N;   // per row: maximum, rescale factor, scale of q
-    int *s_lim = reinterpret_cast<int *>(s_qs + N);                // per row: the last key it sees
+    float *s_red = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * rb;  // [row][warp]
+    float *s_m = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * N + rb, *s_f = s_m + N, *s_qs = s_f + N;
+    int *s_lim = reinterpret_cast<int *>(s_qs + N);  // per row: maximum, rescale factor, scale of q, the last key it sees
     constexpr float kSlack = kF8 ? 4.f : 8.f;        // log2 of the largest weight
     uint32_t sc = 0, g = 0, slot = 0, syncs = 0;
-    // the softmax warps' barrier; like every wait here it gives up after a limit
-    auto softmax_sync = [&]() -> bool {
-      warp_arrive(&bars->sync);
-      return wait_bar_warp(&bars->sync, syncs++ & 1u, abort);
+    // the group's barrier; like every wait here it gives up after a limit
+    auto group_sync = [&]() -> bool {
+      warp_arrive(&bars->sync[w]);
+      return wait_bar_warp(&bars->sync[w], syncs++ & 1u, abort);
     };
     for (bool ok = true; ok;) {
       const int si = slot % kItems;
@@ -445,8 +431,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         constexpr int kLanes = D / 8, kPer = 128 / kLanes;
         const int c = st % kLanes;
 #pragma unroll
-        for (int r0 = 0; r0 < N; r0 += kPer) {
-          const int row = r0 + st / kLanes;
+        for (int r0 = 0; r0 < 16; r0 += kPer) {
+          const int row = rb + r0 + st / kLanes;
           uint4 x = make_uint4(0, 0, 0, 0);
           if (row < nrow) {
             const int tok = row / p.G, gh = row - tok * p.G;
@@ -456,14 +442,14 @@ __global__ void __launch_bounds__(kThreads, 2)
             sts128(sb + C::kOffQ + sw128_offset(row, c * 8, N), x);
           } else {
             // 2^-e q in two e4m3 parts; an infinite or NaN element makes the row's scores NaN
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
             float f[8];
             float am = 0.f;
             bool odd = false;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              f[2 * k] = __uint_as_float(w[k] << 16);
-              f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+              f[2 * k] = __uint_as_float(u[k] << 16);
+              f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -484,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               const float2 h = e4m3x2(hi[k]);
               lo[k] = to_e4m3x2((a - h.x) * 16.f, (b - h.y) * 16.f);
             }
-            if (c == 0) s_qs[row] = __uint_as_float((uint32_t)(127 + e) << 23) * p.c;
+            if (c == 0) s_qs[row - rb] = __uint_as_float((uint32_t)(127 + e) << 23) * p.c;
             const uint2 vh = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
             const uint2 vl = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
             const uint32_t ch = c >> 1, in = (c & 1) * 8;
@@ -497,78 +483,65 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         fence_proxy_async_smem();
         warp_arrive(&bars->q_ready);
-        if (st < N) {
+        if (st < 16) {
           s_m[st] = -INFINITY;
-          s_lim[st] = it.pos0 + min(st, nrow - 1) / p.G;
+          s_lim[st] = it.pos0 + min(rb + st, nrow - 1) / p.G;
         }
-        if (!(ok = softmax_sync())) break;
+        if (!(ok = group_sync())) break;
       }
-      float l[N];
+      float l[16];
 #pragma unroll
-      for (int r = 0; r < N; ++r) l[r] = 0.f;
+      for (int r = 0; r < 16; ++r) l[r] = 0.f;
       for (int j = it.j0; j < it.j1; ++j, ++g) {
-        const uint32_t buf = g % C::kSBufs, tS = tmem + buf * C::kNS + lane_base;
+        const uint32_t buf = g % C::kSBufs, tS = tmem + buf * C::kNS + rb + lane_base;
         if (!(ok = wait_bar_warp(&bars->s_ready[buf], (g / C::kSBufs) & 1u, abort))) break;
         tc_fence_after();
         const int key = j * kTileKeys + kk;
-        const bool edge = j * kTileKeys + kTileKeys - 1 > it.pos0;  // some row does not see the whole tile
-        float ks = p.c, ev = 0.f;                                   // e4m3: the key's scale, the value's exponent
+        // ---- scores in log2 units
+        float s[16], ev = 0.f;                            // e4m3: the value's exponent
         if constexpr (kF8) {
           const uint8_t *ss = smem + C::kOffScale + (g % kScaleSlots) * 2 * kTileKeys;
           const uint32_t vc = ss[kTileKeys + kk];
-          const bool there = key < it.pos0 + it.ntok;               // a stale scale may be anything
-          ks = scale_value(ss[kk]);
-          ev = vc == 255 && there ? __int_as_float(0x7fffffff) : there ? (float)((int)vc - 127) : 0.f;
+          const bool there = key < it.pos0 + it.ntok;     // a stale scale may be anything
+          const float ks = scale_value(ss[kk]);
+          ev = !there ? 0.f : vc == 255 ? __int_as_float(0x7fffffff) : (float)((int)vc - 127);
+          float lo[16];
+          tmem_ld16x2(tS, tS + N, s, lo);
+#pragma unroll
+          for (int r = 0; r < 16; r += 4) {
+            const float4 qs = *reinterpret_cast<const float4 *>(s_qs + r);
+            s[r] = fmaf(lo[r], 0.0625f, s[r]) * (ks * qs.x);
+            s[r + 1] = fmaf(lo[r + 1], 0.0625f, s[r + 1]) * (ks * qs.y);
+            s[r + 2] = fmaf(lo[r + 2], 0.0625f, s[r + 2]) * (ks * qs.z);
+            s[r + 3] = fmaf(lo[r + 3], 0.0625f, s[r + 3]) * (ks * qs.w);
+          }
+        } else {
+          tmem_ld16(tS, s);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) s[r] *= p.c;
         }
-        const float ev4 = ev + 4.f;
-        // scores of rows 16 c .. 16 c + 15, in log2 units
-        auto scores = [&](int c, float (&x)[16]) {
-          if constexpr (kF8) {
-            float lo[16];
-            tmem_ld16x2(tS + 16 * c, tS + N + 16 * c, x, lo);
+        tc_fence_before();
+        warp_arrive(&bars->s_free[buf]);
+        if (j * kTileKeys + kTileKeys - 1 > it.pos0) {    // some row does not see the whole tile
 #pragma unroll
-            for (int r = 0; r < 16; r += 4) {
-              const float4 qs = *reinterpret_cast<const float4 *>(s_qs + 16 * c + r);
-              x[r] = fmaf(lo[r], 0.0625f, x[r]) * (ks * qs.x);
-              x[r + 1] = fmaf(lo[r + 1], 0.0625f, x[r + 1]) * (ks * qs.y);
-              x[r + 2] = fmaf(lo[r + 2], 0.0625f, x[r + 2]) * (ks * qs.z);
-              x[r + 3] = fmaf(lo[r + 3], 0.0625f, x[r + 3]) * (ks * qs.w);
-            }
-          } else {
-            tmem_ld16(tS + 16 * c, x);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) x[r] *= ks;
+          for (int r = 0; r < 16; r += 4) {
+            const int4 lim = *reinterpret_cast<const int4 *>(s_lim + r);
+            s[r] = key > lim.x ? -INFINITY : s[r];
+            s[r + 1] = key > lim.y ? -INFINITY : s[r + 1];
+            s[r + 2] = key > lim.z ? -INFINITY : s[r + 2];
+            s[r + 3] = key > lim.w ? -INFINITY : s[r + 3];
           }
-          if (edge) {
-#pragma unroll
-            for (int r = 0; r < 16; r += 4) {
-              const int4 lim = *reinterpret_cast<const int4 *>(s_lim + 16 * c + r);
-              x[r] = key > lim.x ? -INFINITY : x[r];
-              x[r + 1] = key > lim.y ? -INFINITY : x[r + 1];
-              x[r + 2] = key > lim.z ? -INFINITY : x[r + 2];
-              x[r + 3] = key > lim.w ? -INFINITY : x[r + 3];
-            }
-          }
-        };
-        float s[16];
+        }
         // ---- the tile's maxima (of the weights' exponents): per warp, then a row a thread
 #pragma unroll
-        for (int c = 0; c < N / 16; ++c) {
-          scores(c, s);
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const float v = warp_max(s[r] + ev);
-            if (lane == r) s_red[(16 * c + r) * 4 + q4] = v;
-          }
+        for (int r = 0; r < 16; ++r) {
+          const float v = warp_max(s[r] + ev);
+          if (lane == r) s_red[r * 4 + q4] = v;
         }
-        if constexpr (C::kKeep) {
-          tc_fence_before();
-          warp_arrive(&bars->s_free[buf]);
-        }
-        if (!(ok = softmax_sync())) break;
-        if (st < 64) {
+        if (!(ok = group_sync())) break;
+        if (st < 32) {
           bool need = false;
-          if (st < N) {
+          if (st < 16) {
             const float4 v = *reinterpret_cast<const float4 *>(s_red + st * 4);
             const float mt = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)), m = s_m[st];
             need = mt > m + kSlack;
@@ -576,63 +549,58 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (need) s_m[st] = mt;
           }
           need = __any_sync(0xffffffffu, need);
-          if (lane == 0) s_need[2 * (g & 1) + (st >> 5)] = need;
+          if (lane == 0) s_need[g & 1][w] = need;
         }
-        if (!(ok = softmax_sync())) break;
+        if (!(ok = group_sync())) break;
         if (g > 0 && !(ok = wait_bar_warp(&bars->o_done, (g - 1) & 1u, abort))) break;  // W is read, O^T complete
-        if (s_need[2 * (g & 1)] | s_need[2 * (g & 1) + 1]) {
+        if (s_need[g & 1][w]) {
           tc_fence_after();
 #pragma unroll
-          for (int r = 0; r < N; ++r) l[r] *= s_f[r];
-          if (j > it.j0) tmem_scale<C::kNO>(tmem + C::kColO + lane_base, s_f, N);
+          for (int r = 0; r < 16; ++r) l[r] *= s_f[r];
+          if (j > it.j0) {
+#pragma unroll
+            for (int k = 0; k < C::kTP; ++k) tmem_scale16(tmem + C::kColO + k * N + rb + lane_base, s_f);
+          }
         }
         // ---- weights, rounded into their parts, as the second product's B operand: a key's
         // rows are contiguous, 16 bytes a unit
         const uint32_t wp = sb + C::kOffP + kk * 16;
+        if constexpr (!kF8) {
+          uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int c = 0; c < N / 16; ++c) {
-          if constexpr (!C::kKeep) scores(c, s);
-          if constexpr (!kF8) {
-            uint32_t hi[8], lo[8];
-#pragma unroll
-            for (int r = 0; r < 16; r += 2) {
-              const float2 m = *reinterpret_cast<const float2 *>(s_m + 16 * c + r);
-              const float w0 = ex2(s[r] - (m.x == -INFINITY ? 0.f : m.x)), w1 = ex2(s[r + 1] - (m.y == -INFINITY ? 0.f : m.y));
-              l[16 * c + r] += w0;
-              l[16 * c + r + 1] += w1;
-              const uint32_t h = pack_bf16(w0, w1);
-              hi[r / 2] = h;
-              lo[r / 2] = pack_bf16(w0 - __uint_as_float(h << 16), w1 - __uint_as_float(h & 0xffff0000u));
-            }
-            sts128(wp + (2 * c) * 2048, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-            sts128(wp + (2 * c + 1) * 2048, make_uint4(hi[4], hi[5], hi[6], hi[7]));
-            sts128(wp + (N / 8 + 2 * c) * 2048, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-            sts128(wp + (N / 8 + 2 * c + 1) * 2048, make_uint4(lo[4], lo[5], lo[6], lo[7]));
-          } else {
-            uint32_t q[3][4];
-#pragma unroll
-            for (int r = 0; r < 16; r += 2) {
-              const float2 m = *reinterpret_cast<const float2 *>(s_m + 16 * c + r);
-              const float x0 = s[r] - (m.x == -INFINITY ? 0.f : m.x), x1 = s[r + 1] - (m.y == -INFINITY ? 0.f : m.y);
-              l[16 * c + r] += ex2(x0);
-              l[16 * c + r + 1] += ex2(x1);
-              // 16 w in f16 (2^-12 relative), then e4m3 parts of it, each 2^-4 of the one before
-              uint32_t part[3];
-              split_e4m3x2(ex2(x0 + ev4), ex2(x1 + ev4), part);
-#pragma unroll
-              for (int k = 0; k < 3; ++k) {
-                if (r % 4 == 0) q[k][r / 4] = part[k];
-                else q[k][r / 4] |= part[k] << 16;
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-              sts128(wp + (k * (N / 16) + c) * 2048, make_uint4(q[k][0], q[k][1], q[k][2], q[k][3]));
+          for (int r = 0; r < 16; r += 2) {
+            const float2 m = *reinterpret_cast<const float2 *>(s_m + r);
+            const float w0 = ex2(s[r] - (m.x == -INFINITY ? 0.f : m.x)), w1 = ex2(s[r + 1] - (m.y == -INFINITY ? 0.f : m.y));
+            l[r] += w0;
+            l[r + 1] += w1;
+            const uint32_t h = pack_bf16(w0, w1);
+            hi[r / 2] = h;
+            lo[r / 2] = pack_bf16(w0 - __uint_as_float(h << 16), w1 - __uint_as_float(h & 0xffff0000u));
           }
-        }
-        if constexpr (!C::kKeep) {
-          tc_fence_before();
-          warp_arrive(&bars->s_free[buf]);
+          sts128(wp + (2 * w) * 2048, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          sts128(wp + (2 * w + 1) * 2048, make_uint4(hi[4], hi[5], hi[6], hi[7]));
+          sts128(wp + (N / 8 + 2 * w) * 2048, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+          sts128(wp + (N / 8 + 2 * w + 1) * 2048, make_uint4(lo[4], lo[5], lo[6], lo[7]));
+        } else {
+          const float ev4 = ev + 4.f;  // weights times 16: at most 2^8
+          uint32_t q[3][4];
+#pragma unroll
+          for (int r = 0; r < 16; r += 2) {
+            const float2 m = *reinterpret_cast<const float2 *>(s_m + r);
+            const float x0 = s[r] - (m.x == -INFINITY ? 0.f : m.x), x1 = s[r + 1] - (m.y == -INFINITY ? 0.f : m.y);
+            l[r] += ex2(x0);
+            l[r + 1] += ex2(x1);
+            uint32_t part[3];
+            split_e4m3x2(ex2(x0 + ev4), ex2(x1 + ev4), part);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+              if (r % 4 == 0) q[k][r / 4] = part[k];
+              else q[k][r / 4] |= part[k] << 16;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            sts128(wp + (k * (N / 16) + w) * 2048, make_uint4(q[k][0], q[k][1], q[k][2], q[k][3]));
         }
         if (j == it.j1 - 1) {
           // the last tile: its values have landed, and rows behind the cache's end become zeros
@@ -640,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const uint32_t vs = sc + NS * (2 * jj + 1);  // K of every tile and V of the earlier ones come first
           for (int h = 0; h < NS && ok; ++h) ok = wait_bar_warp(&bars->full[(vs + h) % ST], ((vs + h) / ST) & 1u, abort);
           if (!ok) break;
-          if (key >= it.pos0 + it.ntok) {
+          if (w == 0 && key >= it.pos0 + it.ntok) {
             if constexpr (NS == 2) {
               const uint32_t a = sb + ((vs + (kk >> 6)) % ST) * kStageBytes + (kk & 63) * 128;
 #pragma unroll
@@ -664,47 +632,56 @@ __global__ void __launch_bounds__(kThreads, 2)
       sc += NS * 2 * n;
       // ---- sums over the keys; the item's outputs or its partial result
       const int bad = s_bad[si];
-      float *red = s_red;  // the maxima of the last tile have been read
 #pragma unroll
-      for (int r = 0; r < N; ++r) {
+      for (int r = 0; r < 16; ++r) {  // the maxima of the last tile have been read
         float v = l[r];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == (r & 31)) red[r * 4 + q4] = v;
+        if (lane == r) s_red[r * 4 + q4] = v;
       }
-      if (!(ok = softmax_sync())) break;
+      if (!(ok = group_sync())) break;
       if (!(ok = wait_bar_warp(&bars->o_done, (g - 1) & 1u, abort))) break;
       tc_fence_after();
-      float o[C::kNO];
-      tmem_ld<C::kNO>(tmem + C::kColO + lane_base, o);
+      float o[16];
+      {
+        float o1[16];
+        tmem_ld16x2(tmem + C::kColO + rb + lane_base, tmem + C::kColO + N + rb + lane_base, o, o1);
+        if constexpr (kF8) {
+          float o2[16];
+          tmem_ld16(tmem + C::kColO + 2 * N + rb + lane_base, o2);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[r] = (o[r] + 0.0625f * (o1[r] + 0.0625f * o2[r])) * 0.0625f;
+        } else {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[r] += o1[r];
+        }
+      }
       tc_fence_before();
       const int ch = D == 128 ? kk : 16 * q4 + lane;   // channel of this TMEM lane
       const bool has = D == 128 || lane < 16;
       const int pslot = 2 * blockIdx.x + (it.kind == 1 ? 1 : 0);
 #pragma unroll
-      for (int r = 0; r < N; ++r) {
-        const float4 v = *reinterpret_cast<const float4 *>(red + r * 4);
-        const float lt = (v.x + v.y) + (v.z + v.w);
-        float x;
-        if constexpr (!kF8) x = o[r] + o[N + r];
-        else x = (o[r] + 0.0625f * (o[N + r] + 0.0625f * o[2 * N + r])) * 0.0625f;
-        if (r < nrow && has) {
+      for (int r = 0; r < 16; ++r) {
+        const int row = rb + r;
+        if (row < nrow && has) {
+          const float4 v = *reinterpret_cast<const float4 *>(s_red + r * 4);
+          const float lt = (v.x + v.y) + (v.z + v.w);
           if (it.kind == 0) {
             if (!bad) {
-              const int tok = r / p.G, gh = r - tok * p.G;
-              p.o[((size_t)(it.row0 + tok) * p.H + it.hk * p.G + gh) * D + ch] = __float2bfloat16_rn(lt == 0.f ? 0.f : x / lt);
+              const int tok = row / p.G, gh = row - tok * p.G;
+              p.o[((size_t)(it.row0 + tok) * p.H + it.hk * p.G + gh) * D + ch] = __float2bfloat16_rn(lt == 0.f ? 0.f : o[r] / lt);
             }
           } else {
-            p.part[((size_t)pslot * N + r) * D + ch] = x;
-            if (ch == 0) p.ml[(size_t)pslot * N + r] = make_float2(s_m[r], lt);
+            p.part[((size_t)pslot * N + row) * D + ch] = o[r];
+            if (ch == 0) p.ml[(size_t)pslot * N + row] = make_float2(s_m[r], lt);
           }
         }
       }
-      if (st == 0) {
+      if (st == 0 && w == 0) {
         if (it.kind != 0) p.skip[pslot] = bad;
         if (bad && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_BAD_SLOT);
       }
-      if (!(ok = softmax_sync())) break;  // red is rewritten by the next item
+      if (!(ok = group_sync())) break;  // s_red and s_m are rewritten by the next item
       warp_arrive(&bars->item_empty[si]);
     }
   }
@@ -723,7 +700,7 @@ cudaError_t launch(const AttnParams &p, const CUtensorMap &tk, const CUtensorMap
   const int bytes = (int)Cfg<D, kF8, N>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  kernel<<<ctas, kThreads, bytes, stream>>>(tk, tv, p);
+  kernel<<<ctas, Cfg<D, kF8, N>::kThreads, bytes, stream>>>(tk, tv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_merge<D, N, true>(p, ctas, stream);
 }
