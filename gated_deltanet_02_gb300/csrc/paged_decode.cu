@@ -10,12 +10,14 @@
 // rescaled), which leaves the result unchanged: m is a common factor.
 //
 // Precision: scores, m, sums and O^T are fp32.  The weights enter the second
-// product as two bf16 parts (bf16 cache; 2^-16 relative) or three e4m3 parts
-// (e4m3 cache; 2^-12), so the output's rounding to bf16 is the only one that
-// counts.  With an e4m3 cache both products run on the stored values
+// product as two parts, bf16 (together 2^-16 relative) or e4m3 (e4m3 cache;
+// 2^-8 relative, on average less than half of what rounding them to bf16 would
+// do, and 2^-18 of the largest weight), so the output's rounding to bf16 is the
+// one that counts.  With an e4m3 cache both products run on the stored values
 // (kind::f8f6f4): q is split into two e4m3 parts of 4 bits (bf16 has 8) with a
-// power-of-two scale per row, the key's scale multiplies its score, and the
-// value's scale 2^e is folded into the weight's exponent: W = 2^(S + e - m)
+// power-of-two scale per row, exact but for elements below 2^-10 of the row's
+// largest, where a step is 2^-16 of it; the key's scale multiplies its score, and
+// the value's scale 2^e is folded into the weight's exponent: W = 2^(S + e - m)
 // with m the maximum of S + e, while the sums use 2^(S - m).
 //
 // Bound: HBM, one read of the cache; 2 CTAs per SM, each with a ring of 16 KiB
@@ -42,18 +44,16 @@ constexpr uint32_t kStageBytes = 16384;
 template <int D, bool kF8, int N>
 struct Cfg {
   static constexpr int kTQ = kF8 ? 2 : 1;            // parts of q
-  static constexpr int kTP = kF8 ? 3 : 2;            // parts of a weight
-  static constexpr int kNS = N * kTQ, kNO = N * kTP;  // columns of S^T and O^T
+  static constexpr int kTP = 2;                      // parts of a weight
+  static constexpr int kNO = N * kTP;                // columns of O^T (S^T has N)
   static constexpr int kEsz = kF8 ? 1 : 2;
   static constexpr int kTileStages = D * kEsz * kTileKeys > (int)kStageBytes ? 2 : 1;
-  // S^T of two tiles where TMEM holds them (256 columns a CTA)
-  static constexpr int kSBufs = 2 * kNS + kNO <= 256 ? 2 : 1;
   static constexpr int kGroups = N / 16;             // softmax warpgroups, 16 rows each
   static constexpr int kThreads = 64 + 128 * kGroups;
   static constexpr uint32_t kBytesQ = N * kTQ * D * kEsz;
   static constexpr uint32_t kBytesP = N * kTP * kTileKeys * kEsz;
   static constexpr uint32_t kBytesScale = kF8 ? kScaleSlots * 2 * kTileKeys : 0;
-  static constexpr uint32_t kBytesRows = 4 * N * 4 + 4 * N * 4;  // [row][warp] maxima or sums; m, f, limit, q scale
+  static constexpr uint32_t kBytesRows = 4 * N * 4 + 5 * N * 4;  // [row][warp] maxima or sums, then five numbers a row
   static constexpr uint32_t kBytesBars = 640;
   static constexpr uint32_t kFixed = kBytesQ + kBytesP + kBytesScale + kBytesRows + kBytesBars + 1024;
   // two CTAs of an SM share 228 KiB, 1 KiB of each reserved
@@ -62,7 +62,7 @@ struct Cfg {
   static constexpr uint32_t kSmem = kFixed + kStages * kStageBytes;
   static constexpr uint32_t kOffQ = kStages * kStageBytes, kOffP = kOffQ + kBytesQ, kOffScale = kOffP + kBytesP,
                             kOffRows = kOffScale + kBytesScale, kOffBars = kOffRows + kBytesRows;
-  static constexpr uint32_t kColO = kSBufs * kNS;
+  static constexpr uint32_t kColO = 2 * N;
   static constexpr uint32_t kCols = kColO + kNO <= 64 ? 64 : kColO + kNO <= 128 ? 128 : 256;
   static_assert(kColO + kNO <= 256, "two CTAs share the SM's 512 columns");
   static_assert(kStages >= 2 * kTileStages, "K and V tiles of one step");
@@ -86,6 +86,11 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 __device__ __forceinline__ float warp_max(float x) {
   float y;
@@ -117,21 +122,19 @@ __device__ __forceinline__ uint64_t desc_sw64(uint32_t saddr, uint32_t lbo, uint
   return d;
 }
 
-// Two weights as three e4m3 parts each (bytes 0 and 1 of part[]): the value
-// rounded, then 16 times and 256 times what is left.
-__device__ __forceinline__ void split_e4m3x2(float w0, float w1, uint32_t (&part)[3]) {
+// Two weights as two e4m3 parts each (bytes 0 and 1): the value rounded (from
+// its f16), then 16 times what is left.
+__device__ __forceinline__ void split_e4m3x2(float w0, float w1, uint32_t &hi, uint32_t &lo) {
   uint32_t x, y;
+  unsigned short e, f;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(w1), "f"(w0));
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    unsigned short e;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(e) : "r"(x));
-    part[k] = e;
-    if (k == 2) break;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(e));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(y));
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(0x4c004c00u));  // 16
-  }
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(e) : "r"(x));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(e));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(y));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(0x4c004c00u));  // 16
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(f) : "r"(x));
+  hi = e;
+  lo = f;
 }
 
 // Matrix without swizzle, MN-major: 16-byte units of consecutive rows, a unit's
@@ -170,7 +173,8 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars *bars = reinterpret_cast<Bars *>(smem + C::kOffBars);
   static_assert(sizeof(Bars) <= C::kBytesBars, "barrier block");
-  __shared__ int s_need[2][W];  // [tile parity]: a row's maximum moves
+  __shared__ __align__(16) int s_flag[2][W][4];  // [tile parity][group][warp]: a row's maximum moves
+  __shared__ int s_unset[W];                     // a row of the group has no maximum yet
   __shared__ int s_bad[kItems];
   volatile int *abort = &bars->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -322,17 +326,17 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
   } else if (warp == 1) {
     if (lane == 0) {
       // ============ MMA issue ============
-      constexpr uint32_t id_s = kF8 ? idesc_f8(128, C::kNS, false, false) : idesc_bf16(128, C::kNS, false, false);
+      constexpr uint32_t id_s = kF8 ? idesc_f8(128, N, false, false) : idesc_bf16(128, N, false, false);
       constexpr uint32_t id_o = kF8 ? idesc_f8(D, C::kNO, true, true) : idesc_bf16(D, C::kNO, true, true);
       const uint32_t sb = smem_u32(smem), sQ = sb + C::kOffQ, sP = sb + C::kOffP;
       uint32_t sc = 0, g = 0, slot = 0;
       auto issue_s = [&](uint32_t gi) -> bool {
         for (int h = 0; h < NS; ++h)
           if (!wait_bar(&bars->full[(sc + h) % ST], ((sc + h) / ST) & 1u, abort)) return false;
-        const uint32_t buf = gi % C::kSBufs;
-        if (!wait_bar(&bars->s_free[buf], ((gi / C::kSBufs) & 1u) ^ 1u, abort)) return false;
+        const uint32_t buf = gi & 1;
+        if (!wait_bar(&bars->s_free[buf], ((gi >> 1) & 1u) ^ 1u, abort)) return false;
         tc_fence_after();
-        const uint32_t d = tmem + buf * C::kNS;
+        const uint32_t d = tmem + buf * N;
         if constexpr (!kF8) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
@@ -340,13 +344,15 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
             umma_bf16(d, desc_sw128(a, 16, 1024), desc_sw128(sQ + (ks >> 2) * (N * 128) + (ks & 3) * 32, 16, 1024), id_s, ks > 0);
           }
         } else {
+          // both parts of q against the same keys
           const uint32_t a = sb + (sc % ST) * kStageBytes;
 #pragma unroll
-          for (int ks = 0; ks < D / 32; ++ks) {
+          for (int ks = 0; ks < 2 * (D / 32); ++ks) {
+            const uint32_t k = ks % (D / 32) * 32, b = sQ + ks / (D / 32) * (N * D) + k;
             if (D == 128)
-              umma_f8(d, desc_sw128(a + ks * 32, 16, 1024), desc_sw128(sQ + ks * 32, 16, 1024), id_s, ks > 0);
+              umma_f8(d, desc_sw128(a + k, 16, 1024), desc_sw128(b, 16, 1024), id_s, ks > 0);
             else
-              umma_f8(d, desc_sw64(a + ks * 32, 16, 512), desc_sw64(sQ + ks * 32, 16, 512), id_s, ks > 0);
+              umma_f8(d, desc_sw64(a + k, 16, 512), desc_sw64(b, 16, 512), id_s, ks > 0);
           }
         }
         umma_commit(&bars->s_ready[buf]);
@@ -392,8 +398,6 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
         if (kind < 0) break;
         if (!wait_bar(&bars->q_ready, slot & 1u, abort)) break;
         ++slot;
-        // S of a tile goes before O of the one before it; with one S buffer it is
-        // free once that tile's weights are formed, which is when O can go too
         for (int j = 0; j < n && ok; ++j) {
           ok = issue_s(g + j);
           if (ok && j > 0) ok = issue_o(g + j - 1, j == 1);
@@ -410,8 +414,10 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
     const uint32_t sb = smem_u32(smem);
     float *s_red = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * rb;  // [row][warp]
-    float *s_m = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * N + rb, *s_f = s_m + N, *s_qs = s_f + N;
-    int *s_lim = reinterpret_cast<int *>(s_qs + N);  // per row: maximum, rescale factor, scale of q, the last key it sees
+    // per row: maximum (0 while there is none), its step in this tile, the
+    // factor of that step, the scale of q, the last key that it sees
+    float *s_m = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * N + rb, *s_d = s_m + N, *s_f = s_d + N, *s_qs = s_f + N;
+    int *s_lim = reinterpret_cast<int *>(s_qs + N);
     constexpr float kSlack = kF8 ? 4.f : 8.f;        // log2 of the largest weight
     uint32_t sc = 0, g = 0, slot = 0, syncs = 0;
     // the group's barrier; like every wait here it gives up after a limit
@@ -468,7 +474,7 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
               const float a = odd ? __int_as_float(0x7fffffff) : f[2 * k] * down, b = odd ? a : f[2 * k + 1] * down;
               hi[k] = to_e4m3x2(a, b);
               const float2 h = e4m3x2(hi[k]);
-              lo[k] = to_e4m3x2((a - h.x) * 16.f, (b - h.y) * 16.f);
+              lo[k] = to_e4m3x2(a - h.x, b - h.y);
             }
             if (c == 0) s_qs[row - rb] = __uint_as_float((uint32_t)(127 + e) << 23) * p.c;
             const uint2 vh = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
@@ -484,83 +490,100 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
         fence_proxy_async_smem();
         warp_arrive(&bars->q_ready);
         if (st < 16) {
-          s_m[st] = -INFINITY;
+          s_m[st] = 0.f;
           s_lim[st] = it.pos0 + min(rb + st, nrow - 1) / p.G;
         }
         if (!(ok = group_sync())) break;
       }
+      bool has_max = false;  // of the row st (threads 0 .. 15 of the group)
       float l[16];
 #pragma unroll
       for (int r = 0; r < 16; ++r) l[r] = 0.f;
       for (int j = it.j0; j < it.j1; ++j, ++g) {
-        const uint32_t buf = g % C::kSBufs, tS = tmem + buf * C::kNS + rb + lane_base;
-        if (!(ok = wait_bar_warp(&bars->s_ready[buf], (g / C::kSBufs) & 1u, abort))) break;
+        const uint32_t buf = g & 1, tS = tmem + buf * N + rb + lane_base;
+        if (!(ok = wait_bar_warp(&bars->s_ready[buf], (g >> 1) & 1u, abort))) break;
         tc_fence_after();
         const int key = j * kTileKeys + kk;
-        // ---- scores in log2 units
-        float s[16], ev = 0.f;                            // e4m3: the value's exponent
+        // ---- scores in log2 units, less the row's maximum
+        float x[16], ev = 0.f;                            // e4m3: the value's exponent
+        tmem_ld16(tS, x);
+        float ks = p.c;
         if constexpr (kF8) {
           const uint8_t *ss = smem + C::kOffScale + (g % kScaleSlots) * 2 * kTileKeys;
           const uint32_t vc = ss[kTileKeys + kk];
           const bool there = key < it.pos0 + it.ntok;     // a stale scale may be anything
-          const float ks = scale_value(ss[kk]);
+          ks = scale_value(ss[kk]);
           ev = !there ? 0.f : vc == 255 ? __int_as_float(0x7fffffff) : (float)((int)vc - 127);
-          float lo[16];
-          tmem_ld16x2(tS, tS + N, s, lo);
-#pragma unroll
-          for (int r = 0; r < 16; r += 4) {
-            const float4 qs = *reinterpret_cast<const float4 *>(s_qs + r);
-            s[r] = fmaf(lo[r], 0.0625f, s[r]) * (ks * qs.x);
-            s[r + 1] = fmaf(lo[r + 1], 0.0625f, s[r + 1]) * (ks * qs.y);
-            s[r + 2] = fmaf(lo[r + 2], 0.0625f, s[r + 2]) * (ks * qs.z);
-            s[r + 3] = fmaf(lo[r + 3], 0.0625f, s[r + 3]) * (ks * qs.w);
-          }
-        } else {
-          tmem_ld16(tS, s);
-#pragma unroll
-          for (int r = 0; r < 16; ++r) s[r] *= p.c;
         }
         tc_fence_before();
         warp_arrive(&bars->s_free[buf]);
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const float4 m = *reinterpret_cast<const float4 *>(s_m + r);
+          float4 q = make_float4(ks, ks, ks, ks);
+          if constexpr (kF8) {
+            const float4 qs = *reinterpret_cast<const float4 *>(s_qs + r);
+            q = make_float4(ks * qs.x, ks * qs.y, ks * qs.z, ks * qs.w);
+          }
+          x[r] = fmaf(x[r], q.x, -m.x);
+          x[r + 1] = fmaf(x[r + 1], q.y, -m.y);
+          x[r + 2] = fmaf(x[r + 2], q.z, -m.z);
+          x[r + 3] = fmaf(x[r + 3], q.w, -m.w);
+        }
         if (j * kTileKeys + kTileKeys - 1 > it.pos0) {    // some row does not see the whole tile
 #pragma unroll
           for (int r = 0; r < 16; r += 4) {
             const int4 lim = *reinterpret_cast<const int4 *>(s_lim + r);
-            s[r] = key > lim.x ? -INFINITY : s[r];
-            s[r + 1] = key > lim.y ? -INFINITY : s[r + 1];
-            s[r + 2] = key > lim.z ? -INFINITY : s[r + 2];
-            s[r + 3] = key > lim.w ? -INFINITY : s[r + 3];
+            x[r] = key > lim.x ? -INFINITY : x[r];
+            x[r + 1] = key > lim.y ? -INFINITY : x[r + 1];
+            x[r + 2] = key > lim.z ? -INFINITY : x[r + 2];
+            x[r + 3] = key > lim.w ? -INFINITY : x[r + 3];
           }
         }
-        // ---- the tile's maxima (of the weights' exponents): per warp, then a row a thread
+        // ---- does a row's maximum move?  (In its first tile always; later once in a while.)
+        {
+          float t = x[0];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float v = warp_max(s[r] + ev);
-          if (lane == r) s_red[r * 4 + q4] = v;
+          for (int r = 1; r < 15; r += 2) t = max3(t, x[r], x[r + 1]);
+          const bool any = __any_sync(0xffffffffu, fmaxf(t, x[15]) + ev > kSlack);
+          if (lane == 0) s_flag[g & 1][w][q4] = any || j == it.j0;
         }
         if (!(ok = group_sync())) break;
-        if (st < 32) {
-          bool need = false;
-          if (st < 16) {
-            const float4 v = *reinterpret_cast<const float4 *>(s_red + st * 4);
-            const float mt = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)), m = s_m[st];
-            need = mt > m + kSlack;
-            s_f[st] = need ? ex2(m - mt) : 1.f;
-            if (need) s_m[st] = mt;
+        const int4 fl = *reinterpret_cast<const int4 *>(s_flag[g & 1][w]);
+        const bool moves = fl.x | fl.y | fl.z | fl.w | (j > it.j0 && s_unset[w]);
+        if (moves) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float v = warp_max(x[r] + ev);
+            if (lane == r) s_red[r * 4 + q4] = v;
           }
-          need = __any_sync(0xffffffffu, need);
-          if (lane == 0) s_need[g & 1][w] = need;
+          if (!(ok = group_sync())) break;
+          if (st < 32) {
+            if (st < 16) {
+              const float4 v = *reinterpret_cast<const float4 *>(s_red + st * 4);
+              const float t = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+              const float d = t > (has_max ? kSlack : -INFINITY) ? t : 0.f;
+              has_max |= t > -INFINITY;
+              s_d[st] = d;
+              s_f[st] = ex2(-d);
+              s_m[st] += d;
+            }
+            const bool unset = __any_sync(0xffffffffu, st < 16 && !has_max);
+            if (st == 0) s_unset[w] = unset;
+          }
+          if (!(ok = group_sync())) break;
+#pragma unroll
+          for (int r = 0; r < 16; r += 4) {
+            const float4 d = *reinterpret_cast<const float4 *>(s_d + r), f = *reinterpret_cast<const float4 *>(s_f + r);
+            x[r] -= d.x, x[r + 1] -= d.y, x[r + 2] -= d.z, x[r + 3] -= d.w;
+            l[r] *= f.x, l[r + 1] *= f.y, l[r + 2] *= f.z, l[r + 3] *= f.w;
+          }
         }
-        if (!(ok = group_sync())) break;
         if (g > 0 && !(ok = wait_bar_warp(&bars->o_done, (g - 1) & 1u, abort))) break;  // W is read, O^T complete
-        if (s_need[g & 1][w]) {
+        if (moves && j > it.j0) {
           tc_fence_after();
 #pragma unroll
-          for (int r = 0; r < 16; ++r) l[r] *= s_f[r];
-          if (j > it.j0) {
-#pragma unroll
-            for (int k = 0; k < C::kTP; ++k) tmem_scale16(tmem + C::kColO + k * N + rb + lane_base, s_f);
-          }
+          for (int k = 0; k < C::kTP; ++k) tmem_scale16(tmem + C::kColO + k * N + rb + lane_base, s_f);
         }
         // ---- weights, rounded into their parts, as the second product's B operand: a key's
         // rows are contiguous, 16 bytes a unit
@@ -569,8 +592,7 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
           uint32_t hi[8], lo[8];
 #pragma unroll
           for (int r = 0; r < 16; r += 2) {
-            const float2 m = *reinterpret_cast<const float2 *>(s_m + r);
-            const float w0 = ex2(s[r] - (m.x == -INFINITY ? 0.f : m.x)), w1 = ex2(s[r + 1] - (m.y == -INFINITY ? 0.f : m.y));
+            const float w0 = ex2(x[r]), w1 = ex2(x[r + 1]);
             l[r] += w0;
             l[r + 1] += w1;
             const uint32_t h = pack_bf16(w0, w1);
@@ -583,24 +605,18 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
           sts128(wp + (N / 8 + 2 * w + 1) * 2048, make_uint4(lo[4], lo[5], lo[6], lo[7]));
         } else {
           const float ev4 = ev + 4.f;  // weights times 16: at most 2^8
-          uint32_t q[3][4];
+          uint32_t hi[4], lo[4];
 #pragma unroll
           for (int r = 0; r < 16; r += 2) {
-            const float2 m = *reinterpret_cast<const float2 *>(s_m + r);
-            const float x0 = s[r] - (m.x == -INFINITY ? 0.f : m.x), x1 = s[r + 1] - (m.y == -INFINITY ? 0.f : m.y);
-            l[r] += ex2(x0);
-            l[r + 1] += ex2(x1);
-            uint32_t part[3];
-            split_e4m3x2(ex2(x0 + ev4), ex2(x1 + ev4), part);
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-              if (r % 4 == 0) q[k][r / 4] = part[k];
-              else q[k][r / 4] |= part[k] << 16;
-            }
+            l[r] += ex2(x[r]);
+            l[r + 1] += ex2(x[r + 1]);
+            uint32_t h, e;
+            split_e4m3x2(ex2(x[r] + ev4), ex2(x[r + 1] + ev4), h, e);
+            hi[r / 4] = r % 4 ? hi[r / 4] | h << 16 : h;
+            lo[r / 4] = r % 4 ? lo[r / 4] | e << 16 : e;
           }
-#pragma unroll
-          for (int k = 0; k < 3; ++k)
-            sts128(wp + (k * (N / 16) + w) * 2048, make_uint4(q[k][0], q[k][1], q[k][2], q[k][3]));
+          sts128(wp + w * 2048, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          sts128(wp + (N / 16 + w) * 2048, make_uint4(lo[0], lo[1], lo[2], lo[3]));
         }
         if (j == it.j1 - 1) {
           // the last tile: its values have landed, and rows behind the cache's end become zeros
@@ -646,15 +662,8 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
       {
         float o1[16];
         tmem_ld16x2(tmem + C::kColO + rb + lane_base, tmem + C::kColO + N + rb + lane_base, o, o1);
-        if constexpr (kF8) {
-          float o2[16];
-          tmem_ld16(tmem + C::kColO + 2 * N + rb + lane_base, o2);
 #pragma unroll
-          for (int r = 0; r < 16; ++r) o[r] = (o[r] + 0.0625f * (o1[r] + 0.0625f * o2[r])) * 0.0625f;
-        } else {
-#pragma unroll
-          for (int r = 0; r < 16; ++r) o[r] += o1[r];
-        }
+        for (int r = 0; r < 16; ++r) o[r] = kF8 ? 0.0625f * (o[r] + 0.0625f * o1[r]) : o[r] + o1[r];
       }
       tc_fence_before();
       const int ch = D == 128 ? kk : 16 * q4 + lane;   // channel of this TMEM lane
@@ -673,7 +682,7 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
             }
           } else {
             p.part[((size_t)pslot * N + row) * D + ch] = o[r];
-            if (ch == 0) p.ml[(size_t)pslot * N + row] = make_float2(s_m[r], lt);
+            if (ch == 0) p.ml[(size_t)pslot * N + row] = make_float2(lt == 0.f ? -INFINITY : s_m[r], lt);
           }
         }
       }
