@@ -25,6 +25,7 @@
 // 0 TMA and the walk over the items, 1 MMA issue, then groups of four softmax
 // warps, a key per thread and 16 rows per group.
 #include "paged_sched.cuh"
+#include "paged_tc.cuh"
 #include "prefill_tc.cuh"
 #include "tc_common.cuh"
 
@@ -82,44 +83,10 @@ struct Bars {
   int abort;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
 __device__ __forceinline__ float warp_max(float x) {
   float y;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// D[tmem] (+)= A[smem] B[smem], e4m3 x e4m3 -> fp32.
-__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool a_mn, bool b_mn) {
-  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);
-}
-// 64-byte swizzle: rows of 64 bytes, 8-row groups 512 bytes apart (layout type 4).
-__device__ __forceinline__ uint64_t desc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)4 << 61;
-  return d;
 }
 
 // Two weights as two e4m3 parts each (bytes 0 and 1): the value rounded (from
@@ -447,38 +414,9 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
           if constexpr (!kF8) {
             sts128(sb + C::kOffQ + sw128_offset(row, c * 8, N), x);
           } else {
-            // 2^-e q in two e4m3 parts; an infinite or NaN element makes the row's scores NaN
-            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-            float f[8];
-            float am = 0.f;
-            bool odd = false;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              f[2 * k] = __uint_as_float(u[k] << 16);
-              f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              odd |= !(fabsf(f[k]) <= 3.4e38f);
-              am = fmaxf(am, fabsf(f[k]));
-            }
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-            // the power of two that brings the largest element into [128, 256)
-            int e = (int)(__float_as_uint(am) >> 23) - 127 - 7;
-            e = min(max(e, -100), 120);
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float a = odd ? __int_as_float(0x7fffffff) : f[2 * k] * down, b = odd ? a : f[2 * k + 1] * down;
-              hi[k] = to_e4m3x2(a, b);
-              const float2 h = e4m3x2(hi[k]);
-              lo[k] = to_e4m3x2(a - h.x, b - h.y);
-            }
-            if (c == 0) s_qs[row - rb] = __uint_as_float((uint32_t)(127 + e) << 23) * p.c;
-            const uint2 vh = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-            const uint2 vl = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            uint2 vh, vl;
+            const float scale = split_q<kLanes>(x, vh, vl);
+            if (c == 0) s_qs[row - rb] = scale * p.c;
             const uint32_t ch = c >> 1, in = (c & 1) * 8;
             auto at = [&](int rr) {
               return D == 128 ? rr * 128u + ((ch ^ (rr & 7u)) << 4) + in : rr * 64u + ((ch ^ ((rr >> 1) & 3u)) << 4) + in;

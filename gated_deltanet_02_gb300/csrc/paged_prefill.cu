@@ -16,12 +16,15 @@
 // other's softmax does:  P0 V, Q0 K' | P1 V, Q1 K' | ...  A softmax thread
 // owns a row, so no reduction crosses threads.  K and V tiles of 128 keys come
 // through a shared-memory ring: TMA, one box per page and 64 channels (bf16);
-// an e4m3 cache is read by four converting warps, which scale the values by
-// their power of two and write the bf16 tile (exact) where TMA would have put it.
+// of an e4m3 cache the keys go into the first product as they are (kind::f8f6f4,
+// q split into two e4m3 parts as in paged_decode.cu; the keys' scales multiply
+// the scores' columns), while four more warps turn the value tiles, times their
+// powers of two, into the bf16 tiles (exact) that the second product reads.
 //
 // Bound: the tensor core for long prompts (two 128 x 128 x D products per tile
 // pair and 128 keys), next to it the exponentials.
 #include "paged_sched.cuh"
+#include "paged_tc.cuh"
 #include "prefill_tc.cuh"
 #include "tc_common.cuh"
 
@@ -40,25 +43,34 @@ constexpr float kSlack = 8.f;  // log2 of the largest weight
 template <int D, bool kF8>
 struct Cfg {
   static constexpr int kThreads = kF8 ? 512 : 384;
-  static constexpr uint32_t kQTile = 128 * D * 2;
-  static constexpr uint32_t kStageBytes = kTileKeys * D * 2;
-  static constexpr int kStages = D == 128 ? (kF8 ? 3 : 4) : 6;
-  // e4m3: tiles as they are in the cache (with their scales), before the conversion
-  static constexpr int kRawStages = kF8 ? (D == 128 ? 3 : 6) : 0;
-  static constexpr uint32_t kRawBytes = kTileKeys * D;
+  static constexpr uint32_t kQTile = 128 * D * 2;             // bf16, or two e4m3 parts
+  static constexpr uint32_t kStageBytes = kTileKeys * D * 2;  // a bf16 tile
+  static constexpr uint32_t kRawBytes = kTileKeys * D;        // an e4m3 tile
+  // bf16: K and V tiles in turn; e4m3: V tiles after their conversion, and K
+  // and V tiles as they are in the cache
+  static constexpr int kStages = kF8 ? 2 : D == 128 ? 4 : 6;
+  static constexpr int kRawK = kF8 ? 3 : 0, kRawV = kF8 ? 2 : 0;
+  static constexpr int kScaleSlots = kF8 ? 8 : 0;             // tiles of key scales as floats
+  static constexpr int kOutCols = kF8 ? 16 : 32;              // channels of the output staging
   static constexpr uint32_t kOffRing = 2 * kQTile;
-  static constexpr uint32_t kOffRaw = kOffRing + kStages * kStageBytes;
-  static constexpr uint32_t kOffScale = kOffRaw + kRawStages * kRawBytes;
-  static constexpr uint32_t kOffOut = kOffScale + kRawStages * kTileKeys;  // 2 KiB per softmax warp
-  static constexpr uint32_t kOffBars = kOffOut + 8 * 2048;
-  static constexpr uint32_t kBytesBars = 1024;
+  static constexpr uint32_t kOffRawK = kOffRing + kStages * kStageBytes;
+  static constexpr uint32_t kOffRawV = kOffRawK + kRawK * kRawBytes;
+  static constexpr uint32_t kOffOut = kOffRawV + kRawV * kRawBytes;
+  static constexpr uint32_t kOffCode = kOffOut + 8 * 32 * kOutCols * 2;   // scale codes beside the raw tiles
+  static constexpr uint32_t kOffScale = kOffCode + (kRawK + kRawV) * kTileKeys;
+  static constexpr uint32_t kOffBars = kOffScale + kScaleSlots * kTileKeys * 4;
+  static constexpr uint32_t kBytesBars = 1024 + (kF8 ? 1024 : 0);         // e4m3: and a scale per q row
   static constexpr uint32_t kSmem = kOffBars + kBytesBars + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
+  // the keys' scales of tile j are read before S of tile j + 1 is issued, so
+  // that a tile at most kRawK ahead can be written meanwhile
+  static_assert(!kF8 || kScaleSlots > kRawK, "scale slots");
   static constexpr uint32_t kColS = 0, kColO = 256;
 };
 
 struct Bars {
-  uint64_t full[6], empty[6], raw_full[6], raw_empty[6];
+  uint64_t full[6], empty[6];             // bf16 tiles
+  uint64_t rawk_full[3], rawk_empty[3], rawv_full[2], rawv_empty[2], scale_ready[8];
   uint64_t s_ready[2], p_ready[2][2], q_ready[2], o_done[2];
   uint64_t item_full[kItems], item_empty[kItems];
   Item item[kItems];
@@ -68,16 +80,6 @@ struct Bars {
   int abort;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
 template <int kRegs>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -111,13 +113,14 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 template <int D, bool kF8>
 __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnParams p,
-                   const uint8_t *k_cache, const uint8_t *v_cache) {
+                   const uint8_t *v_cache) {
   using C = Cfg<D, kF8>;
   constexpr int ST = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars *bars = reinterpret_cast<Bars *>(smem + C::kOffBars);
-  static_assert(sizeof(Bars) <= C::kBytesBars, "barrier block");
+  static_assert(sizeof(Bars) <= 1024, "barrier block");
+  float *s_qs = reinterpret_cast<float *>(smem + C::kOffBars + 1024);  // e4m3: scale of a q row
   volatile int *abort = &bars->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sb = smem_u32(smem);
@@ -127,10 +130,15 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       mbar_init(&bars->full[s], kF8 ? 4 : 1);
       mbar_init(&bars->empty[s], 1);
     }
-    for (int s = 0; s < C::kRawStages; ++s) {
-      mbar_init(&bars->raw_full[s], 1);
-      mbar_init(&bars->raw_empty[s], 4);
+    for (int s = 0; s < C::kRawK; ++s) {
+      mbar_init(&bars->rawk_full[s], 1);
+      mbar_init(&bars->rawk_empty[s], 1 + 4);  // the products, and the scales' readers
     }
+    for (int s = 0; s < C::kRawV; ++s) {
+      mbar_init(&bars->rawv_full[s], 1);
+      mbar_init(&bars->rawv_empty[s], 4);
+    }
+    for (int s = 0; s < C::kScaleSlots; ++s) mbar_init(&bars->scale_ready[s], 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->s_ready[i], 1);
       mbar_init(&bars->p_ready[i][0], 4);
@@ -160,7 +168,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
   const int pages = kTileKeys >> p.page_shift;  // pages of a tile
 
   if (warp < 4) {
-    // registers a thread: 64 + 2 x 184 + 80 of 4 x 128 (e4m3), 80 + 2 x 208 of 3 x 168
+    // registers a thread: 64 + 2 x 192 + 64 of 4 x 128 (e4m3), 80 + 2 x 208 of 3 x 168
     regs_dec<kF8 ? 64 : 80>();
     if (warp == 0) {
       // ============ the walk over the items, and TMA ============
@@ -203,15 +211,21 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
 #pragma unroll
           for (int v = 0; v < 2; ++v, ++sc) {
             if constexpr (kF8) {
-              const uint32_t s = sc % C::kRawStages;
-              if (!(ok = wait_bar_warp(&bars->raw_empty[s], ((sc / C::kRawStages) & 1u) ^ 1u, abort))) break;
-              if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[s], bytes);
+              const uint32_t g = sc >> 1, s = v ? g % C::kRawV : g % C::kRawK;
+              uint64_t *f = v ? &bars->rawv_full[s] : &bars->rawk_full[s];
+              if (!(ok = v ? wait_bar_warp(&bars->rawv_empty[s], ((g / C::kRawV) & 1u) ^ 1u, abort)
+                           : wait_bar_warp(&bars->rawk_empty[s], ((g / C::kRawK) & 1u) ^ 1u, abort)))
+                break;
+              if (lane == 0) mbar_arrive_expect_tx(f, bytes);
               __syncwarp();
               if (op && good) {
-                bulk_load(smem + C::kOffRaw + s * C::kRawBytes + pl * p.page * D, (v ? v_cache : k_cache) + plane * p.page * D,
-                          (uint32_t)p.page * D, &bars->raw_full[s]);
-                bulk_load(smem + C::kOffScale + s * kTileKeys + pl * p.page, (v ? p.v_scale : p.k_scale) + plane * p.page,
-                          (uint32_t)p.page, &bars->raw_full[s]);
+                if (v)
+                  bulk_load(smem + C::kOffRawV + s * C::kRawBytes + pl * p.page * D, v_cache + plane * p.page * D,
+                            (uint32_t)p.page * D, f);
+                else
+                  tma_load_3d(smem + C::kOffRawK + s * C::kRawBytes + pl * p.page * D, &tk, f, 0, 0, (int)plane);
+                bulk_load(smem + C::kOffCode + (v ? C::kRawK + s : s) * kTileKeys + pl * p.page,
+                          (v ? p.v_scale : p.k_scale) + plane * p.page, (uint32_t)p.page, f);
               }
             } else {
               const uint32_t s = sc % ST;
@@ -227,21 +241,50 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       }
     } else if (warp == 1 && lane == 0) {
       // ============ MMA issue ============
-      constexpr uint32_t id_s = idesc_bf16(128, 128, false, false), id_o = idesc_bf16(128, D, false, true);
-      uint32_t sc = 0, slot = 0, np[2] = {0, 0}, nq[2] = {0, 0};
-      // S_w = Q_w K^T from the stage of number k
-      auto issue_s = [&](int w, uint32_t k) {
-        const uint32_t a = sb + w * C::kQTile, b = sb + C::kOffRing + (k % ST) * C::kStageBytes;
+      constexpr uint32_t id_s = kF8 ? idesc_f8(128, 128, false, false) : idesc_bf16(128, 128, false, false);
+      constexpr uint32_t id_o = idesc_bf16(128, D, false, true);
+      uint32_t g = 0, slot = 0, np[2] = {0, 0}, nq[2] = {0, 0};  // g: cache tiles so far
+      // stages of tile g's keys and values
+      auto k_stage = [](uint32_t t) { return kF8 ? t % C::kRawK : 2 * t % ST; };
+      auto v_stage = [](uint32_t t) { return kF8 ? t % ST : (2 * t + 1) % ST; };
+      auto k_landed = [&](uint32_t t) -> bool {
+        if (!(kF8 ? wait_bar(&bars->rawk_full[k_stage(t)], (t / C::kRawK) & 1u, abort)
+                  : wait_bar(&bars->full[k_stage(t)], (2 * t / ST) & 1u, abort)))
+          return false;
+        tc_fence_after();
+        return true;
+      };
+      auto v_landed = [&](uint32_t t) -> bool {
+        if (!wait_bar(&bars->full[v_stage(t)], (kF8 ? t / ST : (2 * t + 1) / ST) & 1u, abort)) return false;
+        tc_fence_after();
+        return true;
+      };
+      // S_w = Q_w K^T
+      auto issue_s = [&](int w, uint32_t t) {
+        const uint32_t a = sb + w * C::kQTile, d = tmem + C::kColS + 128 * w;
+        if constexpr (kF8) {  // both parts of q against the same keys
+          const uint32_t b = sb + C::kOffRawK + k_stage(t) * C::kRawBytes;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
-          umma_bf16(tmem + C::kColS + 128 * w, desc_sw128(a + off, 16, 1024), desc_sw128(b + off, 16, 1024), id_s, ks > 0);
+          for (int ks = 0; ks < 2 * (D / 32); ++ks) {
+            const uint32_t k = ks % (D / 32) * 32, q = a + ks / (D / 32) * (128 * D) + k;
+            if (D == 128)
+              umma_f8(d, desc_sw128(q, 16, 1024), desc_sw128(b + k, 16, 1024), id_s, ks > 0);
+            else
+              umma_f8(d, desc_sw64(q, 16, 512), desc_sw64(b + k, 16, 512), id_s, ks > 0);
+          }
+        } else {
+          const uint32_t b = sb + C::kOffRing + k_stage(t) * C::kStageBytes;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
+            umma_bf16(d, desc_sw128(a + off, 16, 1024), desc_sw128(b + off, 16, 1024), id_s, ks > 0);
+          }
         }
         umma_commit(&bars->s_ready[w]);
       };
       // O_w (+)= P_w V
-      auto issue_o = [&](int w, uint32_t k, bool first) -> bool {
-        const uint32_t b = sb + C::kOffRing + (k % ST) * C::kStageBytes, ph = np[w]++ & 1u;
+      auto issue_o = [&](int w, uint32_t t, bool first) -> bool {
+        const uint32_t b = sb + C::kOffRing + v_stage(t) * C::kStageBytes, ph = np[w]++ & 1u;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
           if (ks % 4 == 0) {  // 64 keys' weights at a time
@@ -253,11 +296,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         }
         return true;
       };
-      auto landed = [&](uint32_t k) -> bool {
-        if (!wait_bar(&bars->full[k % ST], (k / ST) & 1u, abort)) return false;
-        tc_fence_after();
-        return true;
-      };
+      auto k_release = [&](uint32_t t) { umma_commit(kF8 ? &bars->rawk_empty[k_stage(t)] : &bars->empty[k_stage(t)]); };
       for (bool ok = true; ok;) {
         const int si = slot % kItems;
         if (!wait_bar(&bars->item_full[si], (slot / kItems) & 1u, abort)) break;
@@ -266,42 +305,43 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         if (it.kind < 0) break;
         ++slot;
         const int n = it.j1 - it.j0, n0 = last_tile(it, p.G, 0) - it.j0, n1 = last_tile(it, p.G, 1) - it.j0;
-        // tile j of the item: K at stage number sc + 2 j, V behind it
-        if (!(ok = landed(sc))) break;
+        if (!(ok = k_landed(g))) break;
         for (int w = 0; w < 2 && ok; ++w) {
           if ((w ? n1 : n0) <= 0) continue;
           ok = wait_bar(&bars->q_ready[w], nq[w]++ & 1u, abort);
-          if (ok) issue_s(w, sc);
+          if (ok) issue_s(w, g);
         }
         if (!ok) break;
-        umma_commit(&bars->empty[sc % ST]);
-        for (int j = 0; j < n && ok; ++j) {
-          const uint32_t kv = sc + 2 * j + 1, kk = kv + 1;
-          ok = landed(kv) && (j + 1 >= n || landed(kk));
-          if (!ok) break;
+        k_release(g);
+        for (int j = 0; j < n && ok; ++j, ++g) {
+          if (!(ok = v_landed(g))) break;
+          bool waited = false;
           for (int w = 0; w < 2 && ok; ++w) {
             const int nw = w ? n1 : n0;
             if (j < nw) {
-              ok = issue_o(w, kv, j == 0);
+              ok = issue_o(w, g, j == 0);
               if (ok && j + 1 == nw) umma_commit(&bars->o_done[w]);
             }
-            if (ok && j + 1 < nw) issue_s(w, kk);
+            if (ok && j + 1 < nw) {
+              ok = waited || k_landed(g + 1);
+              waited = true;
+              if (ok) issue_s(w, g + 1);
+            }
           }
           if (!ok) break;
-          umma_commit(&bars->empty[kv % ST]);
-          if (j + 1 < n) umma_commit(&bars->empty[kk % ST]);
+          umma_commit(&bars->empty[v_stage(g)]);
+          if (j + 1 < n) k_release(g + 1);
         }
-        sc += 2 * n;
       }
     }
   } else if (warp < 12) {
     // ============ softmax: row tile w, thread = row ============
-    regs_inc<kF8 ? 184 : 208>();
+    regs_inc<kF8 ? 192 : 208>();
     const int w = warp >= 8 ? 1 : 0, q4 = warp & 3;
     const int lrow = 32 * q4 + lane, row = 128 * w + lrow;
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
     const uint32_t tS = tmem + C::kColS + 128 * w + lane_base, tO = tmem + C::kColO + D * w + lane_base;
-    uint32_t sc = 0, slot = 0, ns = 0, nd = 0;
+    uint32_t g = 0, slot = 0, ns = 0, nd = 0;  // g: cache tiles so far
     const uint32_t inv_g = (65535u + p.G) / p.G;  // row / G is row * inv_g >> 16 for row, G <= 256
     // a row's place among the item's rows of q and o, in elements
     auto row_at = [&](const Item &it, int r) -> size_t {
@@ -325,8 +365,19 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
           x[k] = r < nrow ? __ldg(reinterpret_cast<const uint4 *>(p.q + row_at(it, r)) + c) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int k = 0; k < 16 / kPer; ++k)
-          sts128(sb + w * C::kQTile + sw128_offset(32 * q4 + 16 * h + k * kPer + lane / kLanes, c * 8, 128), x[k]);
+        for (int k = 0; k < 16 / kPer; ++k) {
+          const int r = 32 * q4 + 16 * h + k * kPer + lane / kLanes;
+          if constexpr (kF8) {
+            uint2 hi, lo;
+            const float scale = split_q<kLanes>(x[k], hi, lo);
+            if (c == 0) s_qs[128 * w + r] = scale * p.c;
+            const uint32_t ch = c >> 1, at = (D == 128 ? r * 128u + ((ch ^ (r & 7u)) << 4) : r * 64u + ((ch ^ ((r >> 1) & 3u)) << 4)) + (c & 1) * 8;
+            *reinterpret_cast<uint2 *>(smem + w * C::kQTile + at) = hi;
+            *reinterpret_cast<uint2 *>(smem + w * C::kQTile + 128 * D + at) = lo;
+          } else {
+            sts128(sb + w * C::kQTile + sw128_offset(r, c * 8, 128), x[k]);
+          }
+        }
       }
       fence_proxy_async_smem();
       warp_arrive(&bars->q_ready[w]);
@@ -344,6 +395,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       const int lim = it.pos0 + (int)((uint32_t)row * inv_g >> 16);  // the row's last key
       const int first_lim = it.pos0 + (128 * w) / p.G;      // the first row's
       const bool zero0 = last_tile(it, p.G, 0) == it.j1;    // tile 0 looks at the last cache tile
+      const float c = kF8 ? s_qs[row] : p.c;                // written by this warp
       float m = -INFINITY, l = 0.f;
       for (int jj = 0; jj < nw; ++jj) {
         const int j = it.j0 + jj;
@@ -352,6 +404,18 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         float s[128];
         tmem_ld32x2(tS, tS + 32, *reinterpret_cast<float(*)[32]>(s), *reinterpret_cast<float(*)[32]>(s + 32));
         tmem_ld32x2(tS + 64, tS + 96, *reinterpret_cast<float(*)[32]>(s + 64), *reinterpret_cast<float(*)[32]>(s + 96));
+        if constexpr (kF8) {  // the keys' scales
+          const uint32_t ss = (g + jj) % C::kScaleSlots;
+          if (!(ok = wait_bar_warp(&bars->scale_ready[ss], ((g + jj) / C::kScaleSlots) & 1u, abort))) break;
+          const float4 *ks = reinterpret_cast<const float4 *>(smem + C::kOffScale + ss * kTileKeys * 4);
+#pragma unroll
+          for (int k = 0; k < 128; k += 4) {
+            const float4 v = ks[k / 4];
+            const float2 a = __fmul2_rn(make_float2(s[k], s[k + 1]), make_float2(v.x, v.y));
+            const float2 b = __fmul2_rn(make_float2(s[k + 2], s[k + 3]), make_float2(v.z, v.w));
+            s[k] = a.x, s[k + 1] = a.y, s[k + 2] = b.x, s[k + 3] = b.y;
+          }
+        }
         if (j * kTileKeys + kTileKeys - 1 > first_lim) {
           const int left = lim - j * kTileKeys;             // columns 0 .. left are seen
 #pragma unroll
@@ -367,7 +431,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
           }
 #pragma unroll
           for (int u = 0; u < 4; ++u) a[u] = fmaxf(a[u], s[124 + u]);
-          mt = fmaxf(max3(a[0], a[1], a[2]), a[3]) * p.c;
+          mt = fmaxf(max3(a[0], a[1], a[2]), a[3]) * c;
         }
         const bool need = mt > m + kSlack;
         if (__any_sync(0xffffffffu, need)) {
@@ -389,7 +453,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
           }
         }
         const float ms = m == -INFINITY ? 0.f : m;
-        const float2 c2 = make_float2(p.c, p.c), m2 = make_float2(-ms, -ms);
+        const float2 c2 = make_float2(c, c), m2 = make_float2(-ms, -ms);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -404,7 +468,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
           }
           if (h == 0 && jj == nw - 1) {
             // the row tile's last cache tile: its values have landed; rows behind the cache's end become zeros
-            const uint32_t vs = sc + 2 * jj + 1;
+            const uint32_t vs = kF8 ? g + jj : 2 * (g + jj) + 1;
             if (!(ok = wait_bar_warp(&bars->full[vs % ST], (vs / ST) & 1u, abort))) break;
             if (!kF8 && j == it.j1 - 1 && (w == 0 || !zero0) && j * kTileKeys + lrow >= end) {
               const uint32_t a = sb + C::kOffRing + (vs % ST) * C::kStageBytes + lrow * 128;
@@ -424,7 +488,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
       if (!ok) break;
-      sc += 2 * n;
+      g += n;
       // ---- the next item's q, before this item's outputs
       ++slot;
       if (!(ok = wait_bar_warp(&bars->item_full[slot % kItems], (slot / kItems) & 1u, abort))) break;
@@ -437,37 +501,43 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         if (!(ok = wait_bar_warp(&bars->o_done[w], nd++ & 1u, abort))) break;
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        // outputs through shared memory, 32 channels of the warp's 32 rows at a
-        // time, so that 4 lanes write 64 contiguous bytes of a row
-        const uint32_t stage = sb + C::kOffOut + (warp - 4) * 2048;
-        __nv_bfloat16 *dst[4];
-        bool put[4];
+        // outputs through shared memory, kOutCols channels of the warp's 32 rows at
+        // a time, so that neighbouring lanes write neighbouring bytes of a row
+        constexpr int kChunks = C::kOutCols / 8, kRows = 32 / kChunks;  // 16-byte chunks of a row; rows a store
+        const uint32_t stage = sb + C::kOffOut + (warp - 4) * (32 * C::kOutCols * 2);
+        auto at = [&](int r, int ch) {
+          return stage + r * (C::kOutCols * 2) + ((ch ^ ((r >> (kChunks == 4 ? 1 : 2)) & (kChunks - 1))) << 4);
+        };
+        __nv_bfloat16 *dst[kChunks];
+        bool put[kChunks];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 128 * w + 32 * q4 + 8 * i + (lane >> 2);
+        for (int i = 0; i < kChunks; ++i) {
+          const int r = 128 * w + 32 * q4 + kRows * i + lane / kChunks;
           put[i] = it.kind == 0 && !bad && r < it.ntok * p.G;
-          dst[i] = p.o + row_at(it, r) + (lane & 3) * 8;
+          dst[i] = p.o + row_at(it, r) + (lane % kChunks) * 8;
         }
 #pragma unroll
         for (int k = 0; k < D; k += 32) {
           float o[32];
           tmem_ld32(tO + k, o);
           if (it.kind == 0) {
-            __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t u[4];
+            for (int k2 = 0; k2 < 32; k2 += C::kOutCols) {
+              __syncwarp();
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                u[x] = l == 0.f ? 0u : pack_bf16(o[e + 2 * x] * inv, o[e + 2 * x + 1] * inv);
-              sts128(stage + lane * 64 + (((e / 8) ^ ((lane >> 1) & 3)) << 4), make_uint4(u[0], u[1], u[2], u[3]));
-            }
-            __syncwarp();
+              for (int e = 0; e < C::kOutCols; e += 8) {
+                uint32_t u[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = 8 * i + (lane >> 2);
-              const uint4 v = lds128(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
-              if (put[i]) *reinterpret_cast<uint4 *>(dst[i] + k) = v;
+                for (int x = 0; x < 4; ++x)
+                  u[x] = l == 0.f ? 0u : pack_bf16(o[k2 + e + 2 * x] * inv, o[k2 + e + 2 * x + 1] * inv);
+                sts128(at(lane, e / 8), make_uint4(u[0], u[1], u[2], u[3]));
+              }
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < kChunks; ++i) {
+                const uint4 v = lds128(at(kRows * i + lane / kChunks, lane % kChunks));
+                if (put[i]) *reinterpret_cast<uint4 *>(dst[i] + k + k2) = v;
+              }
             }
           } else if (has) {
             float4 *part = reinterpret_cast<float4 *>(p.part) + (pslot * (D / 4) + k / 4) * kPrefillRows + row;
@@ -486,14 +556,14 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       it = nx;
     }
   } else if constexpr (kF8) {
-    // ============ e4m3 cache: raw tile -> values times their scale, as the bf16 tile ============
-    regs_dec<80>();
+    // ============ e4m3 cache: the keys' scales as floats; values times their scale, as the bf16 tile ============
+    regs_dec<64>();
     const int ct = tid - 384;
     constexpr int kLanes = D / 16;                   // lanes of a key's row, 16 values each
     constexpr int kKeys = 128 / kLanes;              // keys a pass of the 128 threads takes: 16 or 32
     constexpr int kPass = kTileKeys / kKeys;
     const int c16 = ct % kLanes, k0 = ct / kLanes;   // key of pass i: i kKeys + k0
-    uint32_t sc = 0, slot = 0;
+    uint32_t g = 0, slot = 0;
     for (bool ok = true; ok;) {
       const int si = slot % kItems;
       if (!(ok = wait_bar_warp(&bars->item_full[si], (slot / kItems) & 1u, abort))) break;
@@ -503,54 +573,58 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       warp_arrive(&bars->item_empty[si]);
       if (kind < 0) break;
       ++slot;
-      for (; j < j1 && ok; ++j) {
-#pragma unroll 1
-        for (int v = 0; v < 2; ++v, ++sc) {
-          const uint32_t rs = sc % C::kRawStages, s = sc % ST;
-          if (!(ok = wait_bar_warp(&bars->raw_full[rs], (sc / C::kRawStages) & 1u, abort))) break;
-          const uint32_t raw = sb + C::kOffRaw + rs * C::kRawBytes;
-          const uint8_t *scale = smem + C::kOffScale + rs * kTileKeys;
-          uint4 y[kPass];
-          uint32_t cd[kPass];
+      for (; j < j1; ++j, ++g) {
+        const uint32_t rk = g % C::kRawK, rv = g % C::kRawV, s = g % ST, ss = g % C::kScaleSlots;
+        if (!(ok = wait_bar_warp(&bars->rawk_full[rk], (g / C::kRawK) & 1u, abort))) break;
+        reinterpret_cast<float *>(smem + C::kOffScale)[ss * kTileKeys + ct] = scale_value(smem[C::kOffCode + rk * kTileKeys + ct]);
+        warp_arrive(&bars->rawk_empty[rk]);
+        warp_arrive(&bars->scale_ready[ss]);
+        if (!(ok = wait_bar_warp(&bars->rawv_full[rv], (g / C::kRawV) & 1u, abort))) break;
+        if (!(ok = wait_bar_warp(&bars->empty[s], ((g / ST) & 1u) ^ 1u, abort))) break;
+        const uint32_t raw = sb + C::kOffRawV + rv * C::kRawBytes;
+        const uint8_t *code = smem + C::kOffCode + (C::kRawK + rv) * kTileKeys;
+        const uint32_t base = sb + C::kOffRing + s * C::kStageBytes;
+        const int there = end - j * kTileKeys;              // keys of the tile that are there
 #pragma unroll
-          for (int i = 0; i < kPass; ++i) {
-            const int key = i * kKeys + k0;
+        for (int i0 = 0; i0 < kPass; i0 += 4) {
+          uint4 y[4];
+          uint32_t cd[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = (i0 + i) * kKeys + k0;
             y[i] = lds128(raw + key * D + c16 * 16);
-            cd[i] = scale[key];
-            if (j * kTileKeys + key >= end) {  // not there: whatever was in the stage
+            cd[i] = code[key];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = (i0 + i) * kKeys + k0;
+            if (key >= there) {                             // whatever was in the stage
               y[i] = make_uint4(0, 0, 0, 0);
               cd[i] = 127;
             }
-          }
-          warp_arrive(&bars->raw_empty[rs]);
-          if (!(ok = wait_bar_warp(&bars->empty[s], ((sc / ST) & 1u) ^ 1u, abort))) break;
-          const uint32_t base = sb + C::kOffRing + s * C::kStageBytes;
-#pragma unroll
-          for (int i = 0; i < kPass; ++i) {
             // 2^(code - 127) 2^120 in two factors within bf16's range
-            const int e = (int)cd[i] - 7;                     // exponent of the product, as 120 + code - 127
+            const int e = (int)cd[i] - 7;                   // exponent of the product, as 120 + code - 127
             const int e1 = min(e, 127), e2 = e - e1;
             const uint32_t f1 = cd[i] == 255 ? 0x7fff7fffu : (uint32_t)(e1 + 127) * 0x00800080u;
-            const uint32_t f2 = (uint32_t)(e2 + 127) * 0x00800080u;
             const uint32_t src[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
             uint32_t o[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              o[2 * k] = mul_bf16x2(e4m3x2_bf16_small(src[k] & 0xffffu), f1);
+              o[2 * k] = mul_bf16x2(e4m3x2_bf16_small(src[k]), f1);
               o[2 * k + 1] = mul_bf16x2(e4m3x2_bf16_small(src[k] >> 16), f1);
             }
             if (e2 > 0) {
+              const uint32_t f2 = (uint32_t)(e2 + 127) * 0x00800080u;
 #pragma unroll
               for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], f2);
             }
-            const int key = i * kKeys + k0;
-            const uint32_t a = base + sw128_offset(key, c16 * 16, 128), b = base + sw128_offset(key, c16 * 16 + 8, 128);
-            sts128(a, make_uint4(o[0], o[1], o[2], o[3]));
-            sts128(b, make_uint4(o[4], o[5], o[6], o[7]));
+            sts128(base + sw128_offset(key, c16 * 16, 128), make_uint4(o[0], o[1], o[2], o[3]));
+            sts128(base + sw128_offset(key, c16 * 16 + 8, 128), make_uint4(o[4], o[5], o[6], o[7]));
           }
-          fence_proxy_async_smem();
-          warp_arrive(&bars->full[s]);
         }
+        warp_arrive(&bars->rawv_empty[rv]);
+        fence_proxy_async_smem();
+        warp_arrive(&bars->full[s]);
       }
     }
   }
@@ -568,10 +642,15 @@ template <int D, bool kF8>
 cudaError_t launch(const AttnParams &p, const void *k_cache, const void *v_cache, int ctas, cudaStream_t stream) {
   using C = Cfg<D, kF8>;
   CUtensorMap tk = {}, tv = {};
-  if (!kF8) {
-    const long long dims[3] = {D, p.page, p.P > 0 ? (long long)p.P * p.Hkv : 1};
+  const long long dims[3] = {D, p.page, p.P > 0 ? (long long)p.P * p.Hkv : 1};
+  if (p.P == 0) k_cache = v_cache = p.q;  // an empty pool: nothing is ever loaded
+  if (kF8) {
+    const int box[3] = {D, p.page, 1};
+    if (!encode_3d_map_swizzled(&tk, k_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, dims, box,
+                                D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
+  } else {
     const int box[3] = {64, p.page, 1};
-    if (p.P == 0) k_cache = v_cache = p.q;  // an empty pool: nothing is ever loaded
     if (!encode_3d_map(&tk, k_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dims, box, true) ||
         !encode_3d_map(&tv, v_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dims, box, true))
       return cudaErrorInvalidValue;
@@ -579,7 +658,7 @@ cudaError_t launch(const AttnParams &p, const void *k_cache, const void *v_cache
   auto kernel = prefill_kernel<D, kF8>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<ctas, C::kThreads, C::kSmem, stream>>>(tk, tv, p, (const uint8_t *)k_cache, (const uint8_t *)v_cache);
+  kernel<<<ctas, C::kThreads, C::kSmem, stream>>>(tk, tv, p, (const uint8_t *)v_cache);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_merge<D, kPrefillRows, false>(p, ctas, stream);
 }

@@ -1,0 +1,85 @@
+// paged_tc.cuh -- device helpers of the two paged-attention kernels: the
+// e4m3 tensor-core instruction, its operands' descriptors, and the split of a
+// query row into e4m3 parts.
+#pragma once
+
+#include "paged.cuh"
+#include "sm100.cuh"
+
+namespace glinattn {
+namespace paged {
+
+using sm100::smem_u32;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// D[tmem] (+)= A[smem] B[smem], e4m3 x e4m3 -> fp32.
+__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+// 64-byte swizzle: rows of 64 bytes, 8-row groups 512 bytes apart (layout type 4).
+__device__ __forceinline__ uint64_t desc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)4 << 61;
+  return d;
+}
+
+// 8 bf16 of a query row (kLanes lanes hold the row) as two e4m3 parts of 2^-e
+// times the value, e bringing the row's largest element into [128, 256); returns
+// 2^e.  bf16's 8 bits are 4 + 4, so the parts are exact but for elements below
+// 2^-10 of the row's largest, where a step is 2^-16 of it.  An infinite or NaN
+// element becomes NaN.
+template <int kLanes>
+__device__ __forceinline__ float split_q(const uint4 &x, uint2 &hi, uint2 &lo) {
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+  float f[8], am = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f[2 * k] = __uint_as_float(u[k] << 16);
+    f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (fabsf(f[k]) <= 3.4e38f) am = fmaxf(am, fabsf(f[k]));
+    else f[k] = __int_as_float(0x7fffffff);
+  }
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+  const int e = min(max((int)(__float_as_uint(am) >> 23) - 127 - 7, -100), 120);
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float a = f[2 * k] * down, b = f[2 * k + 1] * down;
+    h[k] = to_e4m3x2(a, b);
+    const float2 y = e4m3x2(h[k]);
+    l[k] = to_e4m3x2(a - y.x, b - y.y);
+  }
+  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+  return __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
+}  // namespace paged
+}  // namespace glinattn

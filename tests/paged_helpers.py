@@ -59,9 +59,10 @@ def attention_tolerance(c, q, o, a, scale):
     """Elementwise bound: the output's rounding (half a bf16 step of |o|), the
     weights' rounding (half a bf16 step of sum p |v|), and the error of the
     scores.  A score is an fp32 sum of d products, off by at most d 2^-24 times
-    sum |q| |k|; a query split into two e4m3 parts (4 + 4 bits hold bf16's 8;
-    below 2^-14 of the row's largest element the low part's step is 2^-22 of
-    it) adds at most 2^-22 max |q| sum |k|.  An error of ds in the scores moves
+    sum |q| |k|; a query split into two e4m3 parts (4 + 4 bits hold bf16's 8),
+    scaled so that its largest element is at least 2^7, is off by half the
+    smallest e4m3 step, 2^-10, or 2^-17 max |q|, at most: 2^-17 max |q| sum |k|.
+    An error of ds in the scores moves
     an output by at most 2 ds sum p |v|."""
     qa = np.abs(q)
     ds = 0.0
@@ -75,6 +76,6 @@ def attention_tolerance(c, q, o, a, scale):
             for h in range(q.shape[1]):
                 ka = np.abs(k[:pos + 1, h // group])
                 ds = max(ds, float((ka @ qa[i, h]).max()) * c["d"] * 2.0 ** -24 +
-                         float(ka.sum(-1).max()) * float(qa[i, h].max()) * 2.0 ** -22)
+                         float(ka.sum(-1).max()) * float(qa[i, h].max()) * 2.0 ** -17)
     ds = ds * scale + 2.0 ** -20  # and the exponential's own error
     return HALF_BF16 * np.abs(o) + (HALF_BF16 + 2 * ds) * a + 1e-30
