@@ -351,33 +351,47 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     // q of the warp's 32 rows into shared memory, D / 8 lanes a row; rows past
     // the last are zero.  Only for a row tile that has work in the item: its
     // softmax warps then wait for the MMA warp's answer, so that q_ready is
-    // never a phase ahead of its reader.
-    auto load_q = [&](const Item &it) {
-      if (it.kind < 0 || last_tile(it, p.G, w) <= it.j0) return;
+    // never a phase ahead of its reader.  bf16 rows are copied asynchronously
+    // (fetch_q once S of the last tile is there, q_fetched behind that tile's weights).
+    auto fetch_q = [&](const Item &it) {
+      if (kF8 || it.kind < 0 || last_tile(it, p.G, w) <= it.j0) return;
       constexpr int kLanes = D / 8, kPer = 32 / kLanes;
       const int c = lane % kLanes, nrow = it.ntok * p.G;
+#pragma unroll 1
+      for (int k = 0; k < 32; k += kPer) {
+        const int r = 32 * q4 + k + lane / kLanes;
+        const bool has = 128 * w + r < nrow;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sb + w * C::kQTile + sw128_offset(r, c * 8, 128)),
+                     "l"(p.q + (has ? row_at(it, 128 * w + r) + c * 8 : 0)), "r"(has ? 16 : 0)
+                     : "memory");
+      }
+    };
+    auto q_fetched = [&](const Item &it) {
+      if (it.kind < 0 || last_tile(it, p.G, w) <= it.j0) return;
+      if constexpr (kF8) {
+        constexpr int kLanes = D / 8, kPer = 32 / kLanes;
+        const int c = lane % kLanes, nrow = it.ntok * p.G;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint4 x[16 / kPer];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint4 x[16 / kPer];
+          for (int k = 0; k < 16 / kPer; ++k) {
+            const int r = 128 * w + 32 * q4 + 16 * h + k * kPer + lane / kLanes;
+            x[k] = r < nrow ? __ldg(reinterpret_cast<const uint4 *>(p.q + row_at(it, r)) + c) : make_uint4(0, 0, 0, 0);
+          }
 #pragma unroll
-        for (int k = 0; k < 16 / kPer; ++k) {
-          const int r = 128 * w + 32 * q4 + 16 * h + k * kPer + lane / kLanes;
-          x[k] = r < nrow ? __ldg(reinterpret_cast<const uint4 *>(p.q + row_at(it, r)) + c) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int k = 0; k < 16 / kPer; ++k) {
-          const int r = 32 * q4 + 16 * h + k * kPer + lane / kLanes;
-          if constexpr (kF8) {
+          for (int k = 0; k < 16 / kPer; ++k) {
+            const int r = 32 * q4 + 16 * h + k * kPer + lane / kLanes;
             uint2 hi, lo;
             const float scale = split_q<kLanes>(x[k], hi, lo);
             if (c == 0) s_qs[128 * w + r] = scale * p.c;
             const uint32_t ch = c >> 1, at = (D == 128 ? r * 128u + ((ch ^ (r & 7u)) << 4) : r * 64u + ((ch ^ ((r >> 1) & 3u)) << 4)) + (c & 1) * 8;
             *reinterpret_cast<uint2 *>(smem + w * C::kQTile + at) = hi;
             *reinterpret_cast<uint2 *>(smem + w * C::kQTile + 128 * D + at) = lo;
-          } else {
-            sts128(sb + w * C::kQTile + sw128_offset(r, c * 8, 128), x[k]);
           }
         }
+      } else {
+        asm volatile("cp.async.wait_all;" ::: "memory");
       }
       fence_proxy_async_smem();
       warp_arrive(&bars->q_ready[w]);
@@ -386,7 +400,8 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     Item it;
     if (ok) {
       it = bars->item[0];
-      load_q(it);
+      fetch_q(it);
+      q_fetched(it);
     }
     while (ok && it.kind >= 0) {
       const int si = slot % kItems;
@@ -397,6 +412,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       const bool zero0 = last_tile(it, p.G, 0) == it.j1;    // tile 0 looks at the last cache tile
       const float c = kF8 ? s_qs[row] : p.c;                // written by this warp
       float m = -INFINITY, l = 0.f;
+      Item nx = it;
       for (int jj = 0; jj < nw; ++jj) {
         const int j = it.j0 + jj;
         if (!(ok = wait_bar_warp(&bars->s_ready[w], ns++ & 1u, abort))) break;
@@ -404,6 +420,12 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         float s[128];
         tmem_ld32x2(tS, tS + 32, *reinterpret_cast<float(*)[32]>(s), *reinterpret_cast<float(*)[32]>(s + 32));
         tmem_ld32x2(tS + 64, tS + 96, *reinterpret_cast<float(*)[32]>(s + 64), *reinterpret_cast<float(*)[32]>(s + 96));
+        if (jj == nw - 1) {  // the last S of the item's q is here: the next item's q may come
+          const uint32_t ns_ = slot + 1;
+          if (!(ok = wait_bar_warp(&bars->item_full[ns_ % kItems], (ns_ / kItems) & 1u, abort))) break;
+          nx = bars->item[ns_ % kItems];
+          fetch_q(nx);
+        }
         if constexpr (kF8) {  // the keys' scales
           const uint32_t ss = (g + jj) % C::kScaleSlots;
           if (!(ok = wait_bar_warp(&bars->scale_ready[ss], ((g + jj) / C::kScaleSlots) & 1u, abort))) break;
@@ -441,7 +463,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
           l *= f;
           m = mn;
           if (jj > 0) {
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < D; k += 32) {
               float o[32];
               uint32_t u[32];
@@ -491,9 +513,12 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       g += n;
       // ---- the next item's q, before this item's outputs
       ++slot;
-      if (!(ok = wait_bar_warp(&bars->item_full[slot % kItems], (slot / kItems) & 1u, abort))) break;
-      const Item nx = bars->item[slot % kItems];
-      load_q(nx);
+      if (nw <= 0) {
+        if (!(ok = wait_bar_warp(&bars->item_full[slot % kItems], (slot / kItems) & 1u, abort))) break;
+        nx = bars->item[slot % kItems];
+        fetch_q(nx);
+      }
+      q_fetched(nx);
       const int bad = bars->bad[si];
       const bool has = row < it.ntok * p.G;
       const size_t pslot = (size_t)(2 * blockIdx.x + (it.kind == 1 ? 1 : 0));
@@ -516,7 +541,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
           put[i] = it.kind == 0 && !bad && r < it.ntok * p.G;
           dst[i] = p.o + row_at(it, r) + (lane % kChunks) * 8;
         }
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < D; k += 32) {
           float o[32];
           tmem_ld32(tO + k, o);

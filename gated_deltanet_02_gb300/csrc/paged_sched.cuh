@@ -3,7 +3,8 @@
 //
 // The work of a call is a row of units, one unit being the 128 keys of one
 // cache tile for one item; an item is (request, key / value head, tile of query
-// tokens), and its units are the cache tiles that its last token sees (one at
+// tokens), and its units are kItemCost for its own beginning and end (reading q,
+// writing outputs) and then the cache tiles that its last token sees (one at
 // least).  Requests come in order, then heads, then token tiles.  CTA c takes
 // units [c n, (c + 1) n), n = ceil(units / CTAs): every SM reads the same number
 // of cache tiles whatever the lengths are, and a long request is shared by many.
@@ -23,6 +24,11 @@ namespace glinattn {
 namespace paged {
 
 constexpr int kTileKeys = 128;
+// What an item costs beside its cache tiles, in cache tiles: about 3 us against
+// 1.6 us a tile with 256 rows (without it the SMs that get many short items end last:
+// packed prompts of 200 .. 4001 tokens take TPK us instead of 241 us); with
+// few rows a tile is bound by HBM and hides the next item's beginning.
+constexpr int kItemCostMany = 2, kItemCostFew = 0;
 
 // Everything that the attention kernels are told.
 struct AttnParams {
@@ -63,16 +69,15 @@ __device__ __forceinline__ Req load_req(const AttnParams &p, int r) {
 }
 
 // Units of token tile t: the cache tiles up to its last token's position.
-__device__ __forceinline__ int tile_units(const AttnParams &p, const Req &x, int t) {
-  const long long end = (long long)(t + 1) * p.tp;
-  const long long vis = x.pos0 + (end < x.q_len ? end : (long long)x.q_len);
+__device__ __forceinline__ int tile_units(int tp, int pos0, int q_len, int t) {
+  const long long end = (long long)(t + 1) * tp;
+  const long long vis = pos0 + (end < q_len ? end : (long long)q_len);
   return vis <= kTileKeys ? 1 : (int)((vis + kTileKeys - 1) / kTileKeys);
 }
 
-// sum of floor((a i + b) / m) over i in [0, n), by the Euclidean recursion;
-// T holds a n + b.
-template <typename T>
-__device__ inline long long floor_sum(T n, unsigned m, unsigned a, unsigned b) {
+// sum of floor((a i + b) / m) over i in [0, n), by the Euclidean recursion, for
+// n < 2^24 and m <= 128 (then a n + b stays below 2^32 once a and b are reduced).
+__device__ inline long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
   long long s = 0;
   while (true) {
     if (a >= m) {
@@ -83,10 +88,10 @@ __device__ inline long long floor_sum(T n, unsigned m, unsigned a, unsigned b) {
       s += (long long)n * (b / m);
       b %= m;
     }
-    const T y = (T)a * n + b;
+    const unsigned y = a * n + b;
     if (y < m) return s;
     n = y / m;
-    b = (unsigned)(y % m);
+    b = y % m;
     const unsigned x = m;
     m = a;
     a = x;
@@ -99,24 +104,22 @@ __device__ __forceinline__ long long div_pos(long long a, long long b) {
   return ((unsigned long long)(a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
-// Units of the tiles before tile t (t = ntile: of one kv head of the request).
-__device__ inline long long units_before(const AttnParams &p, const Req &x, int t) {
-  long long s = 0;
+// Units and the items' own cost of the tiles before tile t (t = ntile: of one
+// kv head of the request).  Not inlined: the planning code runs once per CTA, and
+// what it costs is mostly the fetching of its instructions.
+static __device__ __noinline__ long long units_before(int tp, int cost, int pos0, int q_len, int ntile, int t) {
+  long long s = (long long)t * cost;
   int n = t;
-  if (t == x.ntile && t > 0) {
-    s = tile_units(p, x, t - 1);  // the last tile may be a short one
+  if (t == ntile && t > 0) {  // the last tile may be a short one
+    s += tile_units(tp, pos0, q_len, t - 1);
     n = t - 1;
   }
   if (n <= 0) return s;
-  const long long room = (long long)kTileKeys - x.pos0;  // tiles that end within the first cache tile: one unit
-  const int z = room < p.tp ? 0 : (int)min((long long)n, div_pos(room, p.tp));
+  const long long room = (long long)kTileKeys - pos0;  // tiles that end within the first cache tile: one unit
+  const int z = room < tp ? 0 : (int)min((long long)n, div_pos(room, tp));
   s += z;
-  if (n > z) {
-    // the first term's tiles end at b - 127; a n + b is below 2^32 for n < 2^22 (a < 128 after the first step)
-    const unsigned b = (unsigned)(x.pos0 + (long long)(z + 1) * p.tp + kTileKeys - 1);
-    s += n < (1 << 22) ? floor_sum<unsigned>(n - z, kTileKeys, (unsigned)p.tp, b)
-                       : floor_sum<unsigned long long>(n - z, kTileKeys, (unsigned)p.tp, b);
-  }
+  // the tiles are of more than 128 rows, and a call has at most 2^30 rows: n < 2^24
+  if (n > z) s += floor_sum((unsigned)(n - z), kTileKeys, (unsigned)tp, (unsigned)(pos0 + (long long)(z + 1) * tp + kTileKeys - 1));
   return s;
 }
 
@@ -139,19 +142,25 @@ struct PlanShared {
 template <bool kOneTile>
 __device__ inline Plan make_plan(const AttnParams &p, PlanShared *sh) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
-  auto head_units = [&](int r, bool flag) -> long long {
-    if (r >= p.R) return 0;
-    const Req x = load_req(p, r);
-    if (!x.ok) {
-      if (flag && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_BAD_COUNT);
-      return 0;
+  Plan pl;
+  pl.r = 0;
+  pl.per = pl.u0 = pl.u1 = pl.off = pl.per_head = 0;
+  // Passes over the requests, nt at a time: the total (pass 0), then the request
+  // that holds the CTA's first unit.  With at most nt requests one pass does both.
+  long long before = 0;
+  bool search = p.R <= nt;
+  for (int base = 0;; base += nt) {
+    const int r = base + tid;
+    long long head = 0;
+    if (r < p.R) {
+      const Req x = load_req(p, r);
+      if (!x.ok && blockIdx.x == 0 && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_BAD_COUNT);
+      if (x.ntile > 0)
+        head = kOneTile ? kItemCostFew + tile_units(p.tp, x.pos0, x.q_len, 0)
+                        : units_before(p.tp, kItemCostMany, x.pos0, x.q_len, x.ntile, x.ntile);
     }
-    if (x.ntile == 0) return 0;
-    return kOneTile ? (long long)tile_units(p, x, 0) : units_before(p, x, x.ntile);
-  };
-  // the CTA's sum (all) and this thread's inclusive prefix (upto)
-  auto scan = [&](long long u, long long &upto, long long &all) {
-    upto = u;
+    const long long u = head * p.Hkv;
+    long long upto = u;  // the CTA's inclusive scan
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, upto, o);
@@ -159,46 +168,37 @@ __device__ inline Plan make_plan(const AttnParams &p, PlanShared *sh) {
     }
     if (lane == 31) sh->scan[warp] = upto;
     __syncthreads();
-    all = 0;
+    long long all = 0;
     for (int w = 0; w < nw; ++w) {
       if (w < warp) upto += sh->scan[w];
       all += sh->scan[w];
     }
-    __syncthreads();
-  };
-  // up to one request a thread: one scan serves for the total and for the search
-  long long mine = head_units(tid, blockIdx.x == 0), upto, total;
-  long long rest = 0;
-  for (int r = tid + nt; r < p.R; r += nt) rest += head_units(r, blockIdx.x == 0);
-  scan(mine * p.Hkv, upto, total);
-  const long long first_chunk = total;
-  if (p.R > nt) {
-    long long a, b;
-    scan(rest * p.Hkv, a, b);
-    total += b;
-  }
-  Plan pl;
-  pl.per = max(1ll, div_pos(total + gridDim.x - 1, gridDim.x));
-  pl.u0 = min((long long)blockIdx.x * pl.per, total);
-  pl.u1 = min(pl.u0 + pl.per, total);
-  pl.r = 0;
-  pl.off = pl.per_head = 0;
-  if (pl.u0 >= pl.u1) return pl;
-  long long before = 0, all = first_chunk;
-  for (int base = 0;;) {
-    const long long u = mine * p.Hkv, a = before + upto - u;
-    if (a <= pl.u0 && pl.u0 < a + u) {
-      sh->first_r = base + tid;
-      sh->first_off = pl.u0 - a;
-      sh->first_per_head = mine;
+    const bool last = base + nt >= p.R;
+    if (search ? base == 0 && p.R <= nt : last) {  // the total is known
+      const long long total = before + all;
+      pl.per = max(1ll, div_pos(total + gridDim.x - 1, gridDim.x));
+      pl.u0 = min((long long)blockIdx.x * pl.per, total);
+      pl.u1 = min(pl.u0 + pl.per, total);
     }
+    if (search) {
+      const long long a = before + upto - u;
+      if (a <= pl.u0 && pl.u0 < a + u) {
+        sh->first_r = r;
+        sh->first_off = pl.u0 - a;
+        sh->first_per_head = head;
+      }
+    }
+    __syncthreads();
     before += all;
-    if (before > pl.u0) break;
-    base += nt;
-    mine = head_units(base + tid, false);
-    scan(mine * p.Hkv, upto, all);
+    if (search && (last || before > pl.u0)) break;
+    if (!search && last) {
+      if (pl.u0 >= pl.u1) break;
+      search = true;
+      before = 0;
+      base = -nt;
+    }
   }
-  __syncthreads();
+  if (pl.u0 >= pl.u1) return pl;
   pl.r = sh->first_r;
   pl.off = sh->first_off;
   pl.per_head = sh->first_per_head;
@@ -218,10 +218,11 @@ struct Item {
 // The items of a CTA, in order (run by one warp, all lanes alike).
 template <bool kOneTile>
 struct Walk {
+  static constexpr int kCost = kOneTile ? kItemCostFew : kItemCostMany;
   const AttnParams &p;
   Plan pl;
   Req x;
-  int r, hk, t, off;
+  int r, hk, t, off;      // off: units of the item that are before this CTA
   long long left, at;
 
   __device__ Walk(const AttnParams &p_, const Plan &pl_, int lane) : p(p_), pl(pl_) {
@@ -234,25 +235,25 @@ struct Walk {
     hk = (int)div_pos(pl.off, pl.per_head);
     const long long y = pl.off - hk * pl.per_head;
     if (!kOneTile) {  // the last tile with units_before <= y, 32 ways at a time
-      int lo = 0, n = x.ntile;
-      while (n > 1) {
+      long long before = 0;
+      for (int n = x.ntile; n > 1;) {
         const int step = (n + 31) >> 5;
-        const bool le = lane == 0 || (lane * step < n && units_before(p, x, lo + lane * step) <= y);
-        const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));
-        lo += k * step;
+        const long long u = units_before(p.tp, kCost, x.pos0, x.q_len, x.ntile, min(t + lane * step, x.ntile));
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, lane == 0 || (lane * step < n && u <= y)));
+        before = __shfl_sync(0xffffffffu, u, k);
+        t += k * step;
         n = min(step, n - k * step);
       }
-      t = lo;
-      off = (int)(y - units_before(p, x, t));
+      off = (int)(y - before);
     } else {
       off = (int)y;
     }
   }
 
-  // The next item; false when the CTA's units are used up.
+  // The next item with cache tiles in this CTA; false when there is none.
   __device__ bool next(Item &it, int lane) {
     if (left <= 0) return false;
-    const int units = tile_units(p, x, t);
+    const int units = kCost + tile_units(p.tp, x.pos0, x.q_len, t);
     const int take = (int)min((long long)(units - off), left);
     it.r = r;
     it.hk = hk;
@@ -260,11 +261,12 @@ struct Walk {
     it.row0 = x.s0 + tok0;
     it.ntok = kOneTile ? x.q_len : min(p.tp, x.q_len - tok0);
     it.pos0 = x.pos0 + tok0;
-    it.j0 = off;
-    it.j1 = off + take;
-    it.kind = off > 0 ? 2 : take == units ? 0 : 1;
+    it.j0 = max(0, off - kCost);
+    it.j1 = max(0, off + take - kCost);
+    if (it.j1 == 0) return false;  // only the item's own cost: it begins in the next CTA
+    it.kind = it.j0 > 0 ? 2 : it.j1 == units - kCost ? 0 : 1;
     if (it.kind == 1 && lane == 0)
-      p.desc[blockIdx.x] = make_int4(it.row0, hk, it.ntok, (int)div_pos(at + units - 1, pl.per));
+      p.desc[blockIdx.x] = make_int4(it.row0, hk, it.ntok, (int)div_pos(at - off + units - 1, pl.per));
     left -= take;
     at += take;
     off = 0;
