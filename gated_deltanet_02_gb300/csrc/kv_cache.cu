@@ -58,6 +58,31 @@ __device__ __forceinline__ uint32_t finite_mag(uint32_t bits16) {
   return a < 0x7f80u ? a : 0u;
 }
 
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {  // a NaN gives way to a number
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Largest finite |x| of a row as bf16 bits; a row is in kLanes lanes, 8 elements
+// each.  Two elements an instruction; rows with infinities (or NaN alone) again
+// with those left out.
+template <int kLanes>
+__device__ __forceinline__ uint32_t row_amax(const uint32_t (&w)[4]) {
+  uint32_t m = max_bf16x2(max_bf16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), max_bf16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) m = max_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  m = max(m & 0xffffu, m >> 16);
+  if (__any_sync(0xffffffffu, m >= 0x7f80u)) {
+    m = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m = max(m, max(finite_mag(w[k]), finite_mag(w[k] >> 16)));
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
+  return m;
+}
+
 // A warp's row: its page and row in the page, or false when nothing is to be moved.
 __device__ __forceinline__ bool locate(const glinattn_kv_args &a, int i, int lane, int &page, int &row) {
   const int r = find_request(a.q_start, a.num_req, i, lane);
@@ -95,47 +120,53 @@ __global__ void __launch_bounds__(32 * kWarps) kv_move_kernel(const glinattn_kv_
   const int lane = threadIdx.x & 31;
   const int i = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (i >= a.num_tok) return;               // whole warps
-  int page = 0, row = 0;
-  if (!locate(a, i, lane, page, row)) return;
   const int H = a.kv_heads, n = 2 * H;      // k rows of every head, then v rows
   const int sub = lane / kLanes, c = lane % kLanes;
-  for (int j0 = 0; j0 < n; j0 += kPer * kRound) {
-    uint4 x[kRound];
-    uint32_t code[kRound];
+  // eight elements of token row j, and their place in the packed arrays
+  auto token_at = [&](int j) {
+    const int h = j < H ? j : j - H;
+    return reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(j < H ? a.k : a.v) + ((size_t)i * H + h) * D + c * 8);
+  };
+  uint4 x[kRound];
+  auto read_tokens = [&](int j0) {
 #pragma unroll
     for (int u = 0; u < kRound; ++u) {
       const int j = j0 + u * kPer + sub;
-      x[u] = make_uint4(0, 0, 0, 0);
-      code[u] = 0;
-      if (j >= n) continue;
-      const int h = j < H ? j : j - H;
-      const size_t tok = ((size_t)i * H + h) * D + c * 8;
-      const size_t cr = ((size_t)page * H + h) * a.page_size + row;
-      if (kAppend) {
-        x[u] = __ldcs(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(j < H ? a.k : a.v) + tok));
-      } else if (kE4m3) {
-        const uint2 y = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint8_t *>(j < H ? a.k_cache : a.v_cache) + cr * D + c * 8);
-        x[u].x = y.x;
-        x[u].y = y.y;
-        code[u] = (j < H ? a.k_scale : a.v_scale)[cr];
-      } else {
-        x[u] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(j < H ? a.k_cache : a.v_cache) + cr * D + c * 8);
+      x[u] = j < n ? __ldcs(token_at(j)) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (kAppend) read_tokens(0);              // in flight while the row is located
+  int page = 0, row = 0;
+  if (!locate(a, i, lane, page, row)) return;
+  for (int j0 = 0; j0 < n; j0 += kPer * kRound) {
+    uint32_t code[kRound];
+    if (kAppend) {
+      if (j0 > 0) read_tokens(j0);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kRound; ++u) {
+        const int j = j0 + u * kPer + sub;
+        x[u] = make_uint4(0, 0, 0, 0);
+        code[u] = 0;
+        if (j >= n) continue;
+        const size_t cr = ((size_t)page * H + (j < H ? j : j - H)) * a.page_size + row;
+        if (kE4m3) {
+          const uint2 y = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint8_t *>(j < H ? a.k_cache : a.v_cache) + cr * D + c * 8);
+          x[u].x = y.x;
+          x[u].y = y.y;
+          code[u] = (j < H ? a.k_scale : a.v_scale)[cr];
+        } else {
+          x[u] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(j < H ? a.k_cache : a.v_cache) + cr * D + c * 8);
+        }
       }
     }
 #pragma unroll
     for (int u = 0; u < kRound; ++u) {
       const int j = j0 + u * kPer + sub;
-      const int h = j < H ? j : j - H;
-      const size_t tok = ((size_t)i * H + h) * D + c * 8;
-      const size_t cr = ((size_t)page * H + h) * a.page_size + row;
+      const size_t cr = ((size_t)page * H + (j < H ? j : j - H)) * a.page_size + row;
       if (kAppend && kE4m3) {
         const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-        uint32_t m = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m = max(m, max(finite_mag(w[k]), finite_mag(w[k] >> 16)));
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const uint32_t sc = scale_code(m);
+        const uint32_t sc = scale_code(row_amax<kLanes>(w));
         const float f = __uint_as_float((254u - sc) << 23);  // 2^-e
         uint32_t q[4];
 #pragma unroll
@@ -158,7 +189,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_move_kernel(const glinattn_kv_
             y = make_uint4(pack_bf16(f0.x * s, f0.y * s), pack_bf16(f1.x * s, f1.y * s), pack_bf16(f2.x * s, f2.y * s),
                            pack_bf16(f3.x * s, f3.y * s));
           }
-          __stcs(reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(j < H ? a.k : a.v) + tok), y);
+          __stcs(token_at(j), y);
         }
       }
     }

@@ -139,6 +139,8 @@ _lib = None
 def library() -> ctypes.CDLL:
     """Load ``libglinattn.so`` (building it first when its sources are newer)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build()
@@ -493,32 +495,43 @@ def glinattn_selective_scan_decode(x, delta, Bm, Cm, A, state_pool, slot_ids, *,
     return y
 
 
+def _check(t, name, dtype, shape, dev):
+    """_need for a tensor that has to be there, with one comparison where all is well."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _need(t, name, dtype, shape, dev)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _cache_dims(k_cache, v_cache, page_table, kv_len, q_start, k_scale, v_scale, dev):
     """The checks that the calls on a paged cache share; (cache dtype, P, Hkv, page, d, R, max_pages)."""
-    if k_cache.dim() != 4:
+    shape = k_cache.shape
+    if len(shape) != 4:
         raise ValueError("k_cache must be [P, Hkv, page, d]")
-    P, Hkv, page, d = k_cache.shape
-    if k_cache.dtype == torch.bfloat16:
+    dtype = k_cache.dtype
+    if dtype is torch.bfloat16:
         code = BF16
         if k_scale is not None or v_scale is not None:
             raise ValueError("k_scale and v_scale belong to an e4m3 cache")
-    elif k_cache.dtype == torch.float8_e4m3fn:
+    elif dtype is torch.float8_e4m3fn:
         code = E4M3
         if k_scale is None or v_scale is None:
             raise ValueError("an e4m3 cache needs k_scale and v_scale")
-        _need(k_scale, "k_scale", torch.uint8, (P, Hkv, page), dev)
-        _need(v_scale, "v_scale", torch.uint8, (P, Hkv, page), dev)
+        _check(k_scale, "k_scale", torch.uint8, shape[:3], dev)
+        _check(v_scale, "v_scale", torch.uint8, shape[:3], dev)
     else:
-        raise TypeError(f"the cache must be bf16 or float8_e4m3fn, got {k_cache.dtype}")
-    _need(k_cache, "k_cache", None, None, dev)
-    _need(v_cache, "v_cache", k_cache.dtype, (P, Hkv, page, d), dev)
+        raise TypeError(f"the cache must be bf16 or float8_e4m3fn, got {dtype}")
+    _check(k_cache, "k_cache", dtype, shape, dev)
+    _check(v_cache, "v_cache", dtype, shape, dev)
     if kv_len.dim() != 1 or page_table.dim() != 2:
         raise ValueError("kv_len must be [R] and page_table [R, max_pages]")
-    R = kv_len.shape[0]
-    _need(kv_len, "kv_len", torch.int32, None, dev)
-    _need(q_start, "q_start", torch.int32, (R + 1,), dev)
-    _need(page_table, "page_table", torch.int32, (R, page_table.shape[1]), dev)
-    return code, P, Hkv, page, d, R, page_table.shape[1]
+    R, max_pages = kv_len.shape[0], page_table.shape[1]
+    _check(kv_len, "kv_len", torch.int32, (R,), dev)
+    _check(q_start, "q_start", torch.int32, (R + 1,), dev)
+    _check(page_table, "page_table", torch.int32, (R, max_pages), dev)
+    return (code, *shape, R, max_pages)
 
 
 def _status_word(dev_status, dev):
@@ -526,12 +539,27 @@ def _status_word(dev_status, dev):
         raise ValueError(f"dev_status must be a 32-bit word on {dev}")
 
 
+def _empty(shape, dtype, dev, stream):
+    """Memory of the stream that the call runs on, so that it is not handed on while the call runs."""
+    if stream is None or dev.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _launch(name, args, stream, dev):
     """One call on the tensors' own device, whichever is current."""
     if dev.type != "cuda":
         raise ValueError(f"the tensors must be on a CUDA device, got {dev}")
-    with torch.cuda.device(dev):
-        _call(name, args, _stream_handle(stream, dev))
+    # the raw handle: a Stream object costs a sixth of a small call
+    handle = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        rc = getattr(library(), name)(args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(library(), name)(args, handle)
+    if rc != 0:
+        raise GlinattnError(rc, name)
 
 
 def glinattn_kv_append(k, v, k_cache, v_cache, page_table, kv_len, q_start, *, k_scale=None, v_scale=None,
@@ -545,11 +573,11 @@ def glinattn_kv_append(k, v, k_cache, v_cache, page_table, kv_len, q_start, *, k
     dev = k.device
     code, P, Hkv, page, d, R, max_pages = _cache_dims(k_cache, v_cache, page_table, kv_len, q_start, k_scale, v_scale, dev)
     n = k.shape[0]
-    _need(k, "k", torch.bfloat16, (n, Hkv, d), dev)
-    _need(v, "v", torch.bfloat16, (n, Hkv, d), dev)
+    _check(k, "k", torch.bfloat16, (n, Hkv, d), dev)
+    _check(v, "v", torch.bfloat16, (n, Hkv, d), dev)
     _status_word(dev_status, dev)
-    a = KvArgs(code, R, n, Hkv, d, page, P, max_pages, _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-               _ptr(v_scale), _ptr(page_table), _ptr(kv_len), _ptr(q_start), _ptr(dev_status))
+    a = KvArgs(code, R, n, Hkv, d, page, P, max_pages, _addr(k), _addr(v), _addr(k_cache), _addr(v_cache), _addr(k_scale),
+               _addr(v_scale), _addr(page_table), _addr(kv_len), _addr(q_start), _addr(dev_status))
     _launch("glinattn_kv_append", a, stream, dev)
     return k_cache, v_cache
 
@@ -568,14 +596,14 @@ def glinattn_kv_gather(k_cache, v_cache, page_table, kv_len, q_start, *, num_tok
             raise ValueError("num_tok is needed when k and v are not given")
         num_tok = (v if k is None else k).shape[0]
     if k is None:
-        k = torch.empty((num_tok, Hkv, d), dtype=torch.bfloat16, device=dev)
+        k = _empty((num_tok, Hkv, d), torch.bfloat16, dev, stream)
     if v is None:
-        v = torch.empty((num_tok, Hkv, d), dtype=torch.bfloat16, device=dev)
-    _need(k, "k", torch.bfloat16, (num_tok, Hkv, d), dev)
-    _need(v, "v", torch.bfloat16, (num_tok, Hkv, d), dev)
+        v = _empty((num_tok, Hkv, d), torch.bfloat16, dev, stream)
+    _check(k, "k", torch.bfloat16, (num_tok, Hkv, d), dev)
+    _check(v, "v", torch.bfloat16, (num_tok, Hkv, d), dev)
     _status_word(dev_status, dev)
-    a = KvArgs(code, R, num_tok, Hkv, d, page, P, max_pages, _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache),
-               _ptr(k_scale), _ptr(v_scale), _ptr(page_table), _ptr(kv_len), _ptr(q_start), _ptr(dev_status))
+    a = KvArgs(code, R, num_tok, Hkv, d, page, P, max_pages, _addr(k), _addr(v), _addr(k_cache), _addr(v_cache),
+               _addr(k_scale), _addr(v_scale), _addr(page_table), _addr(kv_len), _addr(q_start), _addr(dev_status))
     _launch("glinattn_kv_gather", a, stream, dev)
     return k, v
 
@@ -593,20 +621,22 @@ def glinattn_paged_attention(q, k_cache, v_cache, page_table, kv_len, q_start, *
     dev = q.device
     code, P, Hkv, page, d, R, max_pages = _cache_dims(k_cache, v_cache, page_table, kv_len, q_start, k_scale, v_scale, dev)
     n, H = q.shape[0], q.shape[1]
-    _need(q, "q", torch.bfloat16, (n, H, d), dev)
+    _check(q, "q", torch.bfloat16, (n, H, d), dev)
     if o is None:
-        o = torch.empty_like(q)
-    _need(o, "o", torch.bfloat16, (n, H, d), dev)
+        o = _empty((n, H, d), torch.bfloat16, dev, stream)
+    _check(o, "o", torch.bfloat16, (n, H, d), dev)
     _status_word(dev_status, dev)
     a = PagedAttnArgs(code, R, n, H, Hkv, d, page, P, max_pages, n if max_q_len is None else max_q_len,
-                      1.0 / math.sqrt(d) if scale is None else scale, _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                      _ptr(k_scale), _ptr(v_scale), _ptr(page_table), _ptr(kv_len), _ptr(q_start), _ptr(o),
-                      _ptr(dev_status))
-    need = library().glinattn_paged_attention_workspace_size(ctypes.byref(a))
+                      1.0 / math.sqrt(d) if scale is None else scale, _addr(q), _addr(k_cache), _addr(v_cache),
+                      _addr(k_scale), _addr(v_scale), _addr(page_table), _addr(kv_len), _addr(q_start), _addr(o),
+                      _addr(dev_status))
+    need = library().glinattn_paged_attention_workspace_size(a)
     if need:
-        if workspace is None or workspace.numel() * workspace.element_size() < need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        a.workspace = _ptr(workspace)
+        if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+            raise ValueError(f"workspace must be contiguous and on {dev}")
+        if workspace is None or workspace.nbytes < need:
+            workspace = _empty((need,), torch.uint8, dev, stream)
+        a.workspace = workspace.data_ptr()
         a.workspace_bytes = need
     _launch("glinattn_paged_attention", a, stream, dev)
     return o
@@ -625,20 +655,20 @@ def glinattn_accept_drafts(target_probs, draft_probs, draft_tokens, uniforms, *,
     dev = target_probs.device
     if D < 0:
         raise ValueError("target_probs must be [R, D + 1, V]")
-    _need(target_probs, "target_probs", torch.float32, (R, D + 1, V), dev)
+    _check(target_probs, "target_probs", torch.float32, (R, D + 1, V), dev)
     _need(draft_probs, "draft_probs", torch.float32, (R, D, V), dev)
-    _need(draft_tokens, "draft_tokens", torch.int32, (R, D), dev)
-    _need(uniforms, "uniforms", torch.float32, (R, D + 1), dev)
+    _check(draft_tokens, "draft_tokens", torch.int32, (R, D), dev)
+    _check(uniforms, "uniforms", torch.float32, (R, D + 1), dev)
     _need(num_drafts, "num_drafts", torch.int32, (R,), dev)
     if accept is None:
-        accept = torch.empty((R,), dtype=torch.int32, device=dev)
+        accept = _empty((R,), torch.int32, dev, stream)
     if tokens is None:
-        tokens = torch.empty((R, D + 1), dtype=torch.int32, device=dev)
-    _need(accept, "accept", torch.int32, (R,), dev)
-    _need(tokens, "tokens", torch.int32, (R, D + 1), dev)
+        tokens = _empty((R, D + 1), torch.int32, dev, stream)
+    _check(accept, "accept", torch.int32, (R,), dev)
+    _check(tokens, "tokens", torch.int32, (R, D + 1), dev)
     _status_word(dev_status, dev)
-    a = AcceptArgs(R, D, V, _ptr(target_probs), _ptr(draft_probs), _ptr(draft_tokens), _ptr(num_drafts),
-                   _ptr(uniforms), _ptr(accept), _ptr(tokens), _ptr(dev_status))
+    a = AcceptArgs(R, D, V, _addr(target_probs), _addr(draft_probs), _addr(draft_tokens), _addr(num_drafts),
+                   _addr(uniforms), _addr(accept), _addr(tokens), _addr(dev_status))
     _launch("glinattn_accept_drafts", a, stream, dev)
     return accept, tokens
 
