@@ -104,17 +104,6 @@ __device__ __forceinline__ void split_e4m3x2(float w0, float w1, uint32_t &hi, u
   lo = f;
 }
 
-// Matrix without swizzle, MN-major: 16-byte units of consecutive rows, a unit's
-// 8 K indices 16 bytes apart; LBO between groups of 8 K indices, SBO between units.
-__device__ __forceinline__ uint64_t desc_units(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1 << 46;
-  return d;
-}
-
 // Columns a .. a + 15 of this thread's lane, times f[0 .. 15] (shared memory).
 __device__ __forceinline__ void tmem_scale16(uint32_t a, const float *f) {
   float t[16];
@@ -291,79 +280,77 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
       if (ok) ok = load(it.j1 - 1, true, vbase, vids);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ============ MMA issue ============
+    {
+      // ============ MMA issue (one lane) ============
       constexpr uint32_t id_s = kF8 ? idesc_f8(128, N, false, false) : idesc_bf16(128, N, false, false);
       constexpr uint32_t id_o = kF8 ? idesc_f8(D, C::kNO, true, true) : idesc_bf16(D, C::kNO, true, true);
-      const uint32_t sb = smem_u32(smem), sQ = sb + C::kOffQ, sP = sb + C::kOffP;
+      constexpr uint32_t hi_r = kF8 && D == 64 ? desc_hi(512, kSw64) : desc_hi(1024, kSw128);  // K, V, q
+      // weights: 16-byte units of consecutive rows (no swizzle, MN-major), a unit's 8 keys 16
+      // bytes apart, 128 bytes between groups of 8 keys, 2048 between units
+      constexpr uint32_t hi_w = desc_hi(2048, kSwNone);
+      const bool leader = elect_one();
+      const uint32_t sb = smem_u32(smem), q0 = desc_lo(sb + C::kOffQ, 16), p0 = desc_lo(sb + C::kOffP, 128);
+      const uint32_t k0 = desc_lo(sb, 16), v0 = desc_lo(sb, 8192);
       uint32_t sc = 0, g = 0, slot = 0;
       auto issue_s = [&](uint32_t gi) -> bool {
         for (int h = 0; h < NS; ++h)
-          if (!wait_bar(&bars->full[(sc + h) % ST], ((sc + h) / ST) & 1u, abort)) return false;
+          if (!wait_bar_warp(&bars->full[(sc + h) % ST], ((sc + h) / ST) & 1u, abort)) return false;
         const uint32_t buf = gi & 1;
-        if (!wait_bar(&bars->s_free[buf], ((gi >> 1) & 1u) ^ 1u, abort)) return false;
+        if (!wait_bar_warp(&bars->s_free[buf], ((gi >> 1) & 1u) ^ 1u, abort)) return false;
         tc_fence_after();
         const uint32_t d = tmem + buf * N;
-        if constexpr (!kF8) {
+        const uint32_t a0 = k0 + (sc % ST) * (kStageBytes >> 4), a1 = k0 + ((sc + 1) % ST) * (kStageBytes >> 4);
+        if (leader) {
+          if constexpr (!kF8) {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t a = sb + ((sc + (ks >> 2)) % ST) * kStageBytes + (ks & 3) * 32;
-            umma_bf16(d, desc_sw128(a, 16, 1024), desc_sw128(sQ + (ks >> 2) * (N * 128) + (ks & 3) * 32, 16, 1024), id_s, ks > 0);
-          }
-        } else {
-          // both parts of q against the same keys
-          const uint32_t a = sb + (sc % ST) * kStageBytes;
+            for (int ks = 0; ks < D / 16; ++ks)
+              mma_ss<false>(d, (ks < 4 ? a0 : a1) + ((ks & 3) * 32 >> 4), hi_r, q0 + ((ks >> 2) * (N * 128) + (ks & 3) * 32 >> 4), hi_r, id_s,
+                            ks > 0);
+          } else {
+            // both parts of q against the same keys
 #pragma unroll
-          for (int ks = 0; ks < 2 * (D / 32); ++ks) {
-            const uint32_t k = ks % (D / 32) * 32, b = sQ + ks / (D / 32) * (N * D) + k;
-            if (D == 128)
-              umma_f8(d, desc_sw128(a + k, 16, 1024), desc_sw128(b, 16, 1024), id_s, ks > 0);
-            else
-              umma_f8(d, desc_sw64(a + k, 16, 512), desc_sw64(b, 16, 512), id_s, ks > 0);
+            for (int ks = 0; ks < 2 * (D / 32); ++ks) {
+              const uint32_t k = ks % (D / 32) * 32;
+              mma_ss<true>(d, a0 + (k >> 4), hi_r, q0 + (ks / (D / 32) * (N * D) + k >> 4), hi_r, id_s, ks > 0);
+            }
           }
+          umma_commit(&bars->s_ready[buf]);
+          for (int h = 0; h < NS; ++h) umma_commit(&bars->empty[(sc + h) % ST]);
         }
-        umma_commit(&bars->s_ready[buf]);
-        for (int h = 0; h < NS; ++h) umma_commit(&bars->empty[(sc + h) % ST]);
         sc += NS;
         return true;
       };
       auto issue_o = [&](uint32_t gi, bool first) -> bool {
-        if (!wait_bar(&bars->p_ready, gi & 1u, abort)) return false;
+        if (!wait_bar_warp(&bars->p_ready, gi & 1u, abort)) return false;
         for (int h = 0; h < NS; ++h)
-          if (!wait_bar(&bars->full[(sc + h) % ST], ((sc + h) / ST) & 1u, abort)) return false;
+          if (!wait_bar_warp(&bars->full[(sc + h) % ST], ((sc + h) / ST) & 1u, abort)) return false;
         tc_fence_after();
         const uint32_t d = tmem + C::kColO;
-        if constexpr (!kF8) {
+        const uint32_t a0 = v0 + (sc % ST) * (kStageBytes >> 4), a1 = v0 + ((sc + 1) % ST) * (kStageBytes >> 4);
+        if (leader) {
+          if constexpr (!kF8) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            const uint32_t a = NS == 2 ? sb + ((sc + (ks >> 2)) % ST) * kStageBytes + (ks & 3) * 2048
-                                       : sb + (sc % ST) * kStageBytes + ks * 2048;
-            umma_bf16(d, desc_sw128(a, 8192, 1024), desc_units(sP + ks * 256, 128, 2048), id_o,
-                      ks > 0 || !first);
-          }
-        } else {
-          const uint32_t a = sb + (sc % ST) * kStageBytes;
+            for (int ks = 0; ks < 8; ++ks)
+              mma_ss<false>(d, (NS == 1 || ks < 4 ? a0 : a1) + ((NS == 1 ? ks : ks & 3) * 2048 >> 4), hi_r, p0 + (ks * 256 >> 4), hi_w,
+                            id_o, ks > 0 || !first);
+          } else {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            const uint64_t b = desc_units(sP + ks * 512, 128, 2048);
-            if (D == 128)
-              umma_f8(d, desc_sw128(a + ks * 4096, 16, 1024), b, id_o, ks > 0 || !first);
-            else
-              umma_f8(d, desc_sw64(a + ks * 2048, 16, 512), b, id_o, ks > 0 || !first);
+            for (int ks = 0; ks < 4; ++ks)
+              mma_ss<true>(d, a0 + (ks * (32 * D) >> 4), hi_r, p0 + (ks * 512 >> 4), hi_w, id_o, ks > 0 || !first);
           }
+          umma_commit(&bars->o_done);
+          for (int h = 0; h < NS; ++h) umma_commit(&bars->empty[(sc + h) % ST]);
         }
-        umma_commit(&bars->o_done);
-        for (int h = 0; h < NS; ++h) umma_commit(&bars->empty[(sc + h) % ST]);
         sc += NS;
         return true;
       };
       for (bool ok = true; ok;) {
         const int si = slot % kItems;
-        if (!wait_bar(&bars->item_full[si], (slot / kItems) & 1u, abort)) break;
+        if (!wait_bar_warp(&bars->item_full[si], (slot / kItems) & 1u, abort)) break;
         const int kind = bars->item[si].kind, n = bars->item[si].j1 - bars->item[si].j0;
-        mbar_arrive(&bars->item_empty[si]);
+        warp_arrive(&bars->item_empty[si]);
         if (kind < 0) break;
-        if (!wait_bar(&bars->q_ready, slot & 1u, abort)) break;
+        if (!wait_bar_warp(&bars->q_ready, slot & 1u, abort)) break;
         ++slot;
         for (int j = 0; j < n && ok; ++j) {
           ok = issue_s(g + j);

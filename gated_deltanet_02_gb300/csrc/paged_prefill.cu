@@ -251,73 +251,76 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
           }
         }
       }
-    } else if (warp <= C::kIssuers && lane == 0) {
-      // ============ MMA issue: row tiles w0 .. w1 - 1 ============
+    } else if (warp <= C::kIssuers) {
+      // ============ MMA issue (one lane): row tiles w0 .. w1 - 1 ============
       const int w0 = C::kIssuers == 2 ? warp - 1 : 0, w1 = C::kIssuers == 2 ? warp : 2;
       constexpr uint32_t id_s = kF8 ? idesc_f8(128, 128, false, false) : idesc_bf16(128, 128, false, false);
       constexpr uint32_t id_o = idesc_bf16(128, D, false, true);
+      constexpr uint32_t hi_s = kF8 && D == 64 ? desc_hi(512, kSw64) : desc_hi(1024, kSw128);
+      const bool leader = elect_one();
       uint32_t g = 0, slot = 0, np[2] = {0, 0}, nq[2] = {0, 0}, nf[2] = {0, 0};  // g: cache tiles so far
       // stages of tile t's keys and values
       auto k_stage = [](uint32_t t) { return kF8 ? t % C::kRawK : 2 * t % ST; };
       auto v_stage = [](uint32_t t) { return kF8 ? t % ST : (2 * t + 1) % ST; };
       auto k_landed = [&](uint32_t t) -> bool {
-        return kF8 ? wait_bar<false>(&bars->rawk_full[k_stage(t)], (t / C::kRawK) & 1u, abort)
-                   : wait_bar<false>(&bars->full[k_stage(t)], (2 * t / ST) & 1u, abort);
+        return kF8 ? wait_bar_warp<false>(&bars->rawk_full[k_stage(t)], (t / C::kRawK) & 1u, abort)
+                   : wait_bar_warp<false>(&bars->full[k_stage(t)], (2 * t / ST) & 1u, abort);
       };
       auto v_landed = [&](uint32_t t) -> bool {
-        return wait_bar<false>(&bars->full[v_stage(t)], (kF8 ? t / ST : (2 * t + 1) / ST) & 1u, abort);
+        return wait_bar_warp<false>(&bars->full[v_stage(t)], (kF8 ? t / ST : (2 * t + 1) / ST) & 1u, abort);
       };
       // S_w = Q_w K^T; with P beside S the scores before it have to be read
       auto issue_s = [&](int w, uint32_t t) -> bool {
-        if (C::kSepP && !wait_bar<false>(&bars->s_free[w], (nf[w]++ & 1u) ^ 1u, abort)) return false;
+        if (C::kSepP && !wait_bar_warp<false>(&bars->s_free[w], (nf[w]++ & 1u) ^ 1u, abort)) return false;
         tc_fence_after();
-        const uint32_t a = sb + w * C::kQTile, d = tmem + C::kColS + 128 * w;
-        if constexpr (kF8) {  // both parts of q against the same keys
-          const uint32_t b = sb + C::kOffRawK + k_stage(t) * C::kRawBytes;
+        const uint32_t d = tmem + C::kColS + 128 * w, a = desc_lo(sb + w * C::kQTile, 16);
+        const uint32_t b = desc_lo(kF8 ? sb + C::kOffRawK + k_stage(t) * C::kRawBytes : sb + C::kOffRing + k_stage(t) * C::kStageBytes, 16);
+        if (leader) {
+          if constexpr (kF8) {  // both parts of q against the same keys
 #pragma unroll
-          for (int ks = 0; ks < 2 * (D / 32); ++ks) {
-            const uint32_t k = ks % (D / 32) * 32, q = a + ks / (D / 32) * (128 * D) + k;
-            if (D == 128)
-              umma_f8(d, desc_sw128(q, 16, 1024), desc_sw128(b + k, 16, 1024), id_s, ks > 0);
-            else
-              umma_f8(d, desc_sw64(q, 16, 512), desc_sw64(b + k, 16, 512), id_s, ks > 0);
-          }
-        } else {
-          const uint32_t b = sb + C::kOffRing + k_stage(t) * C::kStageBytes;
+            for (int ks = 0; ks < 2 * (D / 32); ++ks) {
+              const uint32_t k = ks % (D / 32) * 32;
+              mma_ss<true>(d, a + (ks / (D / 32) * (128 * D) + k >> 4), hi_s, b + (k >> 4), hi_s, id_s, ks > 0);
+            }
+          } else {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
-            umma_bf16(d, desc_sw128(a + off, 16, 1024), desc_sw128(b + off, 16, 1024), id_s, ks > 0);
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+              mma_ss<false>(d, a + off, hi_s, b + off, hi_s, id_s, ks > 0);
+            }
           }
+          umma_commit(&bars->s_ready[w]);
         }
-        umma_commit(&bars->s_ready[w]);
         return true;
       };
       // O_w (+)= P_w V, 64 keys' weights at a time
       auto issue_o = [&](int w, uint32_t t, bool first) -> bool {
-        const uint32_t b = sb + C::kOffRing + v_stage(t) * C::kStageBytes, ph = np[w]++ & 1u;
+        const uint32_t b = desc_lo(sb + C::kOffRing + v_stage(t) * C::kStageBytes, 16384), ph = np[w]++ & 1u;
+        const uint32_t d = tmem + C::kColO + D * w, a = tmem + C::kColP + C::kPStep * w;
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          if (ks % 4 == 0) {
-            if (!wait_bar<false>(&bars->p_ready[w][ks / 4], ph, abort)) return false;
-            tc_fence_after();
+        for (int h = 0; h < 2; ++h) {
+          if (!wait_bar_warp<false>(&bars->p_ready[w][h], ph, abort)) return false;
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+              mma_ts(d, a + 8 * ks, b + ks * (2048 >> 4), desc_hi(1024, kSw128), id_o, ks > 0 || !first);
           }
-          umma_bf16_tmem_a(tmem + C::kColO + D * w, tmem + C::kColP + C::kPStep * w + 8 * ks, desc_sw128(b + ks * 2048, 16384, 1024),
-                           id_o, ks > 0 || !first);
         }
         return true;
       };
       // a stage is free when every issuer says so: behind its products, or at once
       // (but not before the stage is filled) where its row tiles have none in it
       auto release = [&](uint64_t *bar, bool used) {
+        if (!leader) return;
         if (used) umma_commit(bar);
         else mbar_arrive(bar);
       };
       for (bool ok = true; ok;) {
         const int si = slot % kItems;
-        if (!wait_bar<false>(&bars->item_full[si], (slot / kItems) & 1u, abort)) break;
+        if (!wait_bar_warp<false>(&bars->item_full[si], (slot / kItems) & 1u, abort)) break;
         const Item it = bars->item[si];
-        mbar_arrive(&bars->item_empty[si]);
+        warp_arrive(&bars->item_empty[si]);
         if (it.kind < 0) break;
         ++slot;
         const int n = it.j1 - it.j0;
@@ -330,7 +333,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         // first scores
         if (!(ok = k_landed(g))) break;
         for (int w = w0; w < w1 && ok; ++w)
-          if (nw[w] > 0) ok = wait_bar<false>(&bars->q_ready[w], nq[w]++ & 1u, abort) && issue_s(w, g);
+          if (nw[w] > 0) ok = wait_bar_warp<false>(&bars->q_ready[w], nq[w]++ & 1u, abort) && issue_s(w, g);
         if (!ok) break;
         k_release(0);
         for (int j = 0; j < n && ok; ++j) {
@@ -346,7 +349,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
           for (int w = w0; w < w1 && ok; ++w) {
             if (j < nw[w]) {
               ok = issue_o(w, g + j, j == 0);
-              if (ok && (C::kSepP || j + 1 == nw[w])) umma_commit(&bars->o_done[w]);
+              if (ok && leader && (C::kSepP || j + 1 == nw[w])) umma_commit(&bars->o_done[w]);
             }
             if (ok && !C::kSepP && j + 1 < nw[w]) ok = issue_s(w, g + j + 1);
           }
