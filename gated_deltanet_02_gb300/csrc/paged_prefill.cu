@@ -59,12 +59,10 @@ struct Cfg {
   static constexpr int kStages = kF8 ? 2 : D == 128 ? 4 : 6;
   static constexpr int kRawK = kF8 ? 3 : 0, kRawV = kF8 ? 2 : 0;
   static constexpr int kScaleSlots = kF8 ? 8 : 0;             // tiles of key scales as floats
-  static constexpr int kOutCols = kF8 ? 16 : 32;              // channels of the output staging
   static constexpr uint32_t kOffRing = 2 * kQTile;
   static constexpr uint32_t kOffRawK = kOffRing + kStages * kStageBytes;
   static constexpr uint32_t kOffRawV = kOffRawK + kRawK * kRawBytes;
-  static constexpr uint32_t kOffOut = kOffRawV + kRawV * kRawBytes;
-  static constexpr uint32_t kOffCode = kOffOut + 8 * 32 * kOutCols * 2;   // scale codes beside the raw tiles
+  static constexpr uint32_t kOffCode = kOffRawV + kRawV * kRawBytes;      // scale codes beside the raw tiles
   static constexpr uint32_t kOffScale = kOffCode + (kRawK + kRawV) * kTileKeys;
   static constexpr uint32_t kOffBars = kOffScale + kScaleSlots * kTileKeys * 4;
   static constexpr uint32_t kBytesBars = 1024 + (kF8 ? 1024 : 0);         // e4m3: and a scale per q row
@@ -101,10 +99,10 @@ __device__ __forceinline__ void regs_dec() {
 }
 
 // Tiles [j0, j1) that row tile w of the item looks at: up to its last row's key.
-__device__ __forceinline__ int last_tile(const Item &it, int G, int w) {
+__device__ __forceinline__ int last_tile(const Item &it, int G, uint32_t inv_g, int w) {
   const int nrow = it.ntok * G;
-  const int last = min(128 * (w + 1), nrow) - 1;  // its last row
-  const int end = it.pos0 + last / G + 1;
+  const int last = max(min(128 * (w + 1), nrow) - 1, 0);  // its last row
+  const int end = it.pos0 + (int)((uint32_t)last * inv_g >> 16) + 1;
   const int n = end <= kTileKeys ? 1 : (end + kTileKeys - 1) / kTileKeys;
   return 128 * w >= nrow ? it.j0 : max(it.j0, min(it.j1, n));
 }
@@ -119,6 +117,20 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+
+// 64 bytes to global memory, as two 32-byte stores where the address allows it.
+__device__ __forceinline__ void store64(void *dst, const uint32_t (&u)[16]) {
+  if (((uintptr_t)dst & 31) == 0) {
+#pragma unroll
+    for (int k = 0; k < 16; k += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(reinterpret_cast<uint32_t *>(dst) + k), "r"(u[k]),
+                   "r"(u[k + 1]), "r"(u[k + 2]), "r"(u[k + 3]), "r"(u[k + 4]), "r"(u[k + 5]), "r"(u[k + 6]), "r"(u[k + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; k += 4) reinterpret_cast<uint4 *>(dst)[k / 4] = make_uint4(u[k], u[k + 1], u[k + 2], u[k + 3]);
+  }
 }
 
 template <int D, bool kF8>
@@ -178,6 +190,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
   const uint32_t tmem = bars->tmem;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int pages = kTileKeys >> p.page_shift;  // pages of a tile
+  const uint32_t inv_g = (65535u + p.G) / p.G;  // row / G is row * inv_g >> 16 for row, G <= 256
 
   if (warp < 4) {
     // registers a thread: 64 + 2 x 192 + 64 of 4 x 128 (e4m3), 80 + 2 x 208 of 3 x 168
@@ -325,7 +338,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         ++slot;
         const int n = it.j1 - it.j0;
         int nw[2];
-        for (int w = 0; w < 2; ++w) nw[w] = last_tile(it, p.G, w) - it.j0;
+        for (int w = 0; w < 2; ++w) nw[w] = last_tile(it, p.G, inv_g, w) - it.j0;
         const int most = C::kIssuers == 2 ? nw[w0] : max(nw[0], nw[1]);
         auto k_release = [&](int j) {
           release(kF8 ? &bars->rawk_empty[k_stage(g + j)] : &bars->empty[k_stage(g + j)], j < most);
@@ -369,7 +382,6 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     const uint32_t tS = tmem + C::kColS + 128 * w + lane_base, tO = tmem + C::kColO + D * w + lane_base;
     const uint32_t tP = tmem + C::kColP + C::kPStep * w + lane_base;
     uint32_t g = 0, slot = 0, ns = 0, nd = 0;  // g: cache tiles so far
-    const uint32_t inv_g = (65535u + p.G) / p.G;  // row / G is row * inv_g >> 16 for row, G <= 256
     // a row's place among the item's rows of q and o, in elements
     auto row_at = [&](const Item &it, int r) -> size_t {
       const int tok = (int)((uint32_t)r * inv_g >> 16);
@@ -381,7 +393,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     // never a phase ahead of its reader.  bf16 rows are copied asynchronously
     // (fetch_q once S of the last tile is there, q_fetched behind that tile's weights).
     auto fetch_q = [&](const Item &it) {
-      if (kF8 || it.kind < 0 || last_tile(it, p.G, w) <= it.j0) return;
+      if (kF8 || it.kind < 0 || last_tile(it, p.G, inv_g, w) <= it.j0) return;
       constexpr int kLanes = D / 8, kPer = 32 / kLanes;
       const int c = lane % kLanes, nrow = it.ntok * p.G;
 #pragma unroll 1
@@ -394,7 +406,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       }
     };
     auto q_fetched = [&](const Item &it) {
-      if (it.kind < 0 || last_tile(it, p.G, w) <= it.j0) return;
+      if (it.kind < 0 || last_tile(it, p.G, inv_g, w) <= it.j0) return;
       if constexpr (kF8) {
         constexpr int kLanes = D / 8, kPer = 32 / kLanes;
         const int c = lane % kLanes, nrow = it.ntok * p.G;
@@ -432,10 +444,10 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     }
     while (ok && it.kind >= 0) {
       const int si = slot % kItems;
-      const int n = it.j1 - it.j0, nw = last_tile(it, p.G, w) - it.j0;
+      const int n = it.j1 - it.j0, nw = last_tile(it, p.G, inv_g, w) - it.j0;
       const int end = it.pos0 + it.ntok;                    // keys behind it are not there
       const int lim = it.pos0 + (int)((uint32_t)row * inv_g >> 16);  // the row's last key
-      const int first_lim = it.pos0 + (128 * w) / p.G;      // the first row's
+      const int first_lim = it.pos0 + (int)((uint32_t)(128 * w) * inv_g >> 16);  // the first row's
       const float c = kF8 ? s_qs[row] : p.c;                // written by this warp
       float m = -INFINITY, l = 0.f;
       Item nx = it;
@@ -561,44 +573,18 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         if (!(ok = wait_bar_warp(&bars->o_done[w], nd++ & 1u, abort))) break;
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        // outputs through shared memory, kOutCols channels of the warp's 32 rows at
-        // a time, so that neighbouring lanes write neighbouring bytes of a row
-        constexpr int kChunks = C::kOutCols / 8, kRows = 32 / kChunks;  // 16-byte chunks of a row; rows a store
-        const uint32_t stage = sb + C::kOffOut + (warp - 4) * (32 * C::kOutCols * 2);
-        auto at = [&](int r, int ch) {
-          return stage + r * (C::kOutCols * 2) + ((ch ^ ((r >> (kChunks == 4 ? 1 : 2)) & (kChunks - 1))) << 4);
-        };
-        __nv_bfloat16 *dst[kChunks];
-        bool put[kChunks];
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          const int r = 128 * w + 32 * q4 + kRows * i + lane / kChunks;
-          put[i] = it.kind == 0 && !bad && r < it.ntok * p.G;
-          dst[i] = p.o + row_at(it, r) + (lane % kChunks) * 8;
-        }
+        __nv_bfloat16 *dst = p.o + row_at(it, row);
+        const bool put = it.kind == 0 && has && !bad;
 #pragma unroll 1
         for (int k = 0; k < D; k += 32) {
           float o[32];
           tmem_ld32(tO + k, o);
           if (it.kind == 0) {
+            // 64 contiguous bytes of the lane's row, whole 32-byte sectors
+            uint32_t u[16];
 #pragma unroll
-            for (int k2 = 0; k2 < 32; k2 += C::kOutCols) {
-              __syncwarp();
-#pragma unroll
-              for (int e = 0; e < C::kOutCols; e += 8) {
-                uint32_t u[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                  u[x] = l == 0.f ? 0u : pack_bf16(o[k2 + e + 2 * x] * inv, o[k2 + e + 2 * x + 1] * inv);
-                sts128(at(lane, e / 8), make_uint4(u[0], u[1], u[2], u[3]));
-              }
-              __syncwarp();
-#pragma unroll
-              for (int i = 0; i < kChunks; ++i) {
-                const uint4 v = lds128(at(kRows * i + lane / kChunks, lane % kChunks));
-                if (put[i]) *reinterpret_cast<uint4 *>(dst[i] + k + k2) = v;
-              }
-            }
+            for (int x = 0; x < 16; ++x) u[x] = l == 0.f ? 0u : pack_bf16(o[2 * x] * inv, o[2 * x + 1] * inv);
+            if (put) store64(dst + k, u);
           } else if (has) {
             float4 *part = reinterpret_cast<float4 *>(p.part) + (pslot * (D / 4) + k / 4) * kPrefillRows + row;
 #pragma unroll
