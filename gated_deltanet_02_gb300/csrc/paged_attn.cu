@@ -1,9 +1,8 @@
 // paged_attn.cu -- the host side of glinattn_paged_attention: argument checks,
 // the workspace, and the choice between the kernels.
 //
-// A call whose items (query tokens x heads of a group) have at most 48 rows
-// runs the transposed kernel of paged_decode.cu, in which query rows are the
-// narrow side of the tensor-core tile; any other call, mixtures of prompts and
+// A call whose items (query tokens x heads of a group) have few rows runs the
+// transposed kernel of paged_decode.cu, any other call, mixtures of prompts and
 // single tokens among them, the one of paged_prefill.cu with 256 rows an item.
 #include <math.h>
 
@@ -28,10 +27,19 @@ glinattn_status check(const glinattn_paged_attn_args *a) {
   return GLINATTN_OK;
 }
 
-// Rows of an item: what the kernel's accumulators are built for.
+// Rows of an item: what the kernel's accumulators are built for.  Single tokens
+// and drafts run the kernel for few rows, in which query rows are the narrow side
+// of the tensor-core tile.  64 requests after 8,192 tokens, 4 kv heads of 128:
+//   rows          8    16    24    32    40    48
+//   bf16 few    165   171   182   185   201   206 us
+//        many   171   172   173   175   176   178
+//   e4m3 few     96   102   114   119   164   169
+//        many   263   266   268   271   274   273
 int item_rows(const glinattn_paged_attn_args *a) {
   const long long rows = (long long)a->max_q_len * (a->heads / a->kv_heads);
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= kDecodeRows ? kDecodeRows : kPrefillRows;
+  if (rows <= 16) return 16;
+  if (a->cache_dtype != GLINATTN_E4M3 || rows > 48) return kPrefillRows;
+  return rows <= 32 ? 32 : 48;
 }
 
 int sm_count() {

@@ -23,7 +23,9 @@
 // Bound: HBM, one read of the cache; 2 CTAs per SM, each with a ring of 16 KiB
 // stages (TMA, one box per page), so that about 190 KiB per SM are in flight.  Warps:
 // 0 TMA and the walk over the items, 1 MMA issue, then groups of four softmax
-// warps, a key per thread and 16 rows per group.
+// warps, a key per thread and 16 rows per group (24 rows per group, fewer warps
+// that repeat a tile's fixed cost, took 192 us instead of 164 us for 40 rows of
+// 64 requests after 8,192 tokens in e4m3).
 #include "paged_sched.cuh"
 #include "paged_tc.cuh"
 #include "prefill_tc.cuh"
@@ -49,7 +51,8 @@ struct Cfg {
   static constexpr int kNO = N * kTP;                // columns of O^T (S^T has N)
   static constexpr int kEsz = kF8 ? 1 : 2;
   static constexpr int kTileStages = D * kEsz * kTileKeys > (int)kStageBytes ? 2 : 1;
-  static constexpr int kGroups = N / 16;             // softmax warpgroups, 16 rows each
+  static constexpr int kRows = 16;                   // rows of a softmax group of four warps
+  static constexpr int kGroups = N / kRows;
   static constexpr int kThreads = 64 + 128 * kGroups;
   static constexpr uint32_t kBytesQ = N * kTQ * D * kEsz;
   static constexpr uint32_t kBytesP = N * kTP * kTileKeys * kEsz;
@@ -104,27 +107,27 @@ __device__ __forceinline__ void split_e4m3x2(float w0, float w1, uint32_t &hi, u
   lo = f;
 }
 
-// Columns a .. a + 15 of this thread's lane, times f[0 .. 15] (shared memory).
+// 16 columns from a of this thread's lane, times f[0 ..] (shared memory).
 __device__ __forceinline__ void tmem_scale16(uint32_t a, const float *f) {
   float t[16];
   tmem_ld16(a, t);
-  uint32_t u[16];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(t[j] * f[j]);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16};" ::"r"(a),
-      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
-      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
-      : "memory");
+  for (int k = 0; k < 16; k += 8) {
+    uint32_t u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(t[k + j] * f[k + j]);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a + k), "r"(u[0]), "r"(u[1]),
+                 "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+  }
   tmem_wait_st();
 }
 
 template <int D, bool kF8, int N>
-__global__ void __launch_bounds__(64 + 8 * N, 2)
+__global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
     decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnParams p) {
   using C = Cfg<D, kF8, N>;
-  constexpr int ST = C::kStages, NS = C::kTileStages, W = C::kGroups;
+  constexpr int ST = C::kStages, NS = C::kTileStages, W = C::kGroups, R = C::kRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars *bars = reinterpret_cast<Bars *>(smem + C::kOffBars);
@@ -361,10 +364,10 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
       }
     }
   } else {
-    // ============ softmax: thread = key, group w = rows 16 w .. 16 w + 15 ============
+    // ============ softmax: thread = key, group w = rows R w .. R w + R - 1 ============
     const int w = (warp - 2) >> 2, q4 = warp & 3, kk = 32 * q4 + lane;
     const int st = tid - 64 - 128 * w;               // 0 .. 127
-    const int rb = 16 * w;                           // the group's first row
+    const int rb = R * w;                            // the group's first row
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
     const uint32_t sb = smem_u32(smem);
     float *s_red = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * rb;  // [row][warp]
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
         constexpr int kLanes = D / 8, kPer = 128 / kLanes;
         const int c = st % kLanes;
 #pragma unroll
-        for (int r0 = 0; r0 < 16; r0 += kPer) {
+        for (int r0 = 0; r0 < R; r0 += kPer) {
           const int row = rb + r0 + st / kLanes;
           uint4 x = make_uint4(0, 0, 0, 0);
           if (row < nrow) {
@@ -414,23 +417,23 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
         }
         fence_proxy_async_smem();
         warp_arrive(&bars->q_ready);
-        if (st < 16) {
+        if (st < R) {
           s_m[st] = 0.f;
           s_lim[st] = it.pos0 + min(rb + st, nrow - 1) / p.G;
         }
         if (!(ok = group_sync())) break;
       }
-      bool has_max = false;  // of the row st (threads 0 .. 15 of the group)
-      float l[16];
+      bool has_max = false;  // of the row st (threads 0 .. R - 1 of the group)
+      float2 l[R / 2];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) l[r] = 0.f;
+      for (int r = 0; r < R / 2; ++r) l[r] = make_float2(0.f, 0.f);
       for (int j = it.j0; j < it.j1; ++j, ++g) {
         const uint32_t buf = g & 1, tS = tmem + buf * N + rb + lane_base;
         if (!(ok = wait_bar_warp(&bars->s_ready[buf], (g >> 1) & 1u, abort))) break;
         tc_fence_after();
         const int key = j * kTileKeys + kk;
         // ---- scores in log2 units, less the row's maximum
-        float x[16], ev = 0.f;                            // e4m3: the value's exponent
+        float x[R], ev = 0.f;                             // e4m3: the value's exponent
         tmem_ld16(tS, x);
         float ks = p.c;
         if constexpr (kF8) {
@@ -443,21 +446,21 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
         tc_fence_before();
         warp_arrive(&bars->s_free[buf]);
 #pragma unroll
-        for (int r = 0; r < 16; r += 4) {
+        for (int r = 0; r < R; r += 4) {
           const float4 m = *reinterpret_cast<const float4 *>(s_m + r);
-          float4 q = make_float4(ks, ks, ks, ks);
+          float2 q0 = make_float2(ks, ks), q1 = q0;
           if constexpr (kF8) {
             const float4 qs = *reinterpret_cast<const float4 *>(s_qs + r);
-            q = make_float4(ks * qs.x, ks * qs.y, ks * qs.z, ks * qs.w);
+            q1 = __fmul2_rn(q0, make_float2(qs.z, qs.w));
+            q0 = __fmul2_rn(q0, make_float2(qs.x, qs.y));
           }
-          x[r] = fmaf(x[r], q.x, -m.x);
-          x[r + 1] = fmaf(x[r + 1], q.y, -m.y);
-          x[r + 2] = fmaf(x[r + 2], q.z, -m.z);
-          x[r + 3] = fmaf(x[r + 3], q.w, -m.w);
+          const float2 a = __ffma2_rn(make_float2(x[r], x[r + 1]), q0, make_float2(-m.x, -m.y));
+          const float2 b = __ffma2_rn(make_float2(x[r + 2], x[r + 3]), q1, make_float2(-m.z, -m.w));
+          x[r] = a.x, x[r + 1] = a.y, x[r + 2] = b.x, x[r + 3] = b.y;
         }
         if (j * kTileKeys + kTileKeys - 1 > it.pos0) {    // some row does not see the whole tile
 #pragma unroll
-          for (int r = 0; r < 16; r += 4) {
+          for (int r = 0; r < R; r += 4) {
             const int4 lim = *reinterpret_cast<const int4 *>(s_lim + r);
             x[r] = key > lim.x ? -INFINITY : x[r];
             x[r + 1] = key > lim.y ? -INFINITY : x[r + 1];
@@ -469,8 +472,8 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
         {
           float t = x[0];
 #pragma unroll
-          for (int r = 1; r < 15; r += 2) t = max3(t, x[r], x[r + 1]);
-          const bool any = __any_sync(0xffffffffu, fmaxf(t, x[15]) + ev > kSlack);
+          for (int r = 1; r < R - 1; r += 2) t = max3(t, x[r], x[r + 1]);
+          const bool any = __any_sync(0xffffffffu, fmaxf(t, x[R - 1]) + ev > kSlack);
           if (lane == 0) s_flag[g & 1][w][q4] = any || j == it.j0;
         }
         if (!(ok = group_sync())) break;
@@ -478,13 +481,13 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
         const bool moves = fl.x | fl.y | fl.z | fl.w | (j > it.j0 && s_unset[w]);
         if (moves) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
+          for (int r = 0; r < R; ++r) {
             const float v = warp_max(x[r] + ev);
             if (lane == r) s_red[r * 4 + q4] = v;
           }
           if (!(ok = group_sync())) break;
           if (st < 32) {
-            if (st < 16) {
+            if (st < R) {
               const float4 v = *reinterpret_cast<const float4 *>(s_red + st * 4);
               const float t = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
               const float d = t > (has_max ? kSlack : -INFINITY) ? t : 0.f;
@@ -493,15 +496,16 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
               s_f[st] = ex2(-d);
               s_m[st] += d;
             }
-            const bool unset = __any_sync(0xffffffffu, st < 16 && !has_max);
+            const bool unset = __any_sync(0xffffffffu, st < R && !has_max);
             if (st == 0) s_unset[w] = unset;
           }
           if (!(ok = group_sync())) break;
 #pragma unroll
-          for (int r = 0; r < 16; r += 4) {
+          for (int r = 0; r < R; r += 4) {
             const float4 d = *reinterpret_cast<const float4 *>(s_d + r), f = *reinterpret_cast<const float4 *>(s_f + r);
             x[r] -= d.x, x[r + 1] -= d.y, x[r + 2] -= d.z, x[r + 3] -= d.w;
-            l[r] *= f.x, l[r + 1] *= f.y, l[r + 2] *= f.z, l[r + 3] *= f.w;
+            l[r / 2] = __fmul2_rn(l[r / 2], make_float2(f.x, f.y));
+            l[r / 2 + 1] = __fmul2_rn(l[r / 2 + 1], make_float2(f.z, f.w));
           }
         }
         if (g > 0 && !(ok = wait_bar_warp(&bars->o_done, (g - 1) & 1u, abort))) break;  // W is read, O^T complete
@@ -514,29 +518,28 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
         // rows are contiguous, 16 bytes a unit
         const uint32_t wp = sb + C::kOffP + kk * 16;
         if constexpr (!kF8) {
-          uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int r = 0; r < 16; r += 2) {
-            const float w0 = ex2(x[r]), w1 = ex2(x[r + 1]);
-            l[r] += w0;
-            l[r + 1] += w1;
-            const uint32_t h = pack_bf16(w0, w1);
-            hi[r / 2] = h;
-            lo[r / 2] = pack_bf16(w0 - __uint_as_float(h << 16), w1 - __uint_as_float(h & 0xffff0000u));
+          for (int c = 0; c < R; c += 8) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int r = 0; r < 8; r += 2) {
+              const float2 v = make_float2(ex2(x[c + r]), ex2(x[c + r + 1]));
+              l[(c + r) / 2] = __fadd2_rn(l[(c + r) / 2], v);
+              hi[r / 2] = pack_bf16(v.x, v.y);
+              lo[r / 2] = pack_bf16(v.x - __uint_as_float(hi[r / 2] << 16), v.y - __uint_as_float(hi[r / 2] & 0xffff0000u));
+            }
+            sts128(wp + (rb + c) / 8 * 2048, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            sts128(wp + (N + rb + c) / 8 * 2048, make_uint4(lo[0], lo[1], lo[2], lo[3]));
           }
-          sts128(wp + (2 * w) * 2048, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-          sts128(wp + (2 * w + 1) * 2048, make_uint4(hi[4], hi[5], hi[6], hi[7]));
-          sts128(wp + (N / 8 + 2 * w) * 2048, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-          sts128(wp + (N / 8 + 2 * w + 1) * 2048, make_uint4(lo[4], lo[5], lo[6], lo[7]));
         } else {
           const float ev4 = ev + 4.f;  // weights times 16: at most 2^8
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int r = 0; r < 16; r += 2) {
-            l[r] += ex2(x[r]);
-            l[r + 1] += ex2(x[r + 1]);
+            const float2 v = make_float2(x[r], x[r + 1]), u = __fadd2_rn(v, make_float2(ev4, ev4));
+            l[r / 2] = __fadd2_rn(l[r / 2], make_float2(ex2(v.x), ex2(v.y)));
             uint32_t h, e;
-            split_e4m3x2(ex2(x[r] + ev4), ex2(x[r + 1] + ev4), h, e);
+            split_e4m3x2(ex2(u.x), ex2(u.y), h, e);
             hi[r / 4] = r % 4 ? hi[r / 4] | h << 16 : h;
             lo[r / 4] = r % 4 ? lo[r / 4] | e << 16 : e;
           }
@@ -574,8 +577,8 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
       // ---- sums over the keys; the item's outputs or its partial result
       const int bad = s_bad[si];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {  // the maxima of the last tile have been read
-        float v = l[r];
+      for (int r = 0; r < R; ++r) {  // the maxima of the last tile have been read
+        float v = r & 1 ? l[r / 2].y : l[r / 2].x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         if (lane == r) s_red[r * 4 + q4] = v;
@@ -583,19 +586,19 @@ __global__ void __launch_bounds__(64 + 8 * N, 2)
       if (!(ok = group_sync())) break;
       if (!(ok = wait_bar_warp(&bars->o_done, (g - 1) & 1u, abort))) break;
       tc_fence_after();
-      float o[16];
+      float o[R];
       {
-        float o1[16];
+        float o1[R];
         tmem_ld16x2(tmem + C::kColO + rb + lane_base, tmem + C::kColO + N + rb + lane_base, o, o1);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) o[r] = kF8 ? 0.0625f * (o[r] + 0.0625f * o1[r]) : o[r] + o1[r];
+        for (int r = 0; r < R; ++r) o[r] = kF8 ? 0.0625f * (o[r] + 0.0625f * o1[r]) : o[r] + o1[r];
       }
       tc_fence_before();
       const int ch = D == 128 ? kk : 16 * q4 + lane;   // channel of this TMEM lane
       const bool has = D == 128 || lane < 16;
       const int pslot = 2 * blockIdx.x + (it.kind == 1 ? 1 : 0);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
+      for (int r = 0; r < R; ++r) {
         const int row = rb + r;
         if (row < nrow && has) {
           const float4 v = *reinterpret_cast<const float4 *>(s_red + r * 4);
@@ -655,17 +658,17 @@ cudaError_t launch_decode(const AttnParams &p, bool f8, int d, int rows, const v
   if (!encode_3d_map_swizzled(&tk, k_cache, type, esz, dims, kbox, sw) ||
       !encode_3d_map_swizzled(&tv, v_cache, type, esz, dims, vbox, sw))
     return cudaErrorInvalidValue;
-#define GLINATTN_DECODE(D, F8)                                          \
-  return rows == 16   ? launch<D, F8, 16>(p, tk, tv, ctas, stream)      \
-         : rows == 32 ? launch<D, F8, 32>(p, tk, tv, ctas, stream)      \
-                      : launch<D, F8, kDecodeRows>(p, tk, tv, ctas, stream)
+  // more than 16 rows only with an e4m3 cache (decode_rows)
   if (d == 128) {
-    if (f8) GLINATTN_DECODE(128, true);
-    GLINATTN_DECODE(128, false);
+    if (!f8) return launch<128, false, 16>(p, tk, tv, ctas, stream);
+    return rows == 16   ? launch<128, true, 16>(p, tk, tv, ctas, stream)
+           : rows == 32 ? launch<128, true, 32>(p, tk, tv, ctas, stream)
+                        : launch<128, true, 48>(p, tk, tv, ctas, stream);
   }
-  if (f8) GLINATTN_DECODE(64, true);
-  GLINATTN_DECODE(64, false);
-#undef GLINATTN_DECODE
+  if (!f8) return launch<64, false, 16>(p, tk, tv, ctas, stream);
+  return rows == 16   ? launch<64, true, 16>(p, tk, tv, ctas, stream)
+         : rows == 32 ? launch<64, true, 32>(p, tk, tv, ctas, stream)
+                      : launch<64, true, 48>(p, tk, tv, ctas, stream);
 }
 
 }  // namespace paged

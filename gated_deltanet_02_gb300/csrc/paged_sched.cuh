@@ -413,8 +413,8 @@ cudaError_t launch_merge(const AttnParams &p, int ctas, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, merge_many_rows_kernel<D, kRows>, p);
 }
 
-// rows = 16, 32 or kDecodeRows query rows (tokens x heads of a group) per item
-constexpr int kDecodeRows = 48;
+// Few rows: items of at most 16 query rows (tokens x heads of a group), with an
+// e4m3 cache also 32 or 48.
 cudaError_t launch_decode(const AttnParams &p, bool f8, int d, int rows, const void *k_cache, const void *v_cache,
                           int ctas, cudaStream_t stream);
 
