@@ -24,11 +24,12 @@ namespace glinattn {
 namespace paged {
 
 constexpr int kTileKeys = 128;
-// What an item costs beside its cache tiles, in cache tiles: about 3 us against
-// 1.6 us a tile with 256 rows (without it the SMs that get many short items end last:
-// packed prompts of 200 .. 4001 tokens take TPK us instead of 241 us); with
-// few rows a tile is bound by HBM and hides the next item's beginning.
-constexpr int kItemCostMany = 2, kItemCostFew = 0;
+// What an item costs beside its cache tiles, in cache tiles.  Without it the SMs
+// that get many short items end last: packed prompts of 200 .. 4001 tokens, 16
+// heads over 4, take 189, 169, 154, 157 us with 1, 2, 3, 4 (a prompt of 16,000
+// tokens 762, 707, 670, 680 us).  With few rows a tile is bound by HBM and hides
+// the next item's beginning (0 and 1 measured the same).
+constexpr int kItemCostMany = 3, kItemCostFew = 0;
 
 // Everything that the attention kernels are told.
 struct AttnParams {
@@ -142,25 +143,36 @@ struct PlanShared {
 template <bool kOneTile>
 __device__ inline Plan make_plan(const AttnParams &p, PlanShared *sh) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+  auto head_units = [&](int r) -> long long {  // of one kv head of request r
+    if (r >= p.R) return 0;
+    const Req x = load_req(p, r);
+    if (!x.ok && blockIdx.x == 0 && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_BAD_COUNT);
+    if (x.ntile == 0) return 0;
+    return kOneTile ? kItemCostFew + tile_units(p.tp, x.pos0, x.q_len, 0)
+                    : units_before(p.tp, kItemCostMany, x.pos0, x.q_len, x.ntile, x.ntile);
+  };
   Plan pl;
   pl.r = 0;
   pl.per = pl.u0 = pl.u1 = pl.off = pl.per_head = 0;
-  // Passes over the requests, nt at a time: the total (pass 0), then the request
-  // that holds the CTA's first unit.  With at most nt requests one pass does both.
+  // more requests than threads: their total first
+  const bool one_chunk = p.R <= nt;
+  long long total = 0;
+  if (!one_chunk) {
+    for (int r = tid; r < p.R; r += nt) total += head_units(r);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) sh->scan[warp] = total;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < nw; ++w) total += sh->scan[w];
+    total *= p.Hkv;
+    __syncthreads();
+  }
+  // a scan of nt requests at a time, up to the one that holds the CTA's first unit
   long long before = 0;
-  bool search = p.R <= nt;
   for (int base = 0;; base += nt) {
-    const int r = base + tid;
-    long long head = 0;
-    if (r < p.R) {
-      const Req x = load_req(p, r);
-      if (!x.ok && blockIdx.x == 0 && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_BAD_COUNT);
-      if (x.ntile > 0)
-        head = kOneTile ? kItemCostFew + tile_units(p.tp, x.pos0, x.q_len, 0)
-                        : units_before(p.tp, kItemCostMany, x.pos0, x.q_len, x.ntile, x.ntile);
-    }
-    const long long u = head * p.Hkv;
-    long long upto = u;  // the CTA's inclusive scan
+    const long long head = head_units(base + tid), u = head * p.Hkv;
+    long long upto = u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, upto, o);
@@ -173,32 +185,23 @@ __device__ inline Plan make_plan(const AttnParams &p, PlanShared *sh) {
       if (w < warp) upto += sh->scan[w];
       all += sh->scan[w];
     }
-    const bool last = base + nt >= p.R;
-    if (search ? base == 0 && p.R <= nt : last) {  // the total is known
-      const long long total = before + all;
+    if (base == 0) {
+      if (one_chunk) total = all;
       pl.per = max(1ll, div_pos(total + gridDim.x - 1, gridDim.x));
       pl.u0 = min((long long)blockIdx.x * pl.per, total);
       pl.u1 = min(pl.u0 + pl.per, total);
+      if (pl.u0 >= pl.u1) return pl;  // the same in all threads
     }
-    if (search) {
-      const long long a = before + upto - u;
-      if (a <= pl.u0 && pl.u0 < a + u) {
-        sh->first_r = r;
-        sh->first_off = pl.u0 - a;
-        sh->first_per_head = head;
-      }
+    const long long a = before + upto - u;
+    if (a <= pl.u0 && pl.u0 < a + u) {
+      sh->first_r = base + tid;
+      sh->first_off = pl.u0 - a;
+      sh->first_per_head = head;
     }
     __syncthreads();
     before += all;
-    if (search && (last || before > pl.u0)) break;
-    if (!search && last) {
-      if (pl.u0 >= pl.u1) break;
-      search = true;
-      before = 0;
-      base = -nt;
-    }
+    if (before > pl.u0 || base + nt >= p.R) break;
   }
-  if (pl.u0 >= pl.u1) return pl;
   pl.r = sh->first_r;
   pl.off = sh->first_off;
   pl.per_head = sh->first_per_head;

@@ -279,3 +279,87 @@ def test_far_pages_pass_32_bit_offsets():
         a = glinattn_paged_attention(q, kc, vc, far, kv, qs, max_q_len=n)
         b = glinattn_paged_attention(q, kc[-2:].clone(), vc[-2:].clone(), near, kv, qs, max_q_len=n)
         assert torch.equal(a, b) and float(a.abs().max()) > 0
+
+
+@pytest.mark.parametrize("H,Hkv", [(130, 1), (256, 1), (96, 2)])
+def test_large_groups(H, Hkv):
+    """More heads per kv head than a row tile has rows."""
+    c = paged_case([(3, 140), (1, 1), (2, 300)], Hkv, 64, 16, "bf16", seed=H)
+    _check(c, _q(c, H))
+
+
+@pytest.mark.parametrize("big", [False, True])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_outputs_at_a_16_byte_boundary(cache, big):
+    n = 140 if big else 2
+    c = paged_case([(n, 200), (n, 1000)], 2, 64, 32, cache, seed=15)
+    q = _q(c, 4)
+    want, _ = _run(c, q)
+    flat = torch.full((q.numel() + 16,), 7.0, dtype=torch.bfloat16, device=DEV)
+    o = flat[8:8 + q.numel()].view(q.shape)
+    assert o.data_ptr() % 32 == 16
+    _run(c, q, o=o)
+    assert torch.equal(o, want) and bool((flat[:8] == 7).all()) and bool((flat[8 + q.numel():] == 7).all())
+
+
+@pytest.mark.parametrize("big", [False, True])
+def test_another_stream(big):
+    """Outputs and workspace made by the call belong to the stream that it runs on."""
+    n = 300 if big else 2
+    c = paged_case([(n, 4000), (n, 900)], 2, 128, 16, "bf16", seed=16)
+    q = _q(c, 8)
+    want, _ = _run(c, q)
+    g = dev(c)
+    args, _ = cache_args(g)
+    qd = q.to(DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        outs.append(glinattn_paged_attention(qd, *args, max_q_len=n, stream=side))
+        torch.empty(64 << 20, dtype=torch.uint8, device=DEV).fill_(255)  # on the current stream
+    side.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
+def test_two_calls_at_once():
+    """Decode and prompt calls on two streams, a workspace each."""
+    small = paged_case([(1, 3000 + 7 * r) for r in range(40)], 2, 128, 16, "e4m3", seed=17)
+    large = paged_case([(500, 900), (300, 300)], 2, 128, 16, "bf16", seed=18)
+    jobs = []
+    for c in (small, large):
+        q = _q(c, 8)
+        want, _ = _run(c, q)
+        g = dev(c)
+        args, scales = cache_args(g)
+        jobs.append((q.to(DEV), args, scales, max(n for n, _ in c["lengths"]), want, torch.cuda.Stream(), []))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for q, args, scales, n, _, stream, outs in jobs:
+            outs.append(glinattn_paged_attention(q, *args, **scales, max_q_len=n, stream=stream))
+    torch.cuda.synchronize()
+    for *_, want, _, outs in jobs:
+        assert all(torch.equal(o, want) for o in outs)
+
+
+def test_empty_batches_and_pools():
+    """No request has tokens; no request has a cache; a pool without pages."""
+    c = paged_case([(0, 20), (0, 0)], 1, 64, 16, "bf16", seed=19, num_tok=4)
+    o = torch.full((4, 2, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    got, status = _run(c, _q(c, 2), o=o, max_q_len=4)
+    assert status == 0 and bool((got == 7).all())
+    for n in (2, 100):
+        q = torch.randn((n, 2, 64), device=DEV).to(torch.bfloat16)
+        pool = torch.empty((0, 1, 16, 64), dtype=torch.bfloat16, device=DEV)
+        table = torch.empty((1, 0), dtype=torch.int32, device=DEV)
+        kv = torch.zeros(1, dtype=torch.int32, device=DEV)
+        qs = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+        assert bool((glinattn_paged_attention(q, pool, pool, table, kv, qs, max_q_len=n) == 0).all())
+
+
+@pytest.mark.parametrize("R", [191, 192, 193, 400, 1500])
+def test_more_requests_than_a_planning_pass_takes(R):
+    c = paged_case([((r * 5) % 3, (r * 5) % 3 + (r * 11) % 40) for r in range(R)], 1, 64, 16, "bf16", seed=R)
+    q = _q(c, 2)
+    _check(c, q)
+    _check(c, q, max_q_len=200)      # the kernel for many rows

@@ -83,7 +83,8 @@ def test_cache_call_refusals(name, kw, code):
     (dict(heads=514), UNSUPPORTED), (dict(heads=3), INVALID), (dict(heads=0), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
     (dict(scale=math.inf), INVALID), (dict(scale=math.nan), INVALID), (dict(max_q_len=-1), INVALID),
     (dict(q=None), INVALID), (dict(o=None), INVALID), (dict(q=A + 2), INVALID), (dict(o=A + 4), INVALID),
-    (dict(num_tok=1 << 30), INVALID)])
+    (dict(num_tok=1 << 30), INVALID), (dict(workspace=None), INVALID), (dict(workspace_bytes=64), INVALID),
+    (dict(workspace=16 * A + 8), INVALID), (dict(max_q_len=100, workspace_bytes=1 << 20), INVALID)])
 def test_attention_refusals(kw, code):
     assert G.library().glinattn_paged_attention(ctypes.byref(_attn(**kw)), None) == code
 
@@ -104,6 +105,15 @@ def test_null_structs_and_empty_calls():
     assert lib.glinattn_kv_gather(ctypes.byref(_kv(num_req=0)), None) == 0
     assert lib.glinattn_paged_attention(ctypes.byref(_attn(num_tok=0, q=None, o=None)), None) == 0
     assert lib.glinattn_accept_drafts(ctypes.byref(_acc(num_req=0)), None) == 0
+
+
+def test_workspace_size_goes_by_sizes_alone():
+    lib = G.library()
+    size = lambda **kw: lib.glinattn_paged_attention_workspace_size(ctypes.byref(_attn(**kw)))  # noqa: E731
+    few, many = size(max_q_len=1), size(max_q_len=1000)
+    assert 0 < few < many < 1 << 27
+    assert size(max_q_len=1, num_req=200, num_tok=200, max_pages=4096) == few
+    assert size(num_tok=0) == 0 and size(num_req=0) == 0 and size(head_dim=96) == 0
 
 
 def _cache(P_=4, H=2, page=16, d=64, dtype=torch.bfloat16):
