@@ -264,13 +264,14 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         }
       }
     } else if (warp <= C::kIssuers) {
-      // ============ MMA issue (one lane): row tiles w0 .. w1 - 1 ============
-      const int w0 = C::kIssuers == 2 ? warp - 1 : 0, w1 = C::kIssuers == 2 ? warp : 2;
+      // ============ MMA issue (one lane): kMine row tiles from w0 on ============
+      constexpr int kMine = 2 / C::kIssuers;
+      const int w0 = C::kIssuers == 2 ? warp - 1 : 0;
       constexpr uint32_t id_s = kF8 ? idesc_f8(128, 128, false, false) : idesc_bf16(128, 128, false, false);
       constexpr uint32_t id_o = idesc_bf16(128, D, false, true);
       constexpr uint32_t hi_s = kF8 && D == 64 ? desc_hi(512, kSw64) : desc_hi(1024, kSw128);
       const bool leader = elect_one();
-      uint32_t g = 0, slot = 0, np[2] = {0, 0}, nq[2] = {0, 0}, nf[2] = {0, 0};  // g: cache tiles so far
+      uint32_t g = 0, slot = 0, np[kMine] = {}, nq[kMine] = {}, nf[kMine] = {};  // g: cache tiles so far
       // stages of tile t's keys and values
       auto k_stage = [](uint32_t t) { return kF8 ? t % C::kRawK : 2 * t % ST; };
       auto v_stage = [](uint32_t t) { return kF8 ? t % ST : (2 * t + 1) % ST; };
@@ -282,8 +283,9 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         return wait_bar_warp<false>(&bars->full[v_stage(t)], (kF8 ? t / ST : (2 * t + 1) / ST) & 1u, abort);
       };
       // S_w = Q_w K^T; with P beside S the scores before it have to be read
-      auto issue_s = [&](int w, uint32_t t) -> bool {
-        if (C::kSepP && !wait_bar_warp<false>(&bars->s_free[w], (nf[w]++ & 1u) ^ 1u, abort)) return false;
+      auto issue_s = [&](int i, uint32_t t) -> bool {
+        const int w = w0 + i;
+        if (C::kSepP && !wait_bar_warp<false>(&bars->s_free[w], (nf[i]++ & 1u) ^ 1u, abort)) return false;
         tc_fence_after();
         const uint32_t d = tmem + C::kColS + 128 * w, a = desc_lo(sb + w * C::kQTile, 16);
         const uint32_t b = desc_lo(kF8 ? sb + C::kOffRawK + k_stage(t) * C::kRawBytes : sb + C::kOffRing + k_stage(t) * C::kStageBytes, 16);
@@ -306,8 +308,9 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         return true;
       };
       // O_w (+)= P_w V, 64 keys' weights at a time
-      auto issue_o = [&](int w, uint32_t t, bool first) -> bool {
-        const uint32_t b = desc_lo(sb + C::kOffRing + v_stage(t) * C::kStageBytes, 16384), ph = np[w]++ & 1u;
+      auto issue_o = [&](int i, uint32_t t, bool first) -> bool {
+        const int w = w0 + i;
+        const uint32_t b = desc_lo(sb + C::kOffRing + v_stage(t) * C::kStageBytes, 16384), ph = np[i]++ & 1u;
         const uint32_t d = tmem + C::kColO + D * w, a = tmem + C::kColP + C::kPStep * w;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -328,48 +331,56 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         if (used) umma_commit(bar);
         else mbar_arrive(bar);
       };
-      for (bool ok = true; ok;) {
+      auto k_release = [&](uint32_t t, bool used) { release(kF8 ? &bars->rawk_empty[k_stage(t)] : &bars->empty[k_stage(t)], used); };
+      Item it;
+      int nw[kMine], most;
+      auto next_item = [&]() -> bool {
         const int si = slot % kItems;
-        if (!wait_bar_warp<false>(&bars->item_full[si], (slot / kItems) & 1u, abort)) break;
-        const Item it = bars->item[si];
+        if (!wait_bar_warp<false>(&bars->item_full[si], (slot / kItems) & 1u, abort)) return false;
+        it = bars->item[si];
         warp_arrive(&bars->item_empty[si]);
-        if (it.kind < 0) break;
         ++slot;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) nw[i] = it.kind < 0 ? 0 : last_tile(it, p.G, inv_g, w0 + i) - it.j0;
+        most = max(nw[0], nw[kMine - 1]);
+        return true;
+      };
+      bool ok = next_item();
+      while (ok && it.kind >= 0) {
         const int n = it.j1 - it.j0;
-        int nw[2];
-        for (int w = 0; w < 2; ++w) nw[w] = last_tile(it, p.G, inv_g, w) - it.j0;
-        const int most = C::kIssuers == 2 ? nw[w0] : max(nw[0], nw[1]);
-        auto k_release = [&](int j) {
-          release(kF8 ? &bars->rawk_empty[k_stage(g + j)] : &bars->empty[k_stage(g + j)], j < most);
-        };
         // first scores
         if (!(ok = k_landed(g))) break;
-        for (int w = w0; w < w1 && ok; ++w)
-          if (nw[w] > 0) ok = wait_bar_warp<false>(&bars->q_ready[w], nq[w]++ & 1u, abort) && issue_s(w, g);
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+          if (ok && nw[i] > 0) ok = wait_bar_warp<false>(&bars->q_ready[w0 + i], nq[i]++ & 1u, abort) && issue_s(i, g);
         if (!ok) break;
-        k_release(0);
+        k_release(g, most > 0);
         for (int j = 0; j < n && ok; ++j) {
-          if (C::kSepP && j + 1 < n) {  // the next scores before this tile's second product
+          const bool last = j + 1 == n;
+          if (C::kSepP && !last) {  // the next scores before this tile's second product
             if (!(ok = k_landed(g + j + 1))) break;
-            for (int w = w0; w < w1 && ok; ++w)
-              if (j + 1 < nw[w]) ok = issue_s(w, g + j + 1);
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+              if (ok && j + 1 < nw[i]) ok = issue_s(i, g + j + 1);
             if (!ok) break;
-            k_release(j + 1);
+            k_release(g + j + 1, j + 1 < most);
           }
           if (!(ok = v_landed(g + j))) break;
-          if (!C::kSepP && j + 1 < n && !(ok = k_landed(g + j + 1))) break;
-          for (int w = w0; w < w1 && ok; ++w) {
-            if (j < nw[w]) {
-              ok = issue_o(w, g + j, j == 0);
-              if (ok && leader && (C::kSepP || j + 1 == nw[w])) umma_commit(&bars->o_done[w]);
+          if (!C::kSepP && !last && !(ok = k_landed(g + j + 1))) break;
+#pragma unroll
+          for (int i = 0; i < kMine; ++i) {
+            if (ok && j < nw[i]) {
+              ok = issue_o(i, g + j, j == 0);
+              if (ok && leader && (C::kSepP || j + 1 == nw[i])) umma_commit(&bars->o_done[w0 + i]);
             }
-            if (ok && !C::kSepP && j + 1 < nw[w]) ok = issue_s(w, g + j + 1);
+            if (!C::kSepP && ok && j + 1 < nw[i]) ok = issue_s(i, g + j + 1);
           }
           if (!ok) break;
           release(&bars->empty[v_stage(g + j)], j < most);
-          if (!C::kSepP && j + 1 < n) k_release(j + 1);
+          if (!C::kSepP && !last) k_release(g + j + 1, j + 1 < most);
         }
         g += n;
+        if (ok) ok = next_item();
       }
     }
   } else if (warp < 12) {
@@ -389,69 +400,75 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     // q of the warp's 32 rows into shared memory, D / 8 lanes a row; rows past
     // the last are zero.  Only for a row tile that has work in the item: its
     // softmax warps then wait for the MMA warp's answer, so that q_ready is
-    // never a phase ahead of its reader.  bf16 rows are copied asynchronously
-    // (fetch_q once S of the last tile is there, q_fetched behind that tile's weights).
-    auto fetch_q = [&](const Item &it) {
-      if (kF8 || it.kind < 0 || last_tile(it, p.G, inv_g, w) <= it.j0) return;
-      constexpr int kLanes = D / 8, kPer = 32 / kLanes;
-      const int c = lane % kLanes, nrow = it.ntok * p.G;
+    // never a phase ahead of its reader.  The rows are copied asynchronously
+    // (fetch_q once S of the last tile is there, q_fetched behind that tile's weights);
+    // an e4m3 cache's are split there in place, half a bf16 row where each part goes.
+    constexpr int kLanes = D / 8, kPer = 32 / kLanes, kQU = 2;
+    const int qc = lane % kLanes, qr = 32 * q4 + lane / kLanes;  // the lane's 16 bytes, and its row of the first kPer
+    auto q_at = [&](int r) -> uint32_t {
+      if constexpr (kF8) {
+        constexpr uint32_t kHalf = kLanes / 2;
+        return w * C::kQTile + qc / kHalf * (128 * D) + r * D + (((uint32_t)(qc ^ r) % kHalf) << 4);
+      } else {
+        return w * C::kQTile + sw128_offset(r, qc * 8, 128);
+      }
+    };
+    // (items are read where they are needed: 128 scores a thread leave few registers)
+    auto fetch_q = [&](uint32_t slot) {
+      const Item it = bars->item[slot % kItems];
+      if (it.kind < 0 || last_tile(it, p.G, inv_g, w) <= it.j0) return;
+      const int nrow = it.ntok * p.G;
 #pragma unroll 1
-      for (int k = 0; k < 32; k += kPer) {
-        const int r = 32 * q4 + k + lane / kLanes;
+      for (int r = qr; r < 32 * q4 + 32; r += kPer) {
         const bool has = 128 * w + r < nrow;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sb + w * C::kQTile + sw128_offset(r, c * 8, 128)),
-                     "l"(p.q + (has ? row_at(it, 128 * w + r) + c * 8 : 0)), "r"(has ? 16 : 0)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sb + q_at(r)),
+                     "l"(p.q + (has ? row_at(it, 128 * w + r) + qc * 8 : 0)), "r"(has ? 16 : 0)
                      : "memory");
       }
     };
-    auto q_fetched = [&](const Item &it) {
+    auto q_fetched = [&](uint32_t slot) {
+      const Item &it = bars->item[slot % kItems];
       if (it.kind < 0 || last_tile(it, p.G, inv_g, w) <= it.j0) return;
+      asm volatile("cp.async.wait_all;" ::: "memory");
       if constexpr (kF8) {
-        constexpr int kLanes = D / 8, kPer = 32 / kLanes;
-        const int c = lane % kLanes, nrow = it.ntok * p.G;
+        __syncwarp();
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint4 x[16 / kPer];
+        for (int r0 = qr; r0 < 32 * q4 + 32; r0 += kQU * kPer) {
+          uint4 x[kQU];
 #pragma unroll
-          for (int k = 0; k < 16 / kPer; ++k) {
-            const int r = 128 * w + 32 * q4 + 16 * h + k * kPer + lane / kLanes;
-            x[k] = r < nrow ? __ldg(reinterpret_cast<const uint4 *>(p.q + row_at(it, r)) + c) : make_uint4(0, 0, 0, 0);
-          }
+          for (int k = 0; k < kQU; ++k) x[k] = lds128(sb + q_at(r0 + k * kPer));
+          __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 16 / kPer; ++k) {
-            const int r = 32 * q4 + 16 * h + k * kPer + lane / kLanes;
+          for (int k = 0; k < kQU; ++k) {
+            const int r = r0 + k * kPer;
             uint2 hi, lo;
             const float scale = split_q<kLanes>(x[k], hi, lo);
-            if (c == 0) s_qs[128 * w + r] = scale * p.c;
-            const uint32_t ch = c >> 1, at = (D == 128 ? r * 128u + ((ch ^ (r & 7u)) << 4) : r * 64u + ((ch ^ ((r >> 1) & 3u)) << 4)) + (c & 1) * 8;
+            if (qc == 0) s_qs[128 * w + r] = scale * p.c;
+            const uint32_t ch = qc >> 1, at = (D == 128 ? r * 128u + ((ch ^ (r & 7u)) << 4) : r * 64u + ((ch ^ ((r >> 1) & 3u)) << 4)) + (qc & 1) * 8;
             *reinterpret_cast<uint2 *>(smem + w * C::kQTile + at) = hi;
             *reinterpret_cast<uint2 *>(smem + w * C::kQTile + 128 * D + at) = lo;
           }
         }
-      } else {
-        asm volatile("cp.async.wait_all;" ::: "memory");
       }
       fence_proxy_async_smem();
       warp_arrive(&bars->q_ready[w]);
     };
     bool ok = wait_bar_warp(&bars->item_full[0], 0, abort);
-    Item it;
     if (ok) {
-      it = bars->item[0];
-      fetch_q(it);
-      q_fetched(it);
+      fetch_q(0);
+      q_fetched(0);
     }
-    while (ok && it.kind >= 0) {
-      const int si = slot % kItems;
-      const int n = it.j1 - it.j0, nw = last_tile(it, p.G, inv_g, w) - it.j0;
+    while (ok) {
+      const Item &it = bars->item[slot % kItems];
+      if (it.kind < 0) break;
+      const int j0 = it.j0, n = it.j1 - j0, nw = last_tile(it, p.G, inv_g, w) - j0;
       const int end = it.pos0 + it.ntok;                    // keys behind it are not there
       const int lim = it.pos0 + (int)((uint32_t)row * inv_g >> 16);  // the row's last key
       const int first_lim = it.pos0 + (int)((uint32_t)(128 * w) * inv_g >> 16);  // the first row's
       const float c = kF8 ? s_qs[row] : p.c;                // written by this warp
       float m = -INFINITY, l = 0.f;
-      Item nx = it;
       for (int jj = 0; jj < nw; ++jj) {
-        const int j = it.j0 + jj;
+        const int j = j0 + jj;
         if (!(ok = wait_bar_warp<false>(&bars->s_ready[w], ns++ & 1u, abort))) break;
         tc_fence_after();
         float s[128];
@@ -464,8 +481,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         if (jj == nw - 1) {  // the last S of the item's q is here: the next item's q may come
           const uint32_t ns_ = slot + 1;
           if (!(ok = wait_bar_warp(&bars->item_full[ns_ % kItems], (ns_ / kItems) & 1u, abort))) break;
-          nx = bars->item[ns_ % kItems];
-          fetch_q(nx);
+          fetch_q(ns_);
         }
         if constexpr (kF8) {  // the keys' scales
           const uint32_t ss = (g + jj) % C::kScaleSlots;
@@ -561,11 +577,10 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       ++slot;
       if (nw <= 0) {
         if (!(ok = wait_bar_warp(&bars->item_full[slot % kItems], (slot / kItems) & 1u, abort))) break;
-        nx = bars->item[slot % kItems];
-        fetch_q(nx);
+        fetch_q(slot);
       }
-      q_fetched(nx);
-      const int bad = bars->bad[si];
+      q_fetched(slot);
+      const int si = (slot - 1) % kItems, bad = bars->bad[si];
       const bool has = row < it.ntok * p.G;
       const size_t pslot = (size_t)(2 * blockIdx.x + (it.kind == 1 ? 1 : 0));
       if (nw > 0) {
@@ -598,7 +613,6 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         if (bad && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_BAD_SLOT);
       }
       warp_arrive(&bars->item_empty[si]);
-      it = nx;
     }
   } else if constexpr (kF8) {
     // ============ e4m3 cache: the keys' scales as floats; values times their scale, as the bf16 tile ============
@@ -606,7 +620,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     const int ct = tid - 384;
     constexpr int kLanes = D / 16;                   // lanes of a key's row, 16 values each
     constexpr int kKeys = 128 / kLanes;              // keys a pass of the 128 threads takes: 16 or 32
-    constexpr int kPass = kTileKeys / kKeys;
+    constexpr int kPass = kTileKeys / kKeys, kCU = 2;
     const int c16 = ct % kLanes, k0 = ct / kLanes;   // key of pass i: i kKeys + k0
     uint32_t g = 0, slot = 0;
     for (bool ok = true; ok;) {
@@ -630,18 +644,19 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         const uint8_t *code = smem + C::kOffCode + (C::kRawK + rv) * kTileKeys;
         const uint32_t base = sb + C::kOffRing + s * C::kStageBytes;
         const int there = end - j * kTileKeys;              // keys of the tile that are there
+        // a short loop: the unrolled one takes the softmax's code out of the instruction caches
+#pragma unroll 1
+        for (int i0 = 0; i0 < kPass; i0 += kCU) {
+          uint4 y[kCU];
+          uint32_t cd[kCU];
 #pragma unroll
-        for (int i0 = 0; i0 < kPass; i0 += 4) {
-          uint4 y[4];
-          uint32_t cd[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < kCU; ++i) {
             const int key = (i0 + i) * kKeys + k0;
             y[i] = lds128(raw + key * D + c16 * 16);
             cd[i] = code[key];
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < kCU; ++i) {
             const int key = (i0 + i) * kKeys + k0;
             if (key >= there) {                             // whatever was in the stage
               y[i] = make_uint4(0, 0, 0, 0);

@@ -405,7 +405,9 @@ cudaError_t launch_merge(const AttnParams &p, int ctas, cudaStream_t stream) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas, kFewRows ? kRows : kRows / 32, 1);
+  // rows that an item can have, however many there is room for
+  const int rows = (int)min((long long)kRows, (long long)min(p.max_q, p.tp) * p.G);
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(kFewRows ? rows : (rows + 31) / 32), 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = stream;
   cfg.attrs = &attr;
