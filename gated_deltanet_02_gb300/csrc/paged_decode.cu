@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
     tmem_relinquish();
   }
   tc_fence_before();
-  const Plan plan = make_plan<true>(p, &bars->plan);  // has CTA barriers
+  const Plan plan = make_plan<true, kItemCostFew>(p, &bars->plan);  // has CTA barriers
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
 
   if (warp == 0) {
     // ============ the walk over the items, and TMA (a page per lane) ============
-    Walk<true> walk(p, plan, lane);
+    Walk<true, kItemCostFew> walk(p, plan, lane);
     Item it;
     uint32_t sc = 0;                 // stages used so far
     uint32_t g = 0;                  // tiles so far

@@ -49,8 +49,10 @@ constexpr float kSlack = 8.f;  // log2 of the largest weight
 
 template <int D, bool kF8>
 struct Cfg {
-  static constexpr int kThreads = kF8 ? 512 : 384;
-  static constexpr uint32_t kQTile = 128 * D * 2;             // bf16, or two e4m3 parts
+  static constexpr int kThreads = kF8 ? 512 : 384, kCost = kF8 ? kItemCostManyF8 : kItemCostMany;
+  // q: planes of 256 rows of 128 bytes (64 channels, bf16), or the two e4m3 parts;
+  // they come as the same planes of half the channels each
+  static constexpr uint32_t kQRow = kF8 ? D : 128, kQPlane = 2 * 128 * kQRow, kQPlanes = 512 * D / kQPlane;
   static constexpr uint32_t kStageBytes = kTileKeys * D * 2;  // a bf16 tile
   static constexpr uint32_t kRawBytes = kTileKeys * D;        // an e4m3 tile
   // bf16: K and V tiles in turn; e4m3: V tiles after their conversion, and K
@@ -58,7 +60,7 @@ struct Cfg {
   static constexpr int kStages = kF8 ? 2 : D == 128 ? 4 : 6;
   static constexpr int kRawK = kF8 ? 3 : 0, kRawV = kF8 ? 2 : 0;
   static constexpr int kScaleSlots = kF8 ? 8 : 0;             // tiles of key scales as floats
-  static constexpr uint32_t kOffRing = 2 * kQTile;
+  static constexpr uint32_t kOffRing = kQPlanes * kQPlane;
   static constexpr uint32_t kOffRawK = kOffRing + kStages * kStageBytes;
   static constexpr uint32_t kOffRawV = kOffRawK + kRawK * kRawBytes;
   static constexpr uint32_t kOffCode = kOffRawV + kRawV * kRawBytes;      // scale codes beside the raw tiles
@@ -79,7 +81,7 @@ struct Cfg {
 struct Bars {
   uint64_t full[6], empty[6];             // bf16 tiles
   uint64_t rawk_full[3], rawk_empty[3], rawv_full[2], rawv_empty[2], scale_ready[8];
-  uint64_t s_ready[2], s_free[2], p_ready[2][2], q_ready[2], o_done[2];
+  uint64_t s_ready[2], s_free[2], p_ready[2][2], q_full, q_empty, q_ready[2], o_done[2];
   uint64_t item_full[kItems], item_empty[kItems];
   Item item[kItems];
   PlanShared plan;
@@ -134,8 +136,8 @@ __device__ __forceinline__ void store64(void *dst, const uint32_t (&u)[16]) {
 
 template <int D, bool kF8>
 __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
-    prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnParams p,
-                   const uint8_t *v_cache) {
+    prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                   const __grid_constant__ CUtensorMap tv, const AttnParams p, const uint8_t *v_cache) {
   using C = Cfg<D, kF8>;
   constexpr int ST = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -169,9 +171,11 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       mbar_init(&bars->q_ready[i], 4);
       mbar_init(&bars->o_done[i], 1);
     }
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, C::kIssuers);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bars->item_full[i], 1);
-      mbar_init(&bars->item_empty[i], C::kIssuers + 8 + (kF8 ? 4 : 0));
+      mbar_init(&bars->item_empty[i], 1 + C::kIssuers + 8 + (kF8 ? 4 : 0));
       bars->bad[i] = 0;
     }
     bars->abort = 0;
@@ -183,7 +187,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  const Plan plan = make_plan<false>(p, &bars->plan);
+  const Plan plan = make_plan<false, C::kCost>(p, &bars->plan);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
@@ -196,7 +200,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     regs_dec<kF8 ? 64 : 80>();
     if (warp == 0) {
       // ============ the walk over the items, and TMA ============
-      Walk<false> walk(p, plan, lane);
+      Walk<false, C::kCost> walk(p, plan, lane);
       Item it;
       uint32_t sc = 0, slot = 0;
       for (bool ok = true; ok;) {
@@ -287,20 +291,20 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         const int w = w0 + i;
         if (C::kSepP && !wait_bar_warp<false>(&bars->s_free[w], (nf[i]++ & 1u) ^ 1u, abort)) return false;
         tc_fence_after();
-        const uint32_t d = tmem + C::kColS + 128 * w, a = desc_lo(sb + w * C::kQTile, 16);
+        const uint32_t d = tmem + C::kColS + 128 * w, a = desc_lo(sb + w * (C::kQPlane / 2), 16);
         const uint32_t b = desc_lo(kF8 ? sb + C::kOffRawK + k_stage(t) * C::kRawBytes : sb + C::kOffRing + k_stage(t) * C::kStageBytes, 16);
         if (leader) {
           if constexpr (kF8) {  // both parts of q against the same keys
 #pragma unroll
             for (int ks = 0; ks < 2 * (D / 32); ++ks) {
               const uint32_t k = ks % (D / 32) * 32;
-              mma_ss<true>(d, a + (ks / (D / 32) * (128 * D) + k >> 4), hi_s, b + (k >> 4), hi_s, id_s, ks > 0);
+              mma_ss<true>(d, a + (ks / (D / 32) * C::kQPlane + k >> 4), hi_s, b + (k >> 4), hi_s, id_s, ks > 0);
             }
           } else {
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-              mma_ss<false>(d, a + off, hi_s, b + off, hi_s, id_s, ks > 0);
+              const uint32_t k = (ks & 3) * 32;
+              mma_ss<false>(d, a + ((ks >> 2) * C::kQPlane + k >> 4), hi_s, b + ((ks >> 2) * 16384 + k >> 4), hi_s, id_s, ks > 0);
             }
           }
           umma_commit(&bars->s_ready[w]);
@@ -324,16 +328,20 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         }
         return true;
       };
-      // a stage is free when every issuer says so: behind its products, or at once
-      // (but not before the stage is filled) where its row tiles have none in it
+      Item it;
+      int nw[kMine], most;
+      // a stage (and q) is free when every issuer says so: behind its products, or at
+      // once (but not before it is filled) where its row tiles have none in it
       auto release = [&](uint64_t *bar, bool used) {
         if (!leader) return;
         if (used) umma_commit(bar);
         else mbar_arrive(bar);
       };
+      // behind the products with the item's tile j: is it the last that reads q?
+      auto q_release = [&](int j) {
+        if (j == max(most, 1) - 1) release(&bars->q_empty, most > 0);
+      };
       auto k_release = [&](uint32_t t, bool used) { release(kF8 ? &bars->rawk_empty[k_stage(t)] : &bars->empty[k_stage(t)], used); };
-      Item it;
-      int nw[kMine], most;
       auto next_item = [&]() -> bool {
         const int si = slot % kItems;
         if (!wait_bar_warp<false>(&bars->item_full[si], (slot / kItems) & 1u, abort)) return false;
@@ -345,6 +353,10 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         most = max(nw[0], nw[kMine - 1]);
         return true;
       };
+      auto q_there = [&](int i) -> bool {
+        return kF8 ? wait_bar_warp<false>(&bars->q_ready[w0 + i], nq[i]++ & 1u, abort)
+                   : wait_bar_warp<false>(&bars->q_full, (slot - 1) & 1u, abort);
+      };
       bool ok = next_item();
       while (ok && it.kind >= 0) {
         const int n = it.j1 - it.j0;
@@ -352,9 +364,11 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         if (!(ok = k_landed(g))) break;
 #pragma unroll
         for (int i = 0; i < kMine; ++i)
-          if (ok && nw[i] > 0) ok = wait_bar_warp<false>(&bars->q_ready[w0 + i], nq[i]++ & 1u, abort) && issue_s(i, g);
+          if (ok && nw[i] > 0) ok = q_there(i) && issue_s(i, g);
+        if (C::kIssuers == 2 && ok && most <= 0) ok = wait_bar_warp<false>(&bars->q_full, (slot - 1) & 1u, abort);
         if (!ok) break;
         k_release(g, most > 0);
+        q_release(0);
         for (int j = 0; j < n && ok; ++j) {
           const bool last = j + 1 == n;
           if (C::kSepP && !last) {  // the next scores before this tile's second product
@@ -364,6 +378,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
               if (ok && j + 1 < nw[i]) ok = issue_s(i, g + j + 1);
             if (!ok) break;
             k_release(g + j + 1, j + 1 < most);
+            q_release(j + 1);
           }
           if (!(ok = v_landed(g + j))) break;
           if (!C::kSepP && !last && !(ok = k_landed(g + j + 1))) break;
@@ -377,10 +392,31 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
           }
           if (!ok) break;
           release(&bars->empty[v_stage(g + j)], j < most);
-          if (!C::kSepP && !last) k_release(g + j + 1, j + 1 < most);
+          if (!C::kSepP && !last) {
+            k_release(g + j + 1, j + 1 < most);
+            q_release(j + 1);
+          }
         }
         g += n;
         if (ok) ok = next_item();
+      }
+    } else if (warp == 3) {
+      // ============ q: an item's rows (tokens x heads of the group) are a box ============
+      // Rows behind the item's last hold other tokens' q, or zeros behind the last
+      // token; nothing that comes of them is stored.
+      for (uint32_t slot = 0;; ++slot) {
+        const int si = slot % kItems;
+        if (!wait_bar_warp(&bars->item_full[si], (slot / kItems) & 1u, abort)) break;
+        const int kind = bars->item[si].kind, row0 = bars->item[si].row0, hk = bars->item[si].hk;
+        warp_arrive(&bars->item_empty[si]);
+        if (kind < 0 || !wait_bar_warp(&bars->q_empty, (slot & 1u) ^ 1u, abort)) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->q_full, C::kQPlanes * (uint32_t)(p.tp * p.G) * C::kQRow);
+#pragma unroll
+          for (uint32_t h = 0; h < C::kQPlanes; ++h)
+            tma_load_3d(smem + h * C::kQPlane, &tq, &bars->q_full, (int)(h * C::kQRow / 2), hk * p.G, row0);
+        }
+        __syncwarp();
       }
     }
   } else if (warp < 12) {
@@ -397,67 +433,40 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       const int tok = (int)((uint32_t)r * inv_g >> 16);
       return ((size_t)(it.row0 + tok) * p.H + it.hk * p.G + (r - tok * p.G)) * D;
     };
-    // q of the warp's 32 rows into shared memory, D / 8 lanes a row; rows past
-    // the last are zero.  Only for a row tile that has work in the item: its
-    // softmax warps then wait for the MMA warp's answer, so that q_ready is
-    // never a phase ahead of its reader.  The rows are copied asynchronously
-    // (fetch_q once S of the last tile is there, q_fetched behind that tile's weights);
-    // an e4m3 cache's are split there in place, half a bf16 row where each part goes.
-    constexpr int kLanes = D / 8, kPer = 32 / kLanes, kQU = 2;
-    const int qc = lane % kLanes, qr = 32 * q4 + lane / kLanes;  // the lane's 16 bytes, and its row of the first kPer
-    auto q_at = [&](int r) -> uint32_t {
-      if constexpr (kF8) {
-        constexpr uint32_t kHalf = kLanes / 2;
-        return w * C::kQTile + qc / kHalf * (128 * D) + r * D + (((uint32_t)(qc ^ r) % kHalf) << 4);
-      } else {
-        return w * C::kQTile + sw128_offset(r, qc * 8, 128);
-      }
-    };
-    // (items are read where they are needed: 128 scores a thread leave few registers)
-    auto fetch_q = [&](uint32_t slot) {
-      const Item it = bars->item[slot % kItems];
-      if (it.kind < 0 || last_tile(it, p.G, inv_g, w) <= it.j0) return;
-      const int nrow = it.ntok * p.G;
-#pragma unroll 1
-      for (int r = qr; r < 32 * q4 + 32; r += kPer) {
-        const bool has = 128 * w + r < nrow;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sb + q_at(r)),
-                     "l"(p.q + (has ? row_at(it, 128 * w + r) + qc * 8 : 0)), "r"(has ? 16 : 0)
-                     : "memory");
-      }
-    };
-    auto q_fetched = [&](uint32_t slot) {
+    // An e4m3 cache's q, D / 8 lanes a row: split in place, row by row, half a row
+    // of bf16 where each part goes.  Only for a row tile that has work in the item:
+    // its softmax warps then wait for the MMA warp's answer, so that q_ready is
+    // never a phase ahead of its reader.
+    auto split_rows = [&](uint32_t slot) -> bool {
       const Item &it = bars->item[slot % kItems];
-      if (it.kind < 0 || last_tile(it, p.G, inv_g, w) <= it.j0) return;
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if constexpr (kF8) {
-        __syncwarp();
+      if (!kF8 || it.kind < 0 || last_tile(it, p.G, inv_g, w) <= it.j0) return true;
+      if (!wait_bar_warp(&bars->q_full, slot & 1u, abort)) return false;
+      constexpr uint32_t kLanes = D / 8, kPer = 32 / kLanes, kQU = 2;
+      const uint32_t c = lane % kLanes, half = c / (kLanes / 2);
+      auto at = [&](uint32_t r, uint32_t unit) { return r * C::kQRow + ((unit ^ (D == 128 ? r & 7u : r >> 1 & 3u)) << 4); };
 #pragma unroll 1
-        for (int r0 = qr; r0 < 32 * q4 + 32; r0 += kQU * kPer) {
-          uint4 x[kQU];
+      for (uint32_t r0 = row - lane + lane / kLanes, n = 0; n < kLanes; n += kQU, r0 += kQU * kPer) {
+        uint4 x[kQU];
 #pragma unroll
-          for (int k = 0; k < kQU; ++k) x[k] = lds128(sb + q_at(r0 + k * kPer));
-          __syncwarp();
+        for (uint32_t k = 0; k < kQU; ++k) x[k] = lds128(sb + half * C::kQPlane + at(r0 + k * kPer, c % (kLanes / 2)));
+        __syncwarp();
 #pragma unroll
-          for (int k = 0; k < kQU; ++k) {
-            const int r = r0 + k * kPer;
-            uint2 hi, lo;
-            const float scale = split_q<kLanes>(x[k], hi, lo);
-            if (qc == 0) s_qs[128 * w + r] = scale * p.c;
-            const uint32_t ch = qc >> 1, at = (D == 128 ? r * 128u + ((ch ^ (r & 7u)) << 4) : r * 64u + ((ch ^ ((r >> 1) & 3u)) << 4)) + (qc & 1) * 8;
-            *reinterpret_cast<uint2 *>(smem + w * C::kQTile + at) = hi;
-            *reinterpret_cast<uint2 *>(smem + w * C::kQTile + 128 * D + at) = lo;
-          }
+        for (uint32_t k = 0; k < kQU; ++k) {
+          const uint32_t r = r0 + k * kPer;
+          uint2 hi, lo;
+          const float scale = split_q<kLanes>(x[k], hi, lo);
+          if (c == 0) s_qs[r] = scale * p.c;
+          uint8_t *dst = smem + at(r, c >> 1) + (c & 1) * 8;
+          *reinterpret_cast<uint2 *>(dst) = hi;
+          *reinterpret_cast<uint2 *>(dst + C::kQPlane) = lo;
         }
       }
       fence_proxy_async_smem();
       warp_arrive(&bars->q_ready[w]);
+      return true;
     };
     bool ok = wait_bar_warp(&bars->item_full[0], 0, abort);
-    if (ok) {
-      fetch_q(0);
-      q_fetched(0);
-    }
+    if (ok) ok = split_rows(0);
     while (ok) {
       const Item &it = bars->item[slot % kItems];
       if (it.kind < 0) break;
@@ -477,11 +486,6 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         if (C::kSepP) {
           tc_fence_before();
           warp_arrive(&bars->s_free[w]);
-        }
-        if (jj == nw - 1) {  // the last S of the item's q is here: the next item's q may come
-          const uint32_t ns_ = slot + 1;
-          if (!(ok = wait_bar_warp(&bars->item_full[ns_ % kItems], (ns_ / kItems) & 1u, abort))) break;
-          fetch_q(ns_);
         }
         if constexpr (kF8) {  // the keys' scales
           const uint32_t ss = (g + jj) % C::kScaleSlots;
@@ -575,11 +579,8 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       g += n;
       // ---- the next item's q, before this item's outputs
       ++slot;
-      if (nw <= 0) {
-        if (!(ok = wait_bar_warp(&bars->item_full[slot % kItems], (slot / kItems) & 1u, abort))) break;
-        fetch_q(slot);
-      }
-      q_fetched(slot);
+      if (!(ok = wait_bar_warp(&bars->item_full[slot % kItems], (slot / kItems) & 1u, abort))) break;
+      if (!(ok = split_rows(slot))) break;
       const int si = (slot - 1) % kItems, bad = bars->bad[si];
       const bool has = row < it.ntok * p.G;
       const size_t pslot = (size_t)(2 * blockIdx.x + (it.kind == 1 ? 1 : 0));
@@ -701,9 +702,14 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
 template <int D, bool kF8>
 cudaError_t launch(const AttnParams &p, const void *k_cache, const void *v_cache, int ctas, cudaStream_t stream) {
   using C = Cfg<D, kF8>;
-  CUtensorMap tk = {}, tv = {};
+  CUtensorMap tq = {}, tk = {}, tv = {};
   const long long dims[3] = {D, p.page, p.P > 0 ? (long long)p.P * p.Hkv : 1};
   if (p.P == 0) k_cache = v_cache = p.q;  // an empty pool: nothing is ever loaded
+  const long long q_dims[3] = {D, p.H, p.N};
+  const int q_box[3] = {(int)C::kQRow / 2, p.G, p.tp};
+  if (!encode_3d_map_swizzled(&tq, p.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q_dims, q_box,
+                              C::kQRow == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+    return cudaErrorInvalidValue;
   if (kF8) {
     const int box[3] = {D, p.page, 1};
     if (!encode_3d_map_swizzled(&tk, k_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, dims, box,
@@ -718,7 +724,7 @@ cudaError_t launch(const AttnParams &p, const void *k_cache, const void *v_cache
   auto kernel = prefill_kernel<D, kF8>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<ctas, C::kThreads, C::kSmem, stream>>>(tk, tv, p, (const uint8_t *)v_cache);
+  kernel<<<ctas, C::kThreads, C::kSmem, stream>>>(tq, tk, tv, p, (const uint8_t *)v_cache);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_merge<D, kPrefillRows, false>(p, ctas, stream);
 }

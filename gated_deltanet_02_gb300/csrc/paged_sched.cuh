@@ -3,7 +3,7 @@
 //
 // The work of a call is a row of units, one unit being the 128 keys of one
 // cache tile for one item; an item is (request, key / value head, tile of query
-// tokens), and its units are kItemCost for its own beginning and end (reading q,
+// tokens), and its units are kCost for its own beginning and end (reading q,
 // writing outputs) and then the cache tiles that its last token sees (one at
 // least).  Requests come in order, then heads, then token tiles.  CTA c takes
 // units [c n, (c + 1) n), n = ceil(units / CTAs): every SM reads the same number
@@ -26,10 +26,11 @@ namespace paged {
 constexpr int kTileKeys = 128;
 // What an item costs beside its cache tiles, in cache tiles.  Without it the SMs
 // that get many short items end last: packed prompts of 200 .. 4001 tokens, 16
-// heads over 4, take 189, 169, 154, 157 us with 1, 2, 3, 4 (a prompt of 16,000
-// tokens 762, 707, 670, 680 us).  With few rows a tile is bound by HBM and hides
+// heads over 4, take 159, 144, 149, 155 us with 1, 2, 3, 4 from a bf16 cache (a prompt
+// of 16,000 tokens 701, 670, 671, 676 us) and 238, 212, 194, 194 us from an e4m3 one,
+// whose q is split for every item.  With few rows a tile is bound by HBM and hides
 // the next item's beginning (0 and 1 measured the same).
-constexpr int kItemCostMany = 3, kItemCostFew = 0;
+constexpr int kItemCostMany = 2, kItemCostManyF8 = 3, kItemCostFew = 0;
 
 // Everything that the attention kernels are told.
 struct AttnParams {
@@ -140,7 +141,7 @@ struct PlanShared {
 
 // Called by the whole CTA (blockDim a multiple of 32, at most 512); kOneTile:
 // p.tp covers any range, so that a request has one tile.
-template <bool kOneTile>
+template <bool kOneTile, int kCost>
 __device__ inline Plan make_plan(const AttnParams &p, PlanShared *sh) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
   auto head_units = [&](int r) -> long long {  // of one kv head of request r
@@ -148,8 +149,8 @@ __device__ inline Plan make_plan(const AttnParams &p, PlanShared *sh) {
     const Req x = load_req(p, r);
     if (!x.ok && blockIdx.x == 0 && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_BAD_COUNT);
     if (x.ntile == 0) return 0;
-    return kOneTile ? kItemCostFew + tile_units(p.tp, x.pos0, x.q_len, 0)
-                    : units_before(p.tp, kItemCostMany, x.pos0, x.q_len, x.ntile, x.ntile);
+    return kOneTile ? kCost + tile_units(p.tp, x.pos0, x.q_len, 0)
+                    : units_before(p.tp, kCost, x.pos0, x.q_len, x.ntile, x.ntile);
   };
   Plan pl;
   pl.r = 0;
@@ -219,9 +220,8 @@ struct Item {
 };
 
 // The items of a CTA, in order (run by one warp, all lanes alike).
-template <bool kOneTile>
+template <bool kOneTile, int kCost>
 struct Walk {
-  static constexpr int kCost = kOneTile ? kItemCostFew : kItemCostMany;
   const AttnParams &p;
   Plan pl;
   Req x;
