@@ -15,21 +15,28 @@
 // over S for D = 128 and beside it for D = 64).  For D = 128 one warp issues the
 // MMAs, the row tiles in turn, so that one tile's products run while the other's
 // softmax does:  P0 V, Q0 K' | P1 V, Q1 K' | ...  (with a warp for each tile their
-// products interleave and both tiles' softmaxes run at once: packed prompts 180 us
-// instead of 169 us, e4m3 keys 1115 us instead of 841 us).  For D = 64 the
-// softmaxes take longer than the products: the next S starts as soon as this one
-// is read, and a warp for each tile saves their waiting for each other's
-// hand-overs (together 88 us instead of 107 us for 8191 tokens, 8 heads).  A
-// softmax thread owns a row, so no reduction crosses threads.  K and V tiles of
-// 128 keys come through a shared-memory ring: TMA, one box per page and 64 channels (bf16);
-// of an e4m3 cache the keys go into the first product as they are (kind::f8f6f4,
-// q split into two e4m3 parts as in paged_decode.cu; the keys' scales multiply
-// the scores' columns), while four more warps turn the value tiles, times their
-// powers of two, into the bf16 tiles (exact) that the second product reads.
+// products interleave and both tiles' softmaxes run at once, which took packed
+// prompts 6% and e4m3 keys 30% longer).  For D = 64 the softmaxes take longer than
+// the products: the next S starts as soon as this one is read, and a warp for each
+// tile saves their waiting for each other's hand-overs (together 18% for 8191
+// tokens, 8 heads).  A softmax thread owns a row, so no reduction crosses threads.
+// An item's q is one TMA box per 64 channels, [tokens][heads of the group], that a
+// warp of its own loads as soon as the last product with the q before it is done
+// (copied by the softmax warps it cost every item 2.3 us of their time).  K and V
+// tiles of 128 keys come through a shared-memory ring: TMA, one box per page and
+// 64 channels (bf16); of an e4m3 cache the keys go into the first product as they
+// are (kind::f8f6f4, q split in place into two e4m3 parts as in paged_decode.cu;
+// the keys' scales multiply the scores' columns), while four more warps turn the
+// value tiles, times their powers of two, into the bf16 tiles (exact) that the
+// second product reads.  Everything but the softmax is kept in short loops: its
+// unrolled code streams through the instruction caches (the conversion unrolled
+// over 8 keys instead of 2: 811 instead of 760 us for the chunk below).
 //
 // Bound: the tensor core for long prompts, next to it the softmax of the tile
-// that waits for it: a causal prompt of 16,000 tokens, 16 heads over 4 of 128,
-// takes 670 us, 1565 TFLOP/s.
+// that waits for it.  A causal prompt of 16,000 tokens, 16 heads over 4 of 128,
+// takes 656-663 us, 1590 TFLOP/s; packed prompts of 200 .. 4001 tokens 143 us (1100);
+// 8191 tokens, 8 heads of 64, 80.5 us (854); 4096 tokens behind 12,288 of an e4m3
+// cache, 32 heads over 8, 738 us (1300).
 #include "paged_sched.cuh"
 #include "paged_tc.cuh"
 #include "prefill_tc.cuh"
@@ -65,7 +72,13 @@ struct Cfg {
   static constexpr uint32_t kOffRawV = kOffRawK + kRawK * kRawBytes;
   static constexpr uint32_t kOffCode = kOffRawV + kRawV * kRawBytes;      // scale codes beside the raw tiles
   static constexpr uint32_t kOffScale = kOffCode + (kRawK + kRawV) * kTileKeys;
-  static constexpr uint32_t kOffBars = kOffScale + kScaleSlots * kTileKeys * 4;
+  // bf16, D = 128: 32 rows of 64 output channels for each softmax warp, which TMA
+  // then writes (64 prompts of 100 .. 600 tokens, 16 heads over 4: 77 us, with
+  // stores of the registers 83 us; longer prompts the same).  D = 64 has half the
+  // outputs and gains nothing, e4m3 has no room.
+  static constexpr bool kStaged = !kF8 && D == 128;
+  static constexpr uint32_t kOffOut = kOffScale + kScaleSlots * kTileKeys * 4;
+  static constexpr uint32_t kOffBars = kOffOut + (kStaged ? 8 * 4096 : 0);
   static constexpr uint32_t kBytesBars = 1024 + (kF8 ? 1024 : 0);         // e4m3: and a scale per q row
   static constexpr uint32_t kSmem = kOffBars + kBytesBars + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -120,6 +133,14 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// A box from shared memory, by the calling lane; its stores are one group each.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];\n\tcp.async.bulk.commit_group;" ::"l"(map),
+      "r"(src), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
 // 64 bytes to global memory, as two 32-byte stores where the address allows it.
 __device__ __forceinline__ void store64(void *dst, const uint32_t (&u)[16]) {
   if (((uintptr_t)dst & 31) == 0) {
@@ -137,7 +158,8 @@ __device__ __forceinline__ void store64(void *dst, const uint32_t (&u)[16]) {
 template <int D, bool kF8>
 __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                   const __grid_constant__ CUtensorMap tv, const AttnParams p, const uint8_t *v_cache) {
+                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to, const AttnParams p,
+                   const uint8_t *v_cache) {
   using C = Cfg<D, kF8>;
   constexpr int ST = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -590,8 +612,31 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;
         __nv_bfloat16 *dst = p.o + row_at(it, row);
         const bool put = it.kind == 0 && has && !bad;
+        // a warp whose 32 rows are all there, and whole tokens: a box of them for 64 channels
+        const bool boxes = C::kStaged && it.kind == 0 && !bad && 32 % p.G == 0 && row - lane + 32 <= it.ntok * p.G;
+        if (boxes) {
+          const uint32_t out = sb + C::kOffOut + (warp - 4) * 4096;
+          const int x = it.hk * p.G, y = it.row0 + (row - lane) / p.G;
 #pragma unroll 1
-        for (int k = 0; k < D; k += 32) {
+          for (int k = 0; k < D; k += 64) {
+            float o[64];
+            tmem_ld32x2(tO + k, tO + k + 32, *reinterpret_cast<float(*)[32]>(o), *reinterpret_cast<float(*)[32]>(o + 32));
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last box has been read
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 64; e += 8) {
+              uint32_t u[4];
+#pragma unroll
+              for (int v = 0; v < 4; ++v) u[v] = l == 0.f ? 0u : pack_bf16(o[e + 2 * v] * inv, o[e + 2 * v + 1] * inv);
+              sts128(out + lane * 128 + ((e / 8 ^ (lane & 7)) << 4), make_uint4(u[0], u[1], u[2], u[3]));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tma_store_3d(&to, out, k, x, y);
+          }
+        }
+#pragma unroll 1
+        for (int k = 0; k < D && !boxes; k += 32) {
           float o[32];
           tmem_ld32(tO + k, o);
           if (it.kind == 0) {
@@ -690,6 +735,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     }
   }
 
+  if (C::kStaged && warp >= 4 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (*abort && tid == 0 && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_WAIT_TIMEOUT);
@@ -702,13 +748,16 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
 template <int D, bool kF8>
 cudaError_t launch(const AttnParams &p, const void *k_cache, const void *v_cache, int ctas, cudaStream_t stream) {
   using C = Cfg<D, kF8>;
-  CUtensorMap tq = {}, tk = {}, tv = {};
+  CUtensorMap tq = {}, tk = {}, tv = {}, to = {};
   const long long dims[3] = {D, p.page, p.P > 0 ? (long long)p.P * p.Hkv : 1};
   if (p.P == 0) k_cache = v_cache = p.q;  // an empty pool: nothing is ever loaded
   const long long q_dims[3] = {D, p.H, p.N};
   const int q_box[3] = {(int)C::kQRow / 2, p.G, p.tp};
   if (!encode_3d_map_swizzled(&tq, p.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q_dims, q_box,
                               C::kQRow == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+    return cudaErrorInvalidValue;
+  const int o_box[3] = {64, p.G, 32 / p.G};
+  if (C::kStaged && 32 % p.G == 0 && !encode_3d_map(&to, p.o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q_dims, o_box, true))
     return cudaErrorInvalidValue;
   if (kF8) {
     const int box[3] = {D, p.page, 1};
@@ -724,7 +773,7 @@ cudaError_t launch(const AttnParams &p, const void *k_cache, const void *v_cache
   auto kernel = prefill_kernel<D, kF8>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<ctas, C::kThreads, C::kSmem, stream>>>(tq, tk, tv, p, (const uint8_t *)v_cache);
+  kernel<<<ctas, C::kThreads, C::kSmem, stream>>>(tq, tk, tv, to, p, (const uint8_t *)v_cache);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_merge<D, kPrefillRows, false>(p, ctas, stream);
 }
