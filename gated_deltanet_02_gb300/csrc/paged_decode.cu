@@ -624,7 +624,10 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
-  if (*abort && tid == 0 && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_WAIT_TIMEOUT);
+  if (*abort) {
+    if (tid == 0 && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_WAIT_TIMEOUT);
+    let_copies_land();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);

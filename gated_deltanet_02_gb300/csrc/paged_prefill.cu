@@ -94,8 +94,10 @@ struct Cfg {
 struct Bars {
   uint64_t full[6], empty[6];             // bf16 tiles
   uint64_t rawk_full[3], rawk_empty[3], rawv_full[2], rawv_empty[2], scale_ready[8];
-  uint64_t s_ready[2], s_free[2], p_ready[2][2], q_full, q_empty, q_ready[2], o_done[2];
+  uint64_t s_ready[2], s_free[2], p_ready[2][2], q_empty, q_ready[2], o_done[2];
   uint64_t item_full[kItems], item_empty[kItems];
+  // an item's q; one for each slot, since a row tile without work in an item does not wait for its q
+  uint64_t q_full[kItems];
   Item item[kItems];
   PlanShared plan;
   int bad[kItems];
@@ -193,10 +195,10 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       mbar_init(&bars->q_ready[i], 4);
       mbar_init(&bars->o_done[i], 1);
     }
-    mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, C::kIssuers);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bars->item_full[i], 1);
+      mbar_init(&bars->q_full[i], 1);
       mbar_init(&bars->item_empty[i], 1 + C::kIssuers + 8 + (kF8 ? 4 : 0));
       bars->bad[i] = 0;
     }
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       };
       auto q_there = [&](int i) -> bool {
         return kF8 ? wait_bar_warp<false>(&bars->q_ready[w0 + i], nq[i]++ & 1u, abort)
-                   : wait_bar_warp<false>(&bars->q_full, (slot - 1) & 1u, abort);
+                   : wait_bar_warp<false>(&bars->q_full[(slot - 1) % kItems], ((slot - 1) / kItems) & 1u, abort);
       };
       bool ok = next_item();
       while (ok && it.kind >= 0) {
@@ -387,7 +389,8 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
 #pragma unroll
         for (int i = 0; i < kMine; ++i)
           if (ok && nw[i] > 0) ok = q_there(i) && issue_s(i, g);
-        if (C::kIssuers == 2 && ok && most <= 0) ok = wait_bar_warp<false>(&bars->q_full, (slot - 1) & 1u, abort);
+        if (C::kIssuers == 2 && ok && most <= 0)
+          ok = wait_bar_warp<false>(&bars->q_full[(slot - 1) % kItems], ((slot - 1) / kItems) & 1u, abort);
         if (!ok) break;
         k_release(g, most > 0);
         q_release(0);
@@ -433,10 +436,10 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         warp_arrive(&bars->item_empty[si]);
         if (kind < 0 || !wait_bar_warp(&bars->q_empty, (slot & 1u) ^ 1u, abort)) break;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&bars->q_full, C::kQPlanes * (uint32_t)(p.tp * p.G) * C::kQRow);
+          mbar_arrive_expect_tx(&bars->q_full[si], C::kQPlanes * (uint32_t)(p.tp * p.G) * C::kQRow);
 #pragma unroll
           for (uint32_t h = 0; h < C::kQPlanes; ++h)
-            tma_load_3d(smem + h * C::kQPlane, &tq, &bars->q_full, (int)(h * C::kQRow / 2), hk * p.G, row0);
+            tma_load_3d(smem + h * C::kQPlane, &tq, &bars->q_full[si], (int)(h * C::kQRow / 2), hk * p.G, row0);
         }
         __syncwarp();
       }
@@ -462,7 +465,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
     auto split_rows = [&](uint32_t slot) -> bool {
       const Item &it = bars->item[slot % kItems];
       if (!kF8 || it.kind < 0 || last_tile(it, p.G, inv_g, w) <= it.j0) return true;
-      if (!wait_bar_warp(&bars->q_full, slot & 1u, abort)) return false;
+      if (!wait_bar_warp(&bars->q_full[slot % kItems], (slot / kItems) & 1u, abort)) return false;
       constexpr uint32_t kLanes = D / 8, kPer = 32 / kLanes, kQU = 2;
       const uint32_t c = lane % kLanes, half = c / (kLanes / 2);
       auto at = [&](uint32_t r, uint32_t unit) { return r * C::kQRow + ((unit ^ (D == 128 ? r & 7u : r >> 1 & 3u)) << 4); };
@@ -738,7 +741,10 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
   if (C::kStaged && warp >= 4 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   tc_fence_before();
   __syncthreads();
-  if (*abort && tid == 0 && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_WAIT_TIMEOUT);
+  if (*abort) {
+    if (tid == 0 && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_WAIT_TIMEOUT);
+    let_copies_land();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

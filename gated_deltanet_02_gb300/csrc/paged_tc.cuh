@@ -108,5 +108,12 @@ __device__ __forceinline__ float split_q(const uint4 &x, uint2 &hi, uint2 &lo) {
   return __uint_as_float((uint32_t)(127 + e) << 23);
 }
 
+// After a wait that gave up, before a CTA leaves its shared memory and TMEM: time
+// (1 ms) for the copies and products that it still has in flight.
+__device__ __forceinline__ void let_copies_land() {
+  const uint64_t t0 = sm100::global_timer_ns();
+  while (sm100::global_timer_ns() - t0 < 1000000ull) __nanosleep(1000);
+}
+
 }  // namespace paged
 }  // namespace glinattn

@@ -363,3 +363,35 @@ def test_more_requests_than_a_planning_pass_takes(R):
     q = _q(c, 2)
     _check(c, q)
     _check(c, q, max_q_len=200)      # the kernel for many rows
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,Hkv,d", [(1, 1, 64), (2, 1, 128), (3, 1, 128), (8, 2, 64), (5, 1, 64), (12, 2, 128),
+                                     (32, 1, 128), (33, 1, 64), (64, 1, 64), (100, 1, 128)])
+def test_queries_of_others_do_not_matter(H, Hkv, d, cache):
+    """The rows around a request hold other requests' queries, or none: NaN and infinities there."""
+    c = paged_case([(150, 200), (7, 30), (130, 131), (1, 300), (64, 64)], Hkv, d, 16, cache, seed=H, first=2, num_tok=370)
+    q = _q(c, H)
+    want = torch.from_numpy(_check(c, q)).to(torch.bfloat16)
+    start = c["q_start"].tolist()
+    for r in range(len(c["lengths"])):
+        mine = torch.zeros(c["num_tok"], dtype=torch.bool)
+        mine[start[r]:start[r + 1]] = True
+        bad = q.clone()
+        bad[~mine] = torch.tensor([math.nan, math.inf, -math.inf])[torch.arange(int((~mine).sum())) % 3].to(torch.bfloat16)[:, None, None]
+        got, status = _run(c, bad, o=torch.full_like(q, 7.0).to(DEV))
+        assert status == 0 and torch.equal(got.cpu()[mine], want[mine])
+        assert bool((got.cpu()[:2] == 7).all()) and bool((got.cpu()[start[-1]:] == 7).all())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,Hkv,d", [(4, 1, 128), (6, 2, 128), (2, 2, 64), (16, 1, 64)])
+def test_many_short_prompts(H, Hkv, d, cache):
+    """Several items per SM, most of them of a few cache tiles and with ragged ends."""
+    c = paged_case([(1 + (r * 37) % 260, 1 + (r * 37) % 260 + (r * 53) % 150) for r in range(90)], Hkv, d, 16, cache, seed=H)
+    q = _q(c, H)
+    _check(c, q)
+    first, _ = _run(c, q)
+    for _ in range(10):
+        again, status = _run(c, q)
+        assert status == 0 and torch.equal(again, first)
