@@ -532,14 +532,19 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
             sts128(wp + (N + rb + c) / 8 * 2048, make_uint4(lo[0], lo[1], lo[2], lo[3]));
           }
         } else {
-          const float ev4 = ev + 4.f;  // weights times 16: at most 2^8
+          // weights times 16 and their values' powers of two: at most 2^8; the sum takes
+          // those out again (exact but for sums below 2^-126)
+          const float ev4 = ev + 4.f;
+          const float2 inv = make_float2(ex2(-ev4), ex2(-ev4));
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int r = 0; r < 16; r += 2) {
-            const float2 v = make_float2(x[r], x[r + 1]), u = __fadd2_rn(v, make_float2(ev4, ev4));
-            l[r / 2] = __fadd2_rn(l[r / 2], make_float2(ex2(v.x), ex2(v.y)));
+            float2 u = __fadd2_rn(make_float2(x[r], x[r + 1]), make_float2(ev4, ev4));
+            u.x = ex2(u.x);
+            u.y = ex2(u.y);
+            l[r / 2] = __ffma2_rn(u, inv, l[r / 2]);
             uint32_t h, e;
-            split_e4m3x2(ex2(u.x), ex2(u.y), h, e);
+            split_e4m3x2(u.x, u.y, h, e);
             hi[r / 4] = r % 4 ? hi[r / 4] | h << 16 : h;
             lo[r / 4] = r % 4 ? lo[r / 4] | e << 16 : e;
           }
