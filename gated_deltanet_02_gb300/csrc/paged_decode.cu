@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
         for (int h = 0; h < NS; ++h)
           if (!wait_bar_warp(&bars->full[(sc + h) % ST], ((sc + h) / ST) & 1u, abort)) return false;
         const uint32_t buf = gi & 1;
-        if (!wait_bar_warp(&bars->s_free[buf], ((gi >> 1) & 1u) ^ 1u, abort)) return false;
+        if (!wait_bar_warp<false>(&bars->s_free[buf], ((gi >> 1) & 1u) ^ 1u, abort)) return false;
         tc_fence_after();
         const uint32_t d = tmem + buf * N;
         const uint32_t a0 = k0 + (sc % ST) * (kStageBytes >> 4), a1 = k0 + ((sc + 1) % ST) * (kStageBytes >> 4);
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
         return true;
       };
       auto issue_o = [&](uint32_t gi, bool first) -> bool {
-        if (!wait_bar_warp(&bars->p_ready, gi & 1u, abort)) return false;
+        if (!wait_bar_warp<false>(&bars->p_ready, gi & 1u, abort)) return false;
         for (int h = 0; h < NS; ++h)
           if (!wait_bar_warp(&bars->full[(sc + h) % ST], ((sc + h) / ST) & 1u, abort)) return false;
         tc_fence_after();
@@ -376,23 +376,21 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
     float *s_m = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * N + rb, *s_d = s_m + N, *s_f = s_d + N, *s_qs = s_f + N;
     int *s_lim = reinterpret_cast<int *>(s_qs + N);
     constexpr float kSlack = kF8 ? 4.f : 8.f;        // log2 of the largest weight
-    uint32_t sc = 0, g = 0, slot = 0, syncs = 0;
+    uint32_t g = 0, slot = 0, syncs = 0;
     // the group's barrier; like every wait here it gives up after a limit
     auto group_sync = [&]() -> bool {
       warp_arrive(&bars->sync[w]);
-      return wait_bar_warp(&bars->sync[w], syncs++ & 1u, abort);
+      return wait_bar_warp<false>(&bars->sync[w], syncs++ & 1u, abort);
     };
     for (bool ok = true; ok;) {
-      const int si = slot % kItems;
-      if (!(ok = wait_bar_warp(&bars->item_full[si], (slot / kItems) & 1u, abort))) break;
-      const Item it = bars->item[si];
+      if (!(ok = wait_bar_warp(&bars->item_full[slot % kItems], (slot / kItems) & 1u, abort))) break;
+      const Item &it = bars->item[slot % kItems];                 // read where needed: registers are short
       if (it.kind < 0) break;
       ++slot;
-      const int nrow = it.ntok * p.G, n = it.j1 - it.j0;
       // ---- q: rows of tokens x heads, 8 channels a lane, swizzled; rows past nrow are zero
       {
         constexpr int kLanes = D / 8, kPer = 128 / kLanes;
-        const int c = st % kLanes;
+        const int c = st % kLanes, nrow = it.ntok * p.G;
 #pragma unroll
         for (int r0 = 0; r0 < R; r0 += kPer) {
           const int row = rb + r0 + st / kLanes;
@@ -427,9 +425,11 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
       float2 l[R / 2];
 #pragma unroll
       for (int r = 0; r < R / 2; ++r) l[r] = make_float2(0.f, 0.f);
-      for (int j = it.j0; j < it.j1; ++j, ++g) {
+      const int j1 = it.j1;
+      bool first = true;                               // the item's first tile
+      for (int j = it.j0; j < j1; ++j, ++g, first = false) {
         const uint32_t buf = g & 1, tS = tmem + buf * N + rb + lane_base;
-        if (!(ok = wait_bar_warp(&bars->s_ready[buf], (g >> 1) & 1u, abort))) break;
+        if (!(ok = wait_bar_warp<false>(&bars->s_ready[buf], (g >> 1) & 1u, abort))) break;
         tc_fence_after();
         const int key = j * kTileKeys + kk;
         // ---- scores in log2 units, less the row's maximum
@@ -474,11 +474,11 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
 #pragma unroll
           for (int r = 1; r < R - 1; r += 2) t = max3(t, x[r], x[r + 1]);
           const bool any = __any_sync(0xffffffffu, fmaxf(t, x[R - 1]) + ev > kSlack);
-          if (lane == 0) s_flag[g & 1][w][q4] = any || j == it.j0;
+          if (lane == 0) s_flag[g & 1][w][q4] = any || first;
         }
         if (!(ok = group_sync())) break;
         const int4 fl = *reinterpret_cast<const int4 *>(s_flag[g & 1][w]);
-        const bool moves = fl.x | fl.y | fl.z | fl.w | (j > it.j0 && s_unset[w]);
+        const bool moves = fl.x | fl.y | fl.z | fl.w | (!first && s_unset[w]);
         if (moves) {
 #pragma unroll
           for (int r = 0; r < R; ++r) {
@@ -508,8 +508,8 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
             l[r / 2 + 1] = __fmul2_rn(l[r / 2 + 1], make_float2(f.z, f.w));
           }
         }
-        if (g > 0 && !(ok = wait_bar_warp(&bars->o_done, (g - 1) & 1u, abort))) break;  // W is read, O^T complete
-        if (moves && j > it.j0) {
+        if (g > 0 && !(ok = wait_bar_warp<false>(&bars->o_done, (g - 1) & 1u, abort))) break;  // W is read, O^T complete
+        if (moves && !first) {
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < C::kTP; ++k) tmem_scale16(tmem + C::kColO + k * N + rb + lane_base, s_f);
@@ -551,10 +551,9 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
           sts128(wp + w * 2048, make_uint4(hi[0], hi[1], hi[2], hi[3]));
           sts128(wp + (N / 16 + w) * 2048, make_uint4(lo[0], lo[1], lo[2], lo[3]));
         }
-        if (j == it.j1 - 1) {
+        if (j == j1 - 1) {
           // the last tile: its values have landed, and rows behind the cache's end become zeros
-          const int jj = n - 1;
-          const uint32_t vs = sc + NS * (2 * jj + 1);  // K of every tile and V of the earlier ones come first
+          const uint32_t vs = NS * (2 * g + 1);  // K of every tile and V of the earlier ones come first
           for (int h = 0; h < NS && ok; ++h) ok = wait_bar_warp(&bars->full[(vs + h) % ST], ((vs + h) / ST) & 1u, abort);
           if (!ok) break;
           if (w == 0 && key >= it.pos0 + it.ntok) {
@@ -578,9 +577,8 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
         warp_arrive(&bars->p_ready);
       }
       if (!ok) break;
-      sc += NS * 2 * n;
       // ---- sums over the keys; the item's outputs or its partial result
-      const int bad = s_bad[si];
+      const int si = (slot - 1) % kItems, bad = s_bad[si], nrow = it.ntok * p.G;
 #pragma unroll
       for (int r = 0; r < R; ++r) {  // the maxima of the last tile have been read
         float v = r & 1 ? l[r / 2].y : l[r / 2].x;
@@ -589,7 +587,7 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
         if (lane == r) s_red[r * 4 + q4] = v;
       }
       if (!(ok = group_sync())) break;
-      if (!(ok = wait_bar_warp(&bars->o_done, (g - 1) & 1u, abort))) break;
+      if (!(ok = wait_bar_warp<false>(&bars->o_done, (g - 1) & 1u, abort))) break;
       tc_fence_after();
       float o[R];
       {
