@@ -18,14 +18,20 @@
 // power-of-two scale per row, exact but for elements below 2^-10 of the row's
 // largest, where a step is 2^-16 of it; the key's scale multiplies its score, and
 // the value's scale 2^e is folded into the weight's exponent: W = 2^(S + e - m)
-// with m the maximum of S + e, while the sums use 2^(S - m).
+// with m the maximum of S + e; the sums take 2^e out again.
 //
 // Bound: HBM, one read of the cache; 2 CTAs per SM, each with a ring of 16 KiB
 // stages (TMA, one box per page), so that about 190 KiB per SM are in flight.  Warps:
 // 0 TMA and the walk over the items, 1 MMA issue, then groups of four softmax
 // warps, a key per thread and 16 rows per group (24 rows per group, fewer warps
-// that repeat a tile's fixed cost, took 192 us instead of 164 us for 40 rows of
-// 64 requests after 8,192 tokens in e4m3).
+// that repeat a tile's fixed cost, were 17% slower for 40 rows of e4m3).  With many
+// rows the softmax's instructions count beside the bytes: items are read from shared
+// memory where they are needed, for with 48 rows a thread has 72 registers (kept in
+// registers they cost 64 requests of 40 rows after 32,768 tokens 440 instead of 381 us).
+//
+// 256 single tokens after 1,000 .. 6,000, 16 heads over 4 of 128, bf16: 283-287 us,
+// 6,600 GB/s; the 40 rows above, e4m3: 5,500 GB/s; 4 single tokens: 11 us, launches
+// and latency.
 #include "paged_sched.cuh"
 #include "paged_tc.cuh"
 #include "prefill_tc.cuh"
