@@ -722,6 +722,17 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
               o[2 * k] = mul_bf16x2(e4m3x2_bf16_small(src[k]), f1);
               o[2 * k + 1] = mul_bf16x2(e4m3x2_bf16_small(src[k] >> 16), f1);
             }
+            // NaN (a magnitude of 0x7f), which the moved fields would turn into 480
+            uint32_t nan[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) nan[k] = (src[k] & 0x7f7f7f7fu) + 0x01010101u;
+            if ((nan[0] | nan[1] | nan[2] | nan[3]) & 0x80808080u) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                o[2 * k] |= (__byte_perm(nan[k], 0, 0x1404) >> 15 & 0x00010001u) * 0x7fffu;
+                o[2 * k + 1] |= (__byte_perm(nan[k], 0, 0x3424) >> 15 & 0x00010001u) * 0x7fffu;
+              }
+            }
             if (e2 > 0) {
               const uint32_t f2 = (uint32_t)(e2 + 127) * 0x00800080u;
 #pragma unroll

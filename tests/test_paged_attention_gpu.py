@@ -395,3 +395,23 @@ def test_many_short_prompts(H, Hkv, d, cache):
     for _ in range(10):
         again, status = _run(c, q)
         assert status == 0 and torch.equal(again, first)
+
+
+@pytest.mark.parametrize("big", [False, True])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_below_kv_len_is_seen(d, cache, big):
+    """A NaN element of a value row makes its channel NaN in every row that sees it, a NaN in a key every channel."""
+    n = 150 if big else 3
+    c = paged_case([(n, 200), (n, 200), (n, 160)], 1, d, 16, cache, seed=20)
+    for r, (name, pos, ch) in enumerate([("v_cache", 20, d - 3), ("v_cache", 199 - n // 2, 5)]):
+        c[name].view(torch.uint8 if cache == "e4m3" else torch.int16)[c["table"][r, pos // 16], 0, pos % 16, ch] = 0x7F if cache == "e4m3" else 0x7FC0
+    c["k_cache"].view(torch.uint8 if cache == "e4m3" else torch.int16)[c["table"][2, 9], 0, 6, 1] = 0x7F if cache == "e4m3" else 0x7FC0
+    got, status = _run(c, _q(c, 4))
+    nan = got.float().isnan().cpu()
+    assert status == 0
+    assert bool(nan[:n, :, d - 3].all())
+    assert bool(nan[2 * n - n // 2 - 1:2 * n, :, 5].all())
+    rows = torch.arange(n) + 160 - n >= 150
+    assert bool(nan[2 * n:][rows].all())
+    assert int(nan[:n].sum()) == n * 4               # nothing else, where every row sees it
