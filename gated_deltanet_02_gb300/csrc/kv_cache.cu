@@ -46,14 +46,13 @@ glinattn_status check_cache(int cache_dtype, int num_req, int num_tok, int kv_he
 namespace {
 
 constexpr int kWarps = 4;   // rows per CTA
-constexpr int kRound = 4;   // (head, k / v) rows a lane has in flight
+constexpr int kRound = 4;   // steps of a lane in flight: half of them k rows, half v rows
 
-// Exponent of a row's scale, plus 127, from the largest finite |x| as bf16
-// bits: x = 1.m * 2^(E - 127) <= 1.75 * 2^8 * 2^e.
+// Code (exponent plus 127) of a row's scale from the largest finite |x| as bf16
+// bits, x = 1.m * 2^(E - 127) <= 1.75 * 2^8 * 2^e: e = E - 135, one more where m
+// is above 0x60 (then the addition carries into E); subnormals end at -100.
 __device__ __forceinline__ uint32_t scale_code(uint32_t amax) {
-  const int E = (int)(amax >> 7), m = (int)(amax & 0x7f);
-  const int e = E == 0 ? -100 : E - 127 - 8 + (m > 0x60);
-  return (uint32_t)(min(max(e, -100), 119) + 127);
+  return (uint32_t)min(max((int)((amax + 0x1fu) >> 7) - 8, 27), 246);
 }
 
 __device__ __forceinline__ uint32_t finite_mag(uint32_t bits16) {
@@ -61,29 +60,61 @@ __device__ __forceinline__ uint32_t finite_mag(uint32_t bits16) {
   return a < 0x7f80u ? a : 0u;
 }
 
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {  // a NaN gives way to a number
+// The magnitudes' maximum, with some sign; a NaN gives way to a number.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
-// Largest finite |x| of a row as bf16 bits; a row is in kLanes lanes, 8 elements
-// each.  Two elements an instruction; rows with infinities (or NaN alone) again
+// Largest finite |x| of two rows, as bf16 bits in the halves of the result; a row
+// is in kLanes lanes, 8 elements each.  Rows with infinities (or NaN alone) again
 // with those left out.
 template <int kLanes>
-__device__ __forceinline__ uint32_t row_amax(const uint32_t (&w)[4]) {
-  uint32_t m = max_bf16x2(max_bf16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), max_bf16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+__device__ __forceinline__ uint32_t rows_amax(const uint4 &x, const uint4 &y) {
+  const uint32_t a = max_abs_bf16x2(max_abs_bf16x2(x.x, x.y), max_abs_bf16x2(x.z, x.w));
+  const uint32_t b = max_abs_bf16x2(max_abs_bf16x2(y.x, y.y), max_abs_bf16x2(y.z, y.w));
+  uint32_t m = max_abs_bf16x2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
 #pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) m = max_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
-  m = max(m & 0xffffu, m >> 16);
-  if (__any_sync(0xffffffffu, m >= 0x7f80u)) {
-    m = 0;
+  for (int o = kLanes / 2; o > 0; o >>= 1) m = max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  m &= 0x7fff7fffu;
+  if (__any_sync(0xffffffffu, ((m + 0x00800080u) & 0x80008000u) != 0)) {
+    const uint32_t w[2][4] = {{x.x, x.y, x.z, x.w}, {y.x, y.y, y.z, y.w}};
+    uint32_t v[2] = {0, 0};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) m = max(m, max(finite_mag(w[k]), finite_mag(w[k] >> 16)));
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int k = 0; k < 4; ++k) v[i] = max(v[i], max(finite_mag(w[i][k]), finite_mag(w[i][k] >> 16)));
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) v[i] = max(v[i], __shfl_xor_sync(0xffffffffu, v[i], o));
+    }
+    m = v[0] | v[1] << 16;
   }
   return m;
+}
+
+// Eight bf16 times 2^-e as e4m3; eight e4m3 times their scale as bf16.
+__device__ __forceinline__ uint2 quantise(const uint4 &x, uint32_t code) {
+  const float f = __uint_as_float((254u - code) << 23);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t q[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 y = __fmul2_rn(make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u)), make_float2(f, f));
+    q[k] = to_e4m3x2(y.x, y.y);
+  }
+  return make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
+}
+__device__ __forceinline__ uint4 dequantise(const uint2 &y, uint32_t code) {
+  const float f = scale_value(code);
+  const uint32_t w[4] = {y.x & 0xffffu, y.x >> 16, y.y & 0xffffu, y.y >> 16};
+  uint32_t q[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 v = __fmul2_rn(e4m3x2(w[k]), make_float2(f, f));
+    q[k] = pack_bf16(v.x, v.y);
+  }
+  return make_uint4(q[0], q[1], q[2], q[3]);
 }
 
 // A warp's row: its page and row in the page, or false when nothing is to be moved.
@@ -119,81 +150,77 @@ template <int D, bool kE4m3, bool kAppend>
 __global__ void __launch_bounds__(32 * kWarps) kv_move_kernel(const glinattn_kv_args a) {
   constexpr int kLanes = D / 8;             // lanes of one (head, k / v) row
   constexpr int kPer = 32 / kLanes;         // such rows a warp moves at a time
+  constexpr int kHeads = kRound / 2 * kPer; // heads of a round
+  constexpr int kEsz = kE4m3 ? 1 : 2;
   check_requests(a);
   const int lane = threadIdx.x & 31;
   const int i = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (i >= a.num_tok) return;               // whole warps
-  const int H = a.kv_heads, n = 2 * H;      // k rows of every head, then v rows
-  const int sub = lane / kLanes, c = lane % kLanes;
-  // eight elements of token row j, and their place in the packed arrays
-  auto token_at = [&](int j) {
-    const int h = j < H ? j : j - H;
-    return reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(j < H ? a.k : a.v) + ((size_t)i * H + h) * D + c * 8);
+  const int H = a.kv_heads, sub = lane / kLanes, c = lane % kLanes;
+  // eight elements of head h in the token's row, its step 0 .. kRound - 1 of a round: k rows, then v rows
+  const size_t token = ((size_t)i * H + sub) * D + c * 8;
+  auto token_at = [&](int u, int h0) {
+    return reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(u < kRound / 2 ? a.k : a.v) + token + (h0 + u % (kRound / 2) * kPer) * D);
   };
+  auto there = [&](int u, int h0) { return h0 + u % (kRound / 2) * kPer + sub < H; };
   uint4 x[kRound];
-  auto read_tokens = [&](int j0) {
+  auto read_tokens = [&](int h0) {
 #pragma unroll
-    for (int u = 0; u < kRound; ++u) {
-      const int j = j0 + u * kPer + sub;
-      x[u] = j < n ? __ldcs(token_at(j)) : make_uint4(0, 0, 0, 0);
-    }
+    for (int u = 0; u < kRound; ++u) x[u] = there(u, h0) ? __ldcs(token_at(u, h0)) : make_uint4(0, 0, 0, 0);
   };
   if (kAppend) read_tokens(0);              // in flight while the row is located
   int page = 0, row = 0;
   if (!locate(a, i, lane, page, row)) return;
-  for (int j0 = 0; j0 < n; j0 += kPer * kRound) {
-    uint32_t code[kRound];
+  size_t cr = ((size_t)page * H + sub) * a.page_size + row;  // the lane's first row of the cache
+  for (int h0 = 0; h0 < H; h0 += kHeads, cr += (size_t)kHeads * a.page_size) {
+    auto cached_at = [&](int u) {
+      const size_t at = cr + (uint32_t)(u % (kRound / 2) * kPer * a.page_size);
+      return reinterpret_cast<uint8_t *>(u < kRound / 2 ? a.k_cache : a.v_cache) + (at * D + c * 8) * kEsz;
+    };
+    auto scale_at = [&](int u) {
+      return (u < kRound / 2 ? a.k_scale : a.v_scale) + (cr + (uint32_t)(u % (kRound / 2) * kPer * a.page_size));
+    };
     if (kAppend) {
-      if (j0 > 0) read_tokens(j0);
+      if (h0 > 0) read_tokens(h0);
+      if constexpr (kE4m3) {
+#pragma unroll
+        for (int u = 0; u < kRound; u += 2) {
+          const uint32_t m = rows_amax<kLanes>(x[u], x[u + 1]);
+          const uint32_t code[2] = {scale_code(m & 0xffffu), scale_code(m >> 16)};
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const uint2 q = quantise(x[u + v], code[v]);
+            if (there(u + v, h0)) {
+              *reinterpret_cast<uint2 *>(cached_at(u + v)) = q;
+              if (c == 0) *scale_at(u + v) = (uint8_t)code[v];
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < kRound; ++u)
+          if (there(u, h0)) *reinterpret_cast<uint4 *>(cached_at(u)) = x[u];
+      }
     } else {
+      uint32_t code[kRound];
 #pragma unroll
       for (int u = 0; u < kRound; ++u) {
-        const int j = j0 + u * kPer + sub;
         x[u] = make_uint4(0, 0, 0, 0);
         code[u] = 0;
-        if (j >= n) continue;
-        const size_t cr = ((size_t)page * H + (j < H ? j : j - H)) * a.page_size + row;
+        if (!there(u, h0)) continue;
         if (kE4m3) {
-          const uint2 y = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint8_t *>(j < H ? a.k_cache : a.v_cache) + cr * D + c * 8);
+          const uint2 y = *reinterpret_cast<const uint2 *>(cached_at(u));
           x[u].x = y.x;
           x[u].y = y.y;
-          code[u] = (j < H ? a.k_scale : a.v_scale)[cr];
+          code[u] = *scale_at(u);
         } else {
-          x[u] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(j < H ? a.k_cache : a.v_cache) + cr * D + c * 8);
+          x[u] = *reinterpret_cast<const uint4 *>(cached_at(u));
         }
       }
-    }
 #pragma unroll
-    for (int u = 0; u < kRound; ++u) {
-      const int j = j0 + u * kPer + sub;
-      const size_t cr = ((size_t)page * H + (j < H ? j : j - H)) * a.page_size + row;
-      if (kAppend && kE4m3) {
-        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-        const uint32_t sc = scale_code(row_amax<kLanes>(w));
-        const float f = __uint_as_float((254u - sc) << 23);  // 2^-e
-        uint32_t q[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          q[k] = to_e4m3x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
-        if (j < n) {
-          *reinterpret_cast<uint2 *>(reinterpret_cast<uint8_t *>(j < H ? a.k_cache : a.v_cache) + cr * D + c * 8) =
-              make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-          if (c == 0) (j < H ? a.k_scale : a.v_scale)[cr] = (uint8_t)sc;
-        }
-      } else if (j < n) {
-        if (kAppend) {
-          *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(j < H ? a.k_cache : a.v_cache) + cr * D + c * 8) = x[u];
-        } else {
-          uint4 y = x[u];
-          if (kE4m3) {
-            const float s = scale_value(code[u]);
-            const float2 f0 = e4m3x2(x[u].x & 0xffffu), f1 = e4m3x2(x[u].x >> 16);
-            const float2 f2 = e4m3x2(x[u].y & 0xffffu), f3 = e4m3x2(x[u].y >> 16);
-            y = make_uint4(pack_bf16(f0.x * s, f0.y * s), pack_bf16(f1.x * s, f1.y * s), pack_bf16(f2.x * s, f2.y * s),
-                           pack_bf16(f3.x * s, f3.y * s));
-          }
-          __stcs(token_at(j), y);
-        }
+      for (int u = 0; u < kRound; ++u) {
+        const uint4 y = kE4m3 ? dequantise(make_uint2(x[u].x, x[u].y), code[u]) : x[u];
+        if (there(u, h0)) __stcs(token_at(u, h0), y);
       }
     }
   }
