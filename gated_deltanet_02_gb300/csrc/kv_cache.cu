@@ -7,12 +7,12 @@
 // 2^-4 relative), and the way back is exact in bf16.
 //
 // Bound: HBM bytes, 2 d bytes of bf16 and d (+ 1) of e4m3 per row and head.
-// One warp owns one packed row: it finds the row's request (32-way search, all
-// lanes), then moves every (head, k / v) row of it, 8 elements a lane, with
-// all loads of a round in flight before the first store.  Appending 8 prompts of
-// 1,500 .. 8,000 tokens (8 heads of 128, e4m3) takes 40.5 us, 5,360 GB/s; gathering 4
-// prefixes of 20,000 .. 32,768 tokens (4 heads) 60 us, 5,680 GB/s; one token of 256
-// requests 3.5 us (other numbers of loads in flight and of warps a CTA measured no better).
+// A warp finds its packed row's request (32-way search, all lanes), then moves
+// every (head, k / v) row of it, 8 elements a lane, with all loads of a round in
+// flight before the first store.  Appending 8 prompts of
+// 1,500 .. 8,000 tokens (8 heads of 128, e4m3) takes 35.5 us, 6,100 GB/s; gathering 4
+// prefixes of 20,000 .. 32,768 tokens (4 heads) 56 us, 6,000 GB/s; one token of 256
+// requests 2.7 us (other numbers of loads in flight and of warps a CTA measured no better).
 #include "paged.cuh"
 
 namespace glinattn {
@@ -45,7 +45,7 @@ glinattn_status check_cache(int cache_dtype, int num_req, int num_tok, int kv_he
 
 namespace {
 
-constexpr int kWarps = 4;   // rows per CTA
+constexpr int kWarps = 4;   // of a CTA
 constexpr int kRound = 4;   // steps of a lane in flight: half of them k rows, half v rows
 
 // Code (exponent plus 127) of a row's scale from the largest finite |x| as bf16
@@ -117,25 +117,36 @@ __device__ __forceinline__ uint4 dequantise(const uint2 &y, uint32_t code) {
   return make_uint4(q[0], q[1], q[2], q[3]);
 }
 
-// A warp's row: its page and row in the page, or false when nothing is to be moved.
-__device__ __forceinline__ bool locate(const glinattn_kv_args &a, int i, int lane, int &page, int &row) {
-  const int r = find_request(a.q_start, a.num_req, i, lane);
-  const int s0 = a.q_start[r], s1 = a.q_start[r + 1], len = a.kv_len[r];
-  if (i < s0 || i >= s1) {
-    // in no request's range; a range that the search cannot land in is the first one's or a decreasing one
-    return false;
+// Where the packed rows of a warp, one after the other, are in the cache.
+struct Place {
+  int r = 0, s1 = 0, pos = 0, page = -1;
+  bool good = false;  // the last row was in a request that is in bounds
+  // Whether row i is to be moved; then `page` and pos % page_size say where.
+  __device__ __forceinline__ bool find(const glinattn_kv_args &a, int i, int lane) {
+    if (good && i < s1) {  // the next position of the same request
+      ++pos;
+    } else {
+      r = find_request(a.q_start, a.num_req, i, lane);
+      const int s0 = a.q_start[r], len = a.kv_len[r];
+      s1 = a.q_start[r + 1];
+      // a row in no request's range: the search lands in the range before it, or in a decreasing one
+      good = i >= s0 && i < s1 && request_ok(s0, s1, len, a.num_tok, (long long)a.max_pages * a.page_size);
+      if (!good) return false;
+      pos = len - (s1 - i);
+      page = -1;
+    }
+    if (pos < 0) return false;
+    const int row = pos & (a.page_size - 1);
+    if (page == -1 || row == 0) {
+      page = a.page_table[(size_t)r * a.max_pages + pos / a.page_size];
+      if (page < 0 || page >= a.num_pages) {
+        if (lane == 0 && a.dev_status) atomicOr(a.dev_status, GLINATTN_DEV_BAD_SLOT);
+        page = -2;
+      }
+    }
+    return page >= 0;
   }
-  if (!request_ok(s0, s1, len, a.num_tok, (long long)a.max_pages * a.page_size)) return false;
-  const int pos = len - (s1 - i);
-  if (pos < 0) return false;
-  page = a.page_table[(size_t)r * a.max_pages + pos / a.page_size];
-  row = pos % a.page_size;
-  if (page < 0 || page >= a.num_pages) {
-    if (lane == 0 && a.dev_status) atomicOr(a.dev_status, GLINATTN_DEV_BAD_SLOT);
-    return false;
-  }
-  return true;
-}
+};
 
 // The ranges themselves are checked once, request by request, by the first CTAs.
 __device__ __forceinline__ void check_requests(const glinattn_kv_args &a) {
@@ -146,7 +157,8 @@ __device__ __forceinline__ void check_requests(const glinattn_kv_args &a) {
       atomicOr(a.dev_status, GLINATTN_DEV_BAD_COUNT);
 }
 
-template <int D, bool kE4m3, bool kAppend>
+// kRows: packed rows of a warp.
+template <int D, bool kE4m3, bool kAppend, int kRows>
 __global__ void __launch_bounds__(32 * kWarps) kv_move_kernel(const glinattn_kv_args a) {
   constexpr int kLanes = D / 8;             // lanes of one (head, k / v) row
   constexpr int kPer = 32 / kLanes;         // such rows a warp moves at a time
@@ -154,73 +166,74 @@ __global__ void __launch_bounds__(32 * kWarps) kv_move_kernel(const glinattn_kv_
   constexpr int kEsz = kE4m3 ? 1 : 2;
   check_requests(a);
   const int lane = threadIdx.x & 31;
-  const int i = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (i >= a.num_tok) return;               // whole warps
+  const int i0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kRows, i1 = min(i0 + kRows, a.num_tok);
   const int H = a.kv_heads, sub = lane / kLanes, c = lane % kLanes;
-  // eight elements of head h in the token's row, its step 0 .. kRound - 1 of a round: k rows, then v rows
-  const size_t token = ((size_t)i * H + sub) * D + c * 8;
-  auto token_at = [&](int u, int h0) {
-    return reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(u < kRound / 2 ? a.k : a.v) + token + (h0 + u % (kRound / 2) * kPer) * D);
-  };
-  auto there = [&](int u, int h0) { return h0 + u % (kRound / 2) * kPer + sub < H; };
-  uint4 x[kRound];
-  auto read_tokens = [&](int h0) {
-#pragma unroll
-    for (int u = 0; u < kRound; ++u) x[u] = there(u, h0) ? __ldcs(token_at(u, h0)) : make_uint4(0, 0, 0, 0);
-  };
-  if (kAppend) read_tokens(0);              // in flight while the row is located
-  int page = 0, row = 0;
-  if (!locate(a, i, lane, page, row)) return;
-  size_t cr = ((size_t)page * H + sub) * a.page_size + row;  // the lane's first row of the cache
-  for (int h0 = 0; h0 < H; h0 += kHeads, cr += (size_t)kHeads * a.page_size) {
-    auto cached_at = [&](int u) {
-      const size_t at = cr + (uint32_t)(u % (kRound / 2) * kPer * a.page_size);
-      return reinterpret_cast<uint8_t *>(u < kRound / 2 ? a.k_cache : a.v_cache) + (at * D + c * 8) * kEsz;
+  Place place;
+  for (int i = i0; i < i1; ++i) {           // whole warps
+    // eight elements of head h in the token's row, its step 0 .. kRound - 1 of a round: k rows, then v rows
+    const size_t token = ((size_t)i * H + sub) * D + c * 8;
+    auto token_at = [&](int u, int h0) {
+      return reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(u < kRound / 2 ? a.k : a.v) + token + (h0 + u % (kRound / 2) * kPer) * D);
     };
-    auto scale_at = [&](int u) {
-      return (u < kRound / 2 ? a.k_scale : a.v_scale) + (cr + (uint32_t)(u % (kRound / 2) * kPer * a.page_size));
+    auto there = [&](int u, int h0) { return h0 + u % (kRound / 2) * kPer + sub < H; };
+    uint4 x[kRound];
+    auto read_tokens = [&](int h0) {
+#pragma unroll
+      for (int u = 0; u < kRound; ++u) x[u] = there(u, h0) ? __ldcs(token_at(u, h0)) : make_uint4(0, 0, 0, 0);
     };
-    if (kAppend) {
-      if (h0 > 0) read_tokens(h0);
-      if constexpr (kE4m3) {
+    if (kAppend) read_tokens(0);              // in flight while the row is located
+    if (!place.find(a, i, lane)) continue;
+    size_t cr = ((size_t)place.page * H + sub) * a.page_size + (place.pos & (a.page_size - 1));  // the lane's first row of the cache
+    for (int h0 = 0; h0 < H; h0 += kHeads, cr += (size_t)kHeads * a.page_size) {
+      auto cached_at = [&](int u) {
+        const size_t at = cr + (uint32_t)(u % (kRound / 2) * kPer * a.page_size);
+        return reinterpret_cast<uint8_t *>(u < kRound / 2 ? a.k_cache : a.v_cache) + (at * D + c * 8) * kEsz;
+      };
+      auto scale_at = [&](int u) {
+        return (u < kRound / 2 ? a.k_scale : a.v_scale) + (cr + (uint32_t)(u % (kRound / 2) * kPer * a.page_size));
+      };
+      if (kAppend) {
+        if (h0 > 0) read_tokens(h0);
+        if constexpr (kE4m3) {
 #pragma unroll
-        for (int u = 0; u < kRound; u += 2) {
-          const uint32_t m = rows_amax<kLanes>(x[u], x[u + 1]);
-          const uint32_t code[2] = {scale_code(m & 0xffffu), scale_code(m >> 16)};
+          for (int u = 0; u < kRound; u += 2) {
+            const uint32_t m = rows_amax<kLanes>(x[u], x[u + 1]);
+            const uint32_t code[2] = {scale_code(m & 0xffffu), scale_code(m >> 16)};
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const uint2 q = quantise(x[u + v], code[v]);
-            if (there(u + v, h0)) {
-              *reinterpret_cast<uint2 *>(cached_at(u + v)) = q;
-              if (c == 0) *scale_at(u + v) = (uint8_t)code[v];
+            for (int v = 0; v < 2; ++v) {
+              const uint2 q = quantise(x[u + v], code[v]);
+              if (there(u + v, h0)) {
+                *reinterpret_cast<uint2 *>(cached_at(u + v)) = q;
+                if (c == 0) *scale_at(u + v) = (uint8_t)code[v];
+              }
             }
           }
+        } else {
+#pragma unroll
+          for (int u = 0; u < kRound; ++u)
+            if (there(u, h0)) *reinterpret_cast<uint4 *>(cached_at(u)) = x[u];
         }
       } else {
+        uint32_t code[kRound];
 #pragma unroll
-        for (int u = 0; u < kRound; ++u)
-          if (there(u, h0)) *reinterpret_cast<uint4 *>(cached_at(u)) = x[u];
-      }
-    } else {
-      uint32_t code[kRound];
-#pragma unroll
-      for (int u = 0; u < kRound; ++u) {
-        x[u] = make_uint4(0, 0, 0, 0);
-        code[u] = 0;
-        if (!there(u, h0)) continue;
-        if (kE4m3) {
-          const uint2 y = *reinterpret_cast<const uint2 *>(cached_at(u));
-          x[u].x = y.x;
-          x[u].y = y.y;
-          code[u] = *scale_at(u);
-        } else {
-          x[u] = *reinterpret_cast<const uint4 *>(cached_at(u));
+        for (int u = 0; u < kRound; ++u) {
+          x[u] = make_uint4(0, 0, 0, 0);
+          code[u] = 0;
+          if (!there(u, h0)) continue;
+          if (kE4m3) {
+            const uint2 y = *reinterpret_cast<const uint2 *>(cached_at(u));
+            x[u].x = y.x;
+            x[u].y = y.y;
+            code[u] = *scale_at(u);
+          } else {
+            x[u] = *reinterpret_cast<const uint4 *>(cached_at(u));
+          }
         }
-      }
 #pragma unroll
-      for (int u = 0; u < kRound; ++u) {
-        const uint4 y = kE4m3 ? dequantise(make_uint2(x[u].x, x[u].y), code[u]) : x[u];
-        if (there(u, h0)) __stcs(token_at(u, h0), y);
+        for (int u = 0; u < kRound; ++u) {
+          const uint4 y = kE4m3 ? dequantise(make_uint2(x[u].x, x[u].y), code[u]) : x[u];
+          if (there(u, h0)) __stcs(token_at(u, h0), y);
+        }
       }
     }
   }
@@ -235,10 +248,24 @@ glinattn_status move(const glinattn_kv_args *a, cudaStream_t stream) {
   if (st != GLINATTN_OK) return st;
   if (a->num_req == 0 || a->num_tok == 0) return GLINATTN_OK;
   if (!a->k || !a->v || (((uintptr_t)a->k | (uintptr_t)a->v) & 15u)) return GLINATTN_ERR_INVALID_ARG;
-  const bool f8 = a->cache_dtype == GLINATTN_E4M3;
-  auto kernel = a->head_dim == 128 ? (f8 ? kv_move_kernel<128, true, kAppend> : kv_move_kernel<128, false, kAppend>)
-                                   : (f8 ? kv_move_kernel<64, true, kAppend> : kv_move_kernel<64, false, kAppend>);
-  kernel<<<(unsigned)((a->num_tok - 1) / kWarps + 1), 32 * kWarps, 0, stream>>>(*a);
+  // Four rows a warp where e4m3 rows are read and there are enough of them to fill
+  // the SMs: the look-ups for the next rows cost little, and a row has few bytes in
+  // flight.  4 heads of 128, one row and four: 4,096 rows 4.2 and 5.1 us, 16,384 rows
+  // 8.6 and 7.7 us, 109,688 rows 60 and 56 us; of bf16 rows 43 and 43.5 us (65,536);
+  // appending 35.5 and 41 us (8 prompts of 1,500 .. 8,000 tokens, 8 heads).
+  auto run = [&](auto kernel, int rows) {
+    kernel<<<(unsigned)((a->num_tok - 1) / (rows * kWarps) + 1), 32 * kWarps, 0, stream>>>(*a);
+  };
+  if (a->cache_dtype == GLINATTN_BF16) {
+    if (a->head_dim == 128) run(kv_move_kernel<128, false, kAppend, 1>, 1);
+    else run(kv_move_kernel<64, false, kAppend, 1>, 1);
+  } else if (kAppend || a->num_tok < 8192) {
+    if (a->head_dim == 128) run(kv_move_kernel<128, true, kAppend, 1>, 1);
+    else run(kv_move_kernel<64, true, kAppend, 1>, 1);
+  } else {
+    if (a->head_dim == 128) run(kv_move_kernel<128, true, false, 4>, 4);
+    else run(kv_move_kernel<64, true, false, 4>, 4);
+  }
   return cudaGetLastError() == cudaSuccess ? GLINATTN_OK : GLINATTN_ERR_CUDA;
 }
 

@@ -153,3 +153,27 @@ def test_far_pages_pass_32_bit_offsets():
     assert not bool(kc[-1, :, 5:].any())
     k2, v2 = glinattn_kv_gather(kc, vc, table, kv, qs, num_tok=5)
     assert torch.equal(k2, k) and torch.equal(v2, v)
+
+
+@pytest.mark.parametrize("d,Hkv,page", [(64, 1, 16), (64, 3, 32), (128, 2, 16), (128, 1, 128)])
+def test_gather_of_many_rows(d, Hkv, page):
+    """A warp's rows that go on in a page, into the next one and into another request; rows at negative positions,
+    in no request, behind a bad page and of a request that is out of bounds stay as they were."""
+    c = paged_case([(2, 300), (4001, 4001), (0, 5), (7, 3), (1, 9), (1, 900), (1, 33), (2700, 5003), (50, 60), (1500, 1700)],
+                   Hkv, d, page, "e4m3", seed=d, num_tok=8300, first=3)
+    g = dev(c)
+    bad_page, bad_len = 7, 8                            # requests
+    g["table"][bad_page, 3000 // page] = c["pages"]
+    g["kv_len"][bad_len] = -1
+    args, kw = cache_args(g)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = [torch.full((c["num_tok"], Hkv, d), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    glinattn_kv_gather(*args, k=out[0], v=out[1], dev_status=status, **kw)
+    assert int(status.item()) == DEV_BAD_SLOT | DEV_BAD_COUNT
+    for x, name in zip(out, ("k", "v")):
+        want = np.full((c["num_tok"], Hkv, d), 7.0)
+        for r, rows in enumerate(rows_of(c, name)):
+            for i, pos in P.positions(c["q_start"], c["kv_len"], r):
+                if pos >= 0 and r != bad_len and not (r == bad_page and pos // page == 3000 // page):
+                    want[i] = rows[pos]
+        assert np.array_equal(x.float().cpu().double().numpy(), want)
