@@ -326,16 +326,24 @@ __global__ void __launch_bounds__(256) merge_few_rows_kernel(const AttnParams p)
   const int c0 = blockIdx.x, row = blockIdx.y;
   const int4 d = p.desc[c0];
   if (d.w < 0 || row >= d.z * p.G) return;
-  if (any_bad(p, c0, d.w)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Partial<kE> a;
-#pragma unroll 4
-  for (int c = c0 + warp; c <= d.w; c += 8) {
+  auto piece = [&](int c, float (&x)[kE]) -> float2 {
     const size_t at = (size_t)(2 * c + (c == c0 ? 1 : 0)) * kRows + row;
-    const float2 ml = p.ml[at];
-    float x[kE];
 #pragma unroll
     for (int e = 0; e < kE; ++e) x[e] = p.part[at * D + lane * kE + e];
+    return p.ml[at];
+  };
+  // the warp's first piece is read beside the flags
+  float first[kE];
+  float2 fml = make_float2(-INFINITY, 0.f);
+  if (c0 + warp <= d.w) fml = piece(c0 + warp, first);
+  if (any_bad(p, c0, d.w)) return;
+  Partial<kE> a;
+  if (c0 + warp <= d.w) a.add(fml.x, fml.y, first);
+#pragma unroll 4
+  for (int c = c0 + warp + 8; c <= d.w; c += 8) {
+    float x[kE];
+    const float2 ml = piece(c, x);
     a.add(ml.x, ml.y, x);
   }
   if (lane == 0) {
@@ -369,22 +377,31 @@ __global__ void __launch_bounds__(256) merge_many_rows_kernel(const AttnParams p
   const int4 d = p.desc[c0];
   const int nrow = d.z * p.G;
   if (d.w < 0 || (int)blockIdx.y * 32 >= nrow) return;
-  if (any_bad(p, c0, d.w)) return;
   const int row = blockIdx.y * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
-  if (row >= nrow) return;
-  Partial<kE> a;
-#pragma unroll 2
-  for (int c = c0; c <= d.w; ++c) {
+  auto piece = [&](int c, float (&x)[kE]) -> float2 {
     const size_t slot = (size_t)(2 * c + (c == c0 ? 1 : 0));
-    const float2 ml = p.ml[slot * kRows + row];
     const float4 *src = reinterpret_cast<const float4 *>(p.part) + (slot * (D / 4) + warp * (kE / 4)) * kRows + row;
-    float x[kE];
 #pragma unroll
     for (int k = 0; k < kE / 4; ++k) {
       const float4 v = src[k * kRows];
       x[4 * k] = v.x, x[4 * k + 1] = v.y, x[4 * k + 2] = v.z, x[4 * k + 3] = v.w;
     }
-    a.add(ml.x, ml.y, x);
+    return p.ml[slot * kRows + row];
+  };
+  // the first two pieces (there are two at least) are read beside the flags
+  float x0[kE], x1[kE];
+  float2 ml0, ml1;
+  if (row < nrow) {
+    ml0 = piece(c0, x0);
+    ml1 = piece(c0 + 1, x1);
+  }
+  if (any_bad(p, c0, d.w) || row >= nrow) return;
+  Partial<kE> a;
+  a.add(ml0.x, ml0.y, x0);
+  a.add(ml1.x, ml1.y, x1);
+  for (int c = c0 + 2; c <= d.w; ++c) {
+    const float2 ml = piece(c, x0);
+    a.add(ml.x, ml.y, x0);
   }
   const int tok = row / p.G, g = row - tok * p.G;
   uint4 *o = reinterpret_cast<uint4 *>(p.o + ((size_t)(d.x + tok) * p.H + d.y * p.G + g) * D + warp * kE);
