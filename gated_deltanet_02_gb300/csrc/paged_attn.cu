@@ -7,9 +7,27 @@
 #include <math.h>
 
 #include "paged_sched.cuh"
+#include "paged_tc.cuh"
 
 namespace glinattn {
 namespace paged {
+
+bool encode_map(CUtensorMap *m, const void *base, CUtensorMapDataType type, int elem_bytes, const long long dims[3],
+                const int box[3], CUtensorMapSwizzle swizzle) {
+  static const auto encode = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+    return (decltype(&cuTensorMapEncodeTiled))(e == cudaSuccess && found == cudaDriverEntryPointSuccess ? f : nullptr);
+  }();
+  if (!encode) return false;
+  const cuuint64_t size[3] = {(cuuint64_t)dims[0], (cuuint64_t)dims[1], (cuuint64_t)dims[2]};
+  const cuuint64_t stride[2] = {size[0] * elem_bytes, size[0] * size[1] * elem_bytes};
+  const cuuint32_t extent[3] = {(cuuint32_t)box[0], (cuuint32_t)box[1], (cuuint32_t)box[2]}, step[3] = {1, 1, 1};
+  return encode(m, type, 3, const_cast<void *>(base), size, stride, extent, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 glinattn_status check(const glinattn_paged_attn_args *a) {

@@ -34,7 +34,6 @@
 // and latency.
 #include "paged_sched.cuh"
 #include "paged_tc.cuh"
-#include "prefill_tc.cuh"
 #include "tc_common.cuh"
 
 namespace glinattn {
@@ -667,8 +666,8 @@ cudaError_t launch_decode(const AttnParams &p, bool f8, int d, int rows, const v
   const int kbox[3] = {inner, p.page, 1};
   const int vbox[3] = {inner, !f8 && d == 128 ? min(p.page, 64) : p.page, 1};
   CUtensorMap tk, tv;
-  if (!encode_3d_map_swizzled(&tk, k_cache, type, esz, dims, kbox, sw) ||
-      !encode_3d_map_swizzled(&tv, v_cache, type, esz, dims, vbox, sw))
+  if (!encode_map(&tk, k_cache, type, esz, dims, kbox, sw) ||
+      !encode_map(&tv, v_cache, type, esz, dims, vbox, sw))
     return cudaErrorInvalidValue;
   // more than 16 rows only with an e4m3 cache (decode_rows)
   if (d == 128) {

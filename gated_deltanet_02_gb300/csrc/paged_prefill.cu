@@ -39,7 +39,6 @@
 // cache, 32 heads over 8, 738 us (1300).
 #include "paged_sched.cuh"
 #include "paged_tc.cuh"
-#include "prefill_tc.cuh"
 #include "tc_common.cuh"
 
 namespace glinattn {
@@ -770,21 +769,21 @@ cudaError_t launch(const AttnParams &p, const void *k_cache, const void *v_cache
   if (p.P == 0) k_cache = v_cache = p.q;  // an empty pool: nothing is ever loaded
   const long long q_dims[3] = {D, p.H, p.N};
   const int q_box[3] = {(int)C::kQRow / 2, p.G, p.tp};
-  if (!encode_3d_map_swizzled(&tq, p.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q_dims, q_box,
+  if (!encode_map(&tq, p.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q_dims, q_box,
                               C::kQRow == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   const int o_box[3] = {64, p.G, 32 / p.G};
-  if (C::kStaged && 32 % p.G == 0 && !encode_3d_map(&to, p.o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q_dims, o_box, true))
+  if (C::kStaged && 32 % p.G == 0 && !encode_map(&to, p.o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q_dims, o_box, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   if (kF8) {
     const int box[3] = {D, p.page, 1};
-    if (!encode_3d_map_swizzled(&tk, k_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, dims, box,
+    if (!encode_map(&tk, k_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, dims, box,
                                 D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
   } else {
     const int box[3] = {64, p.page, 1};
-    if (!encode_3d_map(&tk, k_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dims, box, true) ||
-        !encode_3d_map(&tv, v_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dims, box, true))
+    if (!encode_map(&tk, k_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dims, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_map(&tv, v_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dims, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
   auto kernel = prefill_kernel<D, kF8>;

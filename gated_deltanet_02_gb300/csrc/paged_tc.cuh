@@ -115,5 +115,10 @@ __device__ __forceinline__ void let_copies_land() {
   while (sm100::global_timer_ns() - t0 < 1000000ull) __nanosleep(1000);
 }
 
+// Host: a tiled map of a contiguous array [dims[2], dims[1], dims[0]] of elements
+// of elem_bytes, false when the driver refuses it.
+bool encode_map(CUtensorMap *m, const void *base, CUtensorMapDataType type, int elem_bytes, const long long dims[3],
+                const int box[3], CUtensorMapSwizzle swizzle);
+
 }  // namespace paged
 }  // namespace glinattn

@@ -54,10 +54,6 @@ bool make_act_map(CUtensorMap *m, const void *base, int B, int T, int H, int d);
 bool encode_3d_map(CUtensorMap *m, const void *base, CUtensorMapDataType type, int elem_bytes,
                    const long long dims[3], const int box[3], bool swizzle);
 
-// The same with any of the swizzles.
-bool encode_3d_map_swizzled(CUtensorMap *m, const void *base, CUtensorMapDataType type, int elem_bytes,
-                            const long long dims[3], const int box[3], CUtensorMapSwizzle swizzle);
-
 // 3-D tiled map over rows of `inner` elements: dims (inner, rows, planes),
 // box (box_inner, 64, 1); 128-byte swizzle when `swizzle` is set.
 bool encode_rows_map(CUtensorMap *m, const void *base, CUtensorMapDataType type, int elem_bytes,
