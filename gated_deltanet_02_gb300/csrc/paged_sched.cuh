@@ -423,7 +423,7 @@ cudaError_t launch_merge(const AttnParams &p, int ctas, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   // rows that an item can have, however many there is room for
-  const int rows = (int)min((long long)kRows, (long long)min(p.max_q, p.tp) * p.G);
+  const int rows = (int)max(1ll, min((long long)kRows, (long long)min(p.max_q, p.tp) * p.G));
   cfg.gridDim = dim3((unsigned)ctas, (unsigned)(kFewRows ? rows : (rows + 31) / 32), 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = stream;

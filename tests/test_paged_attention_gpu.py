@@ -415,3 +415,21 @@ def test_nan_below_kv_len_is_seen(d, cache, big):
     rows = torch.arange(n) + 160 - n >= 150
     assert bool(nan[2 * n:][rows].all())
     assert int(nan[:n].sum()) == n * 4               # nothing else, where every row sees it
+
+
+def test_max_q_len_of_zero():
+    """Allowed where no request has new tokens; a request with some is refused."""
+    c = paged_case([(0, 20), (0, 0)], 1, 64, 16, "bf16", seed=21, num_tok=3)
+    o = torch.full((3, 2, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    got, status = _run(c, _q(c, 2), o=o, max_q_len=0)
+    assert status == 0 and bool((got == 7).all())
+    c = paged_case([(0, 20), (3, 9)], 1, 64, 16, "bf16", seed=21)
+    got, status = _run(c, _q(c, 2), o=o, max_q_len=0)
+    assert status == DEV_BAD_COUNT and bool((got == 7).all())
+
+
+@pytest.mark.parametrize("q_len,H,Hkv,d", [(1, 16, 4, 128), (1, 100, 1, 64), (5, 33, 3, 128), (9, 7, 7, 64), (257, 3, 1, 128)])
+def test_every_row_of_a_shared_item_is_joined(q_len, H, Hkv, d):
+    """Long caches cut into pieces, with row counts around the merge's own tiles."""
+    c = paged_case([(q_len, 30000), (q_len, 17000)], Hkv, d, 64, "bf16", seed=22 + q_len)
+    _check(c, _q(c, H))
