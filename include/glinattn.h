@@ -411,7 +411,8 @@ glinattn_status glinattn_selective_scan_decode(const glinattn_scan_decode_args *
  *   k_cache, v_cache [P, Hkv, page, d]   (cache_dtype: GLINATTN_BF16 or GLINATTN_E4M3)
  *   k_scale, v_scale [P, Hkv, page] uint8, with GLINATTN_E4M3 only: one
  *     power-of-two scale per cached row, stored as its exponent plus 127, so a
- *     row's elements stand for e4m3 * 2^(code - 127)
+ *     row's elements stand for e4m3 * 2^(code - 127); codes 27 .. 246, which
+ *     glinattn_kv_append writes, or 255 for NaN
  *   page_table [R, max_pages] int32: position t of request r is row t % page
  *     of page page_table[r, t / page]; entries past a request's last position
  *     are not read
@@ -427,7 +428,9 @@ glinattn_status glinattn_selective_scan_decode(const glinattn_scan_decode_args *
  *   A request whose range or kv_len is out of bounds (a range outside
  *   [0, num_tok] or decreasing, kv_len outside [0, max_pages * page]) sets
  *   GLINATTN_DEV_BAD_COUNT and is skipped; a page id outside [0, P) sets
- *   GLINATTN_DEV_BAD_SLOT and skips what needed that page.  num_req <= 65536.
+ *   GLINATTN_DEV_BAD_SLOT and skips what needed that page.  With a decreasing
+ *   q_start glinattn_kv_append and glinattn_kv_gather may leave out rows of other
+ *   requests too.  num_req <= 65536.
  *
  * glinattn_kv_append -- write the new tokens' keys and values to the cache.
  *   k, v [num_tok, Hkv, d] bf16 are read.  GLINATTN_BF16 copies them.
