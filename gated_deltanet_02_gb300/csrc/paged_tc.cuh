@@ -116,7 +116,7 @@ __device__ __forceinline__ void let_copies_land() {
 }
 
 // Host: a tiled map of a contiguous array [dims[2], dims[1], dims[0]] of elements
-// of elem_bytes, false when the driver refuses it.
+// of elem_bytes, false when it is refused.
 bool encode_map(CUtensorMap *m, const void *base, CUtensorMapDataType type, int elem_bytes, const long long dims[3],
                 const int box[3], CUtensorMapSwizzle swizzle);
 
