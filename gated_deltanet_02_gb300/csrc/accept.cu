@@ -12,11 +12,11 @@
 // owns a request: every warp sums one contiguous piece of the row, all CTAs
 // get all pieces' sums through distributed shared memory, and the CTA whose
 // piece holds the threshold reads that piece again (from L2; its warps sum an
-// eighth each, then one warp walks to the token).  256 threads with 8 elements
-// each in flight and at least 6 CTAs per SM: 256 requests of V = 160,000 take 61 us
-// (70 us with 16 elements and 4 CTAs, 164 us with CTAs of 1024 threads, which
-// pass the cluster's barriers in fewer phases); one request of V = 100,003 takes
-// 9 us in all of these, most of it launch, barriers and the chain of loads.
+// eighth each, then one warp walks to the token).  256 threads with 12 elements
+// each in flight and 5 CTAs per SM: 256 requests of V = 160,000 take 52 us (58 us
+// with 8 elements and 6 CTAs, 53 with 16 and 4, 70 with CTAs of 512 threads; clusters
+// of 4, 2 and 1 CTAs were slower too); one request of V = 100,003 takes 7 us, most of
+// it launch, barriers and the chain of loads.
 #include "common.cuh"
 
 namespace glinattn {
@@ -24,18 +24,24 @@ namespace {
 
 constexpr int kCluster = 8;
 constexpr int kThreads = 256;
-constexpr int kAhead = 8;   // elements of a row that a lane has in flight
+constexpr int kAhead = 12;  // elements of a row that a lane has in flight
 
 typedef unsigned long long u64;
 
-// trunc(w 2^40) for w clamped to [0, 1] (NaN: 0): the 24-bit significand, its
-// leading bit at bit 40 for w = 1, shifted down by the exponent.  Integer
-// instructions: with the conversion instruction from fp32 to 64 bits 256
-// requests of V = 160,000 took 103 us instead of 70 us.
-__device__ __forceinline__ u64 weight(float w) {
-  const uint32_t x = __float_as_uint(fminf(fmaxf(w, 0.f), 1.f));
-  const uint32_t e = (x >> 23) & 0xffu;
-  return ((u64)((x & 0x7fffffu) | 0x800000u) << 17) >> min(127u - e, 63u);
+// trunc(w 2^40) of two weights in [0, 1] as hi 2^20 + lo, hi and lo each below
+// the exponent field of 2^23 (kBias): w 2^20 + 2^23 rounded towards zero holds
+// floor(w 2^20) in its low bits, what that leaves is exact, and so once more.  Two-lane
+// fp32 arithmetic, 3.5 instructions a weight with its share of the sums; shifting
+// the significand in 64 bits, 256 requests of V = 160,000 took 61 us.
+constexpr uint32_t kBias = 0x4b000000u;
+__device__ __forceinline__ void parts(float2 w, uint2 &hi, uint2 &lo) {
+  const float2 one = make_float2(8388608.f, 8388608.f), scale = make_float2(1048576.f, 1048576.f);
+  const float2 x = __fmul2_rn(w, scale);
+  const float2 t = __fadd2_rz(x, one);
+  const float2 f = __fadd2_rn(x, __fadd2_rn(one, make_float2(-t.x, -t.y)));
+  const float2 y = __ffma2_rz(f, scale, one);
+  hi = make_uint2(__float_as_uint(t.x), __float_as_uint(t.y));
+  lo = make_uint2(__float_as_uint(y.x), __float_as_uint(y.y));
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -57,30 +63,52 @@ __device__ __forceinline__ void st_remote(u64 *p, uint32_t rank, u64 v) {
 struct Row {
   const float *p, *q;  // q NULL: none is taken off
   int zero;            // the element without weight (the rejected point mass), or -1
-  // elements b + 32 k < end, k < kAhead, all loaded before the first is used
-  __device__ __forceinline__ void load(int b, int end, u64 (&w)[kAhead]) const {
-    float x[kAhead];
+  // weights of the elements b + 32 k < end, k < kAhead, in [0, 1] (NaN: 0), all loaded before the first is used
+  template <bool kFull>
+  __device__ __forceinline__ void load(int b, int end, float (&x)[kAhead]) const {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) x[k] = b + 32 * k < end ? __ldg(p + b + 32 * k) : 0.f;
+    for (int k = 0; k < kAhead; ++k) x[k] = kFull || b + 32 * k < end ? __ldg(p + b + 32 * k) : 0.f;
     if (q) {
       float y[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) y[k] = b + 32 * k < end ? __ldg(q + b + 32 * k) : 0.f;
+      for (int k = 0; k < kAhead; ++k) y[k] = kFull || b + 32 * k < end ? __ldg(q + b + 32 * k) : 0.f;
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) x[k] -= y[k];
+      for (int k = 0; k < kAhead; ++k) x[k] = __saturatef(x[k] - y[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) x[k] = __saturatef(x[k]);
     }
+    if (zero >= 0) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) w[k] = b + 32 * k == zero ? 0 : weight(x[k]);
+      for (int k = 0; k < kAhead; ++k) x[k] = b + 32 * k == zero ? 0.f : x[k];
+    }
   }
-  // the warp's sum over [v0, v1), in every lane
+  // the warp's sum over [v0, v1), in every lane: at most 2^11 elements a lane, so
+  // that 32 bits hold the sums of their parts (2^20 at most each) once the biases,
+  // which wrap, are taken off
   __device__ __forceinline__ u64 sum(int v0, int v1, int lane) const {
-    u64 s = 0;
-    for (int b = v0 + lane; b < v1; b += 32 * kAhead) {
-      u64 w[kAhead];
-      load(b, v1, w);
+    uint32_t hi = 0, lo = 0, bias = 0;
+    auto add = [&](const float (&x)[kAhead]) {
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) s += w[k];
+      for (int k = 0; k < kAhead; k += 2) {
+        uint2 h, l;
+        parts(make_float2(x[k], x[k + 1]), h, l);
+        hi += h.x + h.y;
+        lo += l.x + l.y;
+      }
+      bias += kBias * kAhead;
+    };
+    int b = v0;
+    float x[kAhead];
+    for (; b + 32 * kAhead <= v1; b += 32 * kAhead) {
+      load<true>(b + lane, v1, x);
+      add(x);
     }
+    if (b < v1) {
+      load<false>(b + lane, v1, x);
+      add(x);
+    }
+    u64 s = ((u64)(hi - bias) << 20) + (lo - bias);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
@@ -96,7 +124,7 @@ __device__ __forceinline__ u64 warp_scan(u64 x, int lane) {  // inclusive
   return x;
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 6) accept_kernel(const glinattn_accept_args a) {
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 5) accept_kernel(const glinattn_accept_args a) {
   constexpr int kWarps = kThreads / 32, kPieces = kCluster * kWarps, kPer = kPieces / 32;
   __shared__ u64 s_piece[2][kPieces];
   __shared__ u64 s_sub[kWarps];
@@ -202,14 +230,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 6) 
       for (int k = 0; k < warp; ++k) run += s_sub[k];
       if (!(run <= t && t < run + s)) return;  // exactly one warp goes on
       for (int b = e0; b < e1; b += 32 * kAhead) {
-        u64 x[kAhead];
-        w.load(b + lane, e1, x);
+        float x[kAhead];
+        w.load<false>(b + lane, e1, x);
 #pragma unroll 1
         for (int k = 0; k < kAhead; ++k) {
-          u64 y = 0;
+          float y = 0.f;
 #pragma unroll
           for (int j = 0; j < kAhead; ++j) y = j == k ? x[j] : y;
-          const u64 c = run + warp_scan(y, lane);
+          uint2 h, l;
+          parts(make_float2(y, 0.f), h, l);
+          const u64 c = run + warp_scan(((u64)(h.x - kBias) << 20) + (l.x - kBias), lane);
           const unsigned over = __ballot_sync(0xffffffffu, c > t);
           if (over) {
             if (lane == 0) {

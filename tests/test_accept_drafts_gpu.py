@@ -121,3 +121,22 @@ def test_drawn_tokens_follow_the_target():
     share = np.bincount(t[:, 0], minlength=V) / R
     sd = np.sqrt(p.numpy() * (1 - p.numpy()) / R)
     assert (np.abs(share - p.numpy()) <= 5 * sd).all()
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -40, 2.0 ** -39, 2.0 ** -30, 2.0 ** -21, 2.0 ** -20, 2.0 ** -19, 1.0, 2.0 ** -126])
+def test_whole_number_weights_at_every_size(scale):
+    """Few units of 2^-40, weights around the border of their parts, subnormals, ones; every draw of a fine grid."""
+    R, V = 400, 37
+    g = torch.Generator().manual_seed(14)
+    w = torch.rand((R, 1, V), generator=g) * 4 * scale
+    w[:, :, 3] = scale
+    w[:, :, 4] = scale * (1 - 2.0 ** -24)
+    w[:, :, 5] = scale * (1 + 2.0 ** -23)
+    w[:, :, 6] = 2.0 ** -149
+    w[:, :, 7] = 2.0 ** -40
+    w[:, :, 8] = 2.0 ** -41
+    u = torch.arange(R, dtype=torch.float32)[:, None] / R
+    _check(w, None, torch.zeros((R, 0), dtype=torch.int32), u)
+    lower = w * torch.rand((R, 1, V), generator=g)   # a residual of two rows, every draft rejected
+    two = torch.cat([w, w], 1)
+    _check(two, lower, torch.full((R, 1), 6, dtype=torch.int32), torch.cat([torch.full((R, 1), 3e38), u], 1))
