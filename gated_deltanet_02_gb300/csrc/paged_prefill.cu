@@ -505,8 +505,12 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         if (!(ok = wait_bar_warp<false>(&bars->s_ready[w], ns++ & 1u, abort))) break;
         tc_fence_after();
         float s[128];
-        tmem_ld32x2(tS, tS + 32, *reinterpret_cast<float(*)[32]>(s), *reinterpret_cast<float(*)[32]>(s + 32));
-        tmem_ld32x2(tS + 64, tS + 96, *reinterpret_cast<float(*)[32]>(s + 64), *reinterpret_cast<float(*)[32]>(s + 96));
+        if constexpr (D == 64) {  // (78 us instead of 80 for 8191 tokens; D = 128 does not gain)
+          tmem_ld128(tS, s);
+        } else {
+          tmem_ld32x2(tS, tS + 32, *reinterpret_cast<float(*)[32]>(s), *reinterpret_cast<float(*)[32]>(s + 32));
+          tmem_ld32x2(tS + 64, tS + 96, *reinterpret_cast<float(*)[32]>(s + 64), *reinterpret_cast<float(*)[32]>(s + 96));
+        }
         if (C::kSepP) {
           tc_fence_before();
           warp_arrive(&bars->s_free[w]);
