@@ -34,9 +34,9 @@
 //
 // Bound: the tensor core for long prompts, next to it the softmax of the tile
 // that waits for it.  A causal prompt of 16,000 tokens, 16 heads over 4 of 128,
-// takes 656-663 us, 1590 TFLOP/s; packed prompts of 200 .. 4001 tokens 143 us (1100);
-// 8191 tokens, 8 heads of 64, 80.5 us (854); 4096 tokens behind 12,288 of an e4m3
-// cache, 32 heads over 8, 738 us (1300).
+// takes 656-663 us, 1590 TFLOP/s; packed prompts of 200 .. 4001 tokens 141.5 us (1110);
+// 8191 tokens, 8 heads of 64, 77.5 us (887); 4096 tokens behind 12,288 of an e4m3
+// cache, 32 heads over 8, 766 us (1256).
 #include "paged_sched.cuh"
 #include "paged_tc.cuh"
 #include "tc_common.cuh"
