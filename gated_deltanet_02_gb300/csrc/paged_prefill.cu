@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars *bars = reinterpret_cast<Bars *>(smem + C::kOffBars);
   static_assert(sizeof(Bars) <= 1024, "barrier block");
+  static_assert(ST <= 6 && C::kRawK <= 3 && C::kRawV <= 2 && C::kScaleSlots <= 8, "barriers of the rings");
   float *s_qs = reinterpret_cast<float *>(smem + C::kOffBars + 1024);  // e4m3: scale of a q row
   volatile int *abort = &bars->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
