@@ -660,7 +660,8 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         }
         tc_fence_before();
       }
-      if (it.kind != 0 && has) p.ml[pslot * kPrefillRows + row] = make_float2(m, l);
+      // a sum beside no maximum is NaN (scores of NaN alone): the merge leaves out pieces whose maximum is -infinity
+      if (it.kind != 0 && has) p.ml[pslot * kPrefillRows + row] = make_float2(m == -INFINITY && l != 0.f ? 0.f : m, l);
       if (lrow == 0) {
         if (it.kind != 0 && w == 0) p.skip[pslot] = bad;
         if (bad && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_BAD_SLOT);

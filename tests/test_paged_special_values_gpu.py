@@ -1,0 +1,105 @@
+"""Paged attention where scores, scales, pages or queries are out of the ordinary."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from gated_deltanet_02_gb300 import glinattn_paged_attention
+from gated_deltanet_02_gb300.glinattn import DEV_BAD_SLOT
+from oracle import paged as P
+
+from paged_helpers import HALF_BF16, attention_tolerance, cache_args, dev, paged_case, rows_of
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+
+
+def _q(c, H, seed=1, size=2.0):
+    g = torch.Generator().manual_seed(seed)
+    return (size * torch.randn((c["num_tok"], H, c["d"]), generator=g)).to(torch.bfloat16)
+
+
+def _run(c, q, **kw):
+    g = dev(c)
+    args, scales = cache_args(g)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    kw.setdefault("max_q_len", max([n for n, _ in c["lengths"]], default=0))
+    o = torch.full_like(q, 7.0).to(DEV)
+    glinattn_paged_attention(q.to(DEV), *args, **scales, dev_status=status, o=o, **kw)
+    torch.cuda.synchronize()
+    return o.cpu(), int(status.item())
+
+
+def _oracle(c, q, scale=None):
+    sc = 1.0 / math.sqrt(c["d"]) if scale is None else scale
+    qd = q.double().numpy()
+    want, a = P.attention(qd, rows_of(c, "k"), rows_of(c, "v"), c["q_start"], c["kv_len"], sc)
+    return want, attention_tolerance(c, qd, want, a, sc)
+
+
+def _check(c, q, scale=None, extra=0.0, **kw):
+    got, status = _run(c, q, scale=scale, **kw)
+    assert status == 0
+    want, tol = _oracle(c, q, scale)
+    err = np.abs(got.double().numpy() - want)
+    assert (err <= tol + extra).all(), (np.nanmax(err / (tol + extra)), int(np.isnan(err).sum()))
+    return got
+
+
+def _set(c, name, r, pos, x):
+    """The row of request r at a position as x (every head), bf16 or e4m3 with scale 1."""
+    at = (int(c["table"][r, pos // c["page"]]), slice(None), pos % c["page"])
+    t = c[name + "_cache"]
+    if c["cache"] == "e4m3":
+        t.view(torch.uint8)[at] = torch.as_tensor(x).expand(c["Hkv"], c["d"]).to(torch.float8_e4m3fn).view(torch.uint8)
+        c[name + "_scale"][at] = 127
+    else:
+        t[at] = torch.as_tensor(x, dtype=t.dtype).expand(c["Hkv"], c["d"])
+
+
+#: one request, its items cut into single tiles; many requests, most items whole
+FEW_AND_MANY = [1, 150]
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [2, 140])
+@pytest.mark.parametrize("R", FEW_AND_MANY)
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_a_query_with_nan_gives_nan(value, R, n, cache):
+    """However its item is shared out; no other row is touched."""
+    c = paged_case([(n, n + 300)] * R, 1, 128, 16, cache, seed=1)
+    q = _q(c, 2)
+    want, _ = _run(c, q)
+    assert not bool(want.isnan().any())
+    rows = [0, n - 1, c["num_tok"] - 1]
+    q[rows, 1, 5] = value
+    got, status = _run(c, q)
+    assert status == 0
+    clear = torch.ones(got.shape[:2], dtype=torch.bool)
+    clear[rows, 1] = False
+    # an infinite element of q gives scores of both infinities, so NaN
+    assert bool(got[rows, 1].isnan().all())
+    assert torch.equal(got[clear], want[clear])
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [2, 140])
+@pytest.mark.parametrize("R", FEW_AND_MANY)
+@pytest.mark.parametrize("tile", [0, 1, 3])
+def test_keys_that_are_all_nan_in_a_tile(tile, R, n, cache):
+    """Every row that sees the tile is NaN, whether or not the tile is a piece of its own."""
+    c = paged_case([(n, 520 + n)] * R, 1, 64, 16, cache, seed=2)
+    r = R // 2
+    for t in range(128 * tile, 128 * tile + 128):
+        at = (int(c["table"][r, t // 16]), 0, t % 16)
+        if cache == "e4m3":
+            c["k_scale"][at] = 255
+        else:
+            c["k_cache"][at] = math.nan
+    q = _q(c, 4)
+    got, status = _run(c, q)
+    assert status == 0
+    mine = torch.zeros(c["num_tok"], dtype=torch.bool)
+    mine[n * r:n * (r + 1)] = True
+    assert bool(got[mine].isnan().all()) and not bool(got[~mine].isnan().any())
