@@ -80,7 +80,7 @@ size_t carve(int ctas, int rows, int d, AttnParams *p, uint8_t *base) {
     return x;
   };
   uint8_t *desc = take((size_t)ctas * sizeof(int4));
-  uint8_t *skip = take((size_t)ctas * 2 * sizeof(int));
+  uint8_t *skip = take((size_t)ctas * 4 * sizeof(int));
   uint8_t *ml = take((size_t)ctas * 2 * rows * sizeof(float2));
   uint8_t *part = take((size_t)ctas * 2 * rows * d * sizeof(float));
   if (p) {

@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
         }
       }
       if (st == 0 && w == 0) {
-        if (it.kind != 0) p.skip[pslot] = bad;
+        if (it.kind != 0) p.skip[2 * pslot] = bad;
         if (bad && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_BAD_SLOT);
       }
       if (!(ok = group_sync())) break;  // s_red and s_m are rewritten by the next item

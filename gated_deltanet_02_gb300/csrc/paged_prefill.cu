@@ -52,6 +52,7 @@ using tc::warp_arrive;
 
 constexpr int kItems = 4;
 constexpr float kSlack = 8.f;  // log2 of the largest weight
+constexpr int kNoTile = 0x7fffffff;
 
 template <int D, bool kF8>
 struct Cfg {
@@ -99,7 +100,7 @@ struct Bars {
   uint64_t q_full[kItems];
   Item item[kItems];
   PlanShared plan;
-  int bad[kItems];
+  int bad[kItems];  // the item's first cache tile with a bad page
   uint32_t tmem;
   int abort;
 };
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       mbar_init(&bars->item_full[i], 1);
       mbar_init(&bars->q_full[i], 1);
       mbar_init(&bars->item_empty[i], 1 + C::kIssuers + 8 + (kF8 ? 4 : 0));
-      bars->bad[i] = 0;
+      bars->bad[i] = kNoTile;
     }
     bars->abort = 0;
     p.desc[blockIdx.x].w = -1;
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         if (!more) it.kind = -1;
         if (lane == 0) {
           bars->item[si] = it;
-          bars->bad[si] = 0;
+          bars->bad[si] = kNoTile;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->item_full[si]);
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
           const int np = min(pages, npage - j * pages);
           const int id = __shfl_sync(0xffffffffu, ids, j * pages - base + pl);
           const bool good = id >= 0 && id < p.P, op = pl < np && col < (kF8 ? 1 : D / 64);
-          if (__any_sync(0xffffffffu, op && !good) && lane == 0) bars->bad[si] = 1;
+          if (__any_sync(0xffffffffu, op && !good) && lane == 0) bars->bad[si] = min(bars->bad[si], j);
           const uint32_t ops = (uint32_t)__popc(__ballot_sync(0xffffffffu, op && good));
           const uint32_t bytes = kF8 ? ops * (uint32_t)p.page * (D + 1) : ops << (p.page_shift + 7);
           const size_t plane = (size_t)(good ? id : 0) * p.Hkv + it.hk;
@@ -610,7 +611,8 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       ++slot;
       if (!(ok = wait_bar_warp(&bars->item_full[slot % kItems], (slot / kItems) & 1u, abort))) break;
       if (!(ok = split_rows(slot))) break;
-      const int si = (slot - 1) % kItems, bad = bars->bad[si];
+      // a bad page counts for the row tiles that read it; the producer may be past this one's last tile
+      const int si = (slot - 1) % kItems, bad = bars->bad[si] < j0 + nw;
       const bool has = row < it.ntok * p.G;
       const size_t pslot = (size_t)(2 * blockIdx.x + (it.kind == 1 ? 1 : 0));
       if (nw > 0) {
@@ -663,7 +665,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       // a sum beside no maximum is NaN (scores of NaN alone): the merge leaves out pieces whose maximum is -infinity
       if (it.kind != 0 && has) p.ml[pslot * kPrefillRows + row] = make_float2(m == -INFINITY && l != 0.f ? 0.f : m, l);
       if (lrow == 0) {
-        if (it.kind != 0 && w == 0) p.skip[pslot] = bad;
+        if (it.kind != 0) p.skip[2 * pslot + w] = bad;
         if (bad && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_BAD_SLOT);
       }
       warp_arrive(&bars->item_empty[si]);

@@ -48,7 +48,7 @@ struct AttnParams {
   // (first row, kv head, tokens, last CTA); per CTA two partial results
   // (0: an item begun before the CTA, 1: one that goes on behind it)
   int4 *desc;              // [CTAs]
-  int *skip;               // [CTAs, 2]: the piece met a bad page
+  int *skip;               // [CTAs, 2, row tile]: rows 128 w .. of the piece met a bad page (few rows: w = 0 alone)
   float2 *ml;              // [CTAs, 2, rows]: maximum (log2 units) and sum
   float *part;             // [CTAs, 2, rows x D], in the order that the merge reads
 };
@@ -307,10 +307,10 @@ struct Partial {
   }
 };
 
-// Whether a piece of the item that begins in CTA c0 met a bad page (whole CTA).
-__device__ __forceinline__ bool any_bad(const AttnParams &p, int c0, int c1) {
+// Whether row tile w of a piece of the item that begins in CTA c0 met a bad page (whole CTA).
+__device__ __forceinline__ bool any_bad(const AttnParams &p, int c0, int c1, int w) {
   int bad = 0;
-  for (int c = c0 + (int)threadIdx.x; c <= c1; c += (int)blockDim.x) bad |= p.skip[2 * c + (c == c0 ? 1 : 0)];
+  for (int c = c0 + (int)threadIdx.x; c <= c1; c += (int)blockDim.x) bad |= p.skip[2 * (2 * c + (c == c0 ? 1 : 0)) + w];
   return __syncthreads_or(bad) != 0;
 }
 
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(256) merge_few_rows_kernel(const AttnParams p)
   float first[kE];
   float2 fml = make_float2(-INFINITY, 0.f);
   if (c0 + warp <= d.w) fml = piece(c0 + warp, first);
-  if (any_bad(p, c0, d.w)) return;
+  if (any_bad(p, c0, d.w, 0)) return;
   Partial<kE> a;
   if (c0 + warp <= d.w) a.add(fml.x, fml.y, first);
 #pragma unroll 4
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(256) merge_many_rows_kernel(const AttnParams p
     ml0 = piece(c0, x0);
     ml1 = piece(c0 + 1, x1);
   }
-  if (any_bad(p, c0, d.w) || row >= nrow) return;
+  if (any_bad(p, c0, d.w, blockIdx.y / 4) || row >= nrow) return;
   Partial<kE> a;
   a.add(ml0.x, ml0.y, x0);
   a.add(ml1.x, ml1.y, x1);

@@ -103,3 +103,23 @@ def test_keys_that_are_all_nan_in_a_tile(tile, R, n, cache):
     mine = torch.zeros(c["num_tok"], dtype=torch.bool)
     mine[n * r:n * (r + 1)] = True
     assert bool(got[mine].isnan().all()) and not bool(got[~mine].isnan().any())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("R", FEW_AND_MANY)
+def test_a_bad_page_that_only_later_rows_read(R, d, cache):
+    """256 rows an item: the last 128 read the page and stay as they were, the first 128 do not read it."""
+    c = paged_case([(256, 256)] * R, 1, d, 16, cache, seed=3)
+    q = _q(c, 1)
+    want, status = _run(c, q)
+    assert status == 0
+    r = R // 2
+    c["table"][r, 11] = c["pages"]
+    for _ in range(5):
+        got, status = _run(c, q)
+        assert status == DEV_BAD_SLOT
+        lost = torch.zeros(c["num_tok"], dtype=torch.bool)
+        lost[256 * r + 128:256 * (r + 1)] = True
+        assert bool((got[lost] == 7).all())
+        assert torch.equal(got[~lost], want[~lost])
