@@ -496,9 +496,9 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
               const float4 v = *reinterpret_cast<const float4 *>(s_red + st * 4);
               const float t = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
               const float d = t > (has_max ? kSlack : -INFINITY) ? t : 0.f;
-              has_max |= t > -INFINITY;
               s_d[st] = d;
-              s_f[st] = ex2(-d);
+              s_f[st] = has_max ? ex2(-d) : 1.f;  // nothing to rescale before the first maximum, which may be far below 0
+              has_max |= t > -INFINITY;
               s_m[st] += d;
             }
             const bool unset = __any_sync(0xffffffffu, st < R && !has_max);

@@ -123,3 +123,26 @@ def test_a_bad_page_that_only_later_rows_read(R, d, cache):
         lost[256 * r + 128:256 * (r + 1)] = True
         assert bool((got[lost] == 7).all())
         assert torch.equal(got[~lost], want[~lost])
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 3, 140])
+@pytest.mark.parametrize("kv", [0, 90, 700])
+@pytest.mark.parametrize("level", [-60.0, -90.0, -400.0, 400.0])
+def test_scores_far_from_zero(level, kv, n, cache):
+    """Softmax does not depend on a common term of the scores."""
+    c = paged_case([(n, kv + n), (n, n)], 2, 128, 16, cache, seed=4, fill=0.5)
+    u = level / (4.0 * math.sqrt(128))               # 4 u sqrt(128): the common term
+    for name in ("k",):
+        rows = [torch.from_numpy(x) for x in rows_of(c, name)]
+        for r, x in enumerate(rows):
+            for t in range(len(x)):
+                at = (int(c["table"][r, t // 16]), slice(None), t % 16)
+                if cache == "e4m3":
+                    v, e = P.quantise((x[t] + u).numpy())
+                    c["k_cache"].view(torch.uint8)[at] = torch.from_numpy(v).float().to(torch.float8_e4m3fn).view(torch.uint8)
+                    c["k_scale"][at] = torch.from_numpy(e + 127).to(torch.uint8)
+                else:
+                    c["k_cache"][at] = (x[t] + u).to(torch.bfloat16)
+    q = (4.0 + 0.25 * torch.randn((c["num_tok"], 8, 128), generator=torch.Generator().manual_seed(5))).to(torch.bfloat16)
+    _check(c, q)
