@@ -18,7 +18,8 @@
 // power-of-two scale per row, exact but for elements below 2^-10 of the row's
 // largest, where a step is 2^-16 of it; the key's scale multiplies its score, and
 // the value's scale 2^e is folded into the weight's exponent: W = 2^(S + e - m)
-// with m the maximum of S + e; the sums take 2^e out again.
+// with m the maximum of S + e.  The sums hold 2^(S - m), between 2^-119 and 2^104 a
+// key for the exponents that a cache can have.
 //
 // Bound: HBM, one read of the cache; 2 CTAs per SM, each with a ring of 16 KiB
 // stages (TMA, one box per page), so that about 190 KiB per SM are in flight.  Warps:
@@ -112,7 +113,7 @@ __device__ __forceinline__ void split_e4m3x2(float w0, float w1, uint32_t &hi, u
   lo = f;
 }
 
-// 16 columns from a of this thread's lane, times f[0 ..] (shared memory).
+// 16 columns from a of this thread's lane, times f[0 ..] (shared memory) twice.
 __device__ __forceinline__ void tmem_scale16(uint32_t a, const float *f) {
   float t[16];
   tmem_ld16(a, t);
@@ -120,7 +121,7 @@ __device__ __forceinline__ void tmem_scale16(uint32_t a, const float *f) {
   for (int k = 0; k < 16; k += 8) {
     uint32_t u[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(t[k + j] * f[k + j]);
+    for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(t[k + j] * f[k + j] * f[k + j]);
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a + k), "r"(u[0]), "r"(u[1]),
                  "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
                  : "memory");
@@ -376,8 +377,9 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
     const uint32_t sb = smem_u32(smem);
     float *s_red = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * rb;  // [row][warp]
-    // per row: maximum (0 while there is none), its step in this tile, the
-    // factor of that step, the scale of q, the last key that it sees
+    // per row: maximum (0 while there is none), its step in this tile, the root of
+    // that step's factor (applied twice: with an e4m3 cache a sum may be far from 1, and
+    // the factor beyond fp32's range), the scale of q, the last key that it sees
     float *s_m = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * N + rb, *s_d = s_m + N, *s_f = s_d + N, *s_qs = s_f + N;
     int *s_lim = reinterpret_cast<int *>(s_qs + N);
     constexpr float kSlack = kF8 ? 4.f : 8.f;        // log2 of the largest weight
@@ -497,7 +499,7 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
               const float t = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
               const float d = t > (has_max ? kSlack : -INFINITY) ? t : 0.f;
               s_d[st] = d;
-              s_f[st] = has_max ? ex2(-d) : 1.f;  // nothing to rescale before the first maximum, which may be far below 0
+              s_f[st] = has_max ? ex2(-0.5f * d) : 1.f;  // nothing to rescale before the first maximum, which may be far below 0
               has_max |= t > -INFINITY;
               s_m[st] += d;
             }
@@ -509,8 +511,9 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
           for (int r = 0; r < R; r += 4) {
             const float4 d = *reinterpret_cast<const float4 *>(s_d + r), f = *reinterpret_cast<const float4 *>(s_f + r);
             x[r] -= d.x, x[r + 1] -= d.y, x[r + 2] -= d.z, x[r + 3] -= d.w;
-            l[r / 2] = __fmul2_rn(l[r / 2], make_float2(f.x, f.y));
-            l[r / 2 + 1] = __fmul2_rn(l[r / 2 + 1], make_float2(f.z, f.w));
+            const float2 f0 = make_float2(f.x, f.y), f1 = make_float2(f.z, f.w);
+            l[r / 2] = __fmul2_rn(__fmul2_rn(l[r / 2], f0), f0);
+            l[r / 2 + 1] = __fmul2_rn(__fmul2_rn(l[r / 2 + 1], f1), f1);
           }
         }
         if (g > 0 && !(ok = wait_bar_warp<false>(&bars->o_done, (g - 1) & 1u, abort))) break;  // W is read, O^T complete
@@ -537,21 +540,25 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
             sts128(wp + (N + rb + c) / 8 * 2048, make_uint4(lo[0], lo[1], lo[2], lo[3]));
           }
         } else {
-          // weights times 16 and their values' powers of two: at most 2^8; the sum takes
-          // those out again (exact but for sums below 2^-126)
-          const float ev4 = ev + 4.f;
-          const float2 inv = make_float2(ex2(-ev4), ex2(-ev4));
+          // One exponential 2^(x + h) for both, the sum's 2^x and the weight, 16 times 2^x and the
+          // value's power of two (at most 2^8).  m being the maximum of S + e, the x that count
+          // for the sum are above -119 - 30 and those of the weight above -e - 36, and all are at
+          // most 4 - e: with h = 23 (e - 90 above 113) the exponential stays between 2^-126 and 2^127
+          // for e in -100 .. 119, and neither loses a key to the other's scale.
+          const float h = fmaxf(23.f, ev - 90.f), down = ex2(-h), up = ex2(ev + 4.f - h);
+          const float2 h2 = make_float2(h, h), down2 = make_float2(down, down), up2 = make_float2(up, up);
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int r = 0; r < 16; r += 2) {
-            float2 u = __fadd2_rn(make_float2(x[r], x[r + 1]), make_float2(ev4, ev4));
+            float2 u = __fadd2_rn(make_float2(x[r], x[r + 1]), h2);
             u.x = ex2(u.x);
             u.y = ex2(u.y);
-            l[r / 2] = __ffma2_rn(u, inv, l[r / 2]);
-            uint32_t h, e;
-            split_e4m3x2(u.x, u.y, h, e);
-            hi[r / 4] = r % 4 ? hi[r / 4] | h << 16 : h;
-            lo[r / 4] = r % 4 ? lo[r / 4] | e << 16 : e;
+            l[r / 2] = __ffma2_rn(u, down2, l[r / 2]);
+            u = __fmul2_rn(u, up2);
+            uint32_t a, b;
+            split_e4m3x2(u.x, u.y, a, b);
+            hi[r / 4] = r % 4 ? hi[r / 4] | a << 16 : a;
+            lo[r / 4] = r % 4 ? lo[r / 4] | b << 16 : b;
           }
           sts128(wp + w * 2048, make_uint4(hi[0], hi[1], hi[2], hi[3]));
           sts128(wp + (N / 16 + w) * 2048, make_uint4(lo[0], lo[1], lo[2], lo[3]));

@@ -296,11 +296,13 @@ struct Walk {
 template <int kE>
 struct Partial {
   float m = -INFINITY, l = 0.f, o[kE] = {};
-  // Adds a piece; one without weight adds nothing, whatever its outputs hold.
+  // Adds a piece; one without weight adds nothing, whatever its outputs hold.  The
+  // maxima of an e4m3 cache hold its values' scales, which the sums do not: a sum may
+  // be far above 1 and a factor below fp32's range, so it is applied in two halves.
   __device__ __forceinline__ void add(float pm, float pl, const float (&x)[kE]) {
     const float mn = fmaxf(m, pm), ms = mn == -INFINITY ? 0.f : mn;
-    const float f = exp2f(m - ms), g = exp2f(pm - ms);
-    l = l * f + (pm == -INFINITY ? 0.f : pl * g);
+    const float f2 = exp2f(0.5f * (m - ms)), g2 = exp2f(0.5f * (pm - ms)), f = f2 * f2, g = g2 * g2;
+    l = l * f2 * f2 + (pm == -INFINITY ? 0.f : pl * g2 * g2);
 #pragma unroll
     for (int e = 0; e < kE; ++e) o[e] = o[e] * f + (pm == -INFINITY ? 0.f : x[e] * g);
     m = mn;

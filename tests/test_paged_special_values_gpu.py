@@ -146,3 +146,41 @@ def test_scores_far_from_zero(level, kv, n, cache):
                     c["k_cache"][at] = (x[t] + u).to(torch.bfloat16)
     q = (4.0 + 0.25 * torch.randn((c["num_tok"], 8, 128), generator=torch.Generator().manual_seed(5))).to(torch.bfloat16)
     _check(c, q)
+
+
+def _repeat(c, R):
+    """The case's requests R times over, all over the same pages."""
+    n = c["num_tok"]
+    start = torch.cat([c["q_start"][:-1] + n * i for i in range(R)] + [torch.tensor([n * R], dtype=torch.int32)])
+    return dict(c, lengths=c["lengths"] * R, num_tok=n * R, table=c["table"].repeat(R, 1), kv_len=c["kv_len"].repeat(R), q_start=start)
+
+
+def _check_repeated(c, q, R, extra=0.0):
+    """Against the oracle with the requests once, and R times over (items cut differently, many tiles each)."""
+    want, tol = _oracle(c, q)
+    got, status = _run(_repeat(c, R), q.repeat(R, 1, 1))
+    assert status == 0
+    err = np.abs(got.double().numpy().reshape(R, *q.shape) - want) / (tol + extra)
+    assert (err <= 1).all(), (np.nanmax(err), int(np.isnan(err).sum()))
+
+
+@pytest.mark.parametrize("R", [1, 150])
+@pytest.mark.parametrize("n", [1, 5, 140])
+@pytest.mark.parametrize("order", [1, -1])
+@pytest.mark.parametrize("codes", [(160, 27), (246, 27), (246, 127), (246, 110), (127, 27), (150, 20 + 27)])
+def test_value_scales_far_apart(codes, order, n, R):
+    """Few value rows of a large scale among many of a small one, or of zeros: no key is missing from the sum."""
+    c = paged_case([(n, 700 + n)] + [(n, 60 + n)] * 3, 1, 64, 16, "e4m3", seed=6)
+    g = torch.Generator().manual_seed(7)
+    c["v_scale"][:] = codes[1]
+    if codes[1] == 27:
+        c["v_cache"].view(torch.uint8)[:] = 0        # rows of zeros have the smallest scale
+    for r, (_, kv) in enumerate(c["lengths"]):
+        at = [3, 40, 190, 640] if order == 1 else [kv - n - 1]
+        for t in at:
+            if t < kv:
+                cell = (int(c["table"][r, t // 16]), 0, t % 16)
+                c["v_scale"][cell] = codes[0]
+                x = torch.randn(64, generator=g) * 100
+                c["v_cache"].view(torch.uint8)[cell] = x.to(torch.float8_e4m3fn).view(torch.uint8)
+    _check_repeated(c, _q(c, 2, size=1.0), R)
