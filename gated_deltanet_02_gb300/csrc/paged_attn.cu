@@ -49,10 +49,10 @@ glinattn_status check(const glinattn_paged_attn_args *a) {
 // and drafts run the kernel for few rows, in which query rows are the narrow side
 // of the tensor-core tile.  64 requests after 8,192 tokens, 4 kv heads of 128:
 //   rows          8    16    24    32    40    48
-//   bf16 few    165   170   (no accumulators for more: an earlier build took 182 .. 206)
-//        many   172   173   175   178   179   179 us
-//   e4m3 few     97   103   106   110   136   141
-//        many   207   208   209   211   211   211
+//   bf16 few    165   170   (no accumulators for more: a build that had them took 182 .. 206)
+//        many   169   170   173   174   176   177 us
+//   e4m3 few     97   103   111   117   150   156
+//        many   209   210   211   213   214   214
 int item_rows(const glinattn_paged_attn_args *a) {
   const long long rows = (long long)a->max_q_len * (a->heads / a->kv_heads);
   if (rows <= 16) return 16;

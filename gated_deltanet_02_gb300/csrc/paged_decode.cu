@@ -10,10 +10,11 @@
 // rescaled), which leaves the result unchanged: m is a common factor.
 //
 // Precision: scores, m, sums and O^T are fp32.  The weights enter the second
-// product as two parts, bf16 (together 2^-16 relative) or e4m3 (e4m3 cache;
-// 2^-8 relative, on average less than half of what rounding them to bf16 would
-// do, and 2^-18 of the largest weight), so the output's rounding to bf16 is the
-// one that counts.  With an e4m3 cache both products run on the stored values
+// product as two bf16 parts (together 2^-16 relative), with an e4m3 cache as three
+// e5m2 parts: 2^-9 of the weight, half of what rounding it to bf16 would do, and
+// 2^-33 of the largest weight times value scale of the row (two e4m3 parts end at 2^-18,
+// and 32,000 keys below that under one dominating key moved an output by 0.11).
+// With an e4m3 cache both products run on the stored values
 // (kind::f8f6f4): q is split into two e4m3 parts of 4 bits (bf16 has 8) with a
 // power-of-two scale per row, exact but for elements below 2^-10 of the row's
 // largest, where a step is 2^-16 of it; the key's scale multiplies its score, and
@@ -28,11 +29,11 @@
 // that repeat a tile's fixed cost, were 17% slower for 40 rows of e4m3).  With many
 // rows the softmax's instructions count beside the bytes: items are read from shared
 // memory where they are needed, for with 48 rows a thread has 72 registers (kept in
-// registers they cost 64 requests of 40 rows after 32,768 tokens 440 instead of 381 us).
+// registers they cost 64 requests of 40 rows after 32,768 tokens 15%).
 //
 // 256 single tokens after 1,000 .. 6,000, 16 heads over 4 of 128, bf16: 283-287 us,
-// 6,600 GB/s; the 40 rows above, e4m3: 5,500 GB/s; 4 single tokens: 11 us, launches
-// and latency.
+// 6,600 GB/s; the 40 rows above, e4m3, with a weight's third part and the bias of its
+// exponential: 430 us, 4,900 GB/s; 4 single tokens: 11 us, launches and latency.
 #include "paged_sched.cuh"
 #include "paged_tc.cuh"
 #include "tc_common.cuh"
@@ -53,7 +54,7 @@ constexpr uint32_t kStageBytes = 16384;
 template <int D, bool kF8, int N>
 struct Cfg {
   static constexpr int kTQ = kF8 ? 2 : 1;            // parts of q
-  static constexpr int kTP = 2;                      // parts of a weight
+  static constexpr int kTP = kF8 ? 3 : 2;            // parts of a weight
   static constexpr int kNO = N * kTP;                // columns of O^T (S^T has N)
   static constexpr int kEsz = kF8 ? 1 : 2;
   static constexpr int kTileStages = D * kEsz * kTileKeys > (int)kStageBytes ? 2 : 1;
@@ -98,19 +99,24 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
-// Two weights as two e4m3 parts each (bytes 0 and 1): the value rounded (from
-// its f16), then 16 times what is left.
-__device__ __forceinline__ void split_e4m3x2(float w0, float w1, uint32_t &hi, uint32_t &lo) {
-  uint32_t x, y;
-  unsigned short e, f;
+// Two weights of at most 2^15 as three e5m2 parts each, the second times 4, the third
+// times 32.  e5m2 is the upper byte of f16: the first two parts are cut off the weight's
+// f16 (parts 0 and 1: bytes 1 and 3), the third is what is left, rounded (bytes 0 and 1).  Off by
+// 2^-9 of the weight's leading power (3 bits a part; 2^-12 for the f16), or by 2^-22
+// where that is more (half the smallest e5m2, over 32).
+__device__ __forceinline__ void split_e5m2x2(float w0, float w1, uint32_t (&part)[3]) {
+  constexpr uint32_t kUp[2] = {0x44004400u, 0x48004800u};  // 4, 8
+  uint32_t x;
+  unsigned short e;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(w1), "f"(w0));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(e) : "r"(x));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(e));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(y));
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(0x4c004c00u));  // 16
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(f) : "r"(x));
-  hi = e;
-  lo = f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    part[i] = x;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(x & 0xff00ff00u));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(kUp[i]));
+  }
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(e) : "r"(x));
+  part[2] = e;
 }
 
 // 16 columns from a of this thread's lane, times f[0 ..] (shared memory) twice.
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
     {
       // ============ MMA issue (one lane) ============
       constexpr uint32_t id_s = kF8 ? idesc_f8(128, N, false, false) : idesc_bf16(128, N, false, false);
-      constexpr uint32_t id_o = kF8 ? idesc_f8(D, C::kNO, true, true) : idesc_bf16(D, C::kNO, true, true);
+      constexpr uint32_t id_o = kF8 ? idesc_f8(D, C::kNO, true, true, true) : idesc_bf16(D, C::kNO, true, true);
       constexpr uint32_t hi_r = kF8 && D == 64 ? desc_hi(512, kSw64) : desc_hi(1024, kSw128);  // K, V, q
       // weights: 16-byte units of consecutive rows (no swizzle, MN-major), a unit's 8 keys 16
       // bytes apart, 128 bytes between groups of 8 keys, 2048 between units
@@ -383,6 +389,7 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
     float *s_m = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * N + rb, *s_d = s_m + N, *s_f = s_d + N, *s_qs = s_f + N;
     int *s_lim = reinterpret_cast<int *>(s_qs + N);
     constexpr float kSlack = kF8 ? 4.f : 8.f;        // log2 of the largest weight
+    constexpr float kTop = 11.f;                     // e4m3: and what its parts are above that, 2^15 at most
     uint32_t g = 0, slot = 0, syncs = 0;
     // the group's barrier; like every wait here it gives up after a limit
     auto group_sync = [&]() -> bool {
@@ -540,28 +547,32 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
             sts128(wp + (N + rb + c) / 8 * 2048, make_uint4(lo[0], lo[1], lo[2], lo[3]));
           }
         } else {
-          // One exponential 2^(x + h) for both, the sum's 2^x and the weight, 16 times 2^x and the
-          // value's power of two (at most 2^8).  m being the maximum of S + e, the x that count
-          // for the sum are above -119 - 30 and those of the weight above -e - 36, and all are at
-          // most 4 - e: with h = 23 (e - 90 above 113) the exponential stays between 2^-126 and 2^127
-          // for e in -100 .. 119, and neither loses a key to the other's scale.
-          const float h = fmaxf(23.f, ev - 90.f), down = ex2(-h), up = ex2(ev + 4.f - h);
+          // One exponential 2^(x + h) for both, the sum's 2^x and the weight, 2^kTop times 2^x and
+          // the value's power of two.  m being the maximum of S + e, the x that count for the sum
+          // are above -119 - 30 and those of the weight above -e - 36, and all are at most 4 - e:
+          // with h = 23 (e - 90 above 113) the exponential stays between 2^-126 and 2^127 for e in
+          // -100 .. 119, and neither loses a key to the other's scale.
+          const float h = fmaxf(23.f, ev - 90.f), down = ex2(-h), up = ex2(ev + kTop - h);
           const float2 h2 = make_float2(h, h), down2 = make_float2(down, down), up2 = make_float2(up, up);
-          uint32_t hi[4], lo[4];
+          uint32_t q[3][4];
 #pragma unroll
-          for (int r = 0; r < 16; r += 2) {
-            float2 u = __fadd2_rn(make_float2(x[r], x[r + 1]), h2);
-            u.x = ex2(u.x);
-            u.y = ex2(u.y);
-            l[r / 2] = __ffma2_rn(u, down2, l[r / 2]);
-            u = __fmul2_rn(u, up2);
-            uint32_t a, b;
-            split_e4m3x2(u.x, u.y, a, b);
-            hi[r / 4] = r % 4 ? hi[r / 4] | a << 16 : a;
-            lo[r / 4] = r % 4 ? lo[r / 4] | b << 16 : b;
+          for (int r = 0; r < 16; r += 4) {
+            uint32_t a[3], b[3];
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              float2 u = __fadd2_rn(make_float2(x[r + k], x[r + k + 1]), h2);
+              u.x = ex2(u.x);
+              u.y = ex2(u.y);
+              l[(r + k) / 2] = __ffma2_rn(u, down2, l[(r + k) / 2]);
+              u = __fmul2_rn(u, up2);
+              split_e5m2x2(u.x, u.y, k ? b : a);
+            }
+            q[0][r / 4] = __byte_perm(a[0], b[0], 0x7531);
+            q[1][r / 4] = __byte_perm(a[1], b[1], 0x7531);
+            q[2][r / 4] = __byte_perm(a[2], b[2], 0x5410);
           }
-          sts128(wp + w * 2048, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-          sts128(wp + (N / 16 + w) * 2048, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+#pragma unroll
+          for (int k = 0; k < 3; ++k) sts128(wp + (k * (N / 16) + w) * 2048, make_uint4(q[k][0], q[k][1], q[k][2], q[k][3]));
         }
         if (j == j1 - 1) {
           // the last tile: its values have landed, and rows behind the cache's end become zeros
@@ -606,7 +617,12 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
         float o1[R];
         tmem_ld16x2(tmem + C::kColO + rb + lane_base, tmem + C::kColO + N + rb + lane_base, o, o1);
 #pragma unroll
-        for (int r = 0; r < R; ++r) o[r] = kF8 ? 0.0625f * (o[r] + 0.0625f * o1[r]) : o[r] + o1[r];
+        for (int r = 0; r < R; ++r) o[r] = kF8 ? o[r] + 0.25f * o1[r] : o[r] + o1[r];
+        if constexpr (kF8) {
+          tmem_ld16(tmem + C::kColO + 2 * N + rb + lane_base, o1);
+#pragma unroll
+          for (int r = 0; r < R; ++r) o[r] = 0x1p-11f * (o[r] + 0.03125f * o1[r]);
+        }
       }
       tc_fence_before();
       const int ch = D == 128 ? kk : 16 * q4 + lane;   // channel of this TMEM lane

@@ -471,6 +471,11 @@ glinattn_status glinattn_kv_gather(const glinattn_kv_args *args, glinattn_stream
  *     o = sum_{j <= p} softmax_j(scale * q . k_j) v_j
  *   A row that sees no key (a negative position) or whose every score is
  *   -infinity gives zeros.  Scores, softmax statistics and sums are fp32.
+ *   With an e4m3 cache and max_q_len * H / Hkv <= 48 a key's weight times its
+ *   value's scale enters the output's sum with an error of 2^-9 of itself, or of
+ *   2^-33 of the row's largest such product where that is more: contributions
+ *   below the latter are lost, also in channels in which the keys with the
+ *   largest products have zeros.
  *
  *   q, o [num_tok, H, d] bf16; Hkv divides H, H / Hkv <= 256.
  *   scale: finite and > 0.  max_q_len: an upper bound of the ranges' lengths

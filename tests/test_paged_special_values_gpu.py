@@ -184,3 +184,39 @@ def test_value_scales_far_apart(codes, order, n, R):
                 x = torch.randn(64, generator=g) * 100
                 c["v_cache"].view(torch.uint8)[cell] = x.to(torch.float8_e4m3fn).view(torch.uint8)
     _check_repeated(c, _q(c, 2, size=1.0), R)
+
+
+@pytest.mark.parametrize("n,H", [(1, 8), (3, 8), (5, 8), (40, 8)])
+@pytest.mark.parametrize("bits", [8, 14, 16, 18, 20, 22, 26])
+@pytest.mark.parametrize("R", [1, 320])
+def test_one_key_over_a_flat_tail(R, bits, n, H):
+    """A key far above some 32,000 equal ones, whose weights add up, over an e4m3 cache: one request, cut into
+    single tiles, and many over the same pages, each in one or two pieces."""
+    kv = 32768
+    c = paged_case([(n, kv)], 1, 64, 64, "e4m3", seed=8)
+    g = torch.Generator().manual_seed(9)
+    c["k_cache"].view(torch.uint8)[:] = 0
+    _set(c, "k", 0, 77, bits * math.log(2.0) * 8.0 / 64.0)       # q of ones, scale 1 / 8
+    c["v_scale"][:] = 127
+    c["v_cache"] = (1.0 + 0.2 * torch.rand(c["v_cache"].shape, generator=g)).to(torch.float8_e4m3fn)
+    _set(c, "v", 0, 77, -1.0)
+    q = torch.ones((n, H, 64), dtype=torch.bfloat16)
+    _check_repeated(c, q, R)
+
+
+@pytest.mark.parametrize("n,H", [(1, 8), (5, 8), (40, 8)])
+@pytest.mark.parametrize("R", [1, 200])
+@pytest.mark.parametrize("spread", [0, 4, 8, 12, 16, 20])
+def test_sparse_value_rows_of_other_scales(spread, n, H, R):
+    """A row of a large scale that is zero in half of the channels: the others' values there are not lost."""
+    c = paged_case([(n, 300 + n)], 1, 64, 16, "e4m3", seed=10)
+    c["v_scale"][:] = 127
+    big = torch.zeros(64)
+    big[:32] = 300.0
+    for t in (5, 150, 290):
+        _set(c, "v", 0, t, big)
+        c["v_scale"][int(c["table"][0, t // 16]), 0, t % 16] = 127 + spread
+    q = _q(c, H, size=0.5)
+    # a weight times its value's scale is held to 2^-33 of the row's largest such product, once a key
+    floor = 2.0 ** -33 * (300 + n) * 448.0 * 2.0 ** spread
+    _check_repeated(c, q, R, extra=floor)
