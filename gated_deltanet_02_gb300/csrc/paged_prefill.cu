@@ -481,7 +481,8 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
           const uint32_t r = r0 + k * kPer;
           uint2 hi, lo;
           const float scale = split_q<kLanes>(x[k], hi, lo);
-          if (c == 0) s_qs[r] = scale * p.c;
+          // never 0, which a masked score of -infinity would turn into NaN: scores (2^24 at most before it) are next to 0 then
+          if (c == 0) s_qs[r] = fmaxf(scale * p.c, 0x1p-126f);
           uint8_t *dst = smem + at(r, c >> 1) + (c & 1) * 8;
           *reinterpret_cast<uint2 *>(dst) = hi;
           *reinterpret_cast<uint2 *>(dst + C::kQPlane) = lo;

@@ -220,3 +220,14 @@ def test_sparse_value_rows_of_other_scales(spread, n, H, R):
     # a weight times its value's scale is held to 2^-33 of the row's largest such product, once a key
     floor = 2.0 ** -33 * (300 + n) * 448.0 * 2.0 ** spread
     _check_repeated(c, q, R, extra=floor)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [2, 140])
+@pytest.mark.parametrize("scale", [1e-12, 1e-20, 1e-30, 1e-38])
+def test_tiny_scales_and_rows_of_zeros(scale, n, cache):
+    """Queries of zeros, or scores of next to nothing: the mean of the visible values."""
+    c = paged_case([(n, 200), (n, n)], 1, 128, 16, cache, seed=11)
+    q = _q(c, 4)
+    q[::3] = 0.0
+    _check(c, q, scale=scale)
