@@ -30,6 +30,8 @@ bool encode_map(CUtensorMap *m, const void *base, CUtensorMapDataType type, int 
 
 namespace {
 
+constexpr float kLog2e = 1.44269504088896341f;
+
 glinattn_status check(const glinattn_paged_attn_args *a) {
   if (!a) return GLINATTN_ERR_INVALID_ARG;
   const glinattn_status st =
@@ -39,7 +41,7 @@ glinattn_status check(const glinattn_paged_attn_args *a) {
   if (a->heads <= 0 || a->heads % a->kv_heads != 0 || a->max_q_len < 0) return GLINATTN_ERR_INVALID_ARG;
   if ((long long)a->num_tok * a->heads > (1ll << 30)) return GLINATTN_ERR_INVALID_ARG;
   if (a->heads / a->kv_heads > kPrefillRows) return GLINATTN_ERR_UNSUPPORTED;
-  if (!(a->scale > 0.f) || isinf(a->scale)) return GLINATTN_ERR_INVALID_ARG;
+  if (!(a->scale > 0.f) || isinf(a->scale * kLog2e)) return GLINATTN_ERR_INVALID_ARG;
   if (a->num_req == 0 || a->num_tok == 0) return GLINATTN_OK;
   if (!a->q || !a->o || (((uintptr_t)a->q | (uintptr_t)a->o) & 15u)) return GLINATTN_ERR_INVALID_ARG;
   return GLINATTN_OK;
@@ -127,7 +129,7 @@ glinattn_status glinattn_paged_attention(const glinattn_paged_attn_args *a, glin
   p.max_pages = a->max_pages;
   p.max_q = a->max_q_len;
   p.tp = rows == kPrefillRows ? kPrefillRows / p.G : 1 << 30;
-  p.c = a->scale * 1.44269504088896341f;
+  p.c = a->scale * kLog2e;
   p.q = reinterpret_cast<const __nv_bfloat16 *>(a->q);
   p.k_scale = a->k_scale;
   p.v_scale = a->v_scale;
