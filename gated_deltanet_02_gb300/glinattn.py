@@ -626,7 +626,11 @@ def glinattn_paged_attention(q, k_cache, v_cache, page_table, kv_len, q_start, *
         o = _empty((n, H, d), torch.bfloat16, dev, stream)
     _check(o, "o", torch.bfloat16, (n, H, d), dev)
     _status_word(dev_status, dev)
-    a = PagedAttnArgs(code, R, n, H, Hkv, d, page, P, max_pages, n if max_q_len is None else max_q_len,
+    if max_q_len is None:
+        max_q_len = n
+    elif not 0 <= max_q_len < 1 << 31:          # ctypes would keep the low bits
+        raise ValueError(f"max_q_len must be in [0, 2^31), got {max_q_len}")
+    a = PagedAttnArgs(code, R, n, H, Hkv, d, page, P, max_pages, max_q_len,
                       1.0 / math.sqrt(d) if scale is None else scale, _addr(q), _addr(k_cache), _addr(v_cache),
                       _addr(k_scale), _addr(v_scale), _addr(page_table), _addr(kv_len), _addr(q_start), _addr(o),
                       _addr(dev_status))

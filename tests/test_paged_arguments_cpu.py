@@ -24,3 +24,12 @@ def test_a_scale_that_overflows_in_log2_units_is_refused(scale):
     assert G.library().glinattn_paged_attention(ctypes.byref(_args(scale=scale)), None) == INVALID
     assert G.library().glinattn_paged_attention_workspace_size(ctypes.byref(_args(scale=scale))) == 0
     assert G.library().glinattn_paged_attention_workspace_size(ctypes.byref(_args(scale=2.3e38))) > 0
+
+
+@pytest.mark.parametrize("n", [1 << 31, 1 << 32, (1 << 32) + 1, -1])
+def test_max_q_len_past_32_bits_is_refused(n):
+    """Not cut to its low bits, which would skip requests or select another kernel."""
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    cache = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="max_q_len"):
+        glinattn_paged_attention(torch.zeros(3, 4, 64, dtype=torch.bfloat16), cache, cache, i(2, 3), i(2), i(3), max_q_len=n)
