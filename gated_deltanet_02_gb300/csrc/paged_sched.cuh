@@ -77,27 +77,31 @@ __device__ __forceinline__ int tile_units(int tp, int pos0, int q_len, int t) {
   return vis <= kTileKeys ? 1 : (int)((vis + kTileKeys - 1) / kTileKeys);
 }
 
-// sum of floor((a i + b) / m) over i in [0, n), by the Euclidean recursion, for
-// n < 2^24 and m <= 128 (then a n + b stays below 2^32 once a and b are reduced).
-__device__ inline long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
-  long long s = 0;
-  while (true) {
-    if (a >= m) {
-      s += (long long)n * ((long long)n - 1) / 2 * (a / m);
-      a %= m;
-    }
-    if (b >= m) {
-      s += (long long)n * (b / m);
-      b %= m;
-    }
-    const unsigned y = a * n + b;
-    if (y < m) return s;
-    n = y / m;
-    b = y % m;
-    const unsigned x = m;
-    m = a;
-    a = x;
+// Sum of floor((a i + b) / 128) over i in [0, n), 128 being the keys of a cache tile: the
+// sum of all a i + b less that of their remainders, over 128.  The remainders repeat
+// every q = 128 / g steps, g the largest power of two in a (128 at most): a whole
+// period meets each of b mod g, b mod g + g, .. once, and what is left of the last period
+// (127 steps at most) is added up, four remainders at a time in the bytes of a word.
+// n < 2^24, a and b below 2^31: sums stay below 2^63.
+__host__ __device__ inline long long tiles_sum(unsigned n, unsigned a, unsigned b) {
+  static_assert(kTileKeys == 128, "remainders of 7 bits");
+  const unsigned low = a & 127u, g = low ? low & (0u - low) : 128u, q = 128u / g;
+  const long long periods = n / q;
+  long long rest = periods * (q * (b & (g - 1u)) + g * (q * (q - 1u) / 2u));
+  const unsigned m = n % q;
+  unsigned x = (b + 3u * low & 127u) << 24 | (b + 2u * low & 127u) << 16 | (b + low & 127u) << 8 | (b & 127u);
+  const unsigned step = (4u * low & 127u) * 0x01010101u;
+  unsigned even = 0, odd = 0;  // two sums each, 32 terms below 2^7
+  unsigned i = 0;
+  for (; i + 4u <= m; i += 4u) {
+    even += x & 0x00ff00ffu;
+    odd += x >> 8 & 0x00ff00ffu;
+    x = x + step & 0x7f7f7f7fu;
   }
+  for (; i < m; ++i, x >>= 8) rest += x & 0x7fu;
+  rest += (even & 0xffffu) + (even >> 16) + (odd & 0xffffu) + (odd >> 16);
+  const long long pairs = (long long)n * ((long long)n - 1) / 2;
+  return (pairs * a + (long long)n * b - rest) / kTileKeys;
 }
 
 // a / b for non-negative numbers, in 32 bits where they fit (a 64-bit division
@@ -121,7 +125,7 @@ static __device__ __noinline__ long long units_before(int tp, int cost, int pos0
   const int z = room < tp ? 0 : (int)min((long long)n, div_pos(room, tp));
   s += z;
   // the tiles are of more than 128 rows, and a call has at most 2^30 rows: n < 2^24
-  if (n > z) s += floor_sum((unsigned)(n - z), kTileKeys, (unsigned)tp, (unsigned)(pos0 + (long long)(z + 1) * tp + kTileKeys - 1));
+  if (n > z) s += tiles_sum((unsigned)(n - z), (unsigned)tp, (unsigned)(pos0 + (long long)(z + 1) * tp + kTileKeys - 1));
   return s;
 }
 
