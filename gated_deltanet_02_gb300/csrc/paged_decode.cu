@@ -16,14 +16,15 @@
 // and 32,000 keys below that under one dominating key moved an output by 0.11).
 // With an e4m3 cache both products run on the stored values
 // (kind::f8f6f4): q is split into two e4m3 parts of 4 bits (bf16 has 8) with a
-// power-of-two scale per row, exact but for elements below 2^-10 of the row's
+// power-of-two scale per row, exact but for elements below 2^-9 of the row's
 // largest, where a step is 2^-16 of it; the key's scale multiplies its score, and
 // the value's scale 2^e is folded into the weight's exponent: W = 2^(S + e - m)
 // with m the maximum of S + e.  The sums hold 2^(S - m), between 2^-119 and 2^104 a
 // key for the exponents that a cache can have.
 //
 // Bound: HBM, one read of the cache; 2 CTAs per SM, each with a ring of 16 KiB
-// stages (TMA, one box per page), so that about 190 KiB per SM are in flight.  Warps:
+// stages (TMA, one box per page), so that about 190 KiB per SM are in flight (128 KiB
+// with 48 rows, where 160 measured the same).  Warps:
 // 0 TMA and the walk over the items, 1 MMA issue, then groups of four softmax
 // warps, a key per thread and 16 rows per group (24 rows per group, fewer warps
 // that repeat a tile's fixed cost, were 17% slower for 40 rows of e4m3).  With many
@@ -246,7 +247,6 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
               const bool in = pages > 1 ? (pl / per == h) : true;
               const int rows = min(p.page, 64);
               const int n = __popc(__ballot_sync(0xffffffffu, lane < np && good && in));
-              // of a 128-key page the second half is loaded only when it has keys
               if (lane == 0) mbar_arrive_expect_tx(&bars->full[s], (uint32_t)(n * rows) * 256u);
               __syncwarp();
               const int l2 = lane & 15, col = lane >> 4;  // lanes 16 .. 31: the second column block
@@ -692,7 +692,7 @@ cudaError_t launch_decode(const AttnParams &p, bool f8, int d, int rows, const v
   if (!encode_map(&tk, k_cache, type, esz, dims, kbox, sw) ||
       !encode_map(&tv, v_cache, type, esz, dims, vbox, sw))
     return cudaErrorInvalidValue;
-  // more than 16 rows only with an e4m3 cache (decode_rows)
+  // more than 16 rows only with an e4m3 cache (item_rows)
   if (d == 128) {
     if (!f8) return launch<128, false, 16>(p, tk, tv, ctas, stream);
     return rows == 16   ? launch<128, true, 16>(p, tk, tv, ctas, stream)

@@ -32,7 +32,8 @@ __host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swizzle) {
 }
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr >> 4) & 0x3FFFu) | (lbo >> 4) << 16; }
 
-// D[tmem] (+)= A[smem] B[smem]: bf16 x bf16, or e4m3 x e4m3, -> fp32.
+// D[tmem] (+)= A[smem] B[smem]: bf16 x bf16, or e4m3 x e4m3 (or e5m2, as the
+// descriptor says), -> fp32.
 template <bool kF8>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi, uint32_t idesc,
                                        uint32_t acc) {
@@ -75,7 +76,8 @@ __host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool a_mn, bool b_
 // 8 bf16 of a query row (kLanes lanes hold the row) as two e4m3 parts of 2^-e
 // times the value, e bringing the row's largest element into [128, 256); returns
 // 2^e.  bf16's 8 bits are 4 + 4, so the parts are exact but for elements below
-// 2^-10 of the row's largest, where a step is 2^-16 of it.  An infinite or NaN
+// 2^-9 of the row's largest (1/4 here, whose last bit is the smallest e4m3), where a
+// step is 2^-16 of it.  An infinite or NaN
 // element becomes NaN.
 template <int kLanes>
 __device__ __forceinline__ float split_q(const uint4 &x, uint2 &hi, uint2 &lo) {

@@ -422,7 +422,8 @@ glinattn_status glinattn_selective_scan_decode(const glinattn_scan_decode_args *
  *     of the packed token arrays (num_tok rows) are the new tokens of request
  *     r, the LAST positions below kv_len[r]: row q_start[r] + i is at position
  *     kv_len[r] - (q_start[r + 1] - q_start[r]) + i.  Rows outside every
- *     request's range (a padded batch) are neither read nor written.
+ *     request's range (a padded batch) are not written; they may be read (they
+ *     are memory of the arrays) but reach no result.
  *   head_dim d is 64 or 128; page is 16, 32, 64 or 128.
  *
  *   A request whose range or kv_len is out of bounds (a range outside
