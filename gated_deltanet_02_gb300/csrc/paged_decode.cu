@@ -446,7 +446,9 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
         if (!(ok = wait_bar_warp<false>(&bars->s_ready[buf], (g >> 1) & 1u, abort))) break;
         tc_fence_after();
         const int key = j * kTileKeys + kk;
-        // ---- scores in log2 units, less the row's maximum
+        // ---- scores in log2 units, less the row's maximum; rounded before the difference, as
+        // the maximum was: with a fused one equal keys of huge scores would differ.  (Another
+        // rounding of the difference, exact near 0, so that the two are not fused after all.)
         float x[R], ev = 0.f;                             // e4m3: the value's exponent
         tmem_ld16(tS, x);
         float ks = p.c;
@@ -468,8 +470,8 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
             q1 = __fmul2_rn(q0, make_float2(qs.z, qs.w));
             q0 = __fmul2_rn(q0, make_float2(qs.x, qs.y));
           }
-          const float2 a = __ffma2_rn(make_float2(x[r], x[r + 1]), q0, make_float2(-m.x, -m.y));
-          const float2 b = __ffma2_rn(make_float2(x[r + 2], x[r + 3]), q1, make_float2(-m.z, -m.w));
+          const float2 a = __fadd2_rz(__fmul2_rn(make_float2(x[r], x[r + 1]), q0), make_float2(-m.x, -m.y));
+          const float2 b = __fadd2_rz(__fmul2_rn(make_float2(x[r + 2], x[r + 3]), q1), make_float2(-m.z, -m.w));
           x[r] = a.x, x[r + 1] = a.y, x[r + 2] = b.x, x[r + 3] = b.y;
         }
         if (j * kTileKeys + kTileKeys - 1 > it.pos0) {    // some row does not see the whole tile

@@ -502,7 +502,8 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       const int lim = it.pos0 + (int)((uint32_t)row * inv_g >> 16);  // the row's last key
       const int first_lim = it.pos0 + (int)((uint32_t)(128 * w) * inv_g >> 16);  // the first row's
       const float c = kF8 ? s_qs[row] : p.c;                // written by this warp
-      float m = -INFINITY, l = 0.f;
+      const float slack = fminf(kSlack / c, 1e38f);
+      float m = -INFINITY, l = 0.f;                         // the maximum in the scores' units, before c
       for (int jj = 0; jj < nw; ++jj) {
         const int j = j0 + jj;
         if (!(ok = wait_bar_warp<false>(&bars->s_ready[w], ns++ & 1u, abort))) break;
@@ -545,9 +546,9 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
           }
 #pragma unroll
           for (int u = 0; u < 4; ++u) a[u] = fmaxf(a[u], s[124 + u]);
-          mt = fmaxf(max3(a[0], a[1], a[2]), a[3]) * c;
+          mt = fmaxf(max3(a[0], a[1], a[2]), a[3]);
         }
-        const bool need = mt > m + kSlack;
+        const bool need = mt > m + slack;
         // the previous P is read and O complete: with P over S this tile's S was issued behind P V
         if (C::kSepP && jj > 0) {
           if (!(ok = wait_bar_warp<false>(&bars->o_done[w], nd++ & 1u, abort))) break;
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         }
         if (__any_sync(0xffffffffu, need)) {
           const float mn = need ? mt : m;
-          const float f = need ? ex2(m - mn) : 1.f;
+          const float f = need ? ex2((m - mn) * c) : 1.f;
           l *= f;
           m = mn;
           if (jj > 0) {
@@ -570,8 +571,16 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
             }
           }
         }
-        const float ms = m == -INFINITY ? 0.f : m;
-        const float2 c2 = make_float2(c, c), m2 = make_float2(-ms, -ms);
+        // S c - m c, fused, is off by the rounding of m c, the same for all keys: next to nothing
+        // for ordinary scores, a factor beyond fp32's range for huge ones.  There, with c cut to
+        // a power of two, it is exact: keys that equal the maximum have weight 1, and
+        // any other, a step of 2^5 (2^4 with that c) below at least, next to none.
+        float cc = c, ms = m == -INFINITY ? 0.f : m * c;
+        if (fabsf(ms) > 0x1p29f) {
+          cc = __uint_as_float(__float_as_uint(c) & 0x7f800000u);
+          ms = m * cc;
+        }
+        const float2 c2 = make_float2(cc, cc), m2 = make_float2(-ms, -ms);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -663,8 +672,10 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         }
         tc_fence_before();
       }
-      // a sum beside no maximum is NaN (scores of NaN alone): the merge leaves out pieces whose maximum is -infinity
-      if (it.kind != 0 && has) p.ml[pslot * kPrefillRows + row] = make_float2(m == -INFINITY && l != 0.f ? 0.f : m, l);
+      // a sum beside no maximum is NaN (scores of NaN alone): the merge leaves out pieces whose maximum is
+      // -infinity; so it is here where the row tile has no work, and c is not this item's
+      const float ml = m > -INFINITY ? m * c : l != 0.f ? 0.f : m;
+      if (it.kind != 0 && has) p.ml[pslot * kPrefillRows + row] = make_float2(ml, l);
       if (lrow == 0) {
         if (it.kind != 0) p.skip[2 * pslot + w] = bad;
         if (bad && p.dev_status) atomicOr(p.dev_status, GLINATTN_DEV_BAD_SLOT);

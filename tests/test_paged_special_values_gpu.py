@@ -231,3 +231,36 @@ def test_tiny_scales_and_rows_of_zeros(scale, n, cache):
     q = _q(c, 4)
     q[::3] = 0.0
     _check(c, q, scale=scale)
+
+
+def _set_all(c, name, x):
+    """Every row of the pool as x [d], quantised for an e4m3 cache."""
+    if c["cache"] == "e4m3":
+        v, e = P.quantise(np.asarray(x, np.float64)[None])
+        c[name + "_cache"].view(torch.uint8)[:] = torch.from_numpy(v[0]).float().to(torch.float8_e4m3fn).view(torch.uint8)
+        c[name + "_scale"][:] = int(e[0]) + 127
+    else:
+        c[name + "_cache"][:] = torch.as_tensor(x, dtype=torch.float64).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 3, 140])
+@pytest.mark.parametrize("R", [1, 100])
+@pytest.mark.parametrize("size", [-1e30, 1e30, -3.3e8, 7.7e10, 1e4])
+def test_equal_scores_of_any_size_share_the_weight(size, R, n, cache):
+    """Keys that are all masked by a huge negative value, or all huge: the mean of the visible values, over many
+    tiles and pieces."""
+    c = paged_case([(n, 600 + n), (n, 90 + n)], 1, 128, 16, cache, seed=12)
+    _set_all(c, "k", np.full(128, size))
+    H = 4
+    q = (torch.tensor([0.37, 0.53, 1.0, 0.01])[None, :, None] * torch.ones((c["num_tok"], H, 128))).to(torch.bfloat16)
+    # equal keys have equal scores, whatever their rounding: sums of 128 equal products are exact up to a common factor
+    v = rows_of(c, "v")
+    want = np.concatenate([np.stack([v[r][:kv - n + i + 1, 0].mean(0) for i in range(n)]) for r, (_, kv) in enumerate(c["lengths"])])
+    size_a = np.concatenate([np.stack([np.abs(v[r][:kv - n + i + 1, 0]).mean(0) for i in range(n)]) for r, (_, kv) in enumerate(c["lengths"])])
+    got, status = _run(_repeat(c, R), q.repeat(R, 1, 1))
+    assert status == 0
+    err = np.abs(got.double().numpy().reshape(R, *q.shape) - want[:, None])
+    # the output's rounding, the weights', 2^-20 for the exponential and the sums
+    tol = HALF_BF16 * np.abs(want) + (HALF_BF16 + 2.0 ** -20) * size_a + 1e-30
+    assert (err <= tol[:, None]).all(), (np.nanmax(err / tol[:, None]), int(np.isnan(err).sum()))
