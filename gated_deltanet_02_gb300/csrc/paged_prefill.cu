@@ -53,6 +53,9 @@ using tc::warp_arrive;
 constexpr int kItems = 4;
 constexpr float kSlack = 8.f;  // log2 of the largest weight
 constexpr int kNoTile = 0x7fffffff;
+// e4m3: the keys' scales are taken times this, for products (2^24 at most) with a scale
+// of 2^119, as rows with an infinity get it, stay finite; the scales of q take it out again.
+constexpr float kKeyScale = 0x1p-24f;
 
 template <int D, bool kF8>
 struct Cfg {
@@ -481,8 +484,9 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
           const uint32_t r = r0 + k * kPer;
           uint2 hi, lo;
           const float scale = split_q<kLanes>(x[k], hi, lo);
-          // never 0, which a masked score of -infinity would turn into NaN: scores (2^24 at most before it) are next to 0 then
-          if (c == 0) s_qs[r] = fmaxf(scale * p.c, 0x1p-126f);
+          // never 0 (nor infinite), which a masked score of -infinity (or one of 0) would turn into
+          // NaN: scores, 2^119 at most before it, are next to 0 then
+          if (c == 0) s_qs[r] = fminf(fmaxf(scale * (p.c / kKeyScale), 0x1p-126f), 3.4e38f);
           uint8_t *dst = smem + at(r, c >> 1) + (c & 1) * 8;
           *reinterpret_cast<uint2 *>(dst) = hi;
           *reinterpret_cast<uint2 *>(dst + C::kQPlane) = lo;
@@ -703,7 +707,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       for (; j < j1; ++j, ++g) {
         const uint32_t rk = g % C::kRawK, rv = g % C::kRawV, s = g % ST, ss = g % C::kScaleSlots;
         if (!(ok = wait_bar_warp(&bars->rawk_full[rk], (g / C::kRawK) & 1u, abort))) break;
-        reinterpret_cast<float *>(smem + C::kOffScale)[ss * kTileKeys + ct] = scale_value(smem[C::kOffCode + rk * kTileKeys + ct]);
+        reinterpret_cast<float *>(smem + C::kOffScale)[ss * kTileKeys + ct] = kKeyScale * scale_value(smem[C::kOffCode + rk * kTileKeys + ct]);
         warp_arrive(&bars->rawk_empty[rk]);
         warp_arrive(&bars->scale_ready[ss]);
         if (!(ok = wait_bar_warp(&bars->rawv_full[rv], (g / C::kRawV) & 1u, abort))) break;

@@ -264,3 +264,28 @@ def test_equal_scores_of_any_size_share_the_weight(size, R, n, cache):
     # the output's rounding, the weights', 2^-20 for the exponential and the sums
     tol = HALF_BF16 * np.abs(want) + (HALF_BF16 + 2.0 ** -20) * size_a + 1e-30
     assert (err <= tol[:, None]).all(), (np.nanmax(err / tol[:, None]), int(np.isnan(err).sum()))
+
+
+@pytest.mark.parametrize("n", [1, 140])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_saturated_keys_in_an_e4m3_cache(sign, n):
+    """A key row with an infinite element is stored as +-448 2^119: it takes all the weight, or none."""
+    c = paged_case([(n, 300 + n)], 1, 64, 16, "e4m3", seed=13)
+    x = torch.zeros(64)
+    x[5] = 448.0 * sign
+    _set(c, "k", 0, 33, x)
+    c["k_scale"][int(c["table"][0, 2]), 0, 1] = 246
+    q = _q(c, 2, size=0.5).abs()
+    q[:, :, 5] = 1.5
+    v = rows_of(c, "v")[0]
+    if sign > 0:
+        got, status = _run(c, q)
+        assert status == 0
+        want = np.broadcast_to(v[33, 0], (n, 2, 64))
+        assert (np.abs(got.double().numpy() - want) <= 2.0 ** -7 * np.abs(want)).all()   # a weight's and the output's rounding
+    else:
+        got, status = _run(c, q)
+        assert status == 0
+        c["k_scale"][int(c["table"][0, 2]), 0, 1] = 127       # -448: no weight either
+        want, tol = _oracle(c, q)
+        assert (np.abs(got.double().numpy() - want) <= tol).all()
