@@ -383,13 +383,15 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
     const uint32_t sb = smem_u32(smem);
     float *s_red = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * rb;  // [row][warp]
-    // per row: maximum (0 while there is none), its step in this tile, the root of
+    // per row: m (0 while there is no maximum), its step in this tile, the root of
     // that step's factor (applied twice: with an e4m3 cache a sum may be far from 1, and
     // the factor beyond fp32's range), the scale of q, the last key that it sees
     float *s_m = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * N + rb, *s_d = s_m + N, *s_f = s_d + N, *s_qs = s_f + N;
     int *s_lim = reinterpret_cast<int *>(s_qs + N);
-    constexpr float kSlack = kF8 ? 4.f : 8.f;        // log2 of the largest weight
-    constexpr float kTop = 11.f;                     // e4m3: and what its parts are above that, 2^15 at most
+    // How far a score may be above the maximum before m moves (log2), and how far above the
+    // maximum m then is: bf16 weights are 1 at most, so that no value overflows.
+    constexpr float kSlack = kF8 ? 4.f : 8.f, kAbove = kF8 ? 0.f : kSlack;
+    constexpr float kTop = 11.f;                     // e4m3: log2 of what the weights' parts are times, 2^15 at most
     uint32_t g = 0, slot = 0, syncs = 0;
     // the group's barrier; like every wait here it gives up after a limit
     auto group_sync = [&]() -> bool {
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
           float t = x[0];
 #pragma unroll
           for (int r = 1; r < R - 1; r += 2) t = max3(t, x[r], x[r + 1]);
-          const bool any = __any_sync(0xffffffffu, fmaxf(t, x[R - 1]) + ev > kSlack);
+          const bool any = __any_sync(0xffffffffu, fmaxf(t, x[R - 1]) + ev > kSlack - kAbove);
           if (lane == 0) s_flag[g & 1][w][q4] = any || first;
         }
         if (!(ok = group_sync())) break;
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
             if (st < R) {
               const float4 v = *reinterpret_cast<const float4 *>(s_red + st * 4);
               const float t = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-              const float d = t > (has_max ? kSlack : -INFINITY) ? t : 0.f;
+              const float d = t > (has_max ? kSlack - kAbove : -INFINITY) ? t + kAbove : 0.f;
               s_d[st] = d;
               s_f[st] = has_max ? ex2(-0.5f * d) : 1.f;  // nothing to rescale before the first maximum, which may be far below 0
               has_max |= t > -INFINITY;

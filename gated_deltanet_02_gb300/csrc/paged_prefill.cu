@@ -51,7 +51,9 @@ using tc::wait_bar_warp;
 using tc::warp_arrive;
 
 constexpr int kItems = 4;
-constexpr float kSlack = 8.f;  // log2 of the largest weight
+// How far a score may be above the running maximum (log2); the weights are taken
+// relative to 2^kSlack times it, so that none is above 1 and no value overflows.
+constexpr float kSlack = 8.f;
 constexpr int kNoTile = 0x7fffffff;
 // e4m3: the keys' scales are taken times this, for products (2^24 at most) with a scale
 // of 2^119, as rows with an infinity get it, stay finite; the scales of q take it out again.
@@ -579,7 +581,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         // for ordinary scores, a factor beyond fp32's range for huge ones.  There, with c cut to
         // a power of two, it is exact: keys that equal the maximum have weight 1, and
         // any other, a step of 2^5 (2^4 with that c) below at least, next to none.
-        float cc = c, ms = m == -INFINITY ? 0.f : m * c;
+        float cc = c, ms = m == -INFINITY ? 0.f : m * c + kSlack;
         if (fabsf(ms) > 0x1p29f) {
           cc = __uint_as_float(__float_as_uint(c) & 0x7f800000u);
           ms = m * cc;
@@ -678,7 +680,7 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
       }
       // a sum beside no maximum is NaN (scores of NaN alone): the merge leaves out pieces whose maximum is
       // -infinity; so it is here where the row tile has no work, and c is not this item's
-      const float ml = m > -INFINITY ? m * c : l != 0.f ? 0.f : m;
+      const float ml = m > -INFINITY ? m * c + kSlack : l != 0.f ? 0.f : m;
       if (it.kind != 0 && has) p.ml[pslot * kPrefillRows + row] = make_float2(ml, l);
       if (lrow == 0) {
         if (it.kind != 0) p.skip[2 * pslot + w] = bad;

@@ -289,3 +289,27 @@ def test_saturated_keys_in_an_e4m3_cache(sign, n):
         c["k_scale"][int(c["table"][0, 2]), 0, 1] = 127       # -448: no weight either
         want, tol = _oracle(c, q)
         assert (np.abs(got.double().numpy() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 3, 140])
+@pytest.mark.parametrize("R", [1, 100])
+@pytest.mark.parametrize("rise", [0.0, 3.0, 5.0])
+def test_values_next_to_the_largest(rise, R, n, cache):
+    """A value of 3e38 (an infinite one as an e4m3 cache stores it) does not overflow, also where its key's score
+    is above all before it by less than what moves the running maximum (rise, in nats)."""
+    c = paged_case([(n, 300 + n), (n, 200 + n)], 1, 128, 16, cache, seed=14)
+    for name in ("k", "v"):
+        _set_all(c, name, np.zeros(128))
+    x = torch.zeros(128)
+    for r in range(2):
+        _set(c, "k", r, 180, math.sqrt(128) * rise / 128)          # q of ones
+        if cache == "e4m3":
+            x[3], x[70] = 448.0, -448.0
+            _set(c, "v", r, 180, x)
+            c["v_scale"][int(c["table"][r, 180 // 16]), 0, 180 % 16] = 246
+        else:
+            x[3], x[70] = 3e38, -3e38
+            _set(c, "v", r, 180, x)
+    q = torch.ones((c["num_tok"], 2, 128), dtype=torch.bfloat16)
+    _check_repeated(c, q, R)
