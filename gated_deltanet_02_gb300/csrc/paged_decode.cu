@@ -65,7 +65,7 @@ struct Cfg {
   static constexpr uint32_t kBytesQ = N * kTQ * D * kEsz;
   static constexpr uint32_t kBytesP = N * kTP * kTileKeys * kEsz;
   static constexpr uint32_t kBytesScale = kF8 ? kScaleSlots * 2 * kTileKeys : 0;
-  static constexpr uint32_t kBytesRows = 4 * N * 4 + 5 * N * 4;  // [row][warp] maxima or sums, then five numbers a row
+  static constexpr uint32_t kBytesRows = 4 * N * 4 + 4 * N * 4;  // [row][warp] maxima or sums, then four numbers a row
   static constexpr uint32_t kBytesBars = 640;
   static constexpr uint32_t kFixed = kBytesQ + kBytesP + kBytesScale + kBytesRows + kBytesBars + 1024;
   // two CTAs of an SM share 228 KiB, 1 KiB of each reserved
@@ -383,10 +383,10 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
     const uint32_t sb = smem_u32(smem);
     float *s_red = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * rb;  // [row][warp]
-    // per row: m (0 while there is no maximum), its step in this tile, the root of
-    // that step's factor (applied twice: with an e4m3 cache a sum may be far from 1, and
-    // the factor beyond fp32's range), the scale of q, the last key that it sees
-    float *s_m = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * N + rb, *s_d = s_m + N, *s_f = s_d + N, *s_qs = s_f + N;
+    // per row: m (0 while there is no maximum), the root of the factor of its step in
+    // this tile (applied twice: with an e4m3 cache a sum may be far from 1, and the
+    // factor beyond fp32's range), the scale of q, the last key that it sees
+    float *s_m = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * N + rb, *s_f = s_m + N, *s_qs = s_f + N;
     int *s_lim = reinterpret_cast<int *>(s_qs + N);
     // How far a score may be above the maximum before m moves (log2), and how far above the
     // maximum m then is: bf16 weights are 1 at most, so that no value overflows.
@@ -448,11 +448,8 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
         if (!(ok = wait_bar_warp<false>(&bars->s_ready[buf], (g >> 1) & 1u, abort))) break;
         tc_fence_after();
         const int key = j * kTileKeys + kk;
-        // ---- scores in log2 units, less the row's maximum; rounded before the difference, as
-        // the maximum was: with a fused one equal keys of huge scores would differ.  (Another
-        // rounding of the difference, exact near 0, so that the two are not fused after all.)
+        // ---- scores in log2 units, less m where `less` is set
         float x[R], ev = 0.f;                             // e4m3: the value's exponent
-        tmem_ld16(tS, x);
         float ks = p.c;
         if constexpr (kF8) {
           const uint8_t *ss = smem + C::kOffScale + (g % kScaleSlots) * 2 * kTileKeys;
@@ -461,31 +458,39 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
           ks = scale_value(ss[kk]);
           ev = !there ? 0.f : vc == 255 ? __int_as_float(0x7fffffff) : (float)((int)vc - 127);
         }
-        tc_fence_before();
-        warp_arrive(&bars->s_free[buf]);
-#pragma unroll
-        for (int r = 0; r < R; r += 4) {
-          const float4 m = *reinterpret_cast<const float4 *>(s_m + r);
-          float2 q0 = make_float2(ks, ks), q1 = q0;
-          if constexpr (kF8) {
-            const float4 qs = *reinterpret_cast<const float4 *>(s_qs + r);
-            q1 = __fmul2_rn(q0, make_float2(qs.z, qs.w));
-            q0 = __fmul2_rn(q0, make_float2(qs.x, qs.y));
-          }
-          const float2 a = __fadd2_rz(__fmul2_rn(make_float2(x[r], x[r + 1]), q0), make_float2(-m.x, -m.y));
-          const float2 b = __fadd2_rz(__fmul2_rn(make_float2(x[r + 2], x[r + 3]), q1), make_float2(-m.z, -m.w));
-          x[r] = a.x, x[r + 1] = a.y, x[r + 2] = b.x, x[r + 3] = b.y;
-        }
-        if (j * kTileKeys + kTileKeys - 1 > it.pos0) {    // some row does not see the whole tile
+        // The product is rounded before the difference, as m was: with a fused one equal keys of
+        // huge scores would differ.  (Another rounding of the difference, exact near 0, so that
+        // the two are not fused after all.)
+        auto scores = [&](bool less) {
+          tmem_ld16(tS, x);
 #pragma unroll
           for (int r = 0; r < R; r += 4) {
-            const int4 lim = *reinterpret_cast<const int4 *>(s_lim + r);
-            x[r] = key > lim.x ? -INFINITY : x[r];
-            x[r + 1] = key > lim.y ? -INFINITY : x[r + 1];
-            x[r + 2] = key > lim.z ? -INFINITY : x[r + 2];
-            x[r + 3] = key > lim.w ? -INFINITY : x[r + 3];
+            const float4 m = *reinterpret_cast<const float4 *>(s_m + r);
+            float2 q0 = make_float2(ks, ks), q1 = q0;
+            if constexpr (kF8) {
+              const float4 qs = *reinterpret_cast<const float4 *>(s_qs + r);
+              q1 = __fmul2_rn(q0, make_float2(qs.z, qs.w));
+              q0 = __fmul2_rn(q0, make_float2(qs.x, qs.y));
+            }
+            float2 a = __fmul2_rn(make_float2(x[r], x[r + 1]), q0), b = __fmul2_rn(make_float2(x[r + 2], x[r + 3]), q1);
+            if (less) {
+              a = __fadd2_rz(a, make_float2(-m.x, -m.y));
+              b = __fadd2_rz(b, make_float2(-m.z, -m.w));
+            }
+            x[r] = a.x, x[r + 1] = a.y, x[r + 2] = b.x, x[r + 3] = b.y;
           }
-        }
+          if (j * kTileKeys + kTileKeys - 1 > it.pos0) {    // some row does not see the whole tile
+#pragma unroll
+            for (int r = 0; r < R; r += 4) {
+              const int4 lim = *reinterpret_cast<const int4 *>(s_lim + r);
+              x[r] = key > lim.x ? -INFINITY : x[r];
+              x[r + 1] = key > lim.y ? -INFINITY : x[r + 1];
+              x[r + 2] = key > lim.z ? -INFINITY : x[r + 2];
+              x[r + 3] = key > lim.w ? -INFINITY : x[r + 3];
+            }
+          }
+        };
+        scores(true);
         // ---- does a row's maximum move?  (In its first tile always; later once in a while.)
         {
           float t = x[0];
@@ -498,6 +503,9 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
         const int4 fl = *reinterpret_cast<const int4 *>(s_flag[g & 1][w]);
         const bool moves = fl.x | fl.y | fl.z | fl.w | (!first && s_unset[w]);
         if (moves) {
+          // from the scores themselves: a difference to an m far below has lost their last digits (masked
+          // keys of -1e30 before ordinary ones)
+          if (!first) scores(false);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const float v = warp_max(x[r] + ev);
@@ -507,12 +515,11 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
           if (st < 32) {
             if (st < R) {
               const float4 v = *reinterpret_cast<const float4 *>(s_red + st * 4);
-              const float t = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-              const float d = t > (has_max ? kSlack - kAbove : -INFINITY) ? t + kAbove : 0.f;
-              s_d[st] = d;
-              s_f[st] = has_max ? ex2(-0.5f * d) : 1.f;  // nothing to rescale before the first maximum, which may be far below 0
-              has_max |= t > -INFINITY;
-              s_m[st] += d;
+              const float t = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)), m = s_m[st];
+              const bool up = has_max ? t - m > kSlack - kAbove : t > -INFINITY;
+              s_f[st] = up && has_max ? ex2(-0.5f * (t + kAbove - m)) : 1.f;  // nothing to rescale before the first maximum
+              if (up) s_m[st] = t + kAbove;
+              has_max |= up;
             }
             const bool unset = __any_sync(0xffffffffu, st < R && !has_max);
             if (st == 0) s_unset[w] = unset;
@@ -520,13 +527,21 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
           if (!(ok = group_sync())) break;
 #pragma unroll
           for (int r = 0; r < R; r += 4) {
-            const float4 d = *reinterpret_cast<const float4 *>(s_d + r), f = *reinterpret_cast<const float4 *>(s_f + r);
-            x[r] -= d.x, x[r + 1] -= d.y, x[r + 2] -= d.z, x[r + 3] -= d.w;
+            const float4 m = *reinterpret_cast<const float4 *>(s_m + r);
+            const float2 a = __fadd2_rz(make_float2(x[r], x[r + 1]), make_float2(-m.x, -m.y));
+            const float2 b = __fadd2_rz(make_float2(x[r + 2], x[r + 3]), make_float2(-m.z, -m.w));
+            x[r] = a.x, x[r + 1] = a.y, x[r + 2] = b.x, x[r + 3] = b.y;
+          }
+#pragma unroll
+          for (int r = 0; r < R; r += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(s_f + r);
             const float2 f0 = make_float2(f.x, f.y), f1 = make_float2(f.z, f.w);
             l[r / 2] = __fmul2_rn(__fmul2_rn(l[r / 2], f0), f0);
             l[r / 2 + 1] = __fmul2_rn(__fmul2_rn(l[r / 2 + 1], f1), f1);
           }
         }
+        tc_fence_before();
+        warp_arrive(&bars->s_free[buf]);                  // (the buffer's next product comes behind this tile's weights)
         if (g > 0 && !(ok = wait_bar_warp<false>(&bars->o_done, (g - 1) & 1u, abort))) break;  // W is read, O^T complete
         if (moves && !first) {
           tc_fence_after();

@@ -313,3 +313,63 @@ def test_values_next_to_the_largest(rise, R, n, cache):
             _set(c, "v", r, 180, x)
     q = torch.ones((c["num_tok"], 2, 128), dtype=torch.bfloat16)
     _check_repeated(c, q, R)
+
+
+def _set_row(c, r, t, x):
+    """The key row of request r at a position as x [d], quantised for an e4m3 cache."""
+    if c["cache"] == "bf16":
+        _set(c, "k", r, t, torch.from_numpy(x))
+        return
+    v, e = P.quantise(x[None])
+    cell = (int(c["table"][r, t // c["page"]]), slice(None), t % c["page"])
+    c["k_cache"].view(torch.uint8)[cell] = torch.from_numpy(v[0]).float().to(torch.float8_e4m3fn).view(torch.uint8)
+    c["k_scale"][cell] = int(e[0]) + 127
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 3, 140])
+@pytest.mark.parametrize("R", [1, 100])
+@pytest.mark.parametrize("low", [-1e3, -1e6, -1e30])
+def test_masked_keys_before_ordinary_ones(low, R, n, cache):
+    """The first 200 keys are masked by a huge negative value: the ordinary ones after them keep their differences."""
+    c = paged_case([(n, 500 + n), (n, 210 + n)], 1, 128, 16, cache, seed=15)
+    q = _q(c, 4)
+    q[:, :, 7] = 3.0
+
+    def mask(value):
+        x = np.zeros(128)
+        x[7] = value
+        for r in range(2):
+            for t in range(200):
+                _set_row(c, r, t, x)
+
+    mask(-200.0)                             # no weight either, and a tolerance of ordinary scores
+    want, tol = _oracle(c, q)
+    mask(low)
+    got, status = _run(_repeat(c, R), q.repeat(R, 1, 1))
+    assert status == 0
+    err = np.abs(got.double().numpy().reshape(R, *q.shape) - want) / tol
+    assert (err <= 1).all(), (np.nanmax(err), int(np.isnan(err).sum()))
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 3, 140])
+@pytest.mark.parametrize("R", [1, 100])
+@pytest.mark.parametrize("levels", [(1e30, 3e30, 7e30), (-7e30, -3e30, -1e30), (-1e30, 1e9, 7e9), (1e5, 1.1e7, 1.3e11)])
+def test_levels_of_huge_scores(levels, R, n, cache):
+    """Keys of three levels of scores far apart, each over several tiles: the mean of the values of the highest one seen."""
+    c = paged_case([(n, 700 + n)], 1, 64, 16, cache, seed=16)
+    kv = 700 + n
+    level = np.where(np.arange(kv) < 150, 0, np.where(np.arange(kv) < 300, 1, 2))
+    for t in range(kv):
+        _set_row(c, 0, t, np.full(64, levels[level[t]]))
+    q = (torch.tensor([0.37, 1.0])[None, :, None] * torch.ones((n, 2, 64))).to(torch.bfloat16)
+    v = rows_of(c, "v")[0][:, 0]
+    top = level == 2
+    got, status = _run(_repeat(c, R), q.repeat(R, 1, 1))
+    assert status == 0
+    got = got.double().numpy().reshape(R, n, 2, 64)
+    for i in range(n):
+        rows = v[:kv - n + i + 1][top[:kv - n + i + 1]]
+        tol = HALF_BF16 * np.abs(rows.mean(0)) + (HALF_BF16 + 2.0 ** -20) * np.abs(rows).mean(0)
+        assert (np.abs(got[:, i] - rows.mean(0)) <= tol).all()
