@@ -5,8 +5,8 @@
 // Mathematics: one pass over the keys with the running maximum m (log2 units)
 // and sum l of the softmax per row,
 //   S = Q K^T,   P = 2^(S - m),   O += P V,   l += sum P,
-// m only moving (and O, l being rescaled) when a tile exceeds it by 2^8: a
-// common factor of P, O and l.  S, m, l and O are fp32; P is rounded to bf16
+// m only moving (and O, l being rescaled) when a tile exceeds it by 2^8 (P is
+// relative to 2^8 times m, 1 at most): a common factor of P, O and l.  S, m, l and O are fp32; P is rounded to bf16
 // for the second product (half a step, 2^-8 relative to a weight), which adds
 // to the output about what its own rounding to bf16 does.
 //
@@ -34,9 +34,9 @@
 //
 // Bound: the tensor core for long prompts, next to it the softmax of the tile
 // that waits for it.  A causal prompt of 16,000 tokens, 16 heads over 4 of 128,
-// takes 656-663 us, 1590 TFLOP/s; packed prompts of 200 .. 4001 tokens 141.5 us (1110);
-// 8191 tokens, 8 heads of 64, 77.5 us (887); 4096 tokens behind 12,288 of an e4m3
-// cache, 32 heads over 8, 766 us (1256).
+// takes 646 us, 1620 TFLOP/s; packed prompts of 200 .. 4001 tokens 142 us (1110);
+// 8191 tokens, 8 heads of 64, 78 us (882); 4096 tokens behind 12,288 of an e4m3
+// cache, 32 heads over 8, 783 us (1229).
 #include "paged_sched.cuh"
 #include "paged_tc.cuh"
 #include "tc_common.cuh"
