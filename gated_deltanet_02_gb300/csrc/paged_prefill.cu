@@ -581,7 +581,8 @@ __global__ void __launch_bounds__(kF8 ? 512 : 384, 1)
         // for ordinary scores, a factor beyond fp32's range for huge ones.  There, with c cut to
         // a power of two, it is exact: keys that equal the maximum have weight 1, and
         // any other, a step of 2^5 (2^4 with that c) below at least, next to none.
-        float cc = c, ms = m == -INFINITY ? 0.f : m * c + kSlack;
+        float cc = c, ms = m * c + kSlack;
+        if (ms == -INFINITY) ms = 0.f;  // no score above -infinity, in these units
         if (fabsf(ms) > 0x1p29f) {
           cc = __uint_as_float(__float_as_uint(c) & 0x7f800000u);
           ms = m * cc;

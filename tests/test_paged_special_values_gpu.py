@@ -373,3 +373,19 @@ def test_levels_of_huge_scores(levels, R, n, cache):
         rows = v[:kv - n + i + 1][top[:kv - n + i + 1]]
         tol = HALF_BF16 * np.abs(rows.mean(0)) + (HALF_BF16 + 2.0 ** -20) * np.abs(rows).mean(0)
         assert (np.abs(got[:, i] - rows.mean(0)) <= tol).all()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 3, 140])
+@pytest.mark.parametrize("R", [1, 100])
+def test_scores_that_overflow_to_minus_infinity(R, n, cache):
+    """Scores are fp32: keys whose scores are below its range count as masked, and rows of them alone give zeros."""
+    c = paged_case([(n, 400 + n)], 1, 64, 16, cache, seed=17)
+    _set_all(c, "k", np.full(64, -1e33))
+    q = torch.ones((n, 2, 64), dtype=torch.bfloat16)
+    got, status = _run(_repeat(c, R), q.repeat(R, 1, 1), scale=1e5)
+    assert status == 0 and bool((got == 0).all())
+    _set_row(c, 0, 250, np.full(64, 1e-3))          # one ordinary key: all the weight
+    got, status = _run(_repeat(c, R), q.repeat(R, 1, 1), scale=1e5)
+    want = rows_of(c, "v")[0][250, 0]
+    assert status == 0 and bool((np.abs(got.double().numpy() - want) <= 2.0 ** -7 * np.abs(want)).all())
