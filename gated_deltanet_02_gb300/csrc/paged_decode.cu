@@ -65,7 +65,7 @@ struct Cfg {
   static constexpr uint32_t kBytesQ = N * kTQ * D * kEsz;
   static constexpr uint32_t kBytesP = N * kTP * kTileKeys * kEsz;
   static constexpr uint32_t kBytesScale = kF8 ? kScaleSlots * 2 * kTileKeys : 0;
-  static constexpr uint32_t kBytesRows = 4 * N * 4 + 4 * N * 4;  // [row][warp] maxima or sums, then four numbers a row
+  static constexpr uint32_t kBytesRows = 4 * N * 4 + 5 * N * 4;  // [row][warp] maxima or sums, then five numbers a row
   static constexpr uint32_t kBytesBars = 640;
   static constexpr uint32_t kFixed = kBytesQ + kBytesP + kBytesScale + kBytesRows + kBytesBars + 1024;
   // two CTAs of an SM share 228 KiB, 1 KiB of each reserved
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
   Bars *bars = reinterpret_cast<Bars *>(smem + C::kOffBars);
   static_assert(sizeof(Bars) <= C::kBytesBars, "barrier block");
   __shared__ __align__(16) int s_flag[2][W][4];  // [tile parity][group][warp]: a row's maximum moves
-  __shared__ int s_unset[W];                     // a row of the group has no maximum yet
+  __shared__ int s_look[W];                      // 1: rows of the group have to be looked at in every tile, 2: huge scores in this one
   __shared__ int s_bad[kItems];
   volatile int *abort = &bars->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -385,9 +385,10 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
     float *s_red = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * rb;  // [row][warp]
     // per row: m (0 while there is no maximum), the root of the factor of its step in
     // this tile (applied twice: with an e4m3 cache a sum may be far from 1, and the
-    // factor beyond fp32's range), the scale of q, the last key that it sees
-    float *s_m = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * N + rb, *s_f = s_m + N, *s_qs = s_f + N;
-    int *s_lim = reinterpret_cast<int *>(s_qs + N);
+    // factor beyond fp32's range), the scale of q, the last key that it sees; with an
+    // e4m3 cache m is m + lo for huge scores, beside which a value's exponent is lost in fp32
+    float *s_m = reinterpret_cast<float *>(smem + C::kOffRows) + 4 * N + rb, *s_f = s_m + N, *s_qs = s_f + N, *s_lo = s_qs + N;
+    int *s_lim = reinterpret_cast<int *>(s_lo + N);
     // How far a score may be above the maximum before m moves (log2), and how far above the
     // maximum m then is: bf16 weights are 1 at most, so that no value overflows.
     constexpr float kSlack = kF8 ? 4.f : 8.f, kAbove = kF8 ? 0.f : kSlack;
@@ -432,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
         fence_proxy_async_smem();
         warp_arrive(&bars->q_ready);
         if (st < R) {
-          s_m[st] = 0.f;
+          s_m[st] = s_lo[st] = 0.f;
           s_lim[st] = it.pos0 + min(rb + st, nrow - 1) / p.G;
         }
         if (!(ok = group_sync())) break;
@@ -501,7 +502,7 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
         }
         if (!(ok = group_sync())) break;
         const int4 fl = *reinterpret_cast<const int4 *>(s_flag[g & 1][w]);
-        const bool moves = fl.x | fl.y | fl.z | fl.w | (!first && s_unset[w]);
+        const bool moves = fl.x | fl.y | fl.z | fl.w | (!first && s_look[w]);
         if (moves) {
           // from the scores themselves: a difference to an m far below has lost their last digits (masked
           // keys of -1e30 before ordinary ones)
@@ -512,25 +513,60 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
             if (lane == r) s_red[r * 4 + q4] = v;
           }
           if (!(ok = group_sync())) break;
+          float old = 0.f;                                // the row's m before a huge score
+          bool huge = false;
           if (st < 32) {
+            bool look = false;
             if (st < R) {
               const float4 v = *reinterpret_cast<const float4 *>(s_red + st * 4);
               const float t = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)), m = s_m[st];
-              const bool up = has_max ? t - m > kSlack - kAbove : t > -INFINITY;
-              s_f[st] = up && has_max ? ex2(-0.5f * (t + kAbove - m)) : 1.f;  // nothing to rescale before the first maximum
-              if (up) s_m[st] = t + kAbove;
-              has_max |= up;
+              huge = kF8 && fabsf(t) > 0x1p20f && fabsf(t) < INFINITY;
+              if (huge) {
+                old = m;
+                s_m[st] = has_max ? fmaxf(m, t) : t;
+              } else {
+                const bool up = has_max ? t - m > kSlack - kAbove : t > -INFINITY;
+                s_f[st] = up && has_max ? ex2(-0.5f * (t + kAbove - m)) : 1.f;  // nothing to rescale before the first maximum
+                if (up) {
+                  s_m[st] = t + kAbove;
+                  s_lo[st] = 0.f;
+                }
+                has_max |= up;
+              }
+              look = !has_max || huge || s_lo[st] != 0.f;
             }
-            const bool unset = __any_sync(0xffffffffu, st < R && !has_max);
-            if (st == 0) s_unset[w] = unset;
+            const int bits = (__any_sync(0xffffffffu, look) ? 1 : 0) | (__any_sync(0xffffffffu, huge) ? 2 : 0);
+            if (st == 0) s_look[w] = bits;
           }
           if (!(ok = group_sync())) break;
+          const int look = s_look[w];
+          if (look & 2) {                                 // the scores less the new m are small again: lo from them
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              const float v = warp_max(__fadd_rn(x[r], -s_m[r]) + ev);
+              if (lane == r) s_red[r * 4 + q4] = v;
+            }
+            if (!(ok = group_sync())) break;
+            if (huge) {
+              const float4 v = *reinterpret_cast<const float4 *>(s_red + st * 4);
+              const float t = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)), was = old - s_m[st] + s_lo[st];
+              const float lo = has_max ? fmaxf(t, was) : t;
+              s_f[st] = has_max ? ex2(-0.5f * (lo - was)) : 1.f;
+              s_lo[st] = lo;
+              has_max = true;
+            }
+            if (!(ok = group_sync())) break;
+          }
 #pragma unroll
           for (int r = 0; r < R; r += 4) {
             const float4 m = *reinterpret_cast<const float4 *>(s_m + r);
             const float2 a = __fadd2_rz(make_float2(x[r], x[r + 1]), make_float2(-m.x, -m.y));
             const float2 b = __fadd2_rz(make_float2(x[r + 2], x[r + 3]), make_float2(-m.z, -m.w));
             x[r] = a.x, x[r + 1] = a.y, x[r + 2] = b.x, x[r + 3] = b.y;
+          }
+          if (kF8 && look) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) x[r] -= s_lo[r];
           }
 #pragma unroll
           for (int r = 0; r < R; r += 4) {
@@ -652,13 +688,18 @@ __global__ void __launch_bounds__(Cfg<D, kF8, N>::kThreads, 2)
         const int row = rb + r;
         if (row < nrow && has) {
           const float4 v = *reinterpret_cast<const float4 *>(s_red + r * 4);
-          const float lt = (v.x + v.y) + (v.z + v.w);
+          float lt = (v.x + v.y) + (v.z + v.w);
           if (it.kind == 0) {
             if (!bad) {
               const int tok = row / p.G, gh = row - tok * p.G;
               p.o[((size_t)(it.row0 + tok) * p.H + it.hk * p.G + gh) * D + ch] = __float2bfloat16_rn(lt == 0.f ? 0.f : o[r] / lt);
             }
           } else {
+            if (kF8 && s_lo[r] != 0.f) {                  // relative to m alone
+              const float f = ex2(0.5f * s_lo[r]);
+              o[r] = o[r] * f * f;
+              lt = lt * f * f;
+            }
             p.part[((size_t)pslot * N + row) * D + ch] = o[r];
             if (ch == 0) p.ml[(size_t)pslot * N + row] = make_float2(lt == 0.f ? -INFINITY : s_m[r], lt);
           }

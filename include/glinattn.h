@@ -477,8 +477,6 @@ glinattn_status glinattn_kv_gather(const glinattn_kv_args *args, glinattn_stream
  *   2^-33 of the row's largest such product where that is more: contributions
  *   below the latter are lost, also in channels in which the keys with the
  *   largest products have zeros.
- *   There, a row whose largest score is beyond 2^24 in size (in log2 units) wants
- *   values of 2^-16 .. 2^12: a larger scale may overflow beside such a score.
  *
  *   q, o [num_tok, H, d] bf16; Hkv divides H, H / Hkv <= 256.
  *   scale: > 0 and finite, in log2 units too (below 2.3e38).  max_q_len: an upper bound of the ranges' lengths

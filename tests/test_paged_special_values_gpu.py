@@ -389,3 +389,24 @@ def test_scores_that_overflow_to_minus_infinity(R, n, cache):
     got, status = _run(_repeat(c, R), q.repeat(R, 1, 1), scale=1e5)
     want = rows_of(c, "v")[0][250, 0]
     assert status == 0 and bool((np.abs(got.double().numpy() - want) <= 2.0 ** -7 * np.abs(want)).all())
+
+
+@pytest.mark.parametrize("n", [1, 5, 140])
+@pytest.mark.parametrize("R", [1, 100])
+@pytest.mark.parametrize("size", [-1e30, -3e6, 4e7, 1e20])
+@pytest.mark.parametrize("codes", [(100, 112), (125, 135), (140, 160), (60, 66), (190, 200)])
+def test_value_scales_beside_huge_scores(codes, size, R, n):
+    """Beside scores that leave no digits for a value's exponent: the mean of the visible values, as ever."""
+    c = paged_case([(n, 600 + n)], 1, 64, 16, "e4m3", seed=18)
+    _set_all(c, "k", np.full(64, size))
+    g = torch.Generator().manual_seed(19)
+    c["v_scale"] = torch.randint(codes[0], codes[1], c["v_scale"].shape, generator=g).to(torch.uint8)
+    q = (torch.tensor([0.37, 1.0, 0.01])[None, :, None] * torch.ones((n, 3, 64))).to(torch.bfloat16)
+    v = rows_of(c, "v")[0][:, 0]
+    got, status = _run(_repeat(c, R), q.repeat(R, 1, 1))
+    assert status == 0
+    got = got.double().numpy().reshape(R, n, 3, 64)
+    for i in range(n):
+        rows = v[:600 + i + 1]
+        tol = HALF_BF16 * np.abs(rows.mean(0)) + (HALF_BF16 + 2.0 ** -20) * np.abs(rows).mean(0)
+        assert (np.abs(got[:, i] - rows.mean(0)) <= tol).all()
