@@ -53,11 +53,11 @@ glinattn_status check(const glinattn_paged_attn_args *a) {
 //   rows          8    16    24    32    40    48
 //   bf16 few    165   170   (no accumulators for more: a build that had them took 182 .. 206)
 //        many   169   170   173   174   176   177 us
-//   e4m3 few     96   103   113   120   155   161
+//   e4m3 few     97   104   115   122   156   163
 //        many   209   210   211   213   214   214
-// One request after 30,000: e4m3 20 .. 37 us against 39, bf16 24 and 26 against 35; four
+// One request after 30,000: e4m3 21 .. 37 us against 39, bf16 24 and 26 against 35; four
 // after 900: e4m3 12 .. 17 against 17 up to 32 rows, 19 and 21 against 18 with 40 and 48, bf16
-// 12.5 and 13.9 against 14.2.  The lengths are not known here, so short caches lose the 2 us.
+// 12.7 and 14.2 against 14.2.  The lengths are not known here, so short caches lose the 2 us.
 int item_rows(const glinattn_paged_attn_args *a) {
   const long long rows = (long long)a->max_q_len * (a->heads / a->kv_heads);
   if (rows <= 16) return 16;

@@ -33,7 +33,7 @@
 // registers they cost 64 requests of 40 rows after 32,768 tokens 15%).
 //
 // 256 single tokens after 1,000 .. 6,000, 16 heads over 4 of 128, bf16: 283-287 us,
-// 6,600 GB/s; the 40 rows above, e4m3: 439 us, 4,800 GB/s (382 us with weights in two
+// 6,600 GB/s; the 40 rows above, e4m3: 445 us, 4,700 GB/s (382 us with weights in two
 // parts and sums that could lose keys); 4 single tokens: 11 us, launches and latency.
 #include "paged_sched.cuh"
 #include "paged_tc.cuh"
