@@ -479,9 +479,9 @@ glinattn_status glinattn_kv_gather(const glinattn_kv_args *args, glinattn_stream
  *   largest products have zeros.
  *
  *   q, o [num_tok, H, d] bf16; Hkv divides H, H / Hkv <= 256.
- *   scale: > 0 and finite, in log2 units too (below 2.3e38).  max_q_len: an upper bound of the ranges' lengths
- *     (it selects the kernel); a longer range sets GLINATTN_DEV_BAD_COUNT and
- *     its request is skipped.
+ *   scale: > 0 and finite, in log2 units too (below 2.3e38).
+ *   max_q_len: an upper bound of the ranges' lengths (it selects the kernel); a
+ *     longer range sets GLINATTN_DEV_BAD_COUNT and its request is skipped.
  *   A request with a bad page among the pages that a group of its query rows
  *   reads leaves those output rows as they were.
  *   Cache rows at and behind kv_len may hold anything, NaN included.  A
