@@ -1,0 +1,330 @@
+// add_rms_norm.cu -- the residual's addition, the root-mean-square norm and its
+// 8-bit output (glinattn_add_rms_norm).
+//
+// Mathematics: h = x + residual, y = h / sqrt(mean(h^2) + eps) * w.  A row is read
+// once and kept in registers: a row's threads hold kChunks chunks of 8
+// elements each, sum their squares, join the sums, and scale.  A scale's block of 32, 64 or 128
+// elements is in 4, 8 or 16 neighbouring lanes.
+//
+// Bound: HBM bytes (x, residual in; residual, y out).
+#include "packed.cuh"
+
+namespace glinattn {
+namespace norm {
+namespace {
+
+using namespace packed;
+
+struct Params {
+  const void *x, *residual;
+  const float *weight;
+  void *residual_out, *y, *scale;
+  long long rows, x_stride;
+  int width, group;
+  float eps;
+};
+
+constexpr float kMinScale = 7.888609052210118e-31f;  // 2^-100
+// Squares of values up to 2^128 times this factor add up without an overflow.
+constexpr float kShrink = 1.262177448353619e-29f;    // 2^-96
+
+template <bool kMax>
+__device__ __forceinline__ float join(float a, float b) {
+  return kMax ? __uint_as_float(max(__float_as_uint(a), __float_as_uint(b))) : a + b;
+}
+
+// The sum (or the maximum of non-negative bits) over a row's `threads` threads, for all of them.
+template <bool kMax>
+__device__ __forceinline__ float over_row(float v, float *shared, int threads) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = join<kMax>(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (threads == 32) return v;
+  const int warps = threads >> 5;
+  __syncthreads();  // the last use of `shared` is over
+  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = shared[0];
+  for (int k = 1; k < warps; ++k) s = join<kMax>(s, shared[k]);
+  return s;
+}
+
+// 1 / sqrt(mean + eps) as a product of two factors: `shrink`, which the values are
+// multiplied with first, and the result.
+__device__ __forceinline__ float inverse_root(float sum, int width, float eps) { return 1.0f / sqrtf(sum / (float)width + eps); }
+
+// The scale of a maximum (its bits), what is stored and what values are multiplied with.
+template <bool kPow2>
+__device__ __forceinline__ float scale_of(uint32_t amax, void *scale, size_t at, bool store) {
+  if (kPow2) {
+    const uint32_t code = scale_code(amax);
+    if (store) reinterpret_cast<uint8_t *>(scale)[at] = (uint8_t)code;
+    return __uint_as_float((254u - code) << 23);
+  }
+  const float s = fmaxf(__uint_as_float(amax) / 448.0f, kMinScale);
+  if (store) reinterpret_cast<float *>(scale)[at] = s;
+  return 1.0f / s;
+}
+
+// kOut: 0 fp32, 1 bf16, 2 e4m3 with fp32 scales, 3 e4m3 with powers of two.
+// kRes: 0 none, 1 bf16, 2 fp32.
+template <bool kXBf16, int kRes, int kOut, int kChunks>
+__global__ void __launch_bounds__(1024) norm_rows_kernel(const Params p) {
+  __shared__ float shared[32];
+  const int threads = blockDim.x;
+  const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  const bool there = row < p.rows;  // whole warps: more than one row a CTA only with 32 threads a row
+  const int chunks = p.width >> 3;
+  float h[kChunks][8];
+  float sum = 0.0f;
+  Raw8<kXBf16> rx[kChunks];
+  Raw8<kRes == 1> rr[kChunks];
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) {
+    const int c = k * threads + threadIdx.x;
+    if (there && c < chunks) {
+      rx[k] = load_raw8<kXBf16>(p.x, (size_t)row * p.x_stride + 8 * c);
+      if (kRes) rr[k] = load_raw8<kRes == 1>(p.residual, (size_t)row * p.width + 8 * c);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) {
+    const int c = k * threads + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[k][i] = 0.0f;
+    if (there && c < chunks) {
+      unpack8(rx[k], h[k]);
+      if (kRes) {
+        float r[8];
+        unpack8(rr[k], r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[k][i] += r[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(h[k][i], h[k][i], sum);
+    }
+  }
+  sum = over_row<false>(sum, shared, threads);
+  if (kRes && there) {
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      const int c = k * threads + threadIdx.x;
+      if (c < chunks) store8<kRes == 1>(p.residual_out, (size_t)row * p.width + 8 * c, h[k]);
+    }
+  }
+  float eps = p.eps;
+  if (!(sum <= 3.0e38f)) {  // uniform over the row: an overflow, an infinity or a NaN
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        h[k][i] *= kShrink;
+        sum = fmaf(h[k][i], h[k][i], sum);
+      }
+    eps = 0.0f;                    // 2^-192 eps
+    sum = over_row<false>(sum, shared, threads);
+  }
+  const float inv = inverse_root(sum, p.width, eps);
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) {
+    const int c = k * threads + threadIdx.x;
+    float w[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+    if (p.weight && c < chunks) unpack8(load_raw8<false>(p.weight, 8 * c), w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[k][i] = h[k][i] * inv * w[i];
+  }
+  if constexpr (kOut < 2) {
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      const int c = k * threads + threadIdx.x;
+      if (there && c < chunks) store8<kOut == 1>(p.y, (size_t)row * p.width + 8 * c, h[k]);
+    }
+  } else {
+    uint32_t top[kChunks];
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      top[k] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top[k] = max(top[k], finite_bits(h[k][i]));
+    }
+    const int lanes = p.group >> 3;
+    if (p.group) {
+      for (int o = 1; o < lanes; o <<= 1)
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) top[k] = max(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
+    } else {
+#pragma unroll
+      for (int k = 1; k < kChunks; ++k) top[0] = max(top[0], top[k]);
+      top[0] = __float_as_uint(over_row<true>(__uint_as_float(top[0]), shared, threads));
+    }
+    float f = 0.0f;
+    if (!p.group) f = scale_of<kOut == 3>(top[0], p.scale, (size_t)row, there && threadIdx.x == 0);
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      const int c = k * threads + threadIdx.x;
+      const bool in = there && c < chunks;
+      if (p.group)
+        f = scale_of<kOut == 3>(top[k], p.scale, (size_t)row * (p.width / p.group) + c / lanes, in && c % lanes == 0);
+      float q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = h[k][i] * f;
+      if (in) *reinterpret_cast<uint2 *>(reinterpret_cast<uint8_t *>(p.y) + (size_t)row * p.width + 8 * c) = to_e4m3x8(q);
+    }
+  }
+}
+
+// Any width and alignment: one CTA a row, the row read again (from L2) for each of its
+// passes; every element is read and written by one thread in the last of them.
+template <bool kXBf16, int kRes, int kOut>
+__global__ void __launch_bounds__(512) norm_any_kernel(const Params p) {
+  __shared__ float shared[32];
+  const long long row = blockIdx.x;
+  const size_t x0 = (size_t)row * p.x_stride, y0 = (size_t)row * p.width;
+  auto at = [&](int i) {
+    float h = load_one<kXBf16>(p.x, x0 + i);
+    if (kRes) h += load_one<kRes == 1>(p.residual, y0 + i);
+    return h;
+  };
+  float sum = 0.0f, shrink = 1.0f, eps = p.eps;
+  for (int i = threadIdx.x; i < p.width; i += blockDim.x) {
+    const float h = at(i);
+    sum = fmaf(h, h, sum);
+  }
+  sum = over_row<false>(sum, shared, blockDim.x);
+  if (!(sum <= 3.0e38f)) {
+    shrink = kShrink, sum = 0.0f, eps = 0.0f;
+    for (int i = threadIdx.x; i < p.width; i += blockDim.x) {
+      const float h = at(i) * shrink;
+      sum = fmaf(h, h, sum);
+    }
+    sum = over_row<false>(sum, shared, blockDim.x);
+  }
+  const float inv = inverse_root(sum, p.width, eps);
+  auto normed = [&](float h, int i) { return h * shrink * inv * (p.weight ? p.weight[i] : 1.0f); };
+  if constexpr (kOut < 2) {
+    for (int i = threadIdx.x; i < p.width; i += blockDim.x) {
+      const float h = at(i);
+      if (kRes) store_one<kRes == 1>(p.residual_out, y0 + i, h);
+      store_one<kOut == 1>(p.y, y0 + i, normed(h, i));
+    }
+  } else {
+    // a group's elements by one warp, a row's by all
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int group = p.group ? p.group : p.width, groups = p.width / group;
+    const int first = p.group ? threadIdx.x >> 5 : 0, step = p.group ? warps : 1;
+    const int begin = p.group ? lane : threadIdx.x, stride = p.group ? 32 : blockDim.x;
+    for (int g = first; g < groups; g += step) {
+      uint32_t top = 0;
+      for (int i = begin; i < group; i += stride) top = max(top, finite_bits(normed(at(g * group + i), g * group + i)));
+      if (p.group) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      } else {
+        top = __float_as_uint(over_row<true>(__uint_as_float(top), shared, blockDim.x));
+      }
+      const float f = scale_of<kOut == 3>(top, p.scale, (size_t)row * groups + g, begin == 0);
+      for (int j = begin; j < group; j += stride) {
+        const int i = g * group + j;
+        const float h = at(i);
+        if (kRes) store_one<kRes == 1>(p.residual_out, y0 + i, h);
+        reinterpret_cast<uint8_t *>(p.y)[y0 + i] = (uint8_t)paged::to_e4m3x2(normed(h, i) * f, 0.0f);
+      }
+    }
+  }
+}
+
+template <bool kXBf16, int kRes, int kOut>
+void launch(const Params &p, bool vector, cudaStream_t s) {
+  const int chunks = p.width >> 3;
+  if (!vector || chunks > 4096) {
+    norm_any_kernel<kXBf16, kRes, kOut><<<(unsigned)p.rows, 512, 0, s>>>(p);
+    return;
+  }
+  auto grid = [&](int threads, int rows) { return dim3((unsigned)((p.rows + rows - 1) / rows)); };
+  auto up = [](int n) { int t = 32; while (t < n) t *= 2; return t; };
+  if (chunks <= 32) {
+    norm_rows_kernel<kXBf16, kRes, kOut, 1><<<grid(32, 4), dim3(32, 4), 0, s>>>(p);
+  } else if (chunks <= 512) {
+    const int t = up((chunks + 1) / 2);
+    norm_rows_kernel<kXBf16, kRes, kOut, 2><<<grid(t, 1), dim3(t, 1), 0, s>>>(p);
+  } else {
+    const int t = up((chunks + 3) / 4);
+    norm_rows_kernel<kXBf16, kRes, kOut, 4><<<grid(t, 1), dim3(t, 1), 0, s>>>(p);
+  }
+}
+
+template <bool kXBf16, int kRes>
+void by_out(const Params &p, int out, bool vector, cudaStream_t s) {
+  switch (out) {
+    case 0: launch<kXBf16, kRes, 0>(p, vector, s); break;
+    case 1: launch<kXBf16, kRes, 1>(p, vector, s); break;
+    case 2: launch<kXBf16, kRes, 2>(p, vector, s); break;
+    default: launch<kXBf16, kRes, 3>(p, vector, s); break;
+  }
+}
+
+size_t size_of(int dtype) { return dtype == GLINATTN_F32 ? 4 : dtype == GLINATTN_BF16 ? 2 : 1; }
+
+bool activation(int dtype) { return dtype == GLINATTN_F32 || dtype == GLINATTN_BF16; }
+
+glinattn_status run(const glinattn_norm_args *a, cudaStream_t stream) {
+  if (!a || !activation(a->in_dtype) || !(activation(a->out_dtype) || a->out_dtype == GLINATTN_E4M3) || a->rows < 0 ||
+      a->width <= 0 || a->x_stride < 0 || !(a->eps >= 1e-20f && a->eps <= 1e20f))
+    return GLINATTN_ERR_INVALID_ARG;
+  const bool e4m3 = a->out_dtype == GLINATTN_E4M3;
+  if (e4m3) {
+    if ((a->scale_dtype != GLINATTN_F32 && a->scale_dtype != GLINATTN_E8M0) || a->group < 0) return GLINATTN_ERR_INVALID_ARG;
+    if (a->group != 0 && a->group != 32 && a->group != 64 && a->group != 128) return GLINATTN_ERR_UNSUPPORTED;
+    if (a->group && a->width % a->group) return GLINATTN_ERR_INVALID_ARG;
+  } else if (a->group || a->scale) {
+    return GLINATTN_ERR_INVALID_ARG;
+  }
+  if ((a->residual == nullptr) != (a->residual_out == nullptr)) return GLINATTN_ERR_INVALID_ARG;
+  if (a->residual && !activation(a->residual_dtype)) return GLINATTN_ERR_INVALID_ARG;
+  if (a->rows == 0) return GLINATTN_OK;
+  const long long stride = a->x_stride ? a->x_stride : a->width;
+  const size_t xs = size_of(a->in_dtype);
+  if (stride < a->width && a->rows > 1) return GLINATTN_ERR_INVALID_ARG;
+  if (!a->x || !a->y || (e4m3 && !a->scale) || !aligned(a->x, xs)) return GLINATTN_ERR_INVALID_ARG;
+  const void *list[] = {a->residual, a->residual_out, a->weight, a->y, a->scale};
+  for (const void *q : list)
+    if (!aligned(q, 16)) return GLINATTN_ERR_INVALID_ARG;
+  // outputs may be their inputs exactly, and otherwise overlap nothing
+  const size_t nx = row_bytes(a->rows, a->width, stride, xs), elements = (size_t)a->rows * a->width;
+  const size_t nr = a->residual ? elements * size_of(a->residual_dtype) : 0, ny = elements * size_of(a->out_dtype);
+  const size_t ns = e4m3 ? (size_t)a->rows * (a->group ? a->width / a->group : 1) * (a->scale_dtype == GLINATTN_F32 ? 4 : 1) : 0;
+  const size_t nw = a->weight ? (size_t)a->width * 4 : 0;
+  const bool x_whole = stride == a->width || a->rows == 1;
+  struct Out { const void *p; size_t n; int dtype; bool may_x, may_res; };
+  const Out outs[] = {{a->residual_out, nr, a->residual_dtype, true, true}, {a->y, ny, a->out_dtype, true, false}, {a->scale, ns, -1, false, false}};
+  for (int i = 0; i < 3; ++i) {
+    const Out &o = outs[i];
+    if (overlap(o.p, o.n, a->x, nx) && !(o.may_x && o.p == a->x && x_whole && o.dtype == a->in_dtype)) return GLINATTN_ERR_INVALID_ARG;
+    if (overlap(o.p, o.n, a->residual, nr) && !(o.may_res && o.p == a->residual)) return GLINATTN_ERR_INVALID_ARG;
+    if (overlap(o.p, o.n, a->weight, nw)) return GLINATTN_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(o.p, o.n, outs[j].p, outs[j].n)) return GLINATTN_ERR_INVALID_ARG;
+  }
+  const Params p = {a->x, a->residual, a->weight, a->residual_out, a->y, a->scale, a->rows, stride, a->width, a->group, a->eps};
+  const bool vector = a->width % 8 == 0 && aligned(a->x, 16) && (a->rows == 1 || (stride * (long long)xs) % 16 == 0);
+  const int out = e4m3 ? (a->scale_dtype == GLINATTN_F32 ? 2 : 3) : a->out_dtype == GLINATTN_F32 ? 0 : 1;
+  const int res = !a->residual ? 0 : a->residual_dtype == GLINATTN_BF16 ? 1 : 2;
+  if (a->in_dtype == GLINATTN_BF16) {
+    if (res == 0) by_out<true, 0>(p, out, vector, stream);
+    else if (res == 1) by_out<true, 1>(p, out, vector, stream);
+    else by_out<true, 2>(p, out, vector, stream);
+  } else {
+    if (res == 0) by_out<false, 0>(p, out, vector, stream);
+    else if (res == 1) by_out<false, 1>(p, out, vector, stream);
+    else by_out<false, 2>(p, out, vector, stream);
+  }
+  return cudaGetLastError() == cudaSuccess ? GLINATTN_OK : GLINATTN_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace norm
+}  // namespace glinattn
+
+extern "C" glinattn_status glinattn_add_rms_norm(const glinattn_norm_args *args, glinattn_stream_t stream) {
+  return glinattn::norm::run(args, (cudaStream_t)stream);
+}

@@ -19,6 +19,13 @@ The entry points keep the C names:
   drafts, a piece of a prompt, packed prompts) over the paged cache
 * ``glinattn_accept_drafts`` -- accepted drafts and the next token from the
   target's probabilities and given random numbers
+* ``glinattn_kv_append_rope`` -- the cache write with the position rotation of
+  queries and keys on the way
+* ``glinattn_short_conv`` / ``glinattn_selective_scan_packed`` -- the state-space
+  block's short convolution, and its scan with step bias, skip and gate, over
+  packed rows with states by slot (single tokens, drafts, packed prompts)
+* ``glinattn_add_rms_norm`` -- residual addition and RMS norm, optionally with an
+  e4m3 output and its scales
 """
 from __future__ import annotations
 
@@ -31,7 +38,7 @@ import torch
 from . import build as _build
 
 GLA, GDN, NLA = 0, 1, 2
-F32, BF16, E4M3 = 0, 1, 2
+F32, BF16, E4M3, E8M0 = 0, 1, 2, 3
 
 DEV_BAD_SLOT = 0x1
 DEV_BAD_GATE = 0x2
@@ -52,6 +59,7 @@ class GlinattnError(RuntimeError):
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 
 
 class PrefillArgs(ctypes.Structure):
@@ -132,6 +140,37 @@ class AcceptArgs(ctypes.Structure):
                 ("dev_status", _vp)]
 
 
+class KvRopeArgs(ctypes.Structure):
+    _fields_ = [("cache_dtype", _i32), ("num_req", _i32), ("num_tok", _i32), ("heads", _i32), ("kv_heads", _i32),
+                ("head_dim", _i32), ("page_size", _i32), ("num_pages", _i32), ("max_pages", _i32), ("rotary_dim", _i32),
+                ("interleaved", _i32), ("rope_scale", ctypes.c_float), ("q_stride", _i64), ("k_stride", _i64),
+                ("v_stride", _i64), ("q_out_stride", _i64), ("q", _vp), ("k", _vp), ("v", _vp), ("inv_freq", _vp),
+                ("q_out", _vp), ("k_cache", _vp), ("v_cache", _vp), ("k_scale", _vp), ("v_scale", _vp),
+                ("page_table", _vp), ("kv_len", _vp), ("q_start", _vp), ("dev_status", _vp)]
+
+
+class ShortConvArgs(ctypes.Structure):
+    _fields_ = [("in_dtype", _i32), ("num_req", _i32), ("num_tok", _i32), ("channels", _i32), ("width", _i32),
+                ("activation", _i32), ("pool_slots", _i32), ("update_state", _i32), ("x_stride", _i64), ("x", _vp),
+                ("w", _vp), ("bias", _vp), ("conv_pool", _vp), ("slot_ids", _vp), ("q_start", _vp), ("resume", _vp),
+                ("count", _vp), ("y", _vp), ("dev_status", _vp)]
+
+
+class ScanPackedArgs(ctypes.Structure):
+    _fields_ = [("in_dtype", _i32), ("out_dtype", _i32), ("num_req", _i32), ("num_tok", _i32), ("channels", _i32),
+                ("state", _i32), ("pool_slots", _i32), ("update_state", _i32), ("max_q_len", _i32), ("x_stride", _i64),
+                ("delta_stride", _i64), ("z_stride", _i64), ("b_stride", _i64), ("c_stride", _i64), ("x", _vp),
+                ("delta", _vp), ("z", _vp), ("Bm", _vp), ("Cm", _vp), ("A", _vp), ("skip", _vp), ("delta_bias", _vp),
+                ("state_pool", _vp), ("slot_ids", _vp), ("q_start", _vp), ("resume", _vp), ("count", _vp), ("y", _vp),
+                ("dev_status", _vp)]
+
+
+class NormArgs(ctypes.Structure):
+    _fields_ = [("in_dtype", _i32), ("residual_dtype", _i32), ("out_dtype", _i32), ("scale_dtype", _i32), ("rows", _i32),
+                ("width", _i32), ("group", _i32), ("eps", ctypes.c_float), ("x_stride", _i64), ("x", _vp),
+                ("residual", _vp), ("weight", _vp), ("residual_out", _vp), ("y", _vp), ("scale", _vp)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -151,7 +190,10 @@ def library() -> ctypes.CDLL:
                                ("glinattn_selective_scan_decode", ScanDecodeArgs),
                                ("glinattn_kv_append", KvArgs), ("glinattn_kv_gather", KvArgs),
                                ("glinattn_paged_attention", PagedAttnArgs),
-                               ("glinattn_accept_drafts", AcceptArgs)):
+                               ("glinattn_accept_drafts", AcceptArgs), ("glinattn_kv_append_rope", KvRopeArgs),
+                               ("glinattn_short_conv", ShortConvArgs),
+                               ("glinattn_selective_scan_packed", ScanPackedArgs),
+                               ("glinattn_add_rms_norm", NormArgs)):
                 f = getattr(lib, name)
                 f.argtypes = [ctypes.POINTER(argt), _vp]
                 f.restype = ctypes.c_int
@@ -675,6 +717,222 @@ def glinattn_accept_drafts(target_probs, draft_probs, draft_tokens, uniforms, *,
                    _addr(uniforms), _addr(accept), _addr(tokens), _addr(dev_status))
     _launch("glinattn_accept_drafts", a, stream, dev)
     return accept, tokens
+
+
+def _rows(t, name, dtype, shape, dev):
+    """Checks of rows that may be slices of wider ones: inside a row contiguous.  Returns their distance in elements."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    stride, width = t.stride(), 1
+    for n, s in zip(shape[:0:-1], stride[:0:-1]):
+        if n != 1 and s != width:
+            raise ValueError(f"{name} must be contiguous within a row")
+        width *= n
+    if shape[0] <= 1:
+        return width
+    if stride[0] < width:
+        raise ValueError(f"rows of {name} must not overlap")
+    return stride[0]
+
+
+def _act(t, name):
+    if t.dtype is torch.bfloat16:
+        return BF16
+    if t.dtype is torch.float32:
+        return F32
+    raise TypeError(f"{name} must be bf16 or fp32, got {t.dtype}")
+
+
+def glinattn_kv_append_rope(q, k, v, inv_freq, k_cache, v_cache, page_table, kv_len, q_start, *, interleaved=False,
+                            rope_scale=1.0, q_out=None, k_scale=None, v_scale=None, dev_status=None, stream=None):
+    """glinattn_kv_append with the position rotation on the way: k is rotated into
+    the cache, q into q_out.  q [num_tok,H,d] (or None: keys and values alone), k, v
+    [num_tok,Hkv,d] bf16, each may be a slice of wider rows; inv_freq
+    [rotary_dim / 2] fp32: pair i of a token at position p turns by p *
+    inv_freq[i]; pairs are the channels (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with interleaved.
+    rope_scale multiplies the rotated channels.  The cache's arguments are
+    glinattn_kv_append's.  q_out is allocated when not given and may be q.  Returns
+    (q_out, k_cache, v_cache)."""
+    dev = k.device
+    code, P, Hkv, page, d, R, max_pages = _cache_dims(k_cache, v_cache, page_table, kv_len, q_start, k_scale, v_scale, dev)
+    n, H = k.shape[0], 0
+    ks, vs = _rows(k, "k", torch.bfloat16, (n, Hkv, d), dev), _rows(v, "v", torch.bfloat16, (n, Hkv, d), dev)
+    qs = qos = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [num_tok, H, d]")
+        H = q.shape[1]
+        qs = _rows(q, "q", torch.bfloat16, (n, H, d), dev)
+        if q_out is None:
+            q_out = _empty((n, H, d), torch.bfloat16, dev, stream)
+        qos = _rows(q_out, "q_out", torch.bfloat16, (n, H, d), dev)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rotary_dim / 2]")
+    _check(inv_freq, "inv_freq", torch.float32, inv_freq.shape, dev)
+    _status_word(dev_status, dev)
+    a = KvRopeArgs(code, R, n, H, Hkv, d, page, P, max_pages, 2 * inv_freq.shape[0], int(bool(interleaved)), rope_scale, qs, ks,
+                   vs, qos, _addr(q), _addr(k), _addr(v), _addr(inv_freq), _addr(q_out), _addr(k_cache), _addr(v_cache),
+                   _addr(k_scale), _addr(v_scale), _addr(page_table), _addr(kv_len), _addr(q_start), _addr(dev_status))
+    _launch("glinattn_kv_append_rope", a, stream, dev)
+    return q_out, k_cache, v_cache
+
+
+def _packed(n, pool, slot_ids, q_start, resume, count, outputs, y, dev_status, dev):
+    """The checks that the calls on packed rows and slots share; the number of requests."""
+    if (pool is None) != (slot_ids is None):
+        raise ValueError("a pool and slot_ids go together")
+    if q_start is not None:
+        if q_start.dim() != 1 or q_start.shape[0] < 1:
+            raise ValueError("q_start must be [R + 1]")
+        R = q_start.shape[0] - 1
+        _check(q_start, "q_start", torch.int32, (R + 1,), dev)
+    else:
+        R = n
+    for t, name in ((slot_ids, "slot_ids"), (resume, "resume"), (count, "count")):
+        if t is not None:
+            _check(t, name, torch.int32, (R,), dev)
+    if not outputs and y is not None:
+        raise ValueError("y is given, but no outputs are wanted")
+    _status_word(dev_status, dev)
+    return R
+
+
+def glinattn_short_conv(x, w, bias=None, conv_pool=None, slot_ids=None, q_start=None, *, resume=None, count=None, silu=True,
+                        update_state=True, outputs=True, y=None, dev_status=None, stream=None):
+    """Causal depthwise convolution of packed rows.  x [num_tok,C] (bf16 or fp32, may
+    be a slice of wider rows), w [C,width] fp32 (width 2, 3 or 4), bias [C] fp32 or None;
+    conv_pool [P,width-1,C] (x's dtype), the last inputs by slot, with slot_ids [R]
+    int32 (both None: zero history, no state kept); q_start [R+1] int32, or None for
+    one token per request; resume [R] int32 (0: from a zero history); count [R] int32:
+    rows of each request that are run (accepted drafts).  update_state=False only
+    verifies, outputs=False only advances the states.  Returns y [num_tok,C], or None."""
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [num_tok, C] and w [C, width]")
+    n, C = x.shape
+    width, dev, act = w.shape[1], x.device, x.dtype
+    code = _act(x, "x")
+    xs = _rows(x, "x", act, (n, C), dev)
+    _check(w, "w", torch.float32, (C, width), dev)
+    if bias is not None:
+        _check(bias, "bias", torch.float32, (C,), dev)
+    P = 0
+    if conv_pool is not None:
+        P = conv_pool.shape[0]
+        _check(conv_pool, "conv_pool", act, (P, width - 1, C), dev)
+    R = _packed(n, conv_pool, slot_ids, q_start, resume, count, outputs, y, dev_status, dev)
+    if outputs:
+        if y is None:
+            y = _empty((n, C), act, dev, stream)
+        _check(y, "y", act, (n, C), dev)
+    a = ShortConvArgs(code, R, n, C, width, int(bool(silu)), P, int(bool(update_state)), xs, _addr(x), _addr(w), _addr(bias),
+                      _addr(conv_pool), _addr(slot_ids), _addr(q_start), _addr(resume), _addr(count), _addr(y),
+                      _addr(dev_status))
+    _launch("glinattn_short_conv", a, stream, dev)
+    return y
+
+
+def glinattn_selective_scan_packed(x, delta, Bm, Cm, A, state_pool=None, slot_ids=None, q_start=None, *, max_q_len=None, z=None,
+                                   skip=None, delta_bias=None, resume=None, count=None, update_state=True, outputs=True,
+                                   out_dtype=None, y=None, dev_status=None, stream=None):
+    """The selective scan of packed rows with its step bias, skip and gate.  x,
+    delta, z [num_tok,D], Bm, Cm [num_tok,N] (bf16 or fp32, each may be a slice of
+    wider rows; z None: no gate); A [D,N], skip, delta_bias [D] fp32 (None: zeros);
+    state_pool [P,D,N] fp32 with slot_ids [R] int32 (both None: from zeros, no state
+    kept).  q_start, resume, count, update_state and outputs are
+    glinattn_short_conv's; max_q_len: an upper bound of the requests' numbers of rows
+    (num_tok when not given; a tight one selects the faster kernel for few rows per
+    request).  Returns y [num_tok,D], or None."""
+    if x.dim() != 2 or A.dim() != 2:
+        raise ValueError("x must be [num_tok, D] and A [D, N]")
+    n, D = x.shape
+    N, dev, act = A.shape[1], x.device, x.dtype
+    code = _act(x, "x")
+    xs, ds = _rows(x, "x", act, (n, D), dev), _rows(delta, "delta", act, (n, D), dev)
+    bs, cs = _rows(Bm, "Bm", act, (n, N), dev), _rows(Cm, "Cm", act, (n, N), dev)
+    zs = 0 if z is None else _rows(z, "z", act, (n, D), dev)
+    _check(A, "A", torch.float32, (D, N), dev)
+    for t, name in ((skip, "skip"), (delta_bias, "delta_bias")):
+        if t is not None:
+            _check(t, name, torch.float32, (D,), dev)
+    P = 0
+    if state_pool is not None:
+        P = state_pool.shape[0]
+        _check(state_pool, "state_pool", torch.float32, (P, D, N), dev)
+    R = _packed(n, state_pool, slot_ids, q_start, resume, count, outputs, y, dev_status, dev)
+    if max_q_len is None:
+        max_q_len = 1 if q_start is None else n
+    elif not 0 <= max_q_len < 1 << 31:          # ctypes would keep the low bits
+        raise ValueError(f"max_q_len must be in [0, 2^31), got {max_q_len}")
+    if outputs:
+        if y is None:
+            y = _empty((n, D), act if out_dtype is None else out_dtype, dev, stream)
+        out = _act(y, "y")
+        _check(y, "y", y.dtype if out_dtype is None else out_dtype, (n, D), dev)
+    else:
+        out = code
+    a = ScanPackedArgs(code, out, R, n, D, N, P, int(bool(update_state)), max_q_len, xs, ds, zs, bs, cs, _addr(x), _addr(delta),
+                       _addr(z), _addr(Bm), _addr(Cm), _addr(A), _addr(skip), _addr(delta_bias), _addr(state_pool),
+                       _addr(slot_ids), _addr(q_start), _addr(resume), _addr(count), _addr(y), _addr(dev_status))
+    _launch("glinattn_selective_scan_packed", a, stream, dev)
+    return y
+
+
+def glinattn_add_rms_norm(x, weight=None, residual=None, *, eps=1e-6, group=0, out_dtype=None, scale_dtype=None, y=None,
+                          residual_out=None, scale=None, stream=None):
+    """Residual addition and root-mean-square norm: h = x + residual, y = h /
+    sqrt(mean(h^2) + eps) * weight.  x [rows,width] (bf16 or fp32, may be a slice of
+    wider rows), weight [width] fp32 or None; residual [rows,width] (bf16 or fp32, its
+    own dtype) or None; residual_out receives h (allocated when not given; may be
+    residual).  out_dtype (x's when not given): bf16, fp32, or float8_e4m3fn with a
+    scale for every `group` elements (0: the row) in scale [rows, groups], float32
+    (max |y| / 448) or float8_e8m0fnu (powers of two; scale_dtype).  Returns
+    (y, residual_out, scale), None for what there is not."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, width]")
+    n, width = x.shape
+    dev = x.device
+    code = _act(x, "x")
+    xs = _rows(x, "x", x.dtype, (n, width), dev)
+    if weight is not None:
+        _check(weight, "weight", torch.float32, (width,), dev)
+    res = F32
+    if residual is not None:
+        res = _act(residual, "residual")
+        _check(residual, "residual", residual.dtype, (n, width), dev)
+        if residual_out is None:
+            residual_out = _empty((n, width), residual.dtype, dev, stream)
+        _check(residual_out, "residual_out", residual.dtype, (n, width), dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs residual")
+    if y is None:
+        y = _empty((n, width), x.dtype if out_dtype is None else out_dtype, dev, stream)
+    _check(y, "y", y.dtype if out_dtype is None else out_dtype, (n, width), dev)
+    sd = F32
+    if y.dtype is torch.float8_e4m3fn:
+        out = E4M3
+        if group not in (0, 32, 64, 128) or (group and width % group):
+            raise ValueError(f"group must be 0, 32, 64 or 128 and divide the width, got {group} for {width}")
+        if scale is None:
+            scale = _empty((n, width // group if group else 1), torch.float32 if scale_dtype is None else scale_dtype, dev, stream)
+        _check(scale, "scale", scale.dtype if scale_dtype is None else scale_dtype, (n, width // group if group else 1), dev)
+        if scale.dtype is torch.float8_e8m0fnu:
+            sd = E8M0
+        elif scale.dtype is not torch.float32:
+            raise TypeError(f"scale must be float32 or float8_e8m0fnu, got {scale.dtype}")
+    else:
+        out = _act(y, "y")
+        if group or scale is not None or scale_dtype is not None:
+            raise ValueError("group and scale belong to a float8_e4m3fn output")
+    a = NormArgs(code, res, out, sd, n, width, group, eps, xs, _addr(x), _addr(residual), _addr(weight), _addr(residual_out),
+                 _addr(y), _addr(scale))
+    _launch("glinattn_add_rms_norm", a, stream, dev)
+    return y, residual_out, scale
 
 
 def version() -> int:

@@ -82,8 +82,9 @@ typedef enum {
  * L2 norm; the normaliser z [.., H, dk] fp32 travels beside the state.
  */
 typedef enum { GLINATTN_GLA = 0, GLINATTN_GDN = 1, GLINATTN_NLA = 2 } glinattn_variant;
-/* GLINATTN_E4M3 is a dtype of the paged key / value cache only. */
-typedef enum { GLINATTN_F32 = 0, GLINATTN_BF16 = 1, GLINATTN_E4M3 = 2 } glinattn_dtype;
+/* GLINATTN_E4M3 is a dtype of the paged key / value cache and of the residual norm's
+   output, GLINATTN_E8M0 (powers of two, exponent plus 127) of that output's scales. */
+typedef enum { GLINATTN_F32 = 0, GLINATTN_BF16 = 1, GLINATTN_E4M3 = 2, GLINATTN_E8M0 = 3 } glinattn_dtype;
 
 /* Bits OR-ed into *dev_status by the kernels. */
 #define GLINATTN_DEV_BAD_SLOT 0x1u    /* slot (or page) id outside its pool: unit skipped */
@@ -551,6 +552,156 @@ typedef struct {
 } glinattn_accept_args;
 
 glinattn_status glinattn_accept_drafts(const glinattn_accept_args *args, glinattn_stream_t stream);
+
+/*
+ * glinattn_kv_append_rope -- glinattn_kv_append with the position rotation applied
+ *   on the way: the new tokens' queries are rotated into q_out, their keys are
+ *   rotated and written to the cache, their values are written as they are.
+ *
+ *   q [num_tok, H, d] bf16 and q_out (the same; may be q itself), or H = 0 and NULL;
+ *   k, v [num_tok, Hkv, d] bf16; rows may be further apart than H d or Hkv d
+ *   elements (slices of a projection's output): *_stride, in elements, a multiple of 8,
+ *   0 for contiguous rows.  Base addresses are 16-byte aligned.
+ *   inv_freq [rotary_dim / 2] fp32, |inv_freq| < 2^24 (otherwise NaN): pair i of a token at
+ *   position p is turned by the angle p * inv_freq[i]; the product is exact and reduced
+ *   to a turn before it is rounded, at any position:
+ *     (a, b) -> rope_scale * (a cos - b sin, b cos + a sin)
+ *   rotary_dim: a multiple of 16, at most d; channels behind it pass unchanged (not
+ *   scaled).  Pair i is channels (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with
+ *   interleaved != 0.  The rotation is fp32; a key is rounded once, to bf16 or to the
+ *   row's e4m3 (scales chosen as in glinattn_kv_append, from the rotated fp32 values).
+ *   Positions, ranges, the cache and its errors are glinattn_kv_append's.  Rows in no
+ *   valid request and tokens at negative positions are not written, in q_out neither;
+ *   a bad page keeps a token's key and value out of the cache, not its query.
+ */
+typedef struct {
+  int32_t cache_dtype;
+  int32_t num_req, num_tok, heads, kv_heads, head_dim, page_size, num_pages, max_pages;
+  int32_t rotary_dim, interleaved;
+  float rope_scale;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  const void *q, *k, *v;
+  const float *inv_freq;
+  void *q_out;
+  void *k_cache, *v_cache;
+  uint8_t *k_scale, *v_scale;
+  const int32_t *page_table, *kv_len, *q_start;
+  uint32_t *dev_status;
+} glinattn_kv_rope_args;
+
+glinattn_status glinattn_kv_append_rope(const glinattn_kv_rope_args *args, glinattn_stream_t stream);
+
+/*
+ * The state-space block's own short convolution and its selective scan, over packed
+ * rows and slot-indexed pools ("Long context, fast inference, smart decoding, and life
+ * beyond attention", chapter "05 · State-space models: the architectural alternative":
+ * the layer's convolution, input-dependent steps and gate).  The two calls below share
+ * these conventions.
+ *
+ *   q_start [R + 1] int32, not decreasing: rows q_start[r] .. q_start[r + 1] - 1 of the
+ *     packed arrays (num_tok rows) are request r's next tokens.  NULL: one token each,
+ *     request r is row r (num_tok = R).  Rows of no request are not written; they may
+ *     be read but reach no result.
+ *   slot_ids [R] int32: request r's state is slot slot_ids[r] of the pool; distinct
+ *     (not checked: duplicates race).  pool and slot_ids both NULL: every request
+ *     starts from zeros and no state is kept.
+ *   resume [R] int32 or NULL (all resume): 0 starts request r from a zero state,
+ *     whatever its slot holds; anything else continues from the slot.
+ *   count [R] int32 or NULL (all): only the first count[r] rows of request r are run,
+ *     the accepted drafts; output rows behind them are left as they were.
+ *   update_state != 0 writes each request's state back to its slot, 0 leaves the pool as it is
+ *     (drafts that are verified).  A request that runs no row leaves its slot as it is.
+ *   y NULL: no outputs, only the states are advanced (accepted drafts, replayed).
+ *   A request whose range or count is out of bounds (a range outside [0, num_tok] or
+ *   decreasing, a count outside [0, its rows]) sets GLINATTN_DEV_BAD_COUNT, a slot outside
+ *   [0, pool_slots) sets GLINATTN_DEV_BAD_SLOT; either skips the request, which leaves its
+ *   outputs and its slot as they were.  With a decreasing q_start rows of other
+ *   requests may be left out too.  R <= 65535.
+ *   Activations are all bf16 or all fp32.  x, delta, z, Bm and Cm may be slices of wider
+ *   rows: *_stride, in elements, is the distance of their rows (0: contiguous), and their
+ *   base needs the alignment of an element only (16 bytes, and a stride that is a
+ *   multiple of 16 bytes, is faster).  y is contiguous, pools and fp32 parameters too, with 16-byte
+ *   aligned bases.  No output may overlap an input other than its own pool.
+ *
+ * glinattn_short_conv -- causal depthwise convolution of `width` taps (2, 3 or 4):
+ *     y_t[c] = act(bias[c] + sum_j w[c][j] x_{t - (width - 1) + j}[c])
+ *   x, y [num_tok, C] (in_dtype)   w [C, width] fp32   bias [C] fp32 or NULL
+ *   conv_pool [P, width - 1, C] (in_dtype): the last width - 1 RAW inputs, oldest first
+ *   activation: 0 none, 1 SiLU (y / (1 + e^-y)).  Sums are fp32, rounded once.
+ */
+typedef struct {
+  int32_t in_dtype, num_req, num_tok, channels, width, activation, pool_slots, update_state;
+  int64_t x_stride;
+  const void *x;
+  const float *w, *bias;
+  void *conv_pool;
+  const int32_t *slot_ids, *q_start, *resume, *count;
+  void *y;
+  uint32_t *dev_status;
+} glinattn_short_conv_args;
+
+glinattn_status glinattn_short_conv(const glinattn_short_conv_args *args, glinattn_stream_t stream);
+
+/*
+ * glinattn_selective_scan_packed -- the selective scan of glinattn_selective_scan with
+ *   what surrounds it in the block, for single tokens, drafts, pieces of prompts
+ *   and packed prompts in one call:
+ *     dt = softplus(delta_t[d] + delta_bias[d])
+ *     h_t[d, n] = exp(dt A[d, n]) h_{t-1}[d, n] + dt Bm_t[n] x_t[d]
+ *     y_t[d] = (sum_n h_t[d, n] Cm_t[n] + skip[d] x_t[d]) * z_t[d] / (1 + e^-z_t[d])
+ *   x, delta, z [num_tok, D]   Bm, Cm [num_tok, N] (in_dtype; z may be NULL: no gate)
+ *   A [D, N], skip [D], delta_bias [D] fp32 (skip and delta_bias may be NULL: zeros)
+ *   state_pool [P, D, N] fp32   y [num_tok, D] (out_dtype)
+ *   N in {8, 16, 32}; any D >= 1.  A <= 0 with |A| < 2.3e38.  All arithmetic is fp32.
+ *   max_q_len: an upper bound of the ranges' lengths (it selects the kernel); a longer
+ *     range sets GLINATTN_DEV_BAD_COUNT and its request is skipped.
+ */
+typedef struct {
+  int32_t in_dtype, out_dtype, num_req, num_tok, channels, state, pool_slots, update_state, max_q_len;
+  int64_t x_stride, delta_stride, z_stride, b_stride, c_stride;
+  const void *x, *delta, *z, *Bm, *Cm;
+  const float *A, *skip, *delta_bias;
+  float *state_pool;
+  const int32_t *slot_ids, *q_start, *resume, *count;
+  void *y;
+  uint32_t *dev_status;
+} glinattn_scan_packed_args;
+
+glinattn_status glinattn_selective_scan_packed(const glinattn_scan_packed_args *args, glinattn_stream_t stream);
+
+/*
+ * glinattn_add_rms_norm -- the residual's addition and the root-mean-square norm in
+ *   front of a layer, optionally with its output in 8 bits:
+ *     h = x + residual (fp32),   residual_out = h,   y = h / sqrt(mean(h^2) + eps) * weight
+ *   x [rows, width] (in_dtype, rows x_stride elements apart, 0: contiguous; its base needs
+ *     the alignment of an element only)
+ *   residual, residual_out [rows, width] (residual_dtype), both or neither
+ *   weight [width] fp32 or NULL (ones)
+ *   y [rows, width] (out_dtype: GLINATTN_BF16, GLINATTN_F32 or GLINATTN_E4M3)
+ *   The norm is that of the fp32 sum, not of the rounded residual_out.  eps in [1e-20, 1e20].
+ *   GLINATTN_E4M3: every `group` elements of a row (0: the whole row; 32, 64 or 128, which
+ *   divides width) have a scale in scale [rows, width / group] (or [rows]), and y holds y / scale
+ *   rounded to the nearest e4m3 (from fp32 values with a relative error of 2^-21 at most):
+ *     scale_dtype GLINATTN_F32: max |y| / 448, at least 2^-100;
+ *     GLINATTN_E8M0: 2^e stored as e + 127, e the smallest integer in [-100, 119] with
+ *     max |y| <= 448 * 2^e (119 when there is none).
+ *   The maximum is that of the finite values; infinities become +-448, NaN stays NaN.
+ *   A row with an infinity gives NaN there and zeros elsewhere; sums of squares that
+ *   overflow fp32 are formed again of scaled values, so finite rows give finite results.
+ *   residual_out may be residual or x, y may be x (same dtype, contiguous); other overlaps
+ *   of outputs with inputs or with each other are refused.
+ */
+typedef struct {
+  int32_t in_dtype, residual_dtype, out_dtype, scale_dtype;
+  int32_t rows, width, group;
+  float eps;
+  int64_t x_stride;
+  const void *x, *residual;
+  const float *weight;
+  void *residual_out, *y, *scale;
+} glinattn_norm_args;
+
+glinattn_status glinattn_add_rms_norm(const glinattn_norm_args *args, glinattn_stream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *glinattn_status_string(glinattn_status status);
