@@ -25,6 +25,7 @@
 // instructions of a half each for its argument, dt x B, h and y, beside loads of B and C and the
 // helpers' share), few_kernel by HBM bytes, the states in and out.
 #include "packed.cuh"
+#include "sm100.cuh"
 
 namespace glinattn {
 namespace scan {
@@ -40,6 +41,10 @@ struct Params {
   float *pool;
   void *y;
   int D, update, out_bf16, bc_vector;
+  // requests in pieces of `piece` rows: per piece that is not its request's last, the state behind
+  // it and the sum of its steps; per request of more than one piece, the state before it
+  int piece;
+  float *ends, *sums, *starts;
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -77,8 +82,17 @@ __device__ __forceinline__ float silu(float z) { return z * rcp_fast(1.0f + exp2
 constexpr int kCh = 32, kL = 32;            // channels of a CTA, rows of a tile
 constexpr int kHelpers = kL * (kCh / 8);    // helper threads: one for 8 channels of one row
 
-template <int N, int kK, int kC>
+template <bool kBf16, int N, int kK, int kC>
 struct Tile {
+  static constexpr int kUnits = 2 * kL * N / 8, kBc = (kUnits + kHelpers - 1) / kHelpers;  // units of 8 of B and C: all, of a thread
+  // One thread a channel: its CTAs are few, and their helper warps are two groups, one for the inputs
+  // and one for the outputs.  Else one group does both in turn.
+  static constexpr bool kTwo = kC == 1 && kBf16;  // in fp32 the buffers would not fit
+  static constexpr int kThreads = kCh / kC * (N / kK) + (kTwo ? 2 : 1) * kHelpers;
+  // Tiles' inputs: asked for kAhead tiles before they become steps, x and z kept until the outputs
+  // are formed (three tiles later; in the next iteration where others do that).
+  static constexpr int kAhead = 2, kStages = kAhead + 3 + kTwo;
+  uint4 raw[kStages][3 + kBc][kBf16 ? 1 : 2][kHelpers];  // x, delta, z, B and C: every input thread's own
   static constexpr int kG = N / kK;              // threads of a channel
   static constexpr int kScan = kCh / kC * kG;    // scan threads
   static constexpr int kPlane = kL * kCh + 4;    // partial sums of one of a channel's threads (4: other banks)
@@ -114,6 +128,11 @@ __device__ __forceinline__ Raw8<kBf16> load_unit(const void *p, size_t at, int l
   return r;
 }
 
+// 16 bytes to shared memory; zeros, and nothing read, where `there` is false.
+__device__ __forceinline__ void copy_async16(void *to, const void *from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_u32(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+
 // kK floats of B or C.
 template <int kK>
 __device__ __forceinline__ void load_states(const float *p, float *f) {
@@ -129,15 +148,89 @@ __device__ __forceinline__ void load_states(const float *p, float *f) {
   }
 }
 
-template <bool kBf16, int N, int kK, int kC, bool kVec>
-__global__ void __launch_bounds__(kCh / kC *(N / kK) + kHelpers, kC == 1 ? 2 : 3) scan_kernel(const Params p) {
-  using T = Tile<N, kK, kC>;
+// What a CTA runs: rows [first, first + rows) of request r, its piece k of `pieces`; `index` is
+// the place of the request's first piece among all requests' pieces that are not their last.
+struct Piece {
+  int r, k, pieces, index, first, rows;
+};
+
+// Block y is request y's first piece for y < R, then come the others' in order.  A warp looks
+// 32 requests at a time for the one that the block is in.
+__device__ __forceinline__ int more_pieces(const Params &p, int r) {
+  if (r >= p.rows.R) return 0;
+  const Request q = request(p.rows, r);
+  return q.ok && q.run > 0 ? (q.run - 1) / p.piece : 0;
+}
+__device__ __forceinline__ Piece find_piece(const Params &p, int y, int lane) {
+  Piece f = {-1, 0, 1, 0, 0, 0};
+  int before = 0;  // pieces that are not the last of the requests before these 32
+  for (int r0 = 0; r0 < p.rows.R; r0 += 32) {
+    const int n = more_pieces(p, r0 + lane);
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const int first = before + upto - n;
+    const int e = y - p.rows.R;  // the block's place among the pieces that are not first
+    const bool here = e < 0 ? y == r0 + lane : n > 0 && e >= first && e < first + n;
+    const unsigned who = __ballot_sync(0xffffffffu, here);
+    if (who) {
+      const int l = __ffs(who) - 1;
+      f.r = r0 + l;
+      f.index = __shfl_sync(0xffffffffu, first, l);
+      f.pieces = __shfl_sync(0xffffffffu, n, l) + 1;
+      f.k = e < 0 ? 0 : e - f.index + 1;
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return f;
+}
+
+// Up to 32 requests: the one with the y-th most rows, so that no long one begins when others end.
+__device__ __forceinline__ int by_length(const Rows &rows, int y, int lane) {
+  int n = -1;
+  if (lane < rows.R) {
+    const Request q = request(rows, lane);
+    n = q.ok ? q.run : 0;
+  }
+  int rank = 0;
+  for (int k = 0; k < rows.R; ++k) {
+    const int other = __shfl_sync(0xffffffffu, n, k);
+    rank += other > n || (other == n && k < lane);
+  }
+  return __ffs(__ballot_sync(0xffffffffu, lane < rows.R && rank == y)) - 1;
+}
+
+// kPass 0: whole requests.  1: pieces that are not their request's last, for their ends alone (the
+// first one's from the request's state, the others' from zeros).  2: all pieces, from the
+// state that the ends before them add up to.
+template <bool kBf16, int N, int kK, int kC, bool kVec, int kPass>
+__global__ void __launch_bounds__(Tile<kBf16, N, kK, kC>::kThreads, kC == 1 ? 1 : 2) scan_kernel(const Params p) {
+  using T = Tile<kBf16, N, kK, kC>;
+  constexpr bool kOut = kPass != 1;
   extern __shared__ __align__(16) uint8_t smem[];
   T &s = *reinterpret_cast<T *>(smem);
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_requests(p.rows, threadIdx.x, blockDim.x);
-  const Request q = request(p.rows, blockIdx.y);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && kPass != 1) check_requests(p.rows, threadIdx.x, blockDim.x);
+  Piece f = {(int)blockIdx.y, 0, 1, 0, 0, 0};
+  if (kPass) f = find_piece(p, blockIdx.y, threadIdx.x & 31);
+  else if (p.rows.R > 1 && p.rows.R <= 32) f.r = by_length(p.rows, blockIdx.y, threadIdx.x & 31);
+  if (f.r < 0 || (kPass == 1 && f.k == f.pieces - 1)) return;
+  Request q = request(p.rows, f.r);
   if (!q.ok || q.run == 0) return;
+  if (kPass) {  // the piece's rows in the request's place
+    q.s0 += f.k * p.piece;
+    q.run = min(p.piece, q.run - f.k * p.piece);
+  }
   const int d0 = blockIdx.x * kCh, tiles = (q.run + kL - 1) / kL;
+  if (threadIdx.x < kCh) {
+    const int d = d0 + threadIdx.x;
+    s.bias[threadIdx.x] = d < p.D && p.delta_bias ? p.delta_bias[d] : 0.0f;
+    s.skip[threadIdx.x] = d < p.D && p.skip ? p.skip[d] : 0.0f;
+  }
+  __syncthreads();
   if (threadIdx.x < T::kScan) {
     // --- scan warps: thread g of channels ch .. ch + kC - 1 has their states g kK .. g kK + kK - 1.
     // Lanes 2 i and 2 i + 1 have the same g, lanes i and i ^ 2 the same channels: loads of shared
@@ -154,8 +247,30 @@ __global__ void __launch_bounds__(kCh / kC *(N / kK) + kHelpers, kC == 1 ? 2 : 3
         const bool in = d + i < p.D;
         const float2 a = in ? reinterpret_cast<const float2 *>(p.A + (size_t)(d + i) * N + g * kK)[k] : make_float2(0.0f, 0.0f);
         A[i][k] = make_float2(a.x * kLog2e, a.y * kLog2e);
-        h[i][k] = in && q.resumed ? reinterpret_cast<const float2 *>(state + i * N)[k] : make_float2(0.0f, 0.0f);
+        h[i][k] = make_float2(0.0f, 0.0f);
+        if (f.k == 0 && in && q.resumed) {
+          const size_t at = ((size_t)f.index * p.D + d + i) * N + g * kK;
+          // the last piece may have written the pool by now: the first pass has kept what was there
+          h[i][k] = kPass == 2 && f.pieces > 1 ? reinterpret_cast<const float2 *>(p.starts + at)[k] : reinterpret_cast<const float2 *>(state + i * N)[k];
+          if (kPass == 1) reinterpret_cast<float2 *>(p.starts + at)[k] = h[i][k];
+        }
       }
+    if (kPass == 2) {
+      for (int e = 0; e < f.k; ++e)
+#pragma unroll
+        for (int i = 0; i < kC; ++i)
+          if (d + i < p.D) {
+            const size_t at = (size_t)(f.index + e) * p.D + d + i;
+            const float sum = p.sums[at];
+#pragma unroll
+            for (int k = 0; k < kK / 2; ++k) {
+              const float2 end = reinterpret_cast<const float2 *>(p.ends + at * N + g * kK)[k];
+              const float2 x = __fmul2_rn(A[i][k], make_float2(sum, sum));
+              h[i][k] = e ? __ffma2_rn(make_float2(exp2_fast(x.x), exp2_fast(x.y)), h[i][k], end) : end;
+            }
+          }
+    }
+    float sum[kC] = {};
     const int steps[2] = {step_at(0, ch >> 3, ch & 7), step_at(1, ch >> 3, ch & 7)};
     const int parts[2] = {part_at(0, ch >> 3, ch & 7), part_at(1, ch >> 3, ch & 7) - kCh};
     // A block of kRows rows: what is read for it, and its decays and terms.  While one block's recurrence
@@ -182,7 +297,7 @@ __global__ void __launch_bounds__(kCh / kC *(N / kK) + kHelpers, kC == 1 ? 2 : 3
 #pragma unroll
       for (int r = 0; r < kRows; ++r) load_states<kK>(&s.c[slot][t0 + r][g * kK], o.c[r]);
     };
-    auto form = [&](Block &w, const Lines &l, int r) {
+    auto form = [&](Block &w, const Lines &l, int r, bool counts) {
 #pragma unroll
       for (int i = 0; i < kC; ++i)
 #pragma unroll
@@ -191,18 +306,21 @@ __global__ void __launch_bounds__(kCh / kC *(N / kK) + kHelpers, kC == 1 ? 2 : 3
           w.a[r][i][k] = make_float2(exp2_fast(e.x), exp2_fast(e.y));
           w.b[r][i][k] = __fmul2_rn(make_float2(l.st[r][2 * i + 1], l.st[r][2 * i + 1]), make_float2(l.b[r][2 * k], l.b[r][2 * k + 1]));
         }
+      if (kPass == 1 && counts)
+#pragma unroll
+        for (int i = 0; i < kC; ++i) sum[i] += l.st[r][2 * i];
     };
     auto run = [&](const Block &w, const Outs &o, int r, float *y) {
 #pragma unroll
       for (int i = 0; i < kC; ++i) {
-        float2 sum;
+        float2 out;
 #pragma unroll
         for (int k = 0; k < kK / 2; ++k) {
           h[i][k] = __ffma2_rn(w.a[r][i][k], h[i][k], w.b[r][i][k]);
           const float2 c2 = make_float2(o.c[r][2 * k], o.c[r][2 * k + 1]);
-          sum = k ? __ffma2_rn(h[i][k], c2, sum) : __fmul2_rn(h[i][k], c2);
+          if (kOut) out = k ? __ffma2_rn(h[i][k], c2, out) : __fmul2_rn(h[i][k], c2);
         }
-        y[i] = sum.x + sum.y;
+        if (kOut) y[i] = out.x + out.y;
       }
     };
     __syncthreads();
@@ -211,9 +329,9 @@ __global__ void __launch_bounds__(kCh / kC *(N / kK) + kHelpers, kC == 1 ? 2 : 3
     Outs o[2];
     fetch(l[0], 0, 0);
     fetch(l[1], 0, kRows);
-    fetch_c(o[0], 0, 0);
+    if (kOut) fetch_c(o[0], 0, 0);
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) form(w[0], l[0], r);
+    for (int r = 0; r < kRows; ++r) form(w[0], l[0], r, true);
     int slot = 0;
     for (int i = 0; i < tiles; ++i) {
       const int next = slot == 2 ? 0 : slot + 1;
@@ -222,15 +340,15 @@ __global__ void __launch_bounds__(kCh / kC *(N / kK) + kHelpers, kC == 1 ? 2 : 3
       for (int m = 0; m < kBlocks; ++m) {
         // behind the last tile lies an old one or nothing: read and formed, not used
         fetch(l[m & 1], m + 2 < kBlocks ? slot : next, kRows * ((m + 2) % kBlocks));
-        fetch_c(o[(m + 1) & 1], m + 1 < kBlocks ? slot : next, kRows * ((m + 1) % kBlocks));
+        if (kOut) fetch_c(o[(m + 1) & 1], m + 1 < kBlocks ? slot : next, kRows * ((m + 1) % kBlocks));
         float y[kRows][kC];
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
           run(w[m & 1], o[m & 1], r, y[r]);
-          form(w[(m + 1) & 1], l[(m + 1) & 1], r);
+          form(w[(m + 1) & 1], l[(m + 1) & 1], r, m + 1 < kBlocks || i + 1 < tiles);
         }
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
+        for (int r = 0; r < kRows && kOut; ++r) {
           float *to = part + (kRows * m + r) * kCh + parts[(kRows * m + r) & 1];
           if constexpr (kC == 1) to[0] = y[r][0];
           else *reinterpret_cast<float2 *>(to) = make_float2(y[r][0], y[r][1]);
@@ -239,49 +357,80 @@ __global__ void __launch_bounds__(kCh / kC *(N / kK) + kHelpers, kC == 1 ? 2 : 3
       slot = next;
       __syncthreads();
     }
-    if (p.update)
+    if (kPass == 1) {
+#pragma unroll
+      for (int i = 0; i < kC; ++i)
+        if (d + i < p.D) {
+          const size_t at = (size_t)(f.index + f.k) * p.D + d + i;
+          if (g == 0) p.sums[at] = sum[i];
+#pragma unroll
+          for (int k = 0; k < kK / 2; ++k) reinterpret_cast<float2 *>(p.ends + at * N + g * kK)[k] = h[i][k];
+        }
+    } else if (p.update && f.k == f.pieces - 1) {
 #pragma unroll
       for (int i = 0; i < kC; ++i)
 #pragma unroll
         for (int k = 0; k < kK / 2; ++k)
           if (d + i < p.D) reinterpret_cast<float2 *>(state + i * N)[k] = h[i][k];
+    }
     return;
   }
   // --- helper warps: thread (t, u) has row t, channels 8 u .. 8 u + 7 of every tile
-  const int j = threadIdx.x - T::kScan, u = j & 3, t = j >> 2, d = d0 + 8 * u, left = min(8, p.D - d);
+  const int helper = threadIdx.x - T::kScan, j = helper % kHelpers, u = j & 3, t = j >> 2, d = d0 + 8 * u, left = min(8, p.D - d);
   const bool in = left > 0;
-  if (j < kCh) {
-    s.bias[j] = d0 + j < p.D && p.delta_bias ? p.delta_bias[d0 + j] : 0.0f;
-    s.skip[j] = d0 + j < p.D && p.skip ? p.skip[d0 + j] : 0.0f;
-  }
-  constexpr int kUnits = 2 * kL * N / 8, kBc = (kUnits + kHelpers - 1) / kHelpers;  // units of 8 elements of B and C: all, of a thread
-  Raw8<kBf16> x, delta, z, bc[kBc];  // of the next tile
-  const bool gate = p.z && p.y;
-  auto load = [&](int i) {
-    const int row = i * kL + t;
-    const size_t r = (size_t)q.s0 + row;
-    if (in && row < q.run) {
-      x = load_unit<kBf16>(p.x, r * p.x_stride + d, left, kVec);
-      delta = load_unit<kBf16>(p.delta, r * p.delta_stride + d, left, kVec);
-      if (gate) z = load_unit<kBf16>(p.z, r * p.z_stride + d, left, kVec);
-    } else {  // a step of softplus(-infinity) = 0, no term
-      const uint32_t inf = kBf16 ? 0xff80ff80u : 0xff800000u;
-      x = {};
+  constexpr int kUnits = T::kUnits, kBc = T::kBc, kWords = kBf16 ? 1 : 2, kStages = T::kStages, kAhead = T::kAhead;
+  const bool out = kOut && p.y, gate = p.z && out;
+  // The inputs come through shared memory, a thread's own and several tiles ahead: registers that
+  // wait for memory would hold up the other loads.  Zeros where there are none.
+  auto bring = [&](int stage, int what, const void *src, size_t at, int n, bool there, bool vector) {
+    uint4 *to = &s.raw[stage][what][0][j];
+    if (vector) {
 #pragma unroll
-      for (int k = 0; k < (kBf16 ? 1 : 2); ++k) delta.w[k] = make_uint4(inf, inf, inf, inf);
-    }
+      for (int k = 0; k < kWords; ++k)
+        copy_async16(to + k * kHelpers, reinterpret_cast<const uint8_t *>(src) + (there ? at * (kBf16 ? 2 : 4) + 16 * k : 0), there);
+    } else {
+      const Raw8<kBf16> v = load_unit<kBf16>(src, at, there ? n : 0, false);
 #pragma unroll
-    for (int m = 0; m < kBc; ++m) {
-      const int e = j + m * kHelpers, line = e / (N / 8), rr = i * kL + (line >> 1), n = (e % (N / 8)) * 8;
-      const bool c = line & 1;
-      bc[m] = {};
-      if ((kUnits % kHelpers && e >= kUnits) || rr >= q.run || (c && !p.y)) continue;
-      bc[m] = load_unit<kBf16>(c ? p.Cm : p.Bm, ((size_t)q.s0 + rr) * (c ? p.c_stride : p.b_stride) + n, 8, p.bc_vector);
+      for (int k = 0; k < kWords; ++k) to[k * kHelpers] = v.w[k];
     }
   };
-  auto produce = [&](int slot) {
+  auto load = [&](int i) {
+    const int row = i * kL + t, stage = i % kStages;
+    const size_t r = (size_t)q.s0 + row;
+    const bool there = in && row < q.run;
+    if (i < tiles) {
+      bring(stage, 0, p.x, r * p.x_stride + d, left, there, kVec);
+      bring(stage, 1, p.delta, r * p.delta_stride + d, left, there, kVec);
+      if (gate) bring(stage, 2, p.z, r * p.z_stride + d, left, there, kVec);
+#pragma unroll
+      for (int m = 0; m < kBc; ++m) {
+        const int e = j + m * kHelpers, line = e / (N / 8), rr = i * kL + (line >> 1), n = (e % (N / 8)) * 8;
+        const bool c = line & 1;
+        if ((kUnits % kHelpers && e >= kUnits) || (c && !out)) continue;
+        bring(stage, 3 + m, c ? p.Cm : p.Bm, ((size_t)q.s0 + rr) * (c ? p.c_stride : p.b_stride) + n, 8, rr < q.run, p.bc_vector);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto take = [&](int stage, int what) {
+    Raw8<kBf16> v;
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) v.w[k] = s.raw[stage][what][k][j];
+    return v;
+  };
+  auto produce = [&](int i, int slot) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    const int stage = i % kStages;
+    const bool there = in && i * kL + t < q.run;
     float *to = &s.step[slot][t][0];
     float xs[8], ds[8], bias[8];
+    Raw8<kBf16> x = take(stage, 0), delta = take(stage, 1);
+    if (!there) {  // a step of softplus(-infinity) = 0
+      const uint32_t inf = kBf16 ? 0xff80ff80u : 0xff800000u;
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) delta.w[k] = make_uint4(inf, inf, inf, inf);
+      x = {};
+    }
     unpack8(x, xs);
     unpack8(delta, ds);
     load_states<8>(&s.bias[8 * u], bias);
@@ -295,19 +444,19 @@ __global__ void __launch_bounds__(kCh / kC *(N / kK) + kHelpers, kC == 1 ? 2 : 3
     for (int m = 0; m < kBc; ++m) {
       const int e = j + m * kHelpers, line = e / (N / 8), n = (e % (N / 8)) * 8;
       if (kUnits % kHelpers && e >= kUnits) continue;
-      float f[8];
-      unpack8(bc[m], f);
+      float v[8];
+      unpack8(take(stage, 3 + m), v);
       float4 *to_bc = reinterpret_cast<float4 *>(line & 1 ? &s.c[slot][line >> 1][n] : &s.b[slot][line >> 1][n]);
-      to_bc[0] = make_float4(f[0], f[1], f[2], f[3]);
-      to_bc[1] = make_float4(f[4], f[5], f[6], f[7]);
+      to_bc[0] = make_float4(v[0], v[1], v[2], v[3]);
+      to_bc[1] = make_float4(v[4], v[5], v[6], v[7]);
     }
   };
-  auto finish = [&](int i, const Raw8<kBf16> &rx, const Raw8<kBf16> &rz) {
-    const int row = i * kL + t;
-    if (!p.y || !in || row >= q.run) return;
+  auto finish = [&](int i) {
+    const int row = i * kL + t, stage = i % kStages;
+    if (!out || !in || row >= q.run) return;
     float f[8], skip[8];
     float2 y[4];
-    unpack8(rx, f);
+    unpack8(take(stage, 0), f);
     load_states<8>(&s.skip[8 * u], skip);
 #pragma unroll
     for (int k = 0; k < 4; ++k) y[k] = __fmul2_rn(make_float2(skip[2 * k], skip[2 * k + 1]), make_float2(f[2 * k], f[2 * k + 1]));
@@ -320,12 +469,12 @@ __global__ void __launch_bounds__(kCh / kC *(N / kK) + kHelpers, kC == 1 ? 2 : 3
       for (int k = 0; k < 4; ++k) y[k] = __fadd2_rn(y[k], make_float2(part[2 * k], part[2 * k + 1]));
     }
     if (gate) {
-      unpack8(rz, f);
+      unpack8(take(stage, 2), f);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float2 z = make_float2(f[2 * k], f[2 * k + 1]), e = __fmul2_rn(z, make_float2(-kLog2e, -kLog2e));
+        const float2 v = make_float2(f[2 * k], f[2 * k + 1]), e = __fmul2_rn(v, make_float2(-kLog2e, -kLog2e));
         const float2 w = __fadd2_rn(make_float2(exp2_fast(e.x), exp2_fast(e.y)), make_float2(1.0f, 1.0f));
-        y[k] = __fmul2_rn(y[k], __fmul2_rn(z, make_float2(rcp_fast(w.x), rcp_fast(w.y))));
+        y[k] = __fmul2_rn(y[k], __fmul2_rn(v, make_float2(rcp_fast(w.x), rcp_fast(w.y))));
       }
     }
 #pragma unroll
@@ -343,29 +492,28 @@ __global__ void __launch_bounds__(kCh / kC *(N / kK) + kHelpers, kC == 1 ? 2 : 3
         }
     }
   };
-  // x and z of the last tile, of the one that is being scanned and of the next
-  Raw8<kBf16> x0, z0, x1, z1, x2, z2;
-  load(0);
-  asm volatile("bar.sync 1, %0;" ::"n"(kHelpers) : "memory");  // bias and skip are there, for the helpers
-  produce(0);
-  x1 = x, z1 = z;
-  load(1);
-  produce(1);
-  x2 = x, z2 = z;
-  load(2);
+  const bool inputs = !T::kTwo || helper < kHelpers, outputs = !T::kTwo || helper >= kHelpers;
+  if (inputs) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(i);
+    // behind the last tile there are two more, of zero steps: their inputs are not read
+    produce(0, 0);
+    load(kAhead);
+    produce(1, 1);
+    load(kAhead + 1);
+  }
   __syncthreads();
   int slot = 2;
   for (int i = 0; i < tiles; ++i) {
-    if (i > 0) finish(i - 1, x0, z0);
-    x0 = x1, z0 = z1, x1 = x2, z1 = z2, x2 = x, z2 = z;
-    if (i + 2 < tiles) {
-      produce(slot);
-      load(i + 3);
+    if (outputs && i > 0) finish(i - 1);
+    if (inputs && i + 2 < tiles) {
+      produce(i + 2, slot);
+      load(i + 2 + kAhead);
     }
     slot = slot == 2 ? 0 : slot + 1;
     __syncthreads();
   }
-  finish(tiles - 1, x0, z0);
+  if (outputs) finish(tiles - 1);
 }
 
 // ---------------------------------------------------------------------------
@@ -460,15 +608,45 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const Params p) {
 // host
 // ---------------------------------------------------------------------------
 
-template <bool kBf16, int N, int kK, int kC, bool kVec>
-cudaError_t launch_scan(const Params &p, cudaStream_t s) {
-  using T = Tile<N, kK, kC>;
+constexpr int kPiece = 512;        // rows of a piece
+constexpr int kPiecedReqs = 1024;  // requests at most: every block looks through their lengths
+
+// Whether requests are run in pieces, which costs a second pass over nearly all rows
+// (without outputs) and balances the SMs.
+bool pieced(int R, int num_tok, int max_len, int D) {
+  if (R > kPiecedReqs || max_len <= 2 * kPiece) return false;
+  // In ns: a tile of 32 rows and channels takes 850 where its CTA has an SM to itself, 1,430 where two share one;
+  // both passes over pieces, on full SMs, take 9.2 a tile.  (One request of 8,192 rows and
+  // 4,096 channels: 217 us whole, 305 in pieces; 2,048 channels: 215 and 175.)
+  const double ctas = (double)R * ((D + kCh - 1) / kCh), tiles = (max_len + kL - 1) / kL;
+  const double whole = ctas <= 152 ? 850.0 * tiles : 1430.0 * tiles * (double)(((long long)ctas + 303) / 304);
+  return 15000.0 + 9.2 * ((double)num_tok / kL) * ((D + kCh - 1) / kCh) < 0.9 * whole;
+}
+size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+template <bool kBf16, int N, int kC, bool kVec, int kPass>
+cudaError_t launch_scan(const Params &p, int pieces, cudaStream_t s) {
+  constexpr int kK = 4;
+  using T = Tile<kBf16, N, kK, kC>;
   static_assert(sizeof(T) <= 227 * 1024, "a tile's buffers have to fit an SM");
-  const cudaError_t e = cudaFuncSetAttribute(scan_kernel<kBf16, N, kK, kC, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(T));
+  const auto kernel = scan_kernel<kBf16, N, kK, kC, kVec, kPass>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(T));
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)((p.D + kCh - 1) / kCh), (unsigned)p.rows.R);
-  scan_kernel<kBf16, N, kK, kC, kVec><<<grid, T::kScan + kHelpers, sizeof(T), s>>>(p);
+  kernel<<<dim3((unsigned)((p.D + kCh - 1) / kCh), (unsigned)(p.rows.R + pieces)), T::kThreads, sizeof(T), s>>>(p);
   return cudaGetLastError();
+}
+
+template <bool kBf16, int N, bool kVec>
+cudaError_t launch_many(const Params &p, cudaStream_t s) {
+  if (p.piece) {
+    const int pieces = p.rows.num_tok / p.piece;
+    const cudaError_t e = launch_scan<kBf16, N, 2, kVec, 1>(p, pieces, s);
+    return e == cudaSuccess ? launch_scan<kBf16, N, 2, kVec, 2>(p, pieces, s) : e;
+  }
+  // one channel a thread, a CTA alone on its SM, while there are as many SMs (4 requests of 4,096 rows and 2,048
+  // channels, 256 CTAs: 217 us, with two channels a thread 182)
+  const bool two = (long long)p.rows.R * ((p.D + kCh - 1) / kCh) > 152;
+  return two ? launch_scan<kBf16, N, 2, kVec, 0>(p, 0, s) : launch_scan<kBf16, N, 1, kVec, 0>(p, 0, s);
 }
 
 template <bool kBf16, int N>
@@ -479,11 +657,7 @@ cudaError_t launch(const Params &p, bool vector, cudaStream_t s) {
     few_kernel<kBf16, N, 1><<<grid(1), kFewThreads, 0, s>>>(p);
     return cudaGetLastError();
   }
-  constexpr int kK = 4;
-  // two channels a thread where that leaves a scan warp for each of the SMs' schedulers
-  const bool two = (long long)p.rows.R * p.D * (N / kK) / 64 >= 608;
-  if (two) return vector ? launch_scan<kBf16, N, kK, 2, true>(p, s) : launch_scan<kBf16, N, kK, 2, false>(p, s);
-  return vector ? launch_scan<kBf16, N, kK, 1, true>(p, s) : launch_scan<kBf16, N, kK, 1, false>(p, s);
+  return vector ? launch_many<kBf16, N, true>(p, s) : launch_many<kBf16, N, false>(p, s);
 }
 
 template <bool kBf16>
@@ -495,12 +669,27 @@ cudaError_t by_state(const Params &p, int N, bool vector, cudaStream_t s) {
 
 bool activation(int dtype) { return dtype == GLINATTN_F32 || dtype == GLINATTN_BF16; }
 
-glinattn_status run(const glinattn_scan_packed_args *a, cudaStream_t stream) {
+glinattn_status check_sizes(const glinattn_scan_packed_args *a) {
   if (!a || !activation(a->in_dtype) || !activation(a->out_dtype) || a->num_req < 0 || a->num_tok < 0 || a->channels <= 0 ||
       a->state <= 0 || a->max_q_len < 0 || a->x_stride < 0 || a->delta_stride < 0 || a->z_stride < 0 || a->b_stride < 0 ||
       a->c_stride < 0)
     return GLINATTN_ERR_INVALID_ARG;
   if ((a->state != 8 && a->state != 16 && a->state != 32) || a->num_req > 65535 || a->channels > (1 << 20)) return GLINATTN_ERR_UNSUPPORTED;
+  return GLINATTN_OK;
+}
+
+// Bytes of the workspace, and where its parts begin; 0 where requests are run whole.
+size_t workspace(const glinattn_scan_packed_args *a, size_t *sums, size_t *starts) {
+  const int longest = a->max_q_len < a->num_tok ? a->max_q_len : a->num_tok;
+  if (a->num_req == 0 || a->num_tok == 0 || !pieced(a->num_req, a->num_tok, longest, a->channels)) return 0;
+  const size_t pieces = (size_t)(a->num_tok / kPiece), ends = pieces * a->channels * a->state * 4, each = up16(pieces * a->channels * 4);
+  if (sums) *sums = ends, *starts = ends + each;
+  return 2 * ends + each;
+}
+
+glinattn_status run(const glinattn_scan_packed_args *a, cudaStream_t stream) {
+  const glinattn_status st = check_sizes(a);
+  if (st != GLINATTN_OK) return st;
   if ((a->state_pool == nullptr) != (a->slot_ids == nullptr) || (a->state_pool && a->pool_slots <= 0)) return GLINATTN_ERR_INVALID_ARG;
   if (!a->q_start && a->num_tok != a->num_req) return GLINATTN_ERR_INVALID_ARG;
   if (a->num_req == 0 || a->num_tok == 0) return GLINATTN_OK;
@@ -533,6 +722,17 @@ glinattn_status run(const glinattn_scan_packed_args *a, cudaStream_t stream) {
   p.x_stride = strides[0], p.delta_stride = strides[1], p.z_stride = strides[2], p.b_stride = strides[3], p.c_stride = strides[4];
   p.A = a->A, p.skip = a->skip, p.delta_bias = a->delta_bias, p.pool = a->state_pool, p.y = a->y;
   p.D = D, p.update = update, p.out_bf16 = a->out_dtype == GLINATTN_BF16;
+  size_t sums = 0, starts = 0;
+  const size_t need = workspace(a, &sums, &starts);
+  p.piece = need ? kPiece : 0;
+  p.ends = p.sums = p.starts = nullptr;
+  if (need) {
+    if (!a->workspace || a->workspace_bytes < need || !aligned(a->workspace, 16)) return GLINATTN_ERR_INVALID_ARG;
+    uint8_t *ws = static_cast<uint8_t *>(a->workspace);
+    p.ends = reinterpret_cast<float *>(ws);
+    p.sums = reinterpret_cast<float *>(ws + sums);
+    p.starts = reinterpret_cast<float *>(ws + starts);
+  }
   bool vec[5];  // rows that can be read 16 bytes at a time
   for (int i = 0; i < 5; ++i)
     vec[i] = !rows[i] || (aligned(rows[i], 16) && (a->num_tok == 1 || strides[i] * (long long)es % 16 == 0));
@@ -545,6 +745,10 @@ glinattn_status run(const glinattn_scan_packed_args *a, cudaStream_t stream) {
 }  // namespace
 }  // namespace scan
 }  // namespace glinattn
+
+extern "C" size_t glinattn_selective_scan_packed_workspace_size(const glinattn_scan_packed_args *args) {
+  return glinattn::scan::check_sizes(args) == GLINATTN_OK ? glinattn::scan::workspace(args, nullptr, nullptr) : 0;
+}
 
 extern "C" glinattn_status glinattn_selective_scan_packed(const glinattn_scan_packed_args *args, glinattn_stream_t stream) {
   return glinattn::scan::run(args, (cudaStream_t)stream);

@@ -162,7 +162,7 @@ class ScanPackedArgs(ctypes.Structure):
                 ("delta_stride", _i64), ("z_stride", _i64), ("b_stride", _i64), ("c_stride", _i64), ("x", _vp),
                 ("delta", _vp), ("z", _vp), ("Bm", _vp), ("Cm", _vp), ("A", _vp), ("skip", _vp), ("delta_bias", _vp),
                 ("state_pool", _vp), ("slot_ids", _vp), ("q_start", _vp), ("resume", _vp), ("count", _vp), ("y", _vp),
-                ("dev_status", _vp)]
+                ("dev_status", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
 
 
 class NormArgs(ctypes.Structure):
@@ -208,6 +208,8 @@ def library() -> ctypes.CDLL:
             lib.glinattn_selective_scan_workspace_size.restype = ctypes.c_size_t
             lib.glinattn_paged_attention_workspace_size.argtypes = [ctypes.POINTER(PagedAttnArgs)]
             lib.glinattn_paged_attention_workspace_size.restype = ctypes.c_size_t
+            lib.glinattn_selective_scan_packed_workspace_size.argtypes = [ctypes.POINTER(ScanPackedArgs)]
+            lib.glinattn_selective_scan_packed_workspace_size.restype = ctypes.c_size_t
             _lib = lib
     return _lib
 
@@ -839,7 +841,7 @@ def glinattn_short_conv(x, w, bias=None, conv_pool=None, slot_ids=None, q_start=
 
 def glinattn_selective_scan_packed(x, delta, Bm, Cm, A, state_pool=None, slot_ids=None, q_start=None, *, max_q_len=None, z=None,
                                    skip=None, delta_bias=None, resume=None, count=None, update_state=True, outputs=True,
-                                   out_dtype=None, y=None, dev_status=None, stream=None):
+                                   out_dtype=None, y=None, workspace=None, dev_status=None, stream=None):
     """The selective scan of packed rows with its step bias, skip and gate.  x,
     delta, z [num_tok,D], Bm, Cm [num_tok,N] (bf16 or fp32, each may be a slice of
     wider rows; z None: no gate); A [D,N], skip, delta_bias [D] fp32 (None: zeros);
@@ -879,6 +881,14 @@ def glinattn_selective_scan_packed(x, delta, Bm, Cm, A, state_pool=None, slot_id
     a = ScanPackedArgs(code, out, R, n, D, N, P, int(bool(update_state)), max_q_len, xs, ds, zs, bs, cs, _addr(x), _addr(delta),
                        _addr(z), _addr(Bm), _addr(Cm), _addr(A), _addr(skip), _addr(delta_bias), _addr(state_pool),
                        _addr(slot_ids), _addr(q_start), _addr(resume), _addr(count), _addr(y), _addr(dev_status))
+    need = library().glinattn_selective_scan_packed_workspace_size(a)
+    if need:
+        if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+            raise ValueError(f"workspace must be contiguous and on {dev}")
+        if workspace is None or workspace.nbytes < need:
+            workspace = _empty((need,), torch.uint8, dev, stream)
+        a.workspace = workspace.data_ptr()
+        a.workspace_bytes = need
     _launch("glinattn_selective_scan_packed", a, stream, dev)
     return y
 

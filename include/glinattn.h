@@ -655,6 +655,10 @@ glinattn_status glinattn_short_conv(const glinattn_short_conv_args *args, glinat
  *   N in {8, 16, 32}; any D >= 1.  A <= 0 with |A| < 2.3e38.  All arithmetic is fp32.
  *   max_q_len: an upper bound of the ranges' lengths (it selects the kernel); a longer
  *     range sets GLINATTN_DEV_BAD_COUNT and its request is skipped.
+ *   workspace: at least glinattn_selective_scan_packed_workspace_size() bytes, 16-byte
+ *     aligned (0 bytes for short requests): the states between the pieces of long
+ *     requests.  The size depends on the sizes of the struct only.  Calls that may overlap
+ *     on the GPU need a workspace each.
  */
 typedef struct {
   int32_t in_dtype, out_dtype, num_req, num_tok, channels, state, pool_slots, update_state, max_q_len;
@@ -665,8 +669,11 @@ typedef struct {
   const int32_t *slot_ids, *q_start, *resume, *count;
   void *y;
   uint32_t *dev_status;
+  void *workspace;
+  size_t workspace_bytes;
 } glinattn_scan_packed_args;
 
+size_t glinattn_selective_scan_packed_workspace_size(const glinattn_scan_packed_args *args);
 glinattn_status glinattn_selective_scan_packed(const glinattn_scan_packed_args *args, glinattn_stream_t stream);
 
 /*

@@ -80,6 +80,31 @@ def test_a_long_prompt():
     check(case([3001], 48, 16, torch.float32, seed=1, slow=True), resume=[0])
 
 
+@pytest.mark.parametrize("N", [8, 16, 32])
+@pytest.mark.parametrize("act", [torch.bfloat16, torch.float32])
+def test_long_and_short_requests(act, N):
+    """Requests that are run in pieces beside short ones, ends at and around a piece's; some continue, some run in part."""
+    lengths = [1500, 3, 0, 2049, 512, 513, 1024, 1025, 1, 1100]
+    c = case(lengths, 40, N, act, seed=N, strided=True, pad=3, first=2)
+    check(c, resume=[r % 3 != 1 for r in range(10)])
+    check(c, count=[1500, 2, 0, 1537, 512, 0, 1000, 1025, 1, 512])
+    c["slots"][3] = -1
+    c["q_start"][-1] = 1 << 20
+    check(c, status=DEV_BAD_SLOT | DEV_BAD_COUNT, max_len=2100)
+
+
+def test_two_calls_with_one_workspace_on_one_stream():
+    """A workspace's leftovers reach no later call; a larger one than needed serves too."""
+    ws = torch.full((1 << 24,), 0xff, dtype=torch.uint8, device=DEV)
+    for seed, n in ((21, 2500), (22, 1200)):
+        c = case([n, 40], 64, 16, torch.bfloat16, seed=seed)
+        args = c["x"], c["delta"], c["B"], c["C"], c["A"]
+        p1, p2 = c["pool"].clone(), c["pool"].clone()
+        a = glinattn_selective_scan_packed(*args, p1, c["slots"], c["q_start"], max_q_len=n, workspace=ws)
+        b = glinattn_selective_scan_packed(*args, p2, c["slots"], c["q_start"], max_q_len=n)
+        assert torch.equal(a, b) and torch.equal(p1, p2) and bool(torch.isfinite(a.float()).all())
+
+
 def test_many_requests():
     lengths = [r % 4 for r in range(700)]
     check(case(lengths, 40, 16, torch.bfloat16, seed=2))
