@@ -91,6 +91,27 @@ __device__ __forceinline__ uint2 to_e4m3x8(const float *f) {
   return make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// z / (1 + e^-z), the exponential and the reciprocal within 2^-22 (and |z| 2^-23) of themselves.
+__device__ __forceinline__ float silu(float z) { return z * rcp_fast(1.0f + exp2_fast(-z * kLog2e)); }
+__device__ __forceinline__ float2 silu2(float2 z) {
+  const float2 e = __fmul2_rn(z, make_float2(-kLog2e, -kLog2e));
+  const float2 w = __fadd2_rn(make_float2(exp2_fast(e.x), exp2_fast(e.y)), make_float2(1.0f, 1.0f));
+  return __fmul2_rn(z, make_float2(rcp_fast(w.x), rcp_fast(w.y)));
+}
+
 // The packed rows and slots of a call (the members that the argument structs share).
 struct Rows {
   int R, num_tok, pool_slots, max_len;  // max_len: no request is longer, else it is skipped

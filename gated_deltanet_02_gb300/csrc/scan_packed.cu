@@ -47,19 +47,6 @@ struct Params {
   float *ends, *sums, *starts;
 };
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float rcp_fast(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 // log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1]; log(1 + e) = e P(e), P of degree 8
 // fitted to log(1 + e) / e on [0, 1] with a relative error of 3e-8, so a small result keeps its
 // relative error.  Two at a time.
@@ -73,7 +60,6 @@ __device__ __forceinline__ float2 softplus2(float2 x) {
   return __ffma2_rn(r, e, make_float2(fmaxf(x.x, 0.0f), fmaxf(x.y, 0.0f)));
 }
 __device__ __forceinline__ float softplus(float x) { return softplus2(make_float2(x, x)).x; }
-__device__ __forceinline__ float silu(float z) { return z * rcp_fast(1.0f + exp2_fast(-z * kLog2e)); }
 
 // ---------------------------------------------------------------------------
 // many rows
@@ -472,9 +458,7 @@ __global__ void __launch_bounds__(Tile<kBf16, N, kK, kC>::kThreads, kC == 1 ? 1 
       unpack8(take(stage, 2), f);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float2 v = make_float2(f[2 * k], f[2 * k + 1]), e = __fmul2_rn(v, make_float2(-kLog2e, -kLog2e));
-        const float2 w = __fadd2_rn(make_float2(exp2_fast(e.x), exp2_fast(e.y)), make_float2(1.0f, 1.0f));
-        y[k] = __fmul2_rn(y[k], __fmul2_rn(v, make_float2(rcp_fast(w.x), rcp_fast(w.y))));
+        y[k] = __fmul2_rn(y[k], silu2(make_float2(f[2 * k], f[2 * k + 1])));
       }
     }
 #pragma unroll

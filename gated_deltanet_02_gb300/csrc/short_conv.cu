@@ -32,27 +32,66 @@ constexpr int kWarps = 4;  // of a CTA
 
 template <bool kBf16, int kVec>
 struct Lane {  // kVec channels of one row as they are in memory
-  Raw8<kBf16> v;
-  float s;
+  uint32_t w[kVec == 1 ? 1 : kBf16 ? kVec / 2 : kVec];
 };
 template <bool kBf16, int kVec>
 __device__ __forceinline__ Lane<kBf16, kVec> load_lane(const void *p, size_t i, bool in) {
   Lane<kBf16, kVec> l = {};
-  if (in) {
-    if constexpr (kVec == 8) l.v = load_raw8<kBf16>(p, i);
-    else l.s = load_one<kBf16>(p, i);
+  if (!in) return l;
+  const uint8_t *at = reinterpret_cast<const uint8_t *>(p) + i * (kBf16 ? 2 : 4);
+  if constexpr (kVec == 1) {
+    l.w[0] = kBf16 ? *reinterpret_cast<const uint16_t *>(at) : *reinterpret_cast<const uint32_t *>(at);
+  } else if constexpr (kBf16) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(at);
+    l.w[0] = v.x, l.w[1] = v.y;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4 *>(at);
+    l.w[0] = v.x, l.w[1] = v.y, l.w[2] = v.z, l.w[3] = v.w;
   }
   return l;
 }
 template <bool kBf16, int kVec>
 __device__ __forceinline__ void open_lane(const Lane<kBf16, kVec> &l, float *f) {
-  if constexpr (kVec == 8) unpack8(l.v, f);
-  else f[0] = l.s;
+  if constexpr (kBf16) {
+    f[0] = bf16_lo(l.w[0]);
+    if constexpr (kVec == 4) f[1] = bf16_hi(l.w[0]), f[2] = bf16_lo(l.w[1]), f[3] = bf16_hi(l.w[1]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) f[k] = __uint_as_float(l.w[k]);
+  }
 }
 template <bool kBf16, int kVec>
 __device__ __forceinline__ void store_lane(void *p, size_t i, const float *f) {
-  if constexpr (kVec == 8) store8<kBf16>(p, i, f);
-  else store_one<kBf16>(p, i, f[0]);
+  uint8_t *at = reinterpret_cast<uint8_t *>(p) + i * (kBf16 ? 2 : 4);
+  if constexpr (kVec == 1) store_one<kBf16>(p, i, f[0]);
+  else if constexpr (kBf16) *reinterpret_cast<uint2 *>(at) = make_uint2(paged::pack_bf16(f[0], f[1]), paged::pack_bf16(f[2], f[3]));
+  else *reinterpret_cast<float4 *>(at) = make_float4(f[0], f[1], f[2], f[3]);
+}
+
+// A lane's weights and bias: kVec channels' are next to each other.
+template <int W, int kVec>
+__device__ __forceinline__ void load_weights(const Params &p, int c, bool in, float (*w)[kVec], float *b) {
+  if constexpr (kVec == 1) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j][0] = in ? p.w[(size_t)c * W + j] : 0.0f;
+    b[0] = in && p.bias ? p.bias[c] : 0.0f;
+  } else {
+    float f[kVec * W];
+#pragma unroll
+    for (int k = 0; k < kVec * W / 4; ++k) {
+      const float4 v = in ? reinterpret_cast<const float4 *>(p.w + (size_t)c * W)[k] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      f[4 * k] = v.x, f[4 * k + 1] = v.y, f[4 * k + 2] = v.z, f[4 * k + 3] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j][i] = f[i * W + j];
+#pragma unroll
+    for (int k = 0; k < kVec / 4; ++k) {
+      const float4 v = in && p.bias ? reinterpret_cast<const float4 *>(p.bias + c)[k] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      b[4 * k] = v.x, b[4 * k + 1] = v.y, b[4 * k + 2] = v.z, b[4 * k + 3] = v.w;
+    }
+  }
 }
 
 // kTile: rows of a warp, kLoad of them in flight at a time.
@@ -67,12 +106,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_kernel(const Params p) {
   const int c = (blockIdx.y * 32 + lane) * kVec;
   const bool in = c < p.C;
   float w[W][kVec], b[kVec];
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-#pragma unroll
-    for (int j = 0; j < W; ++j) w[j][i] = in ? p.w[(size_t)(c + i) * W + j] : 0.0f;
-    b[i] = in && p.bias ? p.bias[c + i] : 0.0f;
-  }
+  load_weights<W, kVec>(p, c, in, w, b);
   float past[W - 1][kVec];  // the last W - 1 inputs, oldest first
   Request q;
   q.ok = false;
@@ -94,16 +128,26 @@ __global__ void __launch_bounds__(32 * kWarps) conv_kernel(const Params p) {
   auto step = [&](int t, const Lane<kBf16, kVec> &raw) {
     float x[kVec], o[kVec];
     open_lane<kBf16, kVec>(raw, x);
+    if constexpr (kVec == 1) {
+      o[0] = b[0];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      o[i] = b[i];
+      for (int j = 0; j < W - 1; ++j) o[0] = fmaf(w[j][0], past[j][0], o[0]);
+      o[0] = fmaf(w[W - 1][0], x[0], o[0]);
+      if (p.silu) o[0] = silu(o[0]);
+    } else {
+      auto two = [](const float *f, int i) { return make_float2(f[i], f[i + 1]); };
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j) o[i] = fmaf(w[j][i], past[j][i], o[i]);
-      o[i] = fmaf(w[W - 1][i], x[i], o[i]);
-      if (p.silu) o[i] = o[i] / (1.0f + expf(-o[i]));
+      for (int i = 0; i < kVec; i += 2) {
+        float2 s = two(b, i);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) s = __ffma2_rn(two(w[j], i), two(past[j], i), s);
+        s = __ffma2_rn(two(w[W - 1], i), two(x, i), s);
+        if (p.silu) s = silu2(s);
+        o[i] = s.x, o[i + 1] = s.y;
+      }
     }
     shift(raw);
-    if (in && p.y) store_lane<kBf16, kVec>(p.y, (size_t)t * p.C + c, o);
+    if (in) store_lane<kBf16, kVec>(p.y, (size_t)t * p.C + c, o);
   };
   // A request's first row: its history, and its state after the rows that it runs.
   auto begin = [&]() {
@@ -150,21 +194,32 @@ __global__ void __launch_bounds__(32 * kWarps) conv_kernel(const Params p) {
     }
   };
   auto live = [&](int t) { return q.ok && p.y && t - q.s0 < q.run; };
+  Lane<kBf16, kVec> next[kLoad];
+  auto ahead = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < kLoad; ++u) next[u] = load_lane<kBf16, kVec>(p.x, x_at(base + u), in && p.y && base + u < t1);
+  };
+  ahead(t0);
+  enter(t0);
   for (int base = t0; base < t1; base += kLoad) {
     Lane<kBf16, kVec> raw[kLoad];
-    if (p.y) {
 #pragma unroll
-      for (int u = 0; u < kLoad; ++u) raw[u] = load_lane<kBf16, kVec>(p.x, x_at(base + u), in && base + u < t1);
+    for (int u = 0; u < kLoad; ++u) raw[u] = next[u];
+    if (kTile > kLoad) ahead(base + kLoad);
+    // all of these rows belong to the request and are this warp's to run
+    if (base + kLoad <= t1 && base + kLoad <= q.s1 && live(base + kLoad - 1) && (q.s0 >= t0 || base - q.s0 >= W - 1)) {
+#pragma unroll
+      for (int u = 0; u < kLoad; ++u) step(base + u, raw[u]);
+      continue;
     }
-#pragma unroll
-    for (int u = 0; u < kLoad; ++u) {
-      const int t = base + u;
-      if (t >= t1) break;
+    const int end = min(base + kLoad, t1);
+#pragma unroll 1
+    for (int t = base; t < end; ++t) {
       if (t >= q.s1) enter(t);
-      const bool others = q.s0 < t0 && t - q.s0 < W - 1;  // run by the warp of the request's first row
       if (!live(t)) continue;
-      if (others) shift(raw[u]);
-      else step(t, raw[u]);
+      const Lane<kBf16, kVec> raw = load_lane<kBf16, kVec>(p.x, x_at(t), in);
+      if (q.s0 < t0 && t - q.s0 < W - 1) shift(raw);  // run by the warp of the request's first row
+      else step(t, raw);
     }
   }
   if (q.s0 >= t0 && q.s1 > t1)  // the first rows of the last request, past the tile's end
@@ -180,14 +235,19 @@ void launch(const Params &p, cudaStream_t s) {
 
 template <bool kBf16, int W>
 void by_size(const Params &p, bool vector, cudaStream_t s) {
-  // rows of a warp: one where every request has one, more rows (whose halo is
-  // read once) where there are enough of them
-  const bool many = p.rows.q_start && (long long)p.rows.num_tok * p.C > (1 << 22);
+  // Rows of a warp: two where every request has one; else as many as leave 16 warps an SM, as a
+  // tile's weights and history are read once.  (20,800 rows of 4,096 channels with 16, 32 and 64:
+  // 75, 65 and 63 us; 256 single tokens of 2,048 channels with 1 and 2: 5.4 and 4.6 us.)
+  constexpr int kVec = 4;
+  const long long units = (long long)p.rows.num_tok * ((p.C + 31) / 32) / (vector ? kVec : 1), enough = 152 * 16;
+  const int tile = !p.rows.q_start || units / 16 < enough ? 2 : units / 64 < enough ? 16 : 64;
   if (vector) {
-    if (many) launch<kBf16, 8, W, 16>(p, s);
-    else launch<kBf16, 8, W, 2>(p, s);
+    if (tile == 64) launch<kBf16, kVec, W, 64>(p, s);
+    else if (tile == 16) launch<kBf16, kVec, W, 16>(p, s);
+    else launch<kBf16, kVec, W, 2>(p, s);
   } else {
-    if (many) launch<kBf16, 1, W, 16>(p, s);
+    if (tile == 64) launch<kBf16, 1, W, 64>(p, s);
+    else if (tile == 16) launch<kBf16, 1, W, 16>(p, s);
     else launch<kBf16, 1, W, 2>(p, s);
   }
 }
@@ -220,7 +280,7 @@ glinattn_status run(const glinattn_short_conv_args *a, cudaStream_t stream) {
   p.rows = {a->num_req, a->num_tok, a->pool_slots, INT32_MAX, a->conv_pool != nullptr, a->q_start, a->slot_ids, a->resume, a->count, a->dev_status};
   p.x = a->x, p.x_stride = stride, p.w = a->w, p.bias = a->bias, p.pool = a->conv_pool, p.y = a->y;
   p.C = a->channels, p.silu = a->activation, p.update = update;
-  const bool vector = a->channels % 8 == 0 && aligned(a->x, 16) && (a->num_tok == 1 || (stride * (long long)es) % 16 == 0);
+  const bool vector = a->channels % 4 == 0 && aligned(a->x, 16) && (a->num_tok == 1 || (stride * (long long)es) % 16 == 0);
   const bool bf16 = a->in_dtype == GLINATTN_BF16;
   switch (a->width) {
     case 2: bf16 ? by_size<true, 2>(p, vector, stream) : by_size<false, 2>(p, vector, stream); break;
