@@ -18,8 +18,8 @@
 // steps, and the last tile's partial sums into outputs (sum over the channel's threads,
 // skip, gate).  One barrier a tile.
 //
-// few_kernel (single tokens, drafts): a thread owns four states of a channel for
-// kReqs requests, all of whose loads are in flight together.
+// few_kernel (single tokens, drafts): a thread owns four states of a channel; the states and
+// first rows of its requests are in flight together.
 //
 // Bound: scan_kernel by instruction issue (per element an exponential and packed fp32
 // instructions of a half each for its argument, dt x B, h and y, beside loads of B and C and the
@@ -506,91 +506,314 @@ __global__ void __launch_bounds__(Tile<kBf16, N, kK, kC>::kThreads, kC == 1 ? 1 
 
 constexpr int kFewThreads = 256, kFewRows = 16;  // requests of more rows take the other kernel
 
+// Four elements as they are in memory, and as floats.
 template <bool kBf16>
-__device__ __forceinline__ float4 load4(const void *p, size_t at, bool vector) {
-  if (!vector) return make_float4(load_one<kBf16>(p, at), load_one<kBf16>(p, at + 1), load_one<kBf16>(p, at + 2), load_one<kBf16>(p, at + 3));
+struct Raw4 {
+  uint32_t w[kBf16 ? 2 : 4];
+};
+template <bool kBf16>
+__device__ __forceinline__ Raw4<kBf16> load4(const void *p, size_t at, bool vector) {
+  Raw4<kBf16> r;
   if constexpr (kBf16) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p) + at);
-    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+    const uint16_t *q = reinterpret_cast<const uint16_t *>(p) + at;
+    if (vector) {
+      const uint2 v = *reinterpret_cast<const uint2 *>(q);
+      r.w[0] = v.x, r.w[1] = v.y;
+    } else {
+      r.w[0] = q[0] | (uint32_t)q[1] << 16, r.w[1] = q[2] | (uint32_t)q[3] << 16;
+    }
   } else {
-    return *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + at);
+    const uint32_t *q = reinterpret_cast<const uint32_t *>(p) + at;
+    if (vector) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(q);
+      r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r.w[k] = q[k];
+    }
+  }
+  return r;
+}
+template <bool kBf16>
+__device__ __forceinline__ void open4(const Raw4<kBf16> &r, float2 *f) {
+  if constexpr (kBf16) {
+    f[0] = make_float2(bf16_lo(r.w[0]), bf16_hi(r.w[0])), f[1] = make_float2(bf16_lo(r.w[1]), bf16_hi(r.w[1]));
+  } else {
+    f[0] = make_float2(__uint_as_float(r.w[0]), __uint_as_float(r.w[1])), f[1] = make_float2(__uint_as_float(r.w[2]), __uint_as_float(r.w[3]));
   }
 }
 
-template <bool kBf16, int N, int kReqs>
-__global__ void __launch_bounds__(kFewThreads) few_kernel(const Params p) {
+// A thread runs kReqs requests one after the other, kBatch rows at a time; the states and the first
+// rows of all of them are asked for before any is run.
+template <bool kBf16, int N, int kReqs, int kBatch>
+__global__ void __launch_bounds__(kFewThreads, 3) few_kernel(const Params p) {
   constexpr int kQ = N / 4;  // threads of a channel, four states each
   if (blockIdx.x == 0) check_requests(p.rows, (long long)blockIdx.y * kFewThreads + threadIdx.x, (long long)gridDim.y * kFewThreads);
   const int g = threadIdx.x % kQ, d = blockIdx.x * (kFewThreads / kQ) + threadIdx.x / kQ;
   const bool in = d < p.D;
   const int dd = in ? d : 0;
-  const float4 a4 = reinterpret_cast<const float4 *>(p.A + (size_t)dd * N)[g];
-  const float A[4] = {a4.x * kLog2e, a4.y * kLog2e, a4.z * kLog2e, a4.w * kLog2e};
-  const float bias = p.delta_bias ? p.delta_bias[dd] : 0.0f, skip = p.skip ? p.skip[dd] : 0.0f;
+  struct Row {
+    uint32_t x, delta, z;
+    Raw4<kBf16> b, c;
+  };
+  auto one = [&](const void *src, size_t at) -> uint32_t {
+    return kBf16 ? (uint32_t) reinterpret_cast<const uint16_t *>(src)[at] << 16 : reinterpret_cast<const uint32_t *>(src)[at];
+  };
+  auto row = [&](Row &v, size_t r) {
+    v.x = one(p.x, r * p.x_stride + dd);
+    v.delta = one(p.delta, r * p.delta_stride + dd);
+    v.b = load4<kBf16>(p.Bm, r * p.b_stride + 4 * g, p.bc_vector);
+    if (!p.y) return;
+    if (p.z) v.z = one(p.z, r * p.z_stride + dd);
+    v.c = load4<kBf16>(p.Cm, r * p.c_stride + 4 * g, p.bc_vector);
+  };
   Request q[kReqs];
   float4 h4[kReqs];
-  struct Row {
-    float x, delta, z;
-    float4 b, c;
-  };
-  auto row = [&](size_t r) {
-    Row v;
-    v.x = load_one<kBf16>(p.x, r * p.x_stride + dd);
-    v.delta = load_one<kBf16>(p.delta, r * p.delta_stride + dd);
-    v.z = p.z && p.y ? load_one<kBf16>(p.z, r * p.z_stride + dd) : 0.0f;
-    v.b = load4<kBf16>(p.Bm, r * p.b_stride + 4 * g, p.bc_vector);
-    v.c = p.y ? load4<kBf16>(p.Cm, r * p.c_stride + 4 * g, p.bc_vector) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    return v;
-  };
-  Row first[kReqs];
+  Row v[kReqs][kBatch];
 #pragma unroll
   for (int i = 0; i < kReqs; ++i) {
     const int r = blockIdx.y * kReqs + i;
+    q[i].ok = false;
     if (r < p.rows.R) q[i] = request(p.rows, r);
-    else q[i].ok = false;
     if (!q[i].ok) q[i].run = 0, q[i].slot = 0, q[i].resumed = false;
   }
 #pragma unroll
   for (int i = 0; i < kReqs; ++i) {
     h4[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (q[i].run == 0) continue;  // whole CTAs
-    if (q[i].resumed && in) h4[i] = reinterpret_cast<const float4 *>(p.pool + ((size_t)q[i].slot * p.D + d) * N)[g];
-    first[i] = row((size_t)q[i].s0);
+    if (q[i].resumed && in && q[i].run > 0) h4[i] = reinterpret_cast<const float4 *>(p.pool + ((size_t)q[i].slot * p.D + d) * N)[g];
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t)
+      if (t < q[i].run) row(v[i][t], (size_t)q[i].s0 + t);
   }
+  const float4 a4 = reinterpret_cast<const float4 *>(p.A + (size_t)dd * N)[g];
+  const float2 A[2] = {make_float2(a4.x * kLog2e, a4.y * kLog2e), make_float2(a4.z * kLog2e, a4.w * kLog2e)};
+  const float bias = p.delta_bias ? p.delta_bias[dd] : 0.0f, skip = p.skip ? p.skip[dd] : 0.0f;
 #pragma unroll
   for (int i = 0; i < kReqs; ++i) {
-    if (q[i].run == 0) continue;
-    float h[4] = {h4[i].x, h4[i].y, h4[i].z, h4[i].w};
-    Row v = first[i];
-    for (int t = 0; t < q[i].run; ++t) {
-      const Row now = v;
-      if (t + 1 < q[i].run) v = row((size_t)q[i].s0 + t + 1);
-      const float dt = softplus(now.delta + bias), dtx = dt * now.x;
-      const float b[4] = {now.b.x, now.b.y, now.b.z, now.b.w}, c[4] = {now.c.x, now.c.y, now.c.z, now.c.w};
-      float y = 0.0f;
+    if (q[i].run == 0) continue;  // whole CTAs
+    float2 h[2] = {make_float2(h4[i].x, h4[i].y), make_float2(h4[i].z, h4[i].w)};
+    for (int t0 = 0; t0 < q[i].run; t0 += kBatch) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        h[k] = fmaf(exp2_fast(dt * A[k]), h[k], dtx * b[k]);
-        y = fmaf(h[k], c[k], y);
+      for (int k = 0; k < kBatch; ++k) {
+        const int t = t0 + k;
+        if (t >= q[i].run) break;
+        const Row now = v[i][k];
+        if (t + kBatch < q[i].run) row(v[i][k], (size_t)q[i].s0 + t + kBatch);
+        const float dt = softplus(__uint_as_float(now.delta) + bias), x = __uint_as_float(now.x), dtx = dt * x;
+        float2 b[2], c[2], y2 = make_float2(0.0f, 0.0f);
+        open4(now.b, b);
+        if (p.y) open4(now.c, c);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const float2 e = __fmul2_rn(A[m], make_float2(dt, dt));
+          h[m] = __ffma2_rn(make_float2(exp2_fast(e.x), exp2_fast(e.y)), h[m], __fmul2_rn(make_float2(dtx, dtx), b[m]));
+          if (p.y) y2 = m ? __ffma2_rn(h[m], c[m], y2) : __fmul2_rn(h[m], c[m]);
+        }
+        if (!p.y) continue;
+        float y = y2.x + y2.y;
+#pragma unroll
+        for (int o = kQ / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+        if (!in || g != 0) continue;
+        y = fmaf(skip, x, y);
+        if (p.z) y *= silu(__uint_as_float(now.z));
+        const size_t at = ((size_t)q[i].s0 + t) * p.D + d;
+        if (p.out_bf16) store_one<true>(p.y, at, y);
+        else store_one<false>(p.y, at, y);
       }
-      if (!p.y) continue;
+    }
+    if (p.update && in)
+      reinterpret_cast<float4 *>(p.pool + ((size_t)q[i].slot * p.D + d) * N)[g] = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+  }
+}
+
+// The same over a ring of buffers that bulk copies fill and empty: a stage is the states of 128 channels
+// and the rows of one request, several are on their way to and from each CTA while one is
+// run.  A thread has all N states of a channel.  A CTA keeps its channels and goes through every
+// `gridDim.x / blocks`-th request.  Rows have to be made of whole 16 bytes.
+constexpr int kRingStages = 8, kRingCh = 128;
+constexpr size_t kRingBytes = 56 * 1024;  // of a CTA: four on an SM
+
+template <bool kBf16, int N>
+struct Ring {
+  static constexpr int kSize = kBf16 ? 2 : 4;
+  static constexpr int kRowBytes = (3 * kRingCh + 2 * N) * kSize, kStateBytes = kRingCh * N * 4;  // x, delta, z, B, C
+};
+struct RingHead {
+  uint64_t full[kRingStages], empty[kRingStages];
+  int4 meta[kRingStages];  // first row, rows, slot, whether it resumes
+};
+
+// Shared -> global, both 16-byte aligned, a multiple of 16 bytes.
+__device__ __forceinline__ void bulk_store(void *to, const void *from, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"((uint64_t)to), "r"(sm100::smem_u32(from)), "r"(bytes) : "memory");
+}
+
+template <bool kBf16, int N>
+__global__ void __launch_bounds__(kRingCh + 32, 4) ring_kernel(const Params p, int blocks, int stages, int stage_bytes) {
+  using G = Ring<kBf16, N>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  RingHead &head = *reinterpret_cast<RingHead *>(smem);
+  uint8_t *ring = smem + ((sizeof(RingHead) + 127) & ~(size_t)127);
+  const int block = blockIdx.x % blocks, r0 = blockIdx.x / blocks, rstep = gridDim.x / blocks;
+  const int d0 = block * kRingCh, width = min(kRingCh, p.D - d0), rows_at = G::kStateBytes;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      sm100::mbar_init(&head.full[i], 1);
+      sm100::mbar_init(&head.empty[i], kRingCh / 32);
+    }
+    sm100::fence_mbar_init();
+  }
+  __syncthreads();
+  auto wait = [&](uint64_t *bar, int parity) {
+    const bool ok = sm100::mbar_wait(bar, (uint32_t)parity & 1u);
+    if (!ok && p.rows.dev_status) atomicOr(p.rows.dev_status, GLINATTN_DEV_WAIT_TIMEOUT);
+    return ok;
+  };
+  if (threadIdx.x >= kRingCh) {
+    // --- the warp that brings: 32 requests are looked up at a time, one lane each
+    const int lane = threadIdx.x & 31;
+    check_requests(p.rows, (long long)blockIdx.x * 32 + lane, (long long)gridDim.x * 32);
+    int stage = 0, round = 0;
+    for (int n0 = r0; n0 < p.rows.R; n0 += 32 * rstep) {
+      Request mine;
+      mine.ok = false;
+      const long long r = n0 + (long long)lane * rstep;
+      if (r < p.rows.R) mine = request(p.rows, (int)r);
+      if (!mine.ok) mine.s0 = 0, mine.run = 0, mine.slot = 0, mine.resumed = false;
+      const int many = min(32, (int)((p.rows.R - n0 + (long long)rstep - 1) / rstep));
+      for (int l = 0; l < many; ++l) {
+        const int s0 = __shfl_sync(0xffffffffu, mine.s0, l), run = __shfl_sync(0xffffffffu, mine.run, l);
+        const int slot = __shfl_sync(0xffffffffu, mine.slot, l), resumed = __shfl_sync(0xffffffffu, (int)mine.resumed, l);
+        if (!__all_sync(0xffffffffu, wait(&head.empty[stage], round ^ 1))) return;
+        uint8_t *to = ring + (size_t)stage * stage_bytes;
+        uint64_t *bar = &head.full[stage];
+        const int parts = (p.y ? (p.z ? 5 : 4) : 3), row_bytes = (width * (p.y && p.z ? 3 : 2) + N * (p.y ? 2 : 1)) * G::kSize;
+        if (lane == 0) {
+          head.meta[stage] = make_int4(s0, run, slot, resumed);
+          const uint32_t bytes = run ? (uint32_t)(run * row_bytes + (resumed ? width * N * 4 : 0)) : 0u;
+          if (bytes) sm100::mbar_arrive_expect_tx(bar, bytes);
+          else sm100::mbar_arrive(bar);
+        }
+        __syncwarp();
+        if (lane == 0 && run && resumed) sm100::bulk_load(to, p.pool + ((size_t)slot * p.D + d0) * N, (uint32_t)(width * N * 4), bar);
+        // x, delta, B, C, z of each row
+        for (int e = lane; e < run * parts; e += 32) {
+          const int t = e / parts, what = e - t * parts;
+          const size_t row = (size_t)s0 + t;
+          const uint8_t *src = reinterpret_cast<const uint8_t *>(what == 0 ? p.x : what == 1 ? p.delta : what == 2 ? p.Bm : what == 3 ? p.Cm : p.z);
+          const long long stride = what == 0 ? p.x_stride : what == 1 ? p.delta_stride : what == 2 ? p.b_stride : what == 3 ? p.c_stride : p.z_stride;
+          const bool states = what == 2 || what == 3;
+          const int at = what == 0 ? 0 : what == 1 ? kRingCh : what == 4 ? 2 * kRingCh : 3 * kRingCh + (what - 2) * N;
+          sm100::bulk_load(to + rows_at + t * G::kRowBytes + at * G::kSize, src + (row * stride + (states ? 0 : d0)) * G::kSize,
+                           (uint32_t)((states ? N : width) * G::kSize), bar);
+        }
+        if (++stage == stages) stage = 0, round ^= 1;
+      }
+    }
+    return;
+  }
+  // --- the warps that run: a thread has a channel.  It goes through its states 16 bytes at a time in an
+  // order of its own, in which 8 neighbouring threads are at different banks.
+  constexpr int kQ = N / 4;
+  const int ch = threadIdx.x, lane = ch & 31, d = d0 + ch, turn = (ch & 7) / (8 / kQ);
+  const bool in = ch < width;
+  const int dd = in ? d : d0;
+  float2 A[kQ][2];
 #pragma unroll
-      for (int o = kQ / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-      if (!in || g != 0) continue;
-      y = fmaf(skip, now.x, y);
-      if (p.z) y *= silu(now.z);
-      const size_t at = ((size_t)q[i].s0 + t) * p.D + d;
+  for (int k = 0; k < kQ; ++k) {
+    const float4 v = reinterpret_cast<const float4 *>(p.A + (size_t)dd * N)[(k + turn) & (kQ - 1)];
+    A[k][0] = make_float2(v.x * kLog2e, v.y * kLog2e), A[k][1] = make_float2(v.z * kLog2e, v.w * kLog2e);
+  }
+  const float bias = p.delta_bias ? p.delta_bias[dd] : 0.0f, skip = p.skip ? p.skip[dd] : 0.0f;
+  const int mine = min(32, width - (ch & ~31)) * N * 4;  // bytes of the warp's states
+  int stage = 0, round = 0, leaving = -1;                // the stage whose states are on their way back
+  for (long long r = r0; r < p.rows.R; r += rstep) {
+    if (!wait(&head.full[stage], round)) return;
+    const int4 m = head.meta[stage];
+    const int s0 = m.x, run = m.y;
+    uint8_t *from = ring + (size_t)stage * stage_bytes;
+    float4 *state = reinterpret_cast<float4 *>(from) + ch * kQ;
+    float2 h[kQ][2];
+#pragma unroll
+    for (int k = 0; k < kQ; ++k) {
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (run && m.w) v = state[(k + turn) & (kQ - 1)];
+      h[k][0] = make_float2(v.x, v.y), h[k][1] = make_float2(v.z, v.w);
+    }
+    for (int t = 0; t < run; ++t) {  // threads without a channel run what lies there, and store nothing
+      const uint8_t *row = from + rows_at + t * G::kRowBytes;
+      const float x = load_one<kBf16>(row, ch), dt = softplus(load_one<kBf16>(row, kRingCh + ch) + bias), dtx = dt * x;
+      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+      for (int k = 0; k < kQ; ++k) {
+        const int at = 4 * ((k + turn) & (kQ - 1));
+        float2 b[2], c[2];
+        open4(load4<kBf16>(row, 3 * kRingCh + at, true), b);
+        if (p.y) open4(load4<kBf16>(row, 3 * kRingCh + N + at, true), c);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 e = __fmul2_rn(A[k][i], make_float2(dt, dt));
+          h[k][i] = __ffma2_rn(make_float2(exp2_fast(e.x), exp2_fast(e.y)), h[k][i], __fmul2_rn(make_float2(dtx, dtx), b[i]));
+          if (p.y) sum[i] = __ffma2_rn(h[k][i], c[i], sum[i]);
+        }
+      }
+      if (!p.y || !in) continue;
+      sum[0] = __fadd2_rn(sum[0], sum[1]);
+      float y = fmaf(skip, x, sum[0].x + sum[0].y);
+      if (p.z) y *= silu(load_one<kBf16>(row, 2 * kRingCh + ch));
+      const size_t at = ((size_t)s0 + t) * p.D + d;
       if (p.out_bf16) store_one<true>(p.y, at, y);
       else store_one<false>(p.y, at, y);
     }
-    if (p.update && in)
-      reinterpret_cast<float4 *>(p.pool + ((size_t)q[i].slot * p.D + d) * N)[g] = make_float4(h[0], h[1], h[2], h[3]);
+    const bool store = p.update && run;
+    if (store) {
+#pragma unroll
+      for (int k = 0; k < kQ; ++k) state[(k + turn) & (kQ - 1)] = make_float4(h[k][0].x, h[k][0].y, h[k][1].x, h[k][1].y);
+      sm100::fence_proxy_async_smem();
+    }
+    __syncwarp();
+    if (lane == 0) {
+      if (store) {
+        if (mine > 0) bulk_store(p.pool + ((size_t)m.z * p.D + d) * N, state, (uint32_t)mine);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        if (leaving >= 0) {
+          asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          sm100::mbar_arrive(&head.empty[leaving]);
+        }
+      } else {
+        if (leaving >= 0) {
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          sm100::mbar_arrive(&head.empty[leaving]);
+        }
+        sm100::mbar_arrive(&head.empty[stage]);
+      }
+    }
+    leaving = store ? stage : -1;
+    if (++stage == stages) stage = 0, round ^= 1;
   }
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
+
+template <bool kBf16, int N>
+cudaError_t launch_ring(const Params &p, cudaStream_t s) {
+  using G = Ring<kBf16, N>;
+  const int stage_bytes = (G::kStateBytes + p.rows.max_len * G::kRowBytes + 127) & ~127;
+  const size_t head = (sizeof(RingHead) + 127) & ~(size_t)127;
+  int stages = (int)((kRingBytes - head) / stage_bytes);  // two at least, with a larger share of the SM where rows are many
+  stages = stages < 2 ? 2 : stages > kRingStages ? kRingStages : stages;
+  static_assert(2 * (G::kStateBytes + kFewRows * G::kRowBytes + 128) <= 200 * 1024, "two stages have to fit");
+  const size_t bytes = head + (size_t)stages * stage_bytes;
+  const cudaError_t e = cudaFuncSetAttribute(ring_kernel<kBf16, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) return e;
+  const int blocks = (p.D + kRingCh - 1) / kRingCh, together = 4 * 152 / blocks;
+  const int per = together < 1 ? 1 : together < p.rows.R ? together : p.rows.R;
+  ring_kernel<kBf16, N><<<(unsigned)(blocks * per), kRingCh + 32, bytes, s>>>(p, blocks, stages, stage_bytes);
+  return cudaGetLastError();
+}
 
 constexpr int kPiece = 512;        // rows of a piece
 constexpr int kPiecedReqs = 1024;  // requests at most: every block looks through their lengths
@@ -638,7 +861,9 @@ cudaError_t launch(const Params &p, bool vector, cudaStream_t s) {
   if (p.rows.max_len <= kFewRows) {
     constexpr int kPer = kFewThreads / (N / 4);
     auto grid = [&](int reqs) { return dim3((unsigned)((p.D + kPer - 1) / kPer), (unsigned)((p.rows.R + reqs - 1) / reqs)); };
-    few_kernel<kBf16, N, 1><<<grid(1), kFewThreads, 0, s>>>(p);
+    if (vector && p.bc_vector) return launch_ring<kBf16, N>(p, s);
+    if (p.rows.max_len == 1) few_kernel<kBf16, N, 2, 1><<<grid(2), kFewThreads, 0, s>>>(p);
+    else few_kernel<kBf16, N, 1, 2><<<grid(1), kFewThreads, 0, s>>>(p);
     return cudaGetLastError();
   }
   return vector ? launch_many<kBf16, N, true>(p, s) : launch_many<kBf16, N, false>(p, s);
