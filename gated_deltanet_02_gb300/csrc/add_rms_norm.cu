@@ -33,18 +33,24 @@ __device__ __forceinline__ float join(float a, float b) {
   return kMax ? __uint_as_float(max(__float_as_uint(a), __float_as_uint(b))) : a + b;
 }
 
-// The sum (or the maximum of non-negative bits) over a row's `threads` threads, for all of them.
+// The sum (or the maximum of non-negative bits) over a row's `threads` threads, for all of them.  Calls
+// take turns with the halves of `shared`, so that one barrier each is enough: a half is written again
+// behind the next call's barrier.
+struct Shared {
+  float half[2][32];
+};
 template <bool kMax>
-__device__ __forceinline__ float over_row(float v, float *shared, int threads) {
+__device__ __forceinline__ float over_row(float v, Shared &shared, int &turn, int threads) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = join<kMax>(v, __shfl_xor_sync(0xffffffffu, v, o));
   if (threads == 32) return v;
   const int warps = threads >> 5;
-  __syncthreads();  // the last use of `shared` is over
-  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+  float *mine = shared.half[turn];
+  turn ^= 1;
+  if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = v;
   __syncthreads();
-  float s = shared[0];
-  for (int k = 1; k < warps; ++k) s = join<kMax>(s, shared[k]);
+  float s = mine[0];
+  for (int k = 1; k < warps; ++k) s = join<kMax>(s, mine[k]);
   return s;
 }
 
@@ -65,110 +71,158 @@ __device__ __forceinline__ float scale_of(uint32_t amax, void *scale, size_t at,
   return 1.0f / s;
 }
 
+__device__ __forceinline__ float2 pair(const float *f, int i) { return make_float2(f[2 * i], f[2 * i + 1]); }
+__device__ __forceinline__ void flat(const float2 *h, float *f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[2 * i] = h[i].x, f[2 * i + 1] = h[i].y;
+}
+
 // kOut: 0 fp32, 1 bf16, 2 e4m3 with fp32 scales, 3 e4m3 with powers of two.
-// kRes: 0 none, 1 bf16, 2 fp32.
+// kRes: 0 none, 1 bf16, 2 fp32.  A CTA goes through every gridDim.x-th (group of) rows: its threads
+// keep their weights, and the next row is on its way while this one's sums are formed.
 template <bool kXBf16, int kRes, int kOut, int kChunks>
-__global__ void __launch_bounds__(1024) norm_rows_kernel(const Params p) {
-  __shared__ float shared[32];
-  const int threads = blockDim.x;
-  const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
-  const bool there = row < p.rows;  // whole warps: more than one row a CTA only with 32 threads a row
-  const int chunks = p.width >> 3;
-  float h[kChunks][8];
-  float sum = 0.0f;
+__global__ void __launch_bounds__(kChunks == 1 ? 128 : kChunks == 2 ? 256 : 512, kChunks == 1 ? 8 : kChunks == 2 ? 3 : 1) norm_rows_kernel(const Params p) {
+  __shared__ Shared shared;
+  const int threads = blockDim.x, chunks = p.width >> 3;
+  int turn = 0;
+  // A thread's weights: in registers, or where these would not be enough in shared memory
+  constexpr bool kKept = kChunks < 4;
+  extern __shared__ float4 weights[];
+  float w[kKept ? kChunks : 1][8];
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) {
+    const int c = k * threads + threadIdx.x;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 1.0f;
+    if (p.weight && c < chunks) unpack8(load_raw8<false>(p.weight, 8 * c), v);
+    if constexpr (kKept) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[k][i] = v[i];
+    } else {  // its own, 16 bytes next to its neighbours'
+      weights[2 * k * threads + threadIdx.x] = make_float4(v[0], v[1], v[2], v[3]);
+      weights[(2 * k + 1) * threads + threadIdx.x] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  }
   Raw8<kXBf16> rx[kChunks];
   Raw8<kRes == 1> rr[kChunks];
-#pragma unroll
-  for (int k = 0; k < kChunks; ++k) {
-    const int c = k * threads + threadIdx.x;
-    if (there && c < chunks) {
-      rx[k] = load_raw8<kXBf16>(p.x, (size_t)row * p.x_stride + 8 * c);
-      if (kRes) rr[k] = load_raw8<kRes == 1>(p.residual, (size_t)row * p.width + 8 * c);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < kChunks; ++k) {
-    const int c = k * threads + threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[k][i] = 0.0f;
-    if (there && c < chunks) {
-      unpack8(rx[k], h[k]);
-      if (kRes) {
-        float r[8];
-        unpack8(rr[k], r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[k][i] += r[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(h[k][i], h[k][i], sum);
-    }
-  }
-  sum = over_row<false>(sum, shared, threads);
-  if (kRes && there) {
+  auto read = [&](long long row) {
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
       const int c = k * threads + threadIdx.x;
-      if (c < chunks) store8<kRes == 1>(p.residual_out, (size_t)row * p.width + 8 * c, h[k]);
-    }
-  }
-  float eps = p.eps;
-  if (!(sum <= 3.0e38f)) {  // uniform over the row: an overflow, an infinity or a NaN
-    sum = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kChunks; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        h[k][i] *= kShrink;
-        sum = fmaf(h[k][i], h[k][i], sum);
+      rx[k] = {};
+      rr[k] = {};
+      if (row < p.rows && c < chunks) {
+        rx[k] = load_raw8<kXBf16>(p.x, (size_t)row * p.x_stride + 8 * c);
+        if (kRes) rr[k] = load_raw8<kRes == 1>(p.residual, (size_t)row * p.width + 8 * c);
       }
-    eps = 0.0f;                    // 2^-192 eps
-    sum = over_row<false>(sum, shared, threads);
-  }
-  const float inv = inverse_root(sum, p.width, eps);
-#pragma unroll
-  for (int k = 0; k < kChunks; ++k) {
-    const int c = k * threads + threadIdx.x;
-    float w[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
-    if (p.weight && c < chunks) unpack8(load_raw8<false>(p.weight, 8 * c), w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[k][i] = h[k][i] * inv * w[i];
-  }
-  if constexpr (kOut < 2) {
+    }
+  };
+  const long long step = (long long)gridDim.x * blockDim.y;
+  long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  read(row);
+  // all threads of a CTA go on while its first row is there (of more than one row a CTA, 32 threads each)
+  for (long long first = (long long)blockIdx.x * blockDim.y; first < p.rows; first += step, row += step) {
+    const bool there = row < p.rows;
+    float2 h[kChunks][4], squares = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
-      const int c = k * threads + threadIdx.x;
-      if (there && c < chunks) store8<kOut == 1>(p.y, (size_t)row * p.width + 8 * c, h[k]);
+      float x[8], r[8];
+      unpack8(rx[k], x);
+      if (kRes) unpack8(rr[k], r);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[k][i] = pair(x, i);
+        if (kRes) h[k][i] = __fadd2_rn(h[k][i], pair(r, i));
+        squares = __ffma2_rn(h[k][i], h[k][i], squares);
+      }
     }
-  } else {
-    uint32_t top[kChunks];
+    read(row + step);
+    float sum = over_row<false>(squares.x + squares.y, shared, turn, threads);
+    if (kRes && there) {
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        const int c = k * threads + threadIdx.x;
+        float o[8];
+        flat(h[k], o);
+        if (c < chunks) store8<kRes == 1>(p.residual_out, (size_t)row * p.width + 8 * c, o);
+      }
+    }
+    float eps = p.eps;
+    if (!(sum <= 3.0e38f)) {  // uniform over the row: an overflow, an infinity or a NaN
+      squares = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          h[k][i] = __fmul2_rn(h[k][i], make_float2(kShrink, kShrink));
+          squares = __ffma2_rn(h[k][i], h[k][i], squares);
+        }
+      eps = 0.0f;                    // 2^-192 eps
+      sum = over_row<false>(squares.x + squares.y, shared, turn, threads);
+    }
+    const float inv = inverse_root(sum, p.width, eps);
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
-      top[k] = 0;
+      float v[8];
+      if constexpr (kKept) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top[k] = max(top[k], finite_bits(h[k][i]));
+        for (int i = 0; i < 8; ++i) v[i] = w[k][i];
+      } else {
+        const float4 lo = weights[2 * k * threads + threadIdx.x], hi = weights[(2 * k + 1) * threads + threadIdx.x];
+        v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[k][i] = __fmul2_rn(__fmul2_rn(h[k][i], make_float2(inv, inv)), pair(v, i));
     }
-    const int lanes = p.group >> 3;
-    if (p.group) {
-      for (int o = 1; o < lanes; o <<= 1)
+    if constexpr (kOut < 2) {
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k) top[k] = max(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
+      for (int k = 0; k < kChunks; ++k) {
+        const int c = k * threads + threadIdx.x;
+        float o[8];
+        flat(h[k], o);
+        if (there && c < chunks) store8<kOut == 1>(p.y, (size_t)row * p.width + 8 * c, o);
+      }
     } else {
+      uint32_t top[kChunks];
 #pragma unroll
-      for (int k = 1; k < kChunks; ++k) top[0] = max(top[0], top[k]);
-      top[0] = __float_as_uint(over_row<true>(__uint_as_float(top[0]), shared, threads));
-    }
-    float f = 0.0f;
-    if (!p.group) f = scale_of<kOut == 3>(top[0], p.scale, (size_t)row, there && threadIdx.x == 0);
+      for (int k = 0; k < kChunks; ++k) {
+        float m = 0.0f;  // fmaxf leaves NaN out
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k) {
-      const int c = k * threads + threadIdx.x;
-      const bool in = there && c < chunks;
-      if (p.group)
-        f = scale_of<kOut == 3>(top[k], p.scale, (size_t)row * (p.width / p.group) + c / lanes, in && c % lanes == 0);
-      float q[8];
+        for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(h[k][i].x), fabsf(h[k][i].y)));
+        top[k] = __float_as_uint(m);
+        if (top[k] == 0x7f800000u) {
+          top[k] = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = h[k][i] * f;
-      if (in) *reinterpret_cast<uint2 *>(reinterpret_cast<uint8_t *>(p.y) + (size_t)row * p.width + 8 * c) = to_e4m3x8(q);
+          for (int i = 0; i < 4; ++i) top[k] = max(top[k], max(finite_bits(h[k][i].x), finite_bits(h[k][i].y)));
+        }
+      }
+      const int lanes = p.group >> 3, shift = 31 - __clz(lanes | 1);  // a power of two
+      if (p.group) {
+        for (int o = 1; o < lanes; o <<= 1)
+#pragma unroll
+          for (int k = 0; k < kChunks; ++k) top[k] = max(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
+      } else {
+#pragma unroll
+        for (int k = 1; k < kChunks; ++k) top[0] = max(top[0], top[k]);
+        top[0] = __float_as_uint(over_row<true>(__uint_as_float(top[0]), shared, turn, threads));
+      }
+      float f = 0.0f;
+      if (!p.group) f = scale_of<kOut == 3>(top[0], p.scale, (size_t)row, there && threadIdx.x == 0);
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        const int c = k * threads + threadIdx.x;
+        const bool in = there && c < chunks;
+        if (p.group)
+          f = scale_of<kOut == 3>(top[k], p.scale, (size_t)row * (chunks >> shift) + (c >> shift), in && (c & (lanes - 1)) == 0);
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = __fmul2_rn(h[k][i], make_float2(f, f));
+          q[2 * i] = v.x, q[2 * i + 1] = v.y;
+        }
+        if (in) *reinterpret_cast<uint2 *>(reinterpret_cast<uint8_t *>(p.y) + (size_t)row * p.width + 8 * c) = to_e4m3x8(q);
+      }
     }
   }
 }
@@ -177,7 +231,8 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(const Params p) {
 // passes; every element is read and written by one thread in the last of them.
 template <bool kXBf16, int kRes, int kOut>
 __global__ void __launch_bounds__(512) norm_any_kernel(const Params p) {
-  __shared__ float shared[32];
+  __shared__ Shared shared;
+  int turn = 0;
   const long long row = blockIdx.x;
   const size_t x0 = (size_t)row * p.x_stride, y0 = (size_t)row * p.width;
   auto at = [&](int i) {
@@ -190,14 +245,14 @@ __global__ void __launch_bounds__(512) norm_any_kernel(const Params p) {
     const float h = at(i);
     sum = fmaf(h, h, sum);
   }
-  sum = over_row<false>(sum, shared, blockDim.x);
+  sum = over_row<false>(sum, shared, turn, blockDim.x);
   if (!(sum <= 3.0e38f)) {
     shrink = kShrink, sum = 0.0f, eps = 0.0f;
     for (int i = threadIdx.x; i < p.width; i += blockDim.x) {
       const float h = at(i) * shrink;
       sum = fmaf(h, h, sum);
     }
-    sum = over_row<false>(sum, shared, blockDim.x);
+    sum = over_row<false>(sum, shared, turn, blockDim.x);
   }
   const float inv = inverse_root(sum, p.width, eps);
   auto normed = [&](float h, int i) { return h * shrink * inv * (p.weight ? p.weight[i] : 1.0f); };
@@ -220,7 +275,7 @@ __global__ void __launch_bounds__(512) norm_any_kernel(const Params p) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       } else {
-        top = __float_as_uint(over_row<true>(__uint_as_float(top), shared, blockDim.x));
+        top = __float_as_uint(over_row<true>(__uint_as_float(top), shared, turn, blockDim.x));
       }
       const float f = scale_of<kOut == 3>(top, p.scale, (size_t)row * groups + g, begin == 0);
       for (int j = begin; j < group; j += stride) {
@@ -236,20 +291,26 @@ __global__ void __launch_bounds__(512) norm_any_kernel(const Params p) {
 template <bool kXBf16, int kRes, int kOut>
 void launch(const Params &p, bool vector, cudaStream_t s) {
   const int chunks = p.width >> 3;
-  if (!vector || chunks > 4096) {
+  if (!vector || chunks > 2048) {
     norm_any_kernel<kXBf16, kRes, kOut><<<(unsigned)p.rows, 512, 0, s>>>(p);
     return;
   }
-  auto grid = [&](int threads, int rows) { return dim3((unsigned)((p.rows + rows - 1) / rows)); };
+  // as many CTAs as the SMs hold, each of them with about the same number of rows
+  auto grid = [&](int threads, int rows, int held) {  // threads that an SM holds
+    const long long all = (p.rows + rows - 1) / rows, most = 152ll * (held / (threads * rows));
+    const long long each = (all + most - 1) / most;
+    return dim3((unsigned)((all + each - 1) / each));
+  };
   auto up = [](int n) { int t = 32; while (t < n) t *= 2; return t; };
   if (chunks <= 32) {
-    norm_rows_kernel<kXBf16, kRes, kOut, 1><<<grid(32, 4), dim3(32, 4), 0, s>>>(p);
-  } else if (chunks <= 512) {
+    norm_rows_kernel<kXBf16, kRes, kOut, 1><<<grid(32, 4, 1024), dim3(32, 4), 0, s>>>(p);
+  } else if (chunks <= 256) {
     const int t = up((chunks + 1) / 2);
-    norm_rows_kernel<kXBf16, kRes, kOut, 2><<<grid(t, 1), dim3(t, 1), 0, s>>>(p);
+    norm_rows_kernel<kXBf16, kRes, kOut, 2><<<grid(t, 1, 3 * 256), dim3(t, 1), 0, s>>>(p);
   } else {
     const int t = up((chunks + 3) / 4);
-    norm_rows_kernel<kXBf16, kRes, kOut, 4><<<grid(t, 1), dim3(t, 1), 0, s>>>(p);
+    cudaFuncSetAttribute(norm_rows_kernel<kXBf16, kRes, kOut, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, 512 * 128);
+    norm_rows_kernel<kXBf16, kRes, kOut, 4><<<grid(t, 1, 512), dim3(t, 1), (size_t)t * 128, s>>>(p);
   }
 }
 
