@@ -722,7 +722,16 @@ def glinattn_accept_drafts(target_probs, draft_probs, draft_tokens, uniforms, *,
 
 
 def _rows(t, name, dtype, shape, dev):
-    """Checks of rows that may be slices of wider ones: inside a row contiguous.  Returns their distance in elements."""
+    """Checks of rows that may be slices of wider ones: inside a row contiguous.  Returns their distance in elements,
+    0 for contiguous rows."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev:
+        if t.is_contiguous():
+            return 0
+        stride = t.stride()      # the usual slice of rows [n, a] or [n, a, b]
+        if stride[-1] == 1 and (len(stride) == 2 or len(stride) == 3 and stride[1] == shape[2]):
+            width = shape[1] if len(stride) == 2 else shape[1] * shape[2]
+            if stride[0] >= width:
+                return stride[0]
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
