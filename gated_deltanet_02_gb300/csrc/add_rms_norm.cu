@@ -59,16 +59,17 @@ __device__ __forceinline__ float over_row(float v, Shared &shared, int &turn, in
 __device__ __forceinline__ float inverse_root(float sum, int width, float eps) { return 1.0f / sqrtf(sum / (float)width + eps); }
 
 // The scale of a maximum (its bits), what is stored and what values are multiplied with.
+// `root`: what the values, and their maximum, still have to be multiplied with (fp32 scales).
 template <bool kPow2>
-__device__ __forceinline__ float scale_of(uint32_t amax, void *scale, size_t at, bool store) {
+__device__ __forceinline__ float scale_of(uint32_t amax, float root, void *scale, size_t at, bool store) {
   if (kPow2) {
     const uint32_t code = scale_code(amax);
     if (store) reinterpret_cast<uint8_t *>(scale)[at] = (uint8_t)code;
     return __uint_as_float((254u - code) << 23);
   }
-  const float s = fmaxf(__uint_as_float(amax) / 448.0f, kMinScale);
+  const float top = __uint_as_float(amax), s = fmaxf(top * root / 448.0f, kMinScale);
   if (store) reinterpret_cast<float *>(scale)[at] = s;
-  return 1.0f / s;
+  return s > kMinScale ? 448.0f / top : root / kMinScale;
 }
 
 __device__ __forceinline__ float2 pair(const float *f, int i) { return make_float2(f[2 * i], f[2 * i + 1]); }
@@ -161,7 +162,11 @@ __global__ void __launch_bounds__(kChunks == 1 ? 128 : kChunks == 2 ? 256 : 512,
       eps = 0.0f;                    // 2^-192 eps
       sum = over_row<false>(squares.x + squares.y, shared, turn, threads);
     }
-    const float inv = inverse_root(sum, p.width, eps);
+    float inv = inverse_root(sum, p.width, eps);
+    // With scales in fp32 y / scale is h w * 448 / max |h w|: the root enters the scale alone, and the
+    // quotient has two roundings less.  Rows with an infinity or NaN get theirs from the root.
+    float root = 1.0f;
+    if (kOut == 2 && inv > 0.0f) root = inv, inv = 1.0f;
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
       float v[8];
@@ -208,13 +213,13 @@ __global__ void __launch_bounds__(kChunks == 1 ? 128 : kChunks == 2 ? 256 : 512,
         top[0] = __float_as_uint(over_row<true>(__uint_as_float(top[0]), shared, turn, threads));
       }
       float f = 0.0f;
-      if (!p.group) f = scale_of<kOut == 3>(top[0], p.scale, (size_t)row, there && threadIdx.x == 0);
+      if (!p.group) f = scale_of<kOut == 3>(top[0], root, p.scale, (size_t)row, there && threadIdx.x == 0);
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) {
         const int c = k * threads + threadIdx.x;
         const bool in = there && c < chunks;
         if (p.group)
-          f = scale_of<kOut == 3>(top[k], p.scale, (size_t)row * (chunks >> shift) + (c >> shift), in && (c & (lanes - 1)) == 0);
+          f = scale_of<kOut == 3>(top[k], root, p.scale, (size_t)row * (chunks >> shift) + (c >> shift), in && (c & (lanes - 1)) == 0);
         float q[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -277,7 +282,7 @@ __global__ void __launch_bounds__(512) norm_any_kernel(const Params p) {
       } else {
         top = __float_as_uint(over_row<true>(__uint_as_float(top), shared, turn, blockDim.x));
       }
-      const float f = scale_of<kOut == 3>(top, p.scale, (size_t)row * groups + g, begin == 0);
+      const float f = scale_of<kOut == 3>(top, 1.0f, p.scale, (size_t)row * groups + g, begin == 0);
       for (int j = begin; j < group; j += stride) {
         const int i = g * group + j;
         const float h = at(i);
