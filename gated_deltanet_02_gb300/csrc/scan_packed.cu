@@ -10,20 +10,30 @@
 // with one exponential per element, and what fills the SMs is that a warp always has
 // the work of several rows in flight.
 //
-// scan_kernel: a CTA owns 32 channels of a request and has two kinds of warps.  The scan
-// warps keep kK states of a channel in each thread and go through tiles of 32 rows that lie
-// ready in shared memory: the steps (dt, dt x), B and C.  A thread forms the decays and terms of
-// the next four rows while it runs the recurrence of these four, so that a warp alone
-// keeps its scheduler busy.  The helper warps turn the inputs of the tile after next into
-// steps, and the last tile's partial sums into outputs (sum over the channel's threads,
-// skip, gate).  One barrier a tile.
+// scan_kernel (prompts and pieces of prompts): a CTA owns 32 channels of a request and has two kinds
+// of warps.  The scan warps keep four states of one or two channels in each thread and go
+// through tiles of 32 rows that lie ready in shared memory: the steps (dt, dt x), B and C.  A thread
+// forms the decays and terms of the next rows while it runs the recurrence of these, so that a
+// warp alone keeps its scheduler busy.  The helper warps turn the inputs of the tile after next into
+// steps, and the last tile's partial sums into outputs (sum over the channel's threads, skip,
+// gate).  One barrier a tile.  Long requests that would leave SMs idle are run in pieces of 512 rows,
+// twice: for the states behind them, and from these for the outputs.
 //
-// few_kernel (single tokens, drafts): a thread owns four states of a channel; the states and
-// first rows of its requests are in flight together.
+// ring_kernel (single tokens, drafts): a thread owns a channel; states and rows come, and states go,
+// by bulk copies through a ring of buffers.  few_kernel does the same from registers where rows are
+// not made of whole 16 bytes.
 //
-// Bound: scan_kernel by instruction issue (per element an exponential and packed fp32
-// instructions of a half each for its argument, dt x B, h and y, beside loads of B and C and the
-// helpers' share), few_kernel by HBM bytes, the states in and out.
+// Bound.  scan_kernel: reads of shared memory.  A warp's 16-byte load takes 4 cycles of the SM's one port, 2
+// where neighbouring lanes share it; per row and four states of a channel B, C, the step and the partial
+// sum take 6 cycles, with two channels a thread 4; the helpers 13 a row.  That is 0.9 cycles an SM for 32
+// elements or more, beside 1 for their exponentials (32 lanes a cycle) and 1 for their packed arithmetic.  One
+// prompt of 8,191 rows, 4,096 channels, 16 states: 204 us (2.6 10^12 elements/s, 1.6 us a tile for each of 128
+// CTAs on 152 SMs); 8 prompts of 200 .. 4,001 rows, 2,048 channels: 240 us (2.8 10^12).
+// ring_kernel: HBM bytes, the states in and out: 256 tokens of 2,048 channels 13.6 us, 5,270 GB/s.
+//
+// Measured and not kept: groups of scan warps that hand the states on from 8 rows to the next 8 (305 us
+// for the prompt above), barriers between the roles instead of one for all (231 us), tiles of 16
+// rows (270 us), inputs read ahead into registers (536 us: waits for one load are waits for all).
 #include "packed.cuh"
 #include "sm100.cuh"
 
@@ -85,7 +95,6 @@ struct Tile {
   float step[3][kL][2 * kCh];                    // (dt, dt x) of the channels, permuted: step_at
   float b[3][kL][N], c[3][kL][N];
   float part[2][kG][kPlane];                     // the channels permuted: part_at
-  float bias[kCh], skip[kCh];
 };
 
 // The permutations keep the banks of 8 neighbouring lanes apart on both sides.  Where the step of
@@ -170,8 +179,10 @@ __device__ __forceinline__ Piece find_piece(const Params &p, int y, int lane) {
       f.k = e < 0 ? 0 : e - f.index + 1;
       break;
     }
-    before += __shfl_sync(0xffffffffu, upto, 31);
+    before = min(before + __shfl_sync(0xffffffffu, upto, 31), 1 << 30);
   }
+  // ranges that overlap (a decreasing q_start) may have more pieces than the workspace has room for
+  if (f.pieces > 1 && f.index + f.pieces - 1 > p.rows.num_tok / p.piece) f.r = -1;
   return f;
 }
 
@@ -211,12 +222,6 @@ __global__ void __launch_bounds__(Tile<kBf16, N, kK, kC>::kThreads, kC == 1 ? 1 
     q.run = min(p.piece, q.run - f.k * p.piece);
   }
   const int d0 = blockIdx.x * kCh, tiles = (q.run + kL - 1) / kL;
-  if (threadIdx.x < kCh) {
-    const int d = d0 + threadIdx.x;
-    s.bias[threadIdx.x] = d < p.D && p.delta_bias ? p.delta_bias[d] : 0.0f;
-    s.skip[threadIdx.x] = d < p.D && p.skip ? p.skip[d] : 0.0f;
-  }
-  __syncthreads();
   if (threadIdx.x < T::kScan) {
     // --- scan warps: thread g of channels ch .. ch + kC - 1 has their states g kK .. g kK + kK - 1.
     // Lanes 2 i and 2 i + 1 have the same g, lanes i and i ^ 2 the same channels: loads of shared
@@ -262,7 +267,7 @@ __global__ void __launch_bounds__(Tile<kBf16, N, kK, kC>::kThreads, kC == 1 ? 1 
     // A block of kRows rows: what is read for it, and its decays and terms.  While one block's recurrence
     // runs, the next one's decays are formed and the one's after that is read: nothing waits
     // for a load, and the exponentials lie between the multiply-adds.
-    constexpr int kRows = 2, kBlocks = kL / kRows;
+    constexpr int kRows = kC == 1 ? 4 : 2, kBlocks = kL / kRows;
     struct Lines {
       float st[kRows][2 * kC], b[kRows][kK];
     };
@@ -366,6 +371,12 @@ __global__ void __launch_bounds__(Tile<kBf16, N, kK, kC>::kThreads, kC == 1 ? 1 
   const bool in = left > 0;
   constexpr int kUnits = T::kUnits, kBc = T::kBc, kWords = kBf16 ? 1 : 2, kStages = T::kStages, kAhead = T::kAhead;
   const bool out = kOut && p.y, gate = p.z && out;
+  float bias[8], skip[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    bias[k] = k < left && p.delta_bias ? p.delta_bias[d + k] : 0.0f;
+    skip[k] = k < left && p.skip ? p.skip[d + k] : 0.0f;
+  }
   // The inputs come through shared memory, a thread's own and several tiles ahead: registers that
   // wait for memory would hold up the other loads.  Zeros where there are none.
   auto bring = [&](int stage, int what, const void *src, size_t at, int n, bool there, bool vector) {
@@ -409,7 +420,7 @@ __global__ void __launch_bounds__(Tile<kBf16, N, kK, kC>::kThreads, kC == 1 ? 1 
     const int stage = i % kStages;
     const bool there = in && i * kL + t < q.run;
     float *to = &s.step[slot][t][0];
-    float xs[8], ds[8], bias[8];
+    float xs[8], ds[8];
     Raw8<kBf16> x = take(stage, 0), delta = take(stage, 1);
     if (!there) {  // a step of softplus(-infinity) = 0
       const uint32_t inf = kBf16 ? 0xff80ff80u : 0xff800000u;
@@ -419,7 +430,6 @@ __global__ void __launch_bounds__(Tile<kBf16, N, kK, kC>::kThreads, kC == 1 ? 1 
     }
     unpack8(x, xs);
     unpack8(delta, ds);
-    load_states<8>(&s.bias[8 * u], bias);
 #pragma unroll
     for (int k = 0; k < 8; k += 2) {
       const float2 dt = softplus2(make_float2(ds[k] + bias[k], ds[k + 1] + bias[k + 1]));
@@ -440,10 +450,9 @@ __global__ void __launch_bounds__(Tile<kBf16, N, kK, kC>::kThreads, kC == 1 ? 1 
   auto finish = [&](int i) {
     const int row = i * kL + t, stage = i % kStages;
     if (!out || !in || row >= q.run) return;
-    float f[8], skip[8];
+    float f[8];
     float2 y[4];
     unpack8(take(stage, 0), f);
-    load_states<8>(&s.skip[8 * u], skip);
 #pragma unroll
     for (int k = 0; k < 4; ++k) y[k] = __fmul2_rn(make_float2(skip[2 * k], skip[2 * k + 1]), make_float2(f[2 * k], f[2 * k + 1]));
 #pragma unroll
@@ -504,7 +513,7 @@ __global__ void __launch_bounds__(Tile<kBf16, N, kK, kC>::kThreads, kC == 1 ? 1 
 // few rows
 // ---------------------------------------------------------------------------
 
-constexpr int kFewThreads = 256, kFewRows = 16;  // requests of more rows take the other kernel
+constexpr int kFewThreads = 256, kFewRows = 24;  // requests of more rows take the other kernel
 
 // Four elements as they are in memory, and as floats.
 template <bool kBf16>
@@ -821,10 +830,10 @@ constexpr int kPiecedReqs = 1024;  // requests at most: every block looks throug
 // Whether requests are run in pieces, which costs a second pass over nearly all rows
 // (without outputs) and balances the SMs.
 bool pieced(int R, int num_tok, int max_len, int D) {
-  if (R > kPiecedReqs || max_len <= 2 * kPiece) return false;
+  if (R > kPiecedReqs || max_len <= 2 * kPiece || num_tok / kPiece + R > 65535) return false;
   // In ns: a tile of 32 rows and channels takes 850 where its CTA has an SM to itself, 1,430 where two share one;
   // both passes over pieces, on full SMs, take 9.2 a tile.  (One request of 8,192 rows and
-  // 4,096 channels: 217 us whole, 305 in pieces; 2,048 channels: 215 and 175.)
+  // 4,096 channels: 210 us whole, 305 in pieces; 2,048 channels: 210 and 169.)
   const double ctas = (double)R * ((D + kCh - 1) / kCh), tiles = (max_len + kL - 1) / kL;
   const double whole = ctas <= 152 ? 850.0 * tiles : 1430.0 * tiles * (double)(((long long)ctas + 303) / 304);
   return 15000.0 + 9.2 * ((double)num_tok / kL) * ((D + kCh - 1) / kCh) < 0.9 * whole;
@@ -851,14 +860,17 @@ cudaError_t launch_many(const Params &p, cudaStream_t s) {
     return e == cudaSuccess ? launch_scan<kBf16, N, 2, kVec, 2>(p, pieces, s) : e;
   }
   // one channel a thread, a CTA alone on its SM, while there are as many SMs (4 requests of 4,096 rows and 2,048
-  // channels, 256 CTAs: 217 us, with two channels a thread 182)
+  // channels, 256 CTAs: 217 us, with two channels a thread 183)
   const bool two = (long long)p.rows.R * ((p.D + kCh - 1) / kCh) > 152;
   return two ? launch_scan<kBf16, N, 2, kVec, 0>(p, 0, s) : launch_scan<kBf16, N, 1, kVec, 0>(p, 0, s);
 }
 
 template <bool kBf16, int N>
 cudaError_t launch(const Params &p, bool vector, cudaStream_t s) {
-  if (p.rows.max_len <= kFewRows) {
+  // Rows one after the other with all states in flight, or 32 channels a CTA: 8 requests of 2,048 channels take 3 + 0.43 us
+  // a row and, up to 32 rows, 7.8 us; 64 requests of 17, 24 and 32 rows 23, 31, 48 us and 46, 48, 50 us.
+  const bool many = (long long)p.rows.R * ((p.D + kCh - 1) / kCh) > 304;
+  if (p.rows.max_len <= (many ? kFewRows : 11)) {
     constexpr int kPer = kFewThreads / (N / 4);
     auto grid = [&](int reqs) { return dim3((unsigned)((p.D + kPer - 1) / kPer), (unsigned)((p.rows.R + reqs - 1) / reqs)); };
     if (vector && p.bc_vector) return launch_ring<kBf16, N>(p, s);

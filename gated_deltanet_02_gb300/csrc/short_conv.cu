@@ -10,7 +10,10 @@
 // rows where they pass the tile's end (they are the ones that need the history), and
 // the next tile leaves them out.  So nothing reads a slot after it was written.
 //
-// Bound: HBM bytes, x in and y out.
+// Bound: HBM bytes, x in and y out, at 27% of the warps an SM can hold (95 registers): 8 prompts of 200 ..
+// 4,001 rows, 4,096 channels in bf16, take 63 us (4,740 GB/s); 256 single tokens of 2,048 channels 4.7 us.  Eight
+// channels a lane took 72 us (182 registers), without reading ahead 80 us, scalar arithmetic with a
+// division 251 us.
 #include "packed.cuh"
 
 namespace glinattn {

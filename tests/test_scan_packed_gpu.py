@@ -213,6 +213,28 @@ def test_bad_requests_are_flagged_and_skipped():
     check(c, status=DEV_BAD_COUNT, max_len=2000)
 
 
+def test_decreasing_ranges_stay_in_bounds():
+    """Valid ranges that overlap, between invalid ones: more pieces than there are rows for; flagged, nothing outside is touched."""
+    n, R = 2000, 17
+    c = case([n] + [0] * (R - 1), 40, 16, torch.bfloat16, seed=16)
+    c["q_start"].copy_(torch.tensor([0, n] * 9, dtype=torch.int32)[:R + 1])
+    for max_len, q_start in ((n, c["q_start"]), (4, c["q_start"] // 500)):
+        word, pool = torch.zeros(1, dtype=torch.int32, device=DEV), c["pool"].clone()
+        glinattn_selective_scan_packed(c["x"], c["delta"], c["B"], c["C"], c["A"], pool, c["slots"], q_start.to(torch.int32), max_q_len=max_len,
+                                       dev_status=word)
+        torch.cuda.synchronize()
+        assert int(word.item()) == DEV_BAD_COUNT
+        other = torch.ones(len(pool), dtype=torch.bool, device=DEV)
+        other[c["slots"].long()] = False
+        assert torch.equal(pool[other], c["pool"][other])
+
+
+@pytest.mark.parametrize("R,top", [(3, 11), (3, 12), (200, 24), (200, 25)])
+def test_ends_of_the_kernels_ranges(R, top):
+    """The longest requests that the kernel for few rows takes, and the shortest that the other does."""
+    check(case([(7 * r) % (top + 1) for r in range(R - 1)] + [top], 72, 16, torch.bfloat16, seed=top), resume=[int(r % 3 != 1) for r in range(R)])
+
+
 def test_special_values():
     """Steps far to either side, an infinity and NaN stay in their channel and behind their row."""
     c = case([40], 24, 16, torch.float32, seed=15)
