@@ -31,6 +31,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 import threading
 
 import torch
@@ -721,6 +722,47 @@ def glinattn_accept_drafts(target_probs, draft_probs, draft_tokens, uniforms, *,
     return accept, tokens
 
 
+_CODES = {_i32: "i", _i64: "q", ctypes.c_float: "f", _vp: "P", ctypes.c_size_t: "N"}
+
+
+def _packer(args):
+    """The bytes of an argument struct from its members, in order (numbers; addresses as integers, 0 for none): a
+    quarter of the time that making the struct itself takes."""
+    return struct.Struct("@" + "".join(_CODES[t] for _, t in args._fields_) + "0P").pack
+
+
+_pack_rope, _pack_conv = _packer(KvRopeArgs), _packer(ShortConvArgs)
+_pack_scan, _pack_norm = _packer(ScanPackedArgs), _packer(NormArgs)
+_raw = {}
+
+
+def _bytes_function(name, restype, *more):
+    """A function of the library that takes its argument struct as bytes."""
+    f = _raw.get(name)
+    if f is None:
+        f = _raw[name] = ctypes.CFUNCTYPE(restype, ctypes.c_char_p, *more)((name, library()))
+    return f
+
+
+def _at(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _run(name, args, stream, dev):
+    """_launch of a struct's bytes."""
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors must be on a CUDA device, got {dev}")
+    f = _raw.get(name) or _bytes_function(name, ctypes.c_int, _vp)
+    handle = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        rc = f(args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(args, handle)
+    if rc != 0:
+        raise GlinattnError(rc, name)
+
+
 def _rows(t, name, dtype, shape, dev):
     """Checks of rows that may be slices of wider ones: inside a row contiguous.  Returns their distance in elements,
     0 for contiguous rows."""
@@ -787,10 +829,10 @@ def glinattn_kv_append_rope(q, k, v, inv_freq, k_cache, v_cache, page_table, kv_
         raise ValueError("inv_freq must be [rotary_dim / 2]")
     _check(inv_freq, "inv_freq", torch.float32, inv_freq.shape, dev)
     _status_word(dev_status, dev)
-    a = KvRopeArgs(code, R, n, H, Hkv, d, page, P, max_pages, 2 * inv_freq.shape[0], int(bool(interleaved)), rope_scale, qs, ks,
-                   vs, qos, _addr(q), _addr(k), _addr(v), _addr(inv_freq), _addr(q_out), _addr(k_cache), _addr(v_cache),
-                   _addr(k_scale), _addr(v_scale), _addr(page_table), _addr(kv_len), _addr(q_start), _addr(dev_status))
-    _launch("glinattn_kv_append_rope", a, stream, dev)
+    a = _pack_rope(code, R, n, H, Hkv, d, page, P, max_pages, 2 * inv_freq.shape[0], int(bool(interleaved)), rope_scale, qs, ks,
+                   vs, qos, _at(q), _at(k), _at(v), _at(inv_freq), _at(q_out), _at(k_cache), _at(v_cache),
+                   _at(k_scale), _at(v_scale), _at(page_table), _at(kv_len), _at(q_start), _at(dev_status))
+    _run("glinattn_kv_append_rope", a, stream, dev)
     return q_out, k_cache, v_cache
 
 
@@ -841,10 +883,10 @@ def glinattn_short_conv(x, w, bias=None, conv_pool=None, slot_ids=None, q_start=
         if y is None:
             y = _empty((n, C), act, dev, stream)
         _check(y, "y", act, (n, C), dev)
-    a = ShortConvArgs(code, R, n, C, width, int(bool(silu)), P, int(bool(update_state)), xs, _addr(x), _addr(w), _addr(bias),
-                      _addr(conv_pool), _addr(slot_ids), _addr(q_start), _addr(resume), _addr(count), _addr(y),
-                      _addr(dev_status))
-    _launch("glinattn_short_conv", a, stream, dev)
+    a = _pack_conv(code, R, n, C, width, int(bool(silu)), P, int(bool(update_state)), xs, _at(x), _at(w), _at(bias),
+                      _at(conv_pool), _at(slot_ids), _at(q_start), _at(resume), _at(count), _at(y),
+                      _at(dev_status))
+    _run("glinattn_short_conv", a, stream, dev)
     return y
 
 
@@ -887,18 +929,18 @@ def glinattn_selective_scan_packed(x, delta, Bm, Cm, A, state_pool=None, slot_id
         _check(y, "y", y.dtype if out_dtype is None else out_dtype, (n, D), dev)
     else:
         out = code
-    a = ScanPackedArgs(code, out, R, n, D, N, P, int(bool(update_state)), max_q_len, xs, ds, zs, bs, cs, _addr(x), _addr(delta),
-                       _addr(z), _addr(Bm), _addr(Cm), _addr(A), _addr(skip), _addr(delta_bias), _addr(state_pool),
-                       _addr(slot_ids), _addr(q_start), _addr(resume), _addr(count), _addr(y), _addr(dev_status))
-    need = library().glinattn_selective_scan_packed_workspace_size(a)
+    a = (code, out, R, n, D, N, P, int(bool(update_state)), max_q_len, xs, ds, zs, bs, cs, _at(x), _at(delta), _at(z), _at(Bm),
+         _at(Cm), _at(A), _at(skip), _at(delta_bias), _at(state_pool), _at(slot_ids), _at(q_start), _at(resume), _at(count),
+         _at(y), _at(dev_status))
+    need = 0
+    if max_q_len > 1:            # single tokens need none
+        need = _bytes_function("glinattn_selective_scan_packed_workspace_size", ctypes.c_size_t)(_pack_scan(*a, 0, 0))
     if need:
         if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
             raise ValueError(f"workspace must be contiguous and on {dev}")
         if workspace is None or workspace.nbytes < need:
             workspace = _empty((need,), torch.uint8, dev, stream)
-        a.workspace = workspace.data_ptr()
-        a.workspace_bytes = need
-    _launch("glinattn_selective_scan_packed", a, stream, dev)
+    _run("glinattn_selective_scan_packed", _pack_scan(*a, workspace.data_ptr() if need else 0, need), stream, dev)
     return y
 
 
@@ -948,9 +990,9 @@ def glinattn_add_rms_norm(x, weight=None, residual=None, *, eps=1e-6, group=0, o
         out = _act(y, "y")
         if group or scale is not None or scale_dtype is not None:
             raise ValueError("group and scale belong to a float8_e4m3fn output")
-    a = NormArgs(code, res, out, sd, n, width, group, eps, xs, _addr(x), _addr(residual), _addr(weight), _addr(residual_out),
-                 _addr(y), _addr(scale))
-    _launch("glinattn_add_rms_norm", a, stream, dev)
+    a = _pack_norm(code, res, out, sd, n, width, group, eps, xs, _at(x), _at(residual), _at(weight), _at(residual_out),
+                 _at(y), _at(scale))
+    _run("glinattn_add_rms_norm", a, stream, dev)
     return y, residual_out, scale
 
 

@@ -40,6 +40,27 @@ def test_struct_layout_matches_header(tmp_path):
     assert got == want + [G.E8M0]
 
 
+def test_packed_bytes_are_the_structs():
+    for args, pack in ((G.KvRopeArgs, G._pack_rope), (G.ShortConvArgs, G._pack_conv), (G.ScanPackedArgs, G._pack_scan), (G.NormArgs, G._pack_norm)):
+        values = [k + 1.5 if t is ctypes.c_float else (k + 1) * 0x01020304 % (1 << 31) for k, (_, t) in enumerate(args._fields_)]
+        got = args.from_buffer_copy(pack(*values))
+        assert len(pack(*values)) == ctypes.sizeof(args)
+        assert [getattr(got, f) for f, _ in args._fields_] == values
+
+
+def test_scan_workspace():
+    lib = G.library()
+    size = lambda **kw: lib.glinattn_selective_scan_packed_workspace_size(ctypes.byref(_scan(**kw)))  # noqa: E731
+    long = dict(num_req=1, num_tok=100000, max_q_len=100000, channels=256)
+    need = size(**long)
+    pieces = 100000 // 512
+    assert need >= pieces * 256 * (2 * 16 + 1) * 4 and size(**dict(long, state=12)) == 0
+    assert size(**dict(long, max_q_len=1000)) == 0 and size(num_req=0) == 0 and size(**dict(long, num_req=2000)) == 0
+    far = dict(x=1 << 40, delta=2 << 40, z=3 << 40, Bm=4 << 40, Cm=5 << 40, y=6 << 40)
+    for kw in (dict(), dict(workspace=A), dict(workspace=A, workspace_bytes=need - 1), dict(workspace=A + 8, workspace_bytes=need)):
+        assert lib.glinattn_selective_scan_packed(ctypes.byref(_scan(**long, **far, **kw)), None) == INVALID
+
+
 def _norm(**kw):
     base = dict(in_dtype=G.BF16, residual_dtype=G.BF16, out_dtype=G.BF16, scale_dtype=G.F32, rows=4, width=256, eps=1e-6, x=A,
                 residual=2 * A, weight=3 * A, residual_out=4 * A, y=5 * A)
