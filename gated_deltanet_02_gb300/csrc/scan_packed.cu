@@ -466,9 +466,7 @@ __global__ void __launch_bounds__(Tile<kBf16, N, kK, kC>::kThreads, kC == 1 ? 1 
     if (gate) {
       unpack8(take(stage, 2), f);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        y[k] = __fmul2_rn(y[k], silu2(make_float2(f[2 * k], f[2 * k + 1])));
-      }
+      for (int k = 0; k < 4; ++k) y[k] = __fmul2_rn(y[k], silu2(make_float2(f[2 * k], f[2 * k + 1])));
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) f[2 * k] = y[k].x, f[2 * k + 1] = y[k].y;
@@ -895,7 +893,8 @@ glinattn_status check_sizes(const glinattn_scan_packed_args *a) {
       a->state <= 0 || a->max_q_len < 0 || a->x_stride < 0 || a->delta_stride < 0 || a->z_stride < 0 || a->b_stride < 0 ||
       a->c_stride < 0)
     return GLINATTN_ERR_INVALID_ARG;
-  if ((a->state != 8 && a->state != 16 && a->state != 32) || a->num_req > 65535 || a->channels > (1 << 20)) return GLINATTN_ERR_UNSUPPORTED;
+  if ((a->state != 8 && a->state != 16 && a->state != 32) || a->num_req > 65535 || a->num_tok > (1 << 30) || a->channels > (1 << 20))
+    return GLINATTN_ERR_UNSUPPORTED;
   return GLINATTN_OK;
 }
 

@@ -259,7 +259,8 @@ glinattn_status run(const glinattn_short_conv_args *a, cudaStream_t stream) {
   if (!a || (a->in_dtype != GLINATTN_F32 && a->in_dtype != GLINATTN_BF16) || a->num_req < 0 || a->num_tok < 0 ||
       a->channels <= 0 || a->x_stride < 0 || (a->activation != 0 && a->activation != 1))
     return GLINATTN_ERR_INVALID_ARG;
-  if (a->width < 2 || a->width > 4 || a->num_req > 65535 || a->channels > (1 << 20)) return GLINATTN_ERR_UNSUPPORTED;
+  if (a->width < 2 || a->width > 4 || a->num_req > 65535 || a->num_tok > (1 << 30) || a->channels > (1 << 20))
+    return GLINATTN_ERR_UNSUPPORTED;
   if ((a->conv_pool == nullptr) != (a->slot_ids == nullptr) || (a->conv_pool && a->pool_slots <= 0)) return GLINATTN_ERR_INVALID_ARG;
   if (!a->q_start && a->num_tok != a->num_req) return GLINATTN_ERR_INVALID_ARG;
   if (a->num_req == 0 || a->num_tok == 0) return GLINATTN_OK;

@@ -98,7 +98,7 @@ def _conv(**kw):
 
 PACKED = [
     (dict(in_dtype=G.E4M3), INVALID), (dict(num_req=-1), INVALID), (dict(num_req=65536), UNSUPPORTED), (dict(num_tok=-1), INVALID),
-    (dict(channels=0), INVALID), (dict(channels=(1 << 20) + 1), UNSUPPORTED), (dict(slot_ids=None), INVALID), (dict(pool_slots=0), INVALID),
+    (dict(num_tok=(1 << 30) + 1), UNSUPPORTED), (dict(channels=0), INVALID), (dict(channels=(1 << 20) + 1), UNSUPPORTED), (dict(slot_ids=None), INVALID), (dict(pool_slots=0), INVALID),
     (dict(q_start=None), INVALID), (dict(slot_ids=5 * A + 2), INVALID), (dict(q_start=6 * A + 1), INVALID), (dict(resume=9 * A + 2), INVALID),
     (dict(count=9 * A + 2), INVALID), (dict(x=None), INVALID), (dict(x=A + 1), INVALID), (dict(x_stride=63), INVALID),
     (dict(x_stride=-64), INVALID), (dict(y=7 * A + 8), INVALID), (dict(y=A), INVALID), (dict(y=4 * A), INVALID),
