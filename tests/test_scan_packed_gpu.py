@@ -229,10 +229,11 @@ def test_decreasing_ranges_stay_in_bounds():
         assert torch.equal(pool[other], c["pool"][other])
 
 
+@pytest.mark.parametrize("act,N", [(torch.bfloat16, 16), (torch.float32, 32), (torch.float32, 8)])
 @pytest.mark.parametrize("R,top", [(3, 11), (3, 12), (200, 24), (200, 25)])
-def test_ends_of_the_kernels_ranges(R, top):
+def test_ends_of_the_kernels_ranges(R, top, act, N):
     """The longest requests that the kernel for few rows takes, and the shortest that the other does."""
-    check(case([(7 * r) % (top + 1) for r in range(R - 1)] + [top], 72, 16, torch.bfloat16, seed=top), resume=[int(r % 3 != 1) for r in range(R)])
+    check(case([(7 * r) % (top + 1) for r in range(R - 1)] + [top], 72, N, act, seed=top), resume=[int(r % 3 != 1) for r in range(R)])
 
 
 def test_special_values():
