@@ -31,6 +31,7 @@ struct Params {
 constexpr float kMinScale = 7.888609052210118e-31f;  // 2^-100
 // Squares of values up to 2^128 times this factor add up without an overflow.
 constexpr float kShrink = 1.262177448353619e-29f;    // 2^-96
+constexpr float kLargest = 3.4028234663852886e38f;   // finite fp32
 
 template <bool kMax>
 __device__ __forceinline__ float join(float a, float b) {
@@ -63,7 +64,8 @@ __device__ __forceinline__ float over_row(float v, Shared &shared, int &turn, in
 __device__ __forceinline__ float inverse_root(float sum, int width, float eps) { return 1.0f / sqrtf(sum / (float)width + eps); }
 
 // The scale of a maximum (its bits), what is stored and what values are multiplied with.
-// `root`: what the values, and their maximum, still have to be multiplied with (fp32 scales).
+// `root`: what the values, and their maximum, still have to be multiplied with (fp32 scales), 1 or in
+// [1, 2): so no factor here leaves fp32, 448 / top neither where top * root / 448 is above 2^-100.
 template <bool kPow2>
 __device__ __forceinline__ float scale_of(uint32_t amax, float root, void *scale, size_t at, bool store) {
   if (kPow2) {
@@ -168,9 +170,14 @@ __global__ void __launch_bounds__(kChunks == 1 ? 128 : kChunks == 2 ? 256 : 512,
     }
     float inv = inverse_root(sum, p.width, eps);
     // With scales in fp32 y / scale is h w * 448 / max |h w|: the root enters the scale alone, and the
-    // quotient has two roundings less.  Rows with an infinity or NaN get theirs from the root.
+    // quotient has two roundings less.  Its power of two, an exact factor, stays with the values, so these are
+    // within a factor of 2 of y: none leaves fp32 that y does not, whatever eps and the weights.  Rows with an
+    // infinity or NaN get theirs from the root.
     float root = 1.0f;
-    if (kOut == 2 && inv > 0.0f) root = inv, inv = 1.0f;
+    if (kOut == 2 && inv > 0.0f) {  // a normal number: in 2^-64 .. 2^34, of shrunken values in 2^-32 .. 2^48
+      root = __uint_as_float((__float_as_uint(inv) & 0x007fffffu) | 0x3f800000u);
+      inv = __uint_as_float(__float_as_uint(inv) & 0x7f800000u);
+    }
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
       float v[8];
@@ -200,8 +207,14 @@ __global__ void __launch_bounds__(kChunks == 1 ? 128 : kChunks == 2 ? 256 : 512,
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(h[k][i].x), fabsf(h[k][i].y)));
         top[k] = __float_as_uint(m);
-        if (top[k] == 0x7f800000u) {
+        if (!(m * root <= kLargest)) {  // outputs that are infinite, or that the root would make so
           top[k] = 0;
+          if (root != 1.0f)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 y = __fmul2_rn(h[k][i], make_float2(root, root));
+              h[k][i] = make_float2(fabsf(y.x) <= kLargest ? h[k][i].x : y.x, fabsf(y.y) <= kLargest ? h[k][i].y : y.y);
+            }
 #pragma unroll
           for (int i = 0; i < 4; ++i) top[k] = max(top[k], max(finite_bits(h[k][i].x), finite_bits(h[k][i].y)));
         }
