@@ -812,9 +812,12 @@ cudaError_t launch_ring(const Params &p, cudaStream_t s) {
   const size_t head = (sizeof(RingHead) + 127) & ~(size_t)127;
   int stages = (int)((kRingBytes - head) / stage_bytes);  // two at least, with a larger share of the SM where rows are many
   stages = stages < 2 ? 2 : stages > kRingStages ? kRingStages : stages;
-  static_assert(2 * (G::kStateBytes + kFewRows * G::kRowBytes + 128) <= 200 * 1024, "two stages have to fit");
   const size_t bytes = head + (size_t)stages * stage_bytes;
-  const cudaError_t e = cudaFuncSetAttribute(ring_kernel<kBf16, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  // The limit is the kernel's, for all host threads: what the largest call takes, whatever this one does.
+  constexpr size_t two = ((sizeof(RingHead) + 127) & ~(size_t)127) + 2 * (G::kStateBytes + kFewRows * G::kRowBytes + 128);
+  constexpr size_t most = two > kRingBytes ? two : kRingBytes;
+  static_assert(most <= 200 * 1024, "two stages have to fit");
+  const cudaError_t e = cudaFuncSetAttribute(ring_kernel<kBf16, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e != cudaSuccess) return e;
   const int blocks = (p.D + kRingCh - 1) / kRingCh, together = 4 * 152 / blocks;
   const int per = together < 1 ? 1 : together < p.rows.R ? together : p.rows.R;
