@@ -674,14 +674,15 @@ __global__ void __launch_bounds__(kRingCh + 32, 4) ring_kernel(const Params p, i
   auto wait = [&](uint64_t *bar, int parity) {
     const bool ok = sm100::mbar_wait(bar, (uint32_t)parity & 1u);
     if (!ok && p.rows.dev_status) atomicOr(p.rows.dev_status, GLINATTN_DEV_WAIT_TIMEOUT);
-    return ok;
+    return __all_sync(0xffffffffu, ok) != 0;  // whole warps go on or leave their loop
   };
+  bool ok = true;  // no wait of the warp has given up
   if (threadIdx.x >= kRingCh) {
     // --- the warp that brings: 32 requests are looked up at a time, one lane each
     const int lane = threadIdx.x & 31;
     check_requests(p.rows, (long long)blockIdx.x * 32 + lane, (long long)gridDim.x * 32);
-    int stage = 0, round = 0;
-    for (int n0 = r0; n0 < p.rows.R; n0 += 32 * rstep) {
+    int stage = 0, round = 0, issued = 0;  // stages filled so far
+    for (int n0 = r0; ok && n0 < p.rows.R; n0 += 32 * rstep) {
       Request mine;
       mine.ok = false;
       const long long r = n0 + (long long)lane * rstep;
@@ -691,7 +692,8 @@ __global__ void __launch_bounds__(kRingCh + 32, 4) ring_kernel(const Params p, i
       for (int l = 0; l < many; ++l) {
         const int s0 = __shfl_sync(0xffffffffu, mine.s0, l), run = __shfl_sync(0xffffffffu, mine.run, l);
         const int slot = __shfl_sync(0xffffffffu, mine.slot, l), resumed = __shfl_sync(0xffffffffu, (int)mine.resumed, l);
-        if (!__all_sync(0xffffffffu, wait(&head.empty[stage], round ^ 1))) return;
+        ok = wait(&head.empty[stage], round ^ 1);
+        if (!ok) break;
         uint8_t *to = ring + (size_t)stage * stage_bytes;
         uint64_t *bar = &head.full[stage];
         const int parts = (p.y ? (p.z ? 5 : 4) : 3), row_bytes = (width * (p.y && p.z ? 3 : 2) + N * (p.y ? 2 : 1)) * G::kSize;
@@ -715,8 +717,14 @@ __global__ void __launch_bounds__(kRingCh + 32, 4) ring_kernel(const Params p, i
                            (uint32_t)((states ? N : width) * G::kSize), bar);
         }
         if (++stage == stages) stage = 0, round ^= 1;
+        ++issued;
       }
     }
+    // After a wait that gave up, here or below, the copies on their way land before the CTA leaves its
+    // shared memory to another: a stage's barrier counts their bytes.
+    if (!__syncthreads_and(ok))
+      for (int i = max(0, issued - stages); i < issued; ++i)
+        if (!sm100::mbar_wait(&head.full[i % stages], (uint32_t)(i / stages) & 1u)) break;
     return;
   }
   // --- the warps that run: a thread has a channel.  It goes through its states 16 bytes at a time in an
@@ -735,7 +743,8 @@ __global__ void __launch_bounds__(kRingCh + 32, 4) ring_kernel(const Params p, i
   const int mine = min(32, width - (ch & ~31)) * N * 4;  // bytes of the warp's states
   int stage = 0, round = 0, leaving = -1;                // the stage whose states are on their way back
   for (long long r = r0; r < p.rows.R; r += rstep) {
-    if (!wait(&head.full[stage], round)) return;
+    ok = wait(&head.full[stage], round);
+    if (!ok) break;
     const int4 m = head.meta[stage];
     const int s0 = m.x, run = m.y;
     uint8_t *from = ring + (size_t)stage * stage_bytes;
@@ -799,6 +808,7 @@ __global__ void __launch_bounds__(kRingCh + 32, 4) ring_kernel(const Params p, i
     if (++stage == stages) stage = 0, round ^= 1;
   }
   if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  __syncthreads_and(ok);
 }
 
 // ---------------------------------------------------------------------------
