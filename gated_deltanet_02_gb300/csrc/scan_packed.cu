@@ -840,14 +840,18 @@ constexpr int kPiecedReqs = 1024;  // requests at most: every block looks throug
 
 // Whether requests are run in pieces, which costs a second pass over nearly all rows
 // (without outputs) and balances the SMs.
-bool pieced(int R, int num_tok, int max_len, int D) {
+bool pieced(int R, int num_tok, int max_len, int D, int N) {
   if (R > kPiecedReqs || max_len <= 2 * kPiece || num_tok / kPiece + R > 65535) return false;
-  // In ns: a tile of 32 rows and channels takes 850 where its CTA has an SM to itself, 1,430 where two share one;
-  // both passes over pieces, on full SMs, take 9.2 a tile.  (One request of 8,192 rows and
+  // In ns, at N = 16 in bf16: a tile of 32 rows and channels takes 850 where its CTA has an SM to itself, 1,430 where two
+  // share one; both passes over pieces, on full SMs, take 9.2 a tile.  (One request of 8,192 rows and
   // 4,096 channels: 210 us whole, 305 in pieces; 2,048 channels: 210 and 169.)
+  // A piece reads what all pieces before it in its request end with, at 3,000 bytes a ns, half of that where
+  // they do not fit in L2.  (One request of 2^17 rows and 2,048 channels: 3.2 ms whole, 3.9 in pieces;
+  // 2^20: 26 and 231; 2^18 and 2^20 rows of 256 channels: 6.3 and 25 whole, 1.4 and 15 in pieces.)
   const double ctas = (double)R * ((D + kCh - 1) / kCh), tiles = (max_len + kL - 1) / kL;
   const double whole = ctas <= 152 ? 850.0 * tiles : 1430.0 * tiles * (double)(((long long)ctas + 303) / 304);
-  return 15000.0 + 9.2 * ((double)num_tok / kL) * ((D + kCh - 1) / kCh) < 0.9 * whole;
+  const double before = 0.5 * ((double)num_tok / kPiece) * ((double)max_len / kPiece) * (double)D * (N + 1) * 4.0;
+  return 15000.0 + 9.2 * ((double)num_tok / kL) * ((D + kCh - 1) / kCh) + before / 3000.0 < 0.9 * whole;
 }
 size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
@@ -914,7 +918,7 @@ glinattn_status check_sizes(const glinattn_scan_packed_args *a) {
 // Bytes of the workspace, and where its parts begin; 0 where requests are run whole.
 size_t workspace(const glinattn_scan_packed_args *a, size_t *sums, size_t *starts) {
   const int longest = a->max_q_len < a->num_tok ? a->max_q_len : a->num_tok;
-  if (a->num_req == 0 || a->num_tok == 0 || !pieced(a->num_req, a->num_tok, longest, a->channels)) return 0;
+  if (a->num_req == 0 || a->num_tok == 0 || !pieced(a->num_req, a->num_tok, longest, a->channels, a->state)) return 0;
   const size_t pieces = (size_t)(a->num_tok / kPiece), ends = pieces * a->channels * a->state * 4, each = up16(pieces * a->channels * 4);
   if (sums) *sums = ends, *starts = ends + each;
   return 2 * ends + each;
