@@ -605,7 +605,9 @@ cudaError_t launch_ring(const RecurParams &p, cudaStream_t stream) {
     if (!encode_3d_map(&tmap, p.S_src, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, dims, box, false))
       return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(decode128_kernel<kRing, kNla, kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the limit is the kernel's, for all host threads: what its largest call takes, whatever this one does
+  constexpr int most = (int)smem_bytes(4, ring_steps(kRing), kRing, kNla);
+  cudaError_t e = cudaFuncSetAttribute(decode128_kernel<kRing, kNla, kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(decode128_kernel<kRing, kNla, kOut>, cudaFuncAttributePreferredSharedMemoryCarveout,
                            (int)cudaSharedmemCarveoutMaxShared);

@@ -13,11 +13,12 @@ DEV = torch.device("cuda:0")
 
 
 def in_threads(calls, times):
-    """The C calls (function, argument struct), each in two threads with a stream of its own; every one has to succeed."""
+    """The C calls (function, argument struct), each in a thread and on a stream of its own; every one has to succeed."""
     refused, streams = [], []
-    start = threading.Barrier(2 * len(calls))
+    start = threading.Barrier(len(calls))
 
     def work(f, args, stream):
+        torch.cuda.set_device(DEV)
         start.wait()
         bad = sum(f(ctypes.byref(args), stream.cuda_stream) != 0 for _ in range(times))
         if bad:
@@ -25,9 +26,8 @@ def in_threads(calls, times):
 
     threads = []
     for f, args in calls:
-        for _ in range(2):
-            streams.append(torch.cuda.Stream(DEV))
-            threads.append(threading.Thread(target=work, args=(f, args, streams[-1])))
+        streams.append(torch.cuda.Stream(DEV))
+        threads.append(threading.Thread(target=work, args=(f, args, streams[-1])))
     for t in threads:
         t.start()
     for t in threads:
@@ -43,11 +43,25 @@ def test_packed_scan_of_single_tokens_beside_drafts():
     x, B = torch.zeros((11, D), device=DEV), torch.zeros((11, N), device=DEV)
     ints = torch.tensor([0, 1, 0, 11], dtype=torch.int32, device=DEV)
     f, keep, calls = G.library().glinattn_selective_scan_packed, [], []
-    for q in (1, 11):
+    for q in (1, 11, 1, 11):
         y = torch.empty_like(x)
         keep.append(y)
         at = ints.data_ptr() + (0 if q == 1 else 8)
         calls.append((f, G.ScanPackedArgs(in_dtype=G.F32, out_dtype=G.F32, num_req=1, num_tok=q, channels=D, state=N, pool_slots=1, max_q_len=q,
                                           x=x.data_ptr(), delta=x.data_ptr(), Bm=B.data_ptr(), Cm=B.data_ptr(), A=A.data_ptr(),
                                           state_pool=pool.data_ptr(), slot_ids=ints.data_ptr(), q_start=at, y=y.data_ptr())))
+    in_threads(calls, 20000)
+
+
+def test_decode_in_both_types():
+    """d = 128: a cluster's buffers hold the token's rows in bf16 or in fp32."""
+    H, d = 1, 128
+    ones, slots = torch.ones(H, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    f, keep, calls = G.library().glinattn_decode, [], []
+    for code, act in ((G.BF16, torch.bfloat16), (G.F32, torch.float32)) * 2:
+        x, o, pool = torch.zeros((1, H, d), dtype=act, device=DEV), torch.zeros((1, H, d), dtype=act, device=DEV), torch.zeros((1, H, d, d), device=DEV)
+        keep += [x, o, pool]
+        calls.append((f, G.DecodeArgs(variant=G.GDN, in_dtype=code, out_dtype=code, num_req=1, heads=H, dk=d, dv=d, pool_slots=1, qk_heads=H,
+                                      q=x.data_ptr(), k=x.data_ptr(), v=x.data_ptr(), alpha=ones.data_ptr(), beta=ones.data_ptr(),
+                                      state_pool=pool.data_ptr(), slot_ids=slots.data_ptr(), o=o.data_ptr())))
     in_threads(calls, 20000)
