@@ -8,10 +8,20 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace glinattn {
 namespace sm100 {
+
+// Host: encode(args...), the driver's tensor-map encoder, for a thread of any kind.  It needs the device's
+// context current, which a thread's first call of the runtime would make so: where it fails, once more after one.
+template <typename F, typename... A>
+inline bool encode_tensor_map(F encode, A... args) {
+  if (encode(args...) == CUDA_SUCCESS) return true;
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode(args...) == CUDA_SUCCESS;
+}
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
