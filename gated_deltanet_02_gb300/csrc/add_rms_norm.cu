@@ -250,7 +250,9 @@ __global__ void __launch_bounds__(kChunks == 1 ? 128 : kChunks == 2 ? 256 : 512,
 }
 
 // Any width and alignment: one CTA a row, the row read again (from L2) for each of its
-// passes; every element is read and written by one thread in the last of them.
+// passes; every element is read and written by one thread in the last of them.  Scalar loads bound it, two readings or, to
+// e4m3, three: 15,001 rows of 4,095 in bf16 with a residual 194 us (2,540 GB/s, 79 with 4,096 in the kernel above), rows of 4,096 off
+// by an element to e4m3 395, 2,048 rows of 32,768 301 us (1,780 GB/s), four rows of 2,047 4.4.
 template <bool kXBf16, int kRes, int kOut>
 __global__ void __launch_bounds__(512) norm_any_kernel(const Params p) {
   __shared__ Shared shared;

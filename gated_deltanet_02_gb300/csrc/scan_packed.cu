@@ -25,10 +25,12 @@
 //
 // Bound.  scan_kernel: reads of shared memory.  A warp's 16-byte load takes 4 cycles of the SM's one port, 2
 // where neighbouring lanes share it; per row and four states of a channel B, C, the step and the partial
-// sum take 6 cycles, with two channels a thread 4; the helpers 13 a row.  That is 0.9 cycles an SM for 32
-// elements or more, beside 1 for their exponentials (32 lanes a cycle) and 1 for their packed arithmetic.  One
-// prompt of 8,191 rows, 4,096 channels, 16 states: 204 us (2.6 10^12 elements/s, 1.6 us a tile for each of 128
-// CTAs on 152 SMs); 8 prompts of 200 .. 4,001 rows, 2,048 channels: 240 us (2.8 10^12).
+// sum take 6 cycles, with two channels a thread 4; the helpers 13 a row.  At 16 states that is 39 cycles a row of
+// 512 elements with one channel a thread, 2.4 for 32 elements, and 1.5 with two (counted: 38.8 M wavefronts beside 25.5 M
+// instructions of the exponential unit), beside 1 for their exponentials (32 lanes a cycle) and 1 for their packed arithmetic.  One
+// prompt of 8,191 rows, 4,096 channels, 16 states: 204 us (2.6 10^12 elements/s, 0.8 us a tile for each of 128
+// CTAs on 152 SMs); 8 prompts of 200 .. 4,001 rows, 2,048 channels: 240 us (2.8 10^12), the port busy 62% of it. With 8 and 32
+// states 179 and 312, 219 and 353 us; in fp32 with 16 states 276 and 326; rows that no 16 bytes fit 570 (4,095 channels) and 434.
 // ring_kernel: HBM bytes, the states in and out: 256 tokens of 2,048 channels 13.6 us, 5,270 GB/s.
 //
 // Measured and not kept: groups of scan warps that hand the states on from 8 rows to the next 8 (305 us
@@ -58,8 +60,9 @@ struct Params {
 };
 
 // log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1]; log(1 + e) = e P(e), P of degree 8
-// fitted to log(1 + e) / e on [0, 1] with a relative error of 3e-8, so a small result keeps its
-// relative error.  Two at a time.
+// fitted to log(1 + e) / e on [0, 1]: the rounded coefficients are within 7.1e-8 of it, from below (6e-8
+// for small e, c[0] being 1 - 2^-24), so a small result keeps its relative error but for the exponential's
+// argument, whose rounding adds about |x| 2^-24 (5e-6 at x = -80).  Two at a time.
 __device__ __forceinline__ float2 softplus2(float2 x) {
   const float2 e = make_float2(exp2_fast(-fabsf(x.x) * kLog2e), exp2_fast(-fabsf(x.y) * kLog2e));
   constexpr float c[9] = {0.9999999403953552f, -0.4999949336051941f, 0.3331909775733948f, -0.2484298199415207f, 0.19106005132198334f,
@@ -882,7 +885,7 @@ cudaError_t launch_many(const Params &p, cudaStream_t s) {
 
 template <bool kBf16, int N>
 cudaError_t launch(const Params &p, bool vector, cudaStream_t s) {
-  // Rows one after the other with all states in flight, or 32 channels a CTA: 8 requests of 2,048 channels take 3 + 0.43 us
+  // Rows one after the other with all states in flight, or 32 channels a CTA; measured at N = 16 in bf16: 8 requests of 2,048 channels take 3 + 0.43 us
   // a row and, up to 32 rows, 7.8 us; 64 requests of 17, 24 and 32 rows 23, 31, 48 us and 46, 48, 50 us.
   const bool many = (long long)p.rows.R * ((p.D + kCh - 1) / kCh) > 304;
   if (p.rows.max_len <= (many ? kFewRows : 11)) {

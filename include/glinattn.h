@@ -616,7 +616,8 @@ glinattn_status glinattn_kv_append_rope(const glinattn_kv_rope_args *args, glina
  *   decreasing, a count outside [0, its rows]) sets GLINATTN_DEV_BAD_COUNT, a slot outside
  *   [0, pool_slots) sets GLINATTN_DEV_BAD_SLOT; either skips the request, which leaves its
  *   outputs and its slot as they were.  With a decreasing q_start rows of other
- *   requests may be left out too.  R <= 65535, num_tok <= 2^30, C and D <= 2^20.
+ *   requests may be left out too.  With R or num_tok 0 nothing is run and nothing flagged.
+ *   R <= 65535, num_tok <= 2^30, C and D <= 2^20.
  *   Activations are all bf16 or all fp32.  x, delta, z, Bm and Cm may be slices of wider
  *   rows: *_stride, in elements, is the distance of their rows (0: contiguous), and their
  *   base needs the alignment of an element only (16 bytes, and a stride that is a
